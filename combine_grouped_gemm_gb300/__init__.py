@@ -17,6 +17,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libmoe.so")
 
 MOE_BF16, MOE_FP8_E4M3, MOE_FP8_E4M3_POW2 = 0, 1, 2
+MOE_F32 = 3   # dtype of a weight gradient only
 MOE_DEV_TIMEOUT, MOE_DEV_BOUNDS, MOE_DEV_SCALE = 1, 2, 4
 MOE_LAYER_EVENTS = 7
 STAGE_NAMES = ["route", "dispatch", "ffn_setup", "ffn_gate_up", "ffn_down", "combine"]
@@ -59,6 +60,12 @@ class LayerOpts(ctypes.Structure):
                 ("side_ctas", ctypes.c_int32), ("placement", ctypes.POINTER(PlacementC))]
 
 
+class GroupCfg(ctypes.Structure):
+    """moe_group_cfg: the shape of one grouped product (rows in all, groups, weights [n][k])."""
+    _fields_ = [("rows", ctypes.c_int32), ("E", ctypes.c_int32), ("n", ctypes.c_int32),
+                ("k", ctypes.c_int32)]
+
+
 class Weights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in
                 ("w13", "w13_scales", "w2", "w2_scales", "ws13", "ws13_scales", "ws2",
@@ -85,6 +92,15 @@ def _load():
         "moe_place_experts": [I, I, I, P, I, P, P, P],
         "moe_query_sizes_placed": [P, I, P],
         "moe_expert_ffn_gather": [P, P, P, P, P, P, P, P, S],
+        "moe_grouped_query": [P, P],
+        "moe_grouped_mm": [P, P, P, P, P, P, S],
+        "moe_grouped_mm_dx": [P, P, P, P, P, P, S],
+        "moe_grouped_mm_dw": [P, P, P, P, P, I, I, P, S],
+        "moe_act_save": [I, I, P, P, P, S],
+        "moe_act_load": [I, I, I, P, P, P, P, P, S],
+        "moe_swiglu_save": [I, I, P, P, P, P, S],
+        "moe_swiglu_grad": [I, I, P, P, P, P, P, S],
+        "moe_combine_grad": [I, I, I, I, P, P, P, P, P, P, P, S],
         "moe_clear_status": [P, S],
         "moe_read_status": [P, P, S],
         "moe_selftest_wait": [P, ctypes.c_int64, S],
@@ -104,7 +120,9 @@ _lib = _load()
 EXPORTED = ["moe_validate", "moe_query_sizes", "moe_route", "moe_route_noalloc", "moe_dispatch",
             "moe_expert_ffn", "moe_combine", "moe_layer", "moe_layer_ex", "moe_dispatch_index",
             "moe_expert_ffn_gather", "moe_place_experts", "moe_query_sizes_placed",
-            "moe_clear_status", "moe_read_status", "moe_selftest_wait",
+            "moe_grouped_query", "moe_grouped_mm", "moe_grouped_mm_dx", "moe_grouped_mm_dw",
+            "moe_act_save", "moe_act_load", "moe_swiglu_save", "moe_swiglu_grad",
+            "moe_combine_grad", "moe_clear_status", "moe_read_status", "moe_selftest_wait",
             "moe_strerror", "moe_abi_version", "moe_last_cuda_error"]
 
 
@@ -292,6 +310,140 @@ def expert_ffn_gather(cfg, x, counts, src_tok, weights: dict, ebuf, shared_out, 
            _lib.moe_expert_ffn_gather(ctypes.byref(make_cfg(cfg)), _p(x), _p(counts), _p(src_tok),
                                       ctypes.byref(w), _p(ebuf), _p(shared_out), _p(ws),
                                       _s(stream)))
+
+
+# ---------------------------------------------------------------------------------------------
+# Training of the expert path (see include/moe.h). Row counts and widths are taken from the
+# tensors; a tensor of another type or size than the call needs is a ValueError.
+# ---------------------------------------------------------------------------------------------
+def _need(fn, name, t, dtype, *shape):
+    """_p(t), for a tensor that must have this element type and shape. int8 and e4m3 tensors
+    count as bytes."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{fn}: {name} must be a CUDA tensor")
+    if t.dtype is not dtype and not (dtype is torch.uint8 and t.dtype in
+                                     (torch.int8, torch.float8_e4m3fn)):
+        raise ValueError(f"{fn}: {name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{fn}: {name} must have shape {shape}, got {tuple(t.shape)}")
+    return _p(t)
+
+
+def grouped_ws_bytes(g: GroupCfg) -> int:
+    """Bytes of the grouped products' workspace for this shape; zero it once before its first
+    use."""
+    n = ctypes.c_size_t(0)
+    _check("moe_grouped_query", _lib.moe_grouped_query(ctypes.byref(g), ctypes.byref(n)))
+    return n.value
+
+
+def _need_ws(fn, g, ws):
+    if not isinstance(ws, torch.Tensor) or ws.numel() * ws.element_size() < grouped_ws_bytes(g):
+        raise ValueError(f"{fn}: ws must be a CUDA tensor of grouped_ws_bytes(cfg) bytes")
+    return _p(ws)
+
+
+def grouped_mm(g: GroupCfg, x, counts, w, y, ws, stream=None):
+    """y[r] = x[r] . w[e]^T for every row r of group e (counts rows each, in group order)."""
+    fn, bf = "moe_grouped_mm", torch.bfloat16
+    _check(fn, _lib.moe_grouped_mm(ctypes.byref(g), _need(fn, "x", x, bf, g.rows, g.k),
+                                   _need(fn, "counts", counts, torch.int32, g.E),
+                                   _need(fn, "w", w, bf, g.E, g.n, g.k),
+                                   _need(fn, "y", y, bf, g.rows, g.n), _need_ws(fn, g, ws),
+                                   _s(stream)))
+
+
+def grouped_mm_dx(g: GroupCfg, dy, counts, w, dx, ws, stream=None):
+    """dx[r] = dy[r] . w[e]: the gradient of grouped_mm's rows."""
+    fn, bf = "moe_grouped_mm_dx", torch.bfloat16
+    _check(fn, _lib.moe_grouped_mm_dx(ctypes.byref(g), _need(fn, "dy", dy, bf, g.rows, g.n),
+                                      _need(fn, "counts", counts, torch.int32, g.E),
+                                      _need(fn, "w", w, bf, g.E, g.n, g.k),
+                                      _need(fn, "dx", dx, bf, g.rows, g.k), _need_ws(fn, g, ws),
+                                      _s(stream)))
+
+
+def grouped_mm_dw(g: GroupCfg, dy, x, counts, dw, ws, accumulate=False, stream=None):
+    """dw[e] = sum of dy[r]^T x[r] over group e's rows (accumulate: added to dw, fp32 only): the
+    gradient of grouped_mm's weights. dw bf16 or fp32."""
+    fn, bf = "moe_grouped_mm_dw", torch.bfloat16
+    f32 = isinstance(dw, torch.Tensor) and dw.dtype is torch.float32
+    _check(fn, _lib.moe_grouped_mm_dw(ctypes.byref(g), _need(fn, "dy", dy, bf, g.rows, g.n),
+                                      _need(fn, "x", x, bf, g.rows, g.k),
+                                      _need(fn, "counts", counts, torch.int32, g.E),
+                                      _need(fn, "dw", dw, torch.float32 if f32 else bf, g.E, g.n,
+                                            g.k),
+                                      MOE_F32 if f32 else MOE_BF16, int(bool(accumulate)),
+                                      _need_ws(fn, g, ws), _s(stream)))
+
+
+def _rows_cols(fn, name, t):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{fn}: {name} must be a 2-D CUDA tensor")
+    return t.shape
+
+
+def act_save(x, q, scales, stream=None):
+    """Keeps bf16 rows x [rows][d] as e4m3 codes q (bytes [rows][d]) and fp32 scales
+    [d/128][rows]."""
+    fn = "moe_act_save"
+    rows, d = _rows_cols(fn, "x", x)
+    _check(fn, _lib.moe_act_save(rows, d, _need(fn, "x", x, torch.bfloat16, rows, d),
+                                 _need(fn, "q", q, torch.uint8, rows, d),
+                                 _need(fn, "scales", scales, torch.float32, d // 128, rows),
+                                 _s(stream)))
+
+
+def act_load(q, scales, index, out, stream=None, status=None):
+    """out[i] = the saved row index[i] in bf16 (index None: row i; -1: zeros)."""
+    fn = "moe_act_load"
+    src, d = _rows_cols(fn, "q", q)
+    rows = _rows_cols(fn, "out", out)[0]
+    _check(fn, _lib.moe_act_load(rows, src, d, _need(fn, "q", q, torch.uint8, src, d),
+                                 _need(fn, "scales", scales, torch.float32, d // 128, src),
+                                 None if index is None else
+                                 _need(fn, "index", index, torch.int32, rows),
+                                 _need(fn, "out", out, torch.bfloat16, rows, d), _p(status),
+                                 _s(stream)))
+
+
+def swiglu_save(gu, a, q, scales, stream=None):
+    """a = silu(g) * u of gu = [g | u] [rows][2f], with gu kept as act_save keeps it."""
+    fn = "moe_swiglu_save"
+    rows, f2 = _rows_cols(fn, "gu", gu)
+    f = f2 // 2
+    _check(fn, _lib.moe_swiglu_save(rows, f, _need(fn, "gu", gu, torch.bfloat16, rows, 2 * f),
+                                    _need(fn, "a", a, torch.bfloat16, rows, f),
+                                    _need(fn, "q", q, torch.uint8, rows, 2 * f),
+                                    _need(fn, "scales", scales, torch.float32, 2 * f // 128, rows),
+                                    _s(stream)))
+
+
+def swiglu_grad(q, scales, da, dgu, a=None, stream=None):
+    """dgu [rows][2f], and a [rows][f] again (None: not wanted), from swiglu_save's codes."""
+    fn = "moe_swiglu_grad"
+    rows, f = _rows_cols(fn, "da", da)
+    _check(fn, _lib.moe_swiglu_grad(rows, f, _need(fn, "q", q, torch.uint8, rows, 2 * f),
+                                    _need(fn, "scales", scales, torch.float32, 2 * f // 128, rows),
+                                    _need(fn, "da", da, torch.bfloat16, rows, f),
+                                    _need(fn, "dgu", dgu, torch.bfloat16, rows, 2 * f),
+                                    None if a is None else
+                                    _need(fn, "a", a, torch.bfloat16, rows, f), _s(stream)))
+
+
+def combine_grad(ebuf, row_of, topk_w, dy, debuf, dtopk_w, stream=None, status=None):
+    """The gradient of combine: debuf (rows of ebuf) and dtopk_w [T][k] from dy [T][d]."""
+    fn, bf = "moe_combine_grad", torch.bfloat16
+    T, d = _rows_cols(fn, "dy", dy)
+    k = _rows_cols(fn, "row_of", row_of)[1]
+    rows = _rows_cols(fn, "ebuf", ebuf)[0]
+    _check(fn, _lib.moe_combine_grad(T, k, d, rows, _need(fn, "ebuf", ebuf, bf, rows, d),
+                                     _need(fn, "row_of", row_of, torch.int32, T, k),
+                                     _need(fn, "topk_w", topk_w, torch.float32, T, k),
+                                     _need(fn, "dy", dy, bf, T, d),
+                                     _need(fn, "debuf", debuf, bf, rows, d),
+                                     _need(fn, "dtopk_w", dtopk_w, torch.float32, T, k),
+                                     _p(status), _s(stream)))
 
 
 def clear_status(ws, stream=None):

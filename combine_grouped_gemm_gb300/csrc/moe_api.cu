@@ -599,6 +599,141 @@ int moe_expert_ffn_gather(const moe_cfg* cfg, const void* x, const int32_t* coun
   return e == cudaSuccess ? MOE_OK : cuda_fail(e);
 }
 
+namespace {
+int check_group(const moe_group_cfg* c) {
+  if (!c || c->rows < 0 || c->E < 1 || c->n < 1 || c->k < 1) return MOE_ERR_INVALID_ARG;
+  if (c->E > 1024 || c->n % 8 || c->k % 8) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+// in0, in1, out, with how many of the three are row tensors (NULL allowed when rows == 0)
+int run_grouped(const moe_group_cfg* cfg, GroupedDir dir, const void* in0, const void* in1,
+                const int32_t* counts, void* out, bool f32, bool accumulate, void* ws,
+                cudaStream_t stream) {
+  const int rc = check_group(cfg);
+  if (rc != MOE_OK) return rc;
+  const bool empty = cfg->rows == 0;
+  if (!(empty && !in0)) MOE_NEED(in0);
+  if (!(empty && !in1 && dir == kGroupedDw)) MOE_NEED(in1);
+  MOE_NEED(counts);
+  if (!(empty && !out && dir != kGroupedDw)) MOE_NEED(out);
+  MOE_NEED(ws);
+  if (empty && dir != kGroupedDw) return MOE_OK;
+  const cudaError_t e =
+      launch_grouped(*cfg, dir, in0, in1, counts, out, f32, accumulate, ws, stream);
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e);
+}
+
+bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+
+int check_rows(int32_t rows, int32_t cols) {
+  if (rows < 0 || cols < 1) return MOE_ERR_INVALID_ARG;
+  return cols % 128 ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+}  // namespace
+
+int moe_grouped_query(const moe_group_cfg* cfg, size_t* ws_bytes) {
+  const int rc = check_group(cfg);
+  if (rc != MOE_OK) return rc;
+  if (!ws_bytes) return MOE_ERR_INVALID_ARG;
+  *ws_bytes = grouped_ws_bytes(*cfg);
+  return MOE_OK;
+}
+
+int moe_grouped_mm(const moe_group_cfg* cfg, const void* x, const int32_t* counts, const void* w,
+                   void* y, void* ws, cudaStream_t stream) {
+  return run_grouped(cfg, kGroupedFwd, x, w, counts, y, false, false, ws, stream);
+}
+
+int moe_grouped_mm_dx(const moe_group_cfg* cfg, const void* dy, const int32_t* counts,
+                      const void* w, void* dx, void* ws, cudaStream_t stream) {
+  return run_grouped(cfg, kGroupedDx, dy, w, counts, dx, false, false, ws, stream);
+}
+
+int moe_grouped_mm_dw(const moe_group_cfg* cfg, const void* dy, const void* x,
+                      const int32_t* counts, void* dw, int32_t dw_dtype, int32_t accumulate,
+                      void* ws, cudaStream_t stream) {
+  if (dw_dtype != MOE_BF16 && dw_dtype != MOE_F32) return MOE_ERR_INVALID_ARG;
+  if (accumulate && dw_dtype != MOE_F32) return MOE_ERR_INVALID_ARG;
+  return run_grouped(cfg, kGroupedDw, dy, x, counts, dw, dw_dtype == MOE_F32, accumulate != 0, ws,
+                     stream);
+}
+
+int moe_act_save(int32_t rows, int32_t d, const void* x, void* q, float* scales,
+                 cudaStream_t stream) {
+  const int rc = check_rows(rows, d);
+  if (rc != MOE_OK || rows == 0) return rc;
+  MOE_NEED(x);
+  MOE_NEED(q);
+  MOE_NEED(scales);
+  const cudaError_t e = launch_quant_rows_e4m3(x, rows, d, q, scales, stream);
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e);
+}
+
+int moe_act_load(int32_t rows, int32_t src_rows, int32_t d, const void* q, const float* scales,
+                 const int32_t* index, void* out, uint32_t* status, cudaStream_t stream) {
+  const int rc = check_rows(rows, d);
+  if (rc != MOE_OK) return rc;
+  if (src_rows < 0 || (!index && src_rows < rows)) return MOE_ERR_INVALID_ARG;
+  if (rows == 0) return MOE_OK;
+  if (src_rows > 0) {
+    MOE_NEED(q);
+    MOE_NEED(scales);
+  }
+  MOE_OPT(index);
+  MOE_NEED(out);
+  if (status && misaligned4(status)) return MOE_ERR_MISALIGNED;
+  const cudaError_t e =
+      launch_act_load(rows, src_rows, d, q, scales, index, out, status, stream);
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e);
+}
+
+int moe_swiglu_save(int32_t rows, int32_t f, const void* gu, void* a, void* q, float* scales,
+                    cudaStream_t stream) {
+  const int rc = check_rows(rows, f);
+  if (rc != MOE_OK || rows == 0) return rc;
+  MOE_NEED(gu);
+  MOE_NEED(a);
+  MOE_NEED(q);
+  MOE_NEED(scales);
+  const cudaError_t e = launch_swiglu_save(rows, f, gu, a, q, scales, stream);
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e);
+}
+
+int moe_swiglu_grad(int32_t rows, int32_t f, const void* q, const float* scales, const void* da,
+                    void* dgu, void* a, cudaStream_t stream) {
+  const int rc = check_rows(rows, f);
+  if (rc != MOE_OK || rows == 0) return rc;
+  MOE_NEED(q);
+  MOE_NEED(scales);
+  MOE_NEED(da);
+  MOE_NEED(dgu);
+  MOE_OPT(a);
+  const cudaError_t e = launch_swiglu_grad(rows, f, q, scales, da, dgu, a, stream);
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e);
+}
+
+int moe_combine_grad(int32_t T, int32_t k, int32_t d, int32_t rows, const void* ebuf,
+                     const int32_t* row_of, const float* topk_w, const void* dy, void* debuf,
+                     float* dtopk_w, uint32_t* status, cudaStream_t stream) {
+  if (T < 0 || k < 1 || d < 1 || rows < 0) return MOE_ERR_INVALID_ARG;
+  if (k > 32 || d % 128 || (long long)T * k > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  if (T == 0) return MOE_OK;
+  if (rows > 0) {
+    MOE_NEED(ebuf);
+    MOE_NEED(debuf);
+    if (ebuf == debuf) return MOE_ERR_INVALID_ARG;
+  }
+  MOE_NEED(row_of);
+  MOE_NEED(topk_w);
+  MOE_NEED(dy);
+  MOE_NEED(dtopk_w);
+  if (status && misaligned4(status)) return MOE_ERR_MISALIGNED;
+  const cudaError_t e = launch_combine_grad(T, k, d, rows, ebuf, row_of, topk_w, dy, debuf,
+                                            dtopk_w, status, stream);
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e);
+}
+
 int moe_clear_status(void* ws, cudaStream_t stream) {
   if (!ws) return MOE_ERR_INVALID_ARG;
   cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(uint32_t), stream);

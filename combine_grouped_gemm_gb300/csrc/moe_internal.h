@@ -183,6 +183,25 @@ cudaError_t launch_ffn_gemm_mx8(const moe_cfg& c, const WsLayout& L, int stage, 
 cudaError_t launch_quant_rows_e4m3(const void* x, int T, int d, void* out, float* scales,
                                    cudaStream_t st, bool pdl = false, bool pow2 = false);
 
+// Training of the expert path. The shapes are checked by the callers (moe_api.cu).
+enum GroupedDir { kGroupedFwd = 0, kGroupedDx = 1, kGroupedDw = 2 };
+// Bytes of the workspace of the grouped products (the status word comes first).
+size_t grouped_ws_bytes(const moe_group_cfg& c);
+// One grouped product. fwd: in0 = x, in1 = w, out = y; dx: dy, w, dx; dw: dy, x, dw.
+cudaError_t launch_grouped(const moe_group_cfg& c, GroupedDir dir, const void* in0, const void* in1,
+                           const int32_t* counts, void* out, bool out_f32, bool accumulate,
+                           void* ws, cudaStream_t st);
+
+cudaError_t launch_act_load(int rows, int src_rows, int d, const void* q, const float* scales,
+                            const int32_t* index, void* out, uint32_t* status, cudaStream_t st);
+cudaError_t launch_swiglu_save(int rows, int f, const void* gu, void* a, void* q, float* scales,
+                               cudaStream_t st);
+cudaError_t launch_swiglu_grad(int rows, int f, const void* q, const float* scales,
+                               const void* da, void* dgu, void* a, cudaStream_t st);
+cudaError_t launch_combine_grad(int T, int k, int d, int rows, const void* ebuf,
+                                const int32_t* row_of, const float* topk_w, const void* dy,
+                                void* debuf, float* dtopk_w, uint32_t* status, cudaStream_t st);
+
 // 2-D row-major tensor map [rows][cols] with a box of box_rows x 128 bytes, 128-byte swizzle.
 bool make_tensor_map_2d(CUtensorMap* m, const void* base, int elem_bytes, uint64_t cols,
                         uint64_t rows, uint32_t box_rows);

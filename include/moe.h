@@ -341,6 +341,98 @@ int moe_expert_ffn_gather(const moe_cfg* cfg, const void* x, const int32_t* coun
                           const int32_t* src_tok, const moe_weights* w, void* ebuf,
                           void* shared_out, void* ws, cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------------------
+ * Training of the expert path
+ *
+ * The gradients of the expert stage and what they need from the forward pass. One training step
+ * of the layer's experts, with the dispatch of a one-rank configuration (R = 1: expert e's rows
+ * are contiguous, in expert order, counts [E]):
+ *   forward : moe_route, moe_dispatch -> moe_grouped_mm (gate/up) -> moe_swiglu_save
+ *             -> moe_grouped_mm (down) -> moe_combine;   moe_act_save keeps x
+ *   backward: moe_combine_grad -> moe_grouped_mm_dx, moe_grouped_mm_dw (down)
+ *             -> moe_swiglu_grad -> moe_grouped_mm_dx (gate/up)
+ *             -> moe_act_load (x's rows) -> moe_grouped_mm_dw (gate/up)
+ *             -> moe_combine with weights of one (dx: the dispatch's gradient)
+ * The pages cover inference only and have no counterpart to these calls.
+ * ------------------------------------------------------------------------------------- */
+
+/* Shape of one grouped product. The row tensors hold the rows of the E groups one group after
+ * another: group e owns rows [s_e, s_e + counts[e]), s_e = counts[0] + ... + counts[e-1]. */
+typedef struct moe_group_cfg {
+  int32_t rows;  /* rows of the row tensors, >= 0; the groups own the first sum(counts) of them */
+  int32_t E;     /* groups (experts), 1 <= E <= 1024 */
+  int32_t n;     /* rows of each group's weight matrix; n % 8 == 0 */
+  int32_t k;     /* its columns; k % 8 == 0 */
+} moe_group_cfg;
+
+/* Bytes of the workspace that the grouped products of this shape take. The first word of the
+ * workspace is its status word (moe_clear_status, moe_read_status); the caller zeroes the
+ * workspace once, before its first use, and every call leaves it ready for the next. Calls that
+ * may overlap on the GPU need workspaces of their own. MOE_ERR_INVALID_ARG for a negative or
+ * zero size, MOE_ERR_UNSUPPORTED for n or k not a multiple of 8 or E > 1024. */
+int moe_grouped_query(const moe_group_cfg* cfg, size_t* ws_bytes);
+
+/* Matrix products grouped by expert, rows of any number per group (0 included). bf16 operands,
+ * sums in fp32. counts: int32 [E] on the device (as moe_dispatch writes them for R = 1), read on
+ * the device, so no call waits for them. A negative count, or counts that pass `rows` in all,
+ * are reported (MOE_DEV_BOUNDS) and cut to what fits. Rows that no group owns are neither read
+ * into a result nor written.
+ *   forward:            y[r]  = bf16( x[r] . W_e^T )        x [rows][k], w [E][n][k], y [rows][n]
+ *   gradient of rows:   dx[r] = bf16( dy[r] . W_e )         dy [rows][n], dx [rows][k]
+ *   gradient of W:      dW_e  = sum over the group's rows of dy[r]^T x[r]         dw [E][n][k]
+ * dw_dtype: MOE_BF16 or MOE_F32. accumulate (MOE_F32 only, else MOE_ERR_INVALID_ARG): dW_e is
+ * added to dw instead of replacing it. An empty group's dW_e is 0. The results do not depend on
+ * the order in which the GPU runs the work (no floating-point atomics). With rows == 0 the row
+ * tensors may be NULL. */
+#define MOE_F32 3 /* dw_dtype only */
+int moe_grouped_mm(const moe_group_cfg* cfg, const void* x, const int32_t* counts, const void* w,
+                   void* y, void* ws, cudaStream_t stream);
+int moe_grouped_mm_dx(const moe_group_cfg* cfg, const void* dy, const int32_t* counts,
+                      const void* w, void* dx, void* ws, cudaStream_t stream);
+int moe_grouped_mm_dw(const moe_group_cfg* cfg, const void* dy, const void* x,
+                      const int32_t* counts, void* dw, int32_t dw_dtype, int32_t accumulate,
+                      void* ws, cudaStream_t stream);
+
+/* Activation checkpoints in 8 bits: bf16 rows kept for the backward pass as e4m3 codes with one
+ * fp32 scale per 128 columns, by the dispatch's rule (scale = amax/448, or 1 if amax is 0; code
+ * = e4m3(x/scale), nearest even, saturating; the amax is over the block's numbers). Scales are
+ * block-major: the scale of block b of row r at scales[b * rows + r]. A NaN stays a NaN; an
+ * infinity makes its block read back as NaN.
+ * moe_act_save: x bf16 [rows][d] -> q [rows][d] bytes, scales [d/128][rows]. d % 128 == 0.
+ * moe_act_load: out[i] = bf16(code * scale) of saved row index[i] (index int32 [rows], NULL: row
+ *   i), out bf16 [rows][d]; src_rows: the saved rows. An index of -1 gives a row of zeros; any
+ *   other index outside [0, src_rows) does too and is reported (MOE_DEV_BOUNDS in status, NULL
+ *   or a device uint32). With the token of each expert row as the index (src_tok of
+ *   moe_dispatch), x is kept once per token, not once per expert row. */
+int moe_act_save(int32_t rows, int32_t d, const void* x, void* q, float* scales,
+                 cudaStream_t stream);
+int moe_act_load(int32_t rows, int32_t src_rows, int32_t d, const void* q, const float* scales,
+                 const int32_t* index, void* out, uint32_t* status, cudaStream_t stream);
+
+/* SwiGLU of the gate/up product, keeping its input in 8 bits. gu bf16 [rows][2f] (gate, then
+ * up), f % 128 == 0: a = bf16(silu(g) * u) [rows][f] from the bf16 values; q [rows][2f] and
+ * scales [2f/128][rows] as moe_act_save(gu). */
+int moe_swiglu_save(int32_t rows, int32_t f, const void* gu, void* a, void* q, float* scales,
+                    cudaStream_t stream);
+
+/* Gradient of that SwiGLU from the saved codes, g and u being code * scale, s = 1/(1+exp(-g)):
+ *   dgu = bf16 of [ da u s (1 + g (1 - s)) | da g s ]   [rows][2f];  da bf16 [rows][f]
+ *   a   = bf16(g s u) [rows][f], the down product's input again (NULL: not wanted). */
+int moe_swiglu_grad(int32_t rows, int32_t f, const void* q, const float* scales, const void* da,
+                    void* dgu, void* a, cudaStream_t stream);
+
+/* Gradient of moe_combine. dy bf16 [T][d]; row_of int32 [T][k] and topk_w fp32 [T][k] as given to
+ * the combine; ebuf bf16 [rows][d] its expert rows:
+ *   debuf[row_of[t][i]] = bf16(topk_w[t][i] * dy[t]);  dtopk_w[t][i] = dy[t] . ebuf[row_of[t][i]]
+ * (summed in fp32 in a fixed order). Rows of debuf that no choice names are not written. A
+ * negative row_of is a choice that the dispatch skipped: its dtopk_w is 0. One at or past rows is
+ * treated so too and reported (MOE_DEV_BOUNDS in status, NULL or a device uint32). The shared
+ * expert's rows have dy itself as gradient. d % 128 == 0, 1 <= k <= 32,
+ * T * k < 2^31. debuf may not be ebuf. */
+int moe_combine_grad(int32_t T, int32_t k, int32_t d, int32_t rows, const void* ebuf,
+                     const int32_t* row_of, const float* topk_w, const void* dy, void* debuf,
+                     float* dtopk_w, uint32_t* status, cudaStream_t stream);
+
 /* Sets the device status word in ws to 0 (enqueued on stream). */
 int moe_clear_status(void* ws, cudaStream_t stream);
 
