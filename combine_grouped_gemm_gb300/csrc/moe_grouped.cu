@@ -4,6 +4,29 @@
 //   dx : dx[r][j]   = sum_i dy[r][i] W_e[i][j]
 //   dw : dW_e[i][j] = sum_r dy[r][i] x[r][j]   (r over the group's rows)
 // bf16 operands, fp32 sums, each result rounded once where it is stored in bf16.
+//
+// One kernel for the three, on the 5th-generation tensor cores with CTA pairs (cta_group::2,
+// M = 256). M is always the output's contiguous dimension, so an accumulator row (one tensor-
+// memory lane, one thread of the epilogue) is an output column and a warp stores 32 consecutive
+// columns at a time; N is the output's row:
+//        M (256)        N (up to TN)            reduction    A                  B
+//   fwd  columns of y   rows of the group       k            W_e, K-major       x, K-major
+//   dx   columns of dx  rows of the group       n            W_e, MN-major      dy, K-major
+//   dw   columns of dW  rows of dW              the rows     x, MN-major        dy, MN-major
+// Weights come through 3-D tensor maps, so what a tile reads past a group's own matrix is zero.
+// In fwd and dx, rows past a group's end only feed accumulator columns that are not stored. In
+// dw they would be summed: the last k-step of a group zeroes what follows its rows in shared
+// memory before the MMA reads it (0 x NaN is not 0, so both operands are).
+//
+// Each pair walks the units (group, 256 output columns, N tile) from its number in steps of the
+// pairs; a group's units are weight-tile-major, so pairs that run side by side share a weight
+// tile through L2. The tables of the units are built by every CTA from the counts itself: one
+// launch, no schedule kernel.
+//
+// Roles in a CTA (320 threads, one CTA per SM): warp 0 TMA producer, warp 1 MMA issuer (leader
+// CTA; in the peer it relays dw's zeroed tails), warps 2..9 epilogue. Loads of both CTAs count on
+// the leader's full barriers, its commits free the stages of both. Accumulators are double
+// buffered. Every wait is bounded.
 #include "moe_device.cuh"
 
 namespace moe {
@@ -47,86 +70,439 @@ __device__ __forceinline__ void group_offsets(const int32_t* counts, int E, int 
   __syncthreads();
 }
 
-constexpr int kTile = 64, kStep = 16;
+// Epilogue warps: two per tensor-memory quarter, or four where the sums of a tile are held in
+// registers (fp32 weight gradients: 64 columns a thread).
+template <bool F32>
+struct GroupedThreads {
+  static constexpr int kEpi = F32 ? 16 : 8;
+  static constexpr int kAll = (2 + kEpi) * 32;
+};
+// fp32 weight gradients: k-steps per tensor-core sum. The tensor core truncates as it adds, an
+// error that grows with the number of additions (2.1e-6 of the result after 2048 products,
+// 4.4e-6 after 4096, against 4e-7 for rounded fp32 sums); sums of 512 rows are therefore read
+// out and added in registers, rounded.
+constexpr int kSumSteps = 8;
 
-// 64x64 output tile, 256 threads, 4x4 outputs each, operands staged in shared memory as floats.
-// fwd/dx: blockIdx.y numbers the 64-row tiles of all groups; dw: blockIdx.z is the group.
-template <int DIR>
-__global__ void __launch_bounds__(256) grouped_kernel(
-    const __nv_bfloat16* __restrict__ in0, const __nv_bfloat16* __restrict__ in1,
-    const int32_t* __restrict__ counts, void* out, int rows, int E, int n, int k, int out_f32,
-    int accumulate, uint32_t* status) {
-  __shared__ int off[kMaxGroups + 1];
-  __shared__ float sa[kStep][kTile + 1], sb[kStep][kTile + 1];
-  group_offsets(counts, E, rows, off, status);
-  int g = 0, r0 = 0, r1 = 0;
+struct GroupedArgs {
+  const int32_t* counts;
+  void* out;
+  uint32_t* status;
+  int rows, E, n, k;
+  int cols;       // output columns (M)
+  int red;        // fwd, dx: length of the reduction
+  int mt;         // ceil(cols / 256)
+  int accumulate;
+};
+
+template <int TN, int STAGES>
+struct GroupedShape {
+  static constexpr int A_BYTES = 128 * 128;
+  static constexpr int B_BYTES = TN / 2 * 128;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int TMEM_COLS = 2 * TN;
+  static constexpr int SMEM = STAGES * STAGE_BYTES + 1024 + 512;
+  static_assert(B_BYTES % 1024 == 0 && TMEM_COLS <= 512 && TMEM_COLS >= 32, "");
+};
+
+struct GroupedUnit {
+  int g;      // group
+  int f0;     // first output column of the pair
+  int n0;     // fwd, dx: first row; dw: first row of dW_g
+  int nlen;   // rows of the tile
+  int r0;     // dw: the group's first row
+  int red;    // length of the reduction
+  int nt;     // N tiles that read this unit's weight tile
+};
+
+template <int DIR, int TN>
+__device__ __forceinline__ GroupedUnit grouped_unit(const GroupedArgs& a, const int* off,
+                                                    const int* tcum, int u) {
+  GroupedUnit r;
+  int m;
   if (DIR == kGroupedDw) {
-    g = blockIdx.z;
-    r0 = off[g];
-    r1 = off[g + 1];
+    r.nt = (a.n + TN - 1) / TN;
+    const int per = a.mt * r.nt;
+    r.g = u / per;
+    const int local = u - r.g * per;
+    m = local / r.nt;
+    r.n0 = (local - m * r.nt) * TN;
+    r.nlen = min(TN, a.n - r.n0);
+    r.r0 = off[r.g];
+    r.red = off[r.g + 1] - r.r0;
   } else {
-    int t = blockIdx.y;
-    for (; g < E; ++g) {
-      const int nt = (off[g + 1] - off[g] + kTile - 1) / kTile;
-      if (t < nt) break;
-      t -= nt;
+    const int t = u / a.mt;
+    int lo = 0, hi = a.E - 1;   // last group whose first tile is <= t (empty groups share it)
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (tcum[mid] <= t) lo = mid;
+      else hi = mid - 1;
     }
-    if (g == E) return;
-    r0 = off[g] + t * kTile;
-    r1 = off[g + 1];
+    r.g = lo;
+    r.nt = tcum[lo + 1] - tcum[lo];
+    const int local = u - tcum[lo] * a.mt;
+    m = local / r.nt;
+    r.n0 = off[lo] + (local - m * r.nt) * TN;
+    r.nlen = min(TN, off[lo + 1] - r.n0);
+    r.r0 = 0;
+    r.red = a.red;
   }
-  // output rows m0.., columns c0.., the reduction's length
-  const int m0 = DIR == kGroupedDw ? blockIdx.y * kTile : r0, c0 = blockIdx.x * kTile;
-  const int m_end = DIR == kGroupedDw ? n : r1;
-  const int cols = DIR == kGroupedFwd ? n : k;
-  const int red = DIR == kGroupedFwd ? k : DIR == kGroupedDx ? n : r1 - r0;
-  const size_t wbase = (size_t)g * n * k;
-  float acc[4][4] = {};
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  for (int p0 = 0; p0 < red; p0 += kStep) {
-    for (int i = threadIdx.x; i < kTile * kStep; i += 256) {
-      int p, m;
-      float va = 0.0f, vb = 0.0f;
-      if (DIR == kGroupedDw) {
-        p = i / kTile, m = i % kTile;
-        if (p0 + p < red) {
-          const size_t r = (size_t)r0 + p0 + p;
-          if (m0 + m < n) va = __bfloat162float(in0[r * n + m0 + m]);
-          if (c0 + m < k) vb = __bfloat162float(in1[r * k + c0 + m]);
+  r.f0 = m * 256;
+  return r;
+}
+
+// A whole warp's wait: every lane gets the same answer, so the warp leaves its loop together.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                          uint32_t* status, uint64_t limit_ns = kWaitLimitNs) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status, limit_ns));
+}
+__device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity,
+                                                  volatile int* abort, uint32_t* status) {
+  return __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity, abort, status));
+}
+
+// Zeroes the reduction rows [from, to) of a stage's MN-major boxes (128-byte rows; the swizzle
+// permutes bytes inside a row only) and orders the writes before the tensor core's reads.
+__device__ __forceinline__ void zero_rows(uint8_t* stage, int boxes, int from, int to, int lane) {
+  const int per = (to - from) * 8;   // 16-byte pieces per box
+  for (int i = lane; i < boxes * per; i += 32) {
+    const int b = i / per, j = i - b * per;
+    *reinterpret_cast<uint4*>(stage + b * 8192 + from * 128 + j * 16) = make_uint4(0, 0, 0, 0);
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+template <int DIR, int TN, int STAGES, bool F32>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>::kAll, 1)
+    grouped_kernel(const GroupedArgs a, const __grid_constant__ CUtensorMap mapA,
+                   const __grid_constant__ CUtensorMap mapB) {
+  using S = GroupedShape<TN, STAGES>;
+  constexpr bool kDw = DIR == kGroupedDw;
+  constexpr int kEpiWarps = GroupedThreads<F32>::kEpi;
+  constexpr int kBoxesB = kDw ? TN / 128 : 0;
+  static_assert(!kDw || TN >= 128, "dw: whole 64-column boxes");
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ int off[kMaxGroups + 1];
+  __shared__ int tcum[kDw ? 1 : kMaxGroups + 1];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * S::STAGE_BYTES);
+  uint64_t* empty = full + STAGES;
+  uint64_t* tfull = empty + STAGES;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* tail = tempty + 2;       // dw, peer: its own loads of a step whose tail it zeroes
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail + STAGES);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == 0;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(&full[i], kDw ? 2 : 1);   // the leader's expect_tx; dw: and the peer
+      mbar_init(&empty[i], 1);
+      mbar_init(&tail[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tfull[i], 1);
+      mbar_init(&tempty[i], 2 * kEpiWarps);
+    }
+    *abort_flag = 0;
+    mbar_fence_init();
+    tma_prefetch_map(&mapA);
+    tma_prefetch_map(&mapB);
+  }
+  group_offsets(a.counts, a.E, a.rows, off, a.status);
+  if (!kDw && warp == 0) {   // token tiles before each group
+    const int per = (a.E + 31) / 32, e0 = min(a.E, lane * per), e1 = min(a.E, e0 + per);
+    int sum = 0;
+    for (int e = e0; e < e1; ++e) sum += (off[e + 1] - off[e] + TN - 1) / TN;
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    int at = incl - sum;
+    for (int e = e0; e < e1; ++e) {
+      tcum[e] = at;
+      at += (off[e + 1] - off[e] + TN - 1) / TN;
+    }
+    if (lane == 31) tcum[a.E] = incl;
+  }
+  if (warp == 1) tmem_alloc_pair(tmem_slot, S::TMEM_COLS);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // the peer's barriers and tensor memory are ready
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int units = kDw ? a.E * a.mt * ((a.n + TN - 1) / TN) : tcum[a.E] * a.mt;
+  constexpr int kNever = 1 << 30;
+  constexpr int kSum = F32 ? kSumSteps : kNever;   // k-steps per tensor-core sum
+
+  if (warp == 0) {
+    // ------------------------------ TMA producer ------------------------------
+    if (lane == 0) {
+      const uint64_t pol_once = l2_policy_evict_first(), pol_keep = l2_policy_evict_last();
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int u = pair; u < units && ok; u += pairs) {
+        const GroupedUnit t = grouped_unit<DIR, TN>(a, off, tcum, u);
+        // each CTA's half of the N tile, a multiple of 16 rows (an MMA takes N in steps of 32)
+        const int half = ((t.nlen + 31) & ~31) >> 1;
+        const int steps = (t.red + 63) >> 6;
+        const uint64_t pol_a = kDw || t.nt > 1 ? pol_keep : pol_once;
+        const int f = t.f0 + static_cast<int>(rank) * 128;
+        const int nb = t.n0 + static_cast<int>(rank) * half;
+        for (int ks = 0; ks < steps; ++ks) {
+          if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, a.status)) {
+            ok = false;
+            break;
+          }
+          uint8_t* sa = smem + stage * S::STAGE_BYTES;
+          uint8_t* sb = sa + S::A_BYTES;
+          const bool cut = kDw && (t.red - ks * 64 < 64) && (t.red & 15);
+          uint32_t bar = cluster_addr(&full[stage], 0);
+          if (leader) {
+            mbar_arrive_expect_tx(&full[stage], (cut ? 1 : 2) * S::STAGE_BYTES);
+          } else if (kDw) {
+            if (cut) {
+              mbar_arrive_expect_tx(&tail[stage], S::STAGE_BYTES);
+              bar = cluster_addr(&tail[stage], rank);
+            } else {
+              mbar_arrive_cluster(bar);
+            }
+          }
+          if (DIR == kGroupedFwd) {
+            tma_load_3d_pair(sa, &mapA, bar, ks * 64, f, t.g, pol_a);
+          } else if (DIR == kGroupedDx) {
+            tma_load_3d_pair(sa, &mapA, bar, f, ks * 64, t.g, pol_a);
+            tma_load_3d_pair(sa + 8192, &mapA, bar, f + 64, ks * 64, t.g, pol_a);
+          } else {
+            tma_load_2d_pair(sa, &mapA, bar, f, t.r0 + ks * 64, pol_a);
+            tma_load_2d_pair(sa + 8192, &mapA, bar, f + 64, t.r0 + ks * 64, pol_a);
+          }
+          if (kDw) {
+#pragma unroll
+            for (int j = 0; j < kBoxesB; ++j)
+              tma_load_2d_pair(sb + j * 8192, &mapB, bar, nb + 64 * j, t.r0 + ks * 64, pol_keep);
+          } else {
+            tma_load_2d_pair(sb, &mapB, bar, ks * 64, nb, pol_keep);
+          }
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1 && leader) {
+    // ------------------------------ MMA issuer ------------------------------
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    int it = 0;
+    for (int u = pair; u < units && ok; u += pairs) {
+      const GroupedUnit t = grouped_unit<DIR, TN>(a, off, tcum, u);
+      const uint32_t n_mma = static_cast<uint32_t>((t.nlen + 31) & ~31);
+      const uint32_t idesc = idesc_bf16(256, n_mma) | (DIR != kGroupedFwd ? kIdescAmn : 0u) |
+                             (kDw ? kIdescBmn : 0u);
+      const int steps = (t.red + 63) >> 6;
+      for (int k0 = 0; k0 < steps && ok; k0 += kSum) {
+        const int k1 = min(steps, k0 + kSum);
+        const int b = it & 1;
+        if (!warp_wait_cluster(&tempty[b], ((it >> 1) & 1) ^ 1u, abort_flag, a.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + b * TN;
+        for (int ks = k0; ks < k1; ++ks) {
+          if (!warp_wait_cluster(&full[stage], phase, abort_flag, a.status)) {
+            ok = false;
+            break;
+          }
+          uint8_t* st = smem + stage * S::STAGE_BYTES;
+          const int left = t.red - ks * 64;
+          const int slices = left >= 64 ? 4 : (left + 15) >> 4;
+          if (kDw && left < 64 && (left & 15)) zero_rows(st, 2 + kBoxesB, left, slices * 16, lane);
+          tc_fence_after();
+          if (lane == 0) {
+            const uint32_t sa = smem_addr(st), sb = sa + S::A_BYTES;
+            for (int kk = 0; kk < slices; ++kk) {
+              const uint64_t da = DIR == kGroupedFwd ? smem_desc_sw128(sa + kk * 32)
+                                                     : smem_desc_sw128_mn(sa + kk * 2048);
+              const uint64_t db = kDw ? smem_desc_sw128_mn(sb + kk * 2048)
+                                      : smem_desc_sw128(sb + kk * 32);
+              mma_f16_pair(d, da, db, idesc, (ks != k0 || kk != 0) ? 1u : 0u);
+            }
+            mma_commit_pair(&empty[stage]);
+          }
+          __syncwarp();
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (ok && lane == 0) mma_commit_pair(&tfull[b]);
+        __syncwarp();
+        ++it;
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------ dw, peer: tails ------------------------------
+    // The peer's loads of a step that ends inside a 16-row slice count on its own barrier; it
+    // zeroes what follows the group's rows in its shared memory, then arrives for the step.
+    if (kDw) {
+      uint32_t phases = 0;   // bit s: parity of the next use of tail[s]
+      int stage = 0;
+      for (int u = pair; u < units; u += pairs) {
+        const GroupedUnit t = grouped_unit<DIR, TN>(a, off, tcum, u);
+        const int steps = (t.red + 63) >> 6;
+        stage = (stage + steps) % STAGES;
+        if ((t.red & 15) == 0) continue;
+        const int last = (stage + STAGES - 1) % STAGES;   // stage of the unit's last step
+        // (many units may pass between two tails; an abort of another role ends the wait)
+        if (!warp_wait(&tail[last], (phases >> last) & 1u, abort_flag, a.status,
+                       30 * kWaitLimitNs))
+          break;
+        phases ^= 1u << last;
+        const int left = t.red - (steps - 1) * 64;
+        zero_rows(smem + last * S::STAGE_BYTES, 2 + kBoxesB, left, (left + 15) & ~15, lane);
+        if (lane == 0) mbar_arrive_cluster(cluster_addr(&full[last], 0));
+        __syncwarp();
+      }
+    }
+  } else {
+    // ------------------------------ epilogue ------------------------------
+    // Warp w reads lanes 32 (w % 4) .. +31 (output columns) of its part of the tile's N columns.
+    const int quarter = warp & 3, part = (warp - 2) >> 2;
+    int it = 0;
+    bool ok = true;
+    for (int u = pair; u < units && ok; u += pairs) {
+      const GroupedUnit t = grouped_unit<DIR, TN>(a, off, tcum, u);
+      const int steps = (t.red + 63) >> 6;
+      const int f = t.f0 + static_cast<int>(rank) * 128 + quarter * 32 + lane;
+      const bool in = f < a.cols;
+      const size_t row0 = (kDw ? (size_t)t.g * a.n : 0) + t.n0;
+      if constexpr (F32) {
+        constexpr int kCols = TN / (kEpiWarps / 4);   // of this warp, in registers
+        float acc[kCols];
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) acc[j] = 0.0f;
+        for (int k0 = 0; k0 < steps; k0 += kSum) {
+          const int b = it & 1;
+          if (!warp_wait(&tfull[b], (it >> 1) & 1, abort_flag, a.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t tb =
+              tmem + (static_cast<uint32_t>(quarter * 32) << 16) + b * TN + part * kCols;
+#pragma unroll
+          for (int c = 0; c < kCols; c += 16) {
+            uint32_t v[16];
+            tmem_ld16(tb + c, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) acc[c + j] += __uint_as_float(v[j]);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(cluster_addr(&tempty[b], 0));
+          ++it;
+        }
+        if (!ok) break;
+        if (!in || (a.accumulate && steps == 0)) continue;
+        float* out = static_cast<float*>(a.out) + (row0 + part * kCols) * a.cols + f;
+        const int mine = t.nlen - part * kCols;   // rows of this warp's part that exist
+#pragma unroll
+        for (int c = 0; c < kCols; c += 16) {
+          float* o = out + (size_t)c * a.cols;
+          if (a.accumulate) {
+            float old[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              old[j] = c + j < mine ? o[(size_t)j * a.cols] : 0.0f;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) acc[c + j] += old[j];
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (c + j < mine) o[(size_t)j * a.cols] = acc[c + j];
         }
       } else {
-        p = i % kStep, m = i / kStep;
-        if (p0 + p < red && m0 + m < m_end)
-          va = __bfloat162float(in0[(size_t)(m0 + m) * red + p0 + p]);
-        if (p0 + p < red && c0 + m < cols)
-          vb = __bfloat162float(DIR == kGroupedFwd
-                                    ? in1[wbase + (size_t)(c0 + m) * k + p0 + p]
-                                    : in1[wbase + (size_t)(p0 + p) * k + c0 + m]);
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + row0 * a.cols + f;
+        if (steps == 0) {   // dw of an empty group
+          for (int p = part; p < t.nlen; p += kEpiWarps / 4)
+            if (in) out[(size_t)p * a.cols] = __float2bfloat16_rn(0.0f);
+          continue;
+        }
+        const int b = it & 1;
+        if (!warp_wait(&tfull[b], (it >> 1) & 1, abort_flag, a.status)) break;
+        tc_fence_after();
+        const uint32_t tb = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + b * TN;
+        for (int c = part * 16; c < t.nlen; c += kEpiWarps * 4) {
+          uint32_t v[16];
+          tmem_ld16(tb + c, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (in && c + j < t.nlen)
+              out[(size_t)(c + j) * a.cols] = __float2bfloat16_rn(__uint_as_float(v[j]));
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(cluster_addr(&tempty[b], 0));
+        ++it;
       }
-      sa[p][m] = va;
-      sb[p][m] = vb;
     }
-    __syncthreads();
-#pragma unroll
-    for (int p = 0; p < kStep; ++p)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] += sa[p][ty * 4 + i] * sb[p][tx + 16 * j];
-    __syncthreads();
   }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int m = m0 + ty * 4 + i, c = c0 + tx + 16 * j;
-      if (m >= m_end || c >= cols) continue;
-      const size_t o = (DIR == kGroupedDw ? wbase : 0) + (size_t)m * cols + c;
-      if (out_f32) {
-        float* f = static_cast<float*>(out) + o;
-        *f = accumulate ? *f + acc[i][j] : acc[i][j];
-      } else {
-        static_cast<__nv_bfloat16*>(out)[o] = __float2bfloat16_rn(acc[i][j]);
-      }
-    }
+
+  // an aborted role leaves copies in flight: they land long before this ends
+  if (*abort_flag) __nanosleep(1000000);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // neither CTA leaves while the other still reads or signals it
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, S::TMEM_COLS);
+  }
+}
+
+template <int DIR, int TN, int STAGES, bool F32>
+cudaError_t run_grouped_kernel(const GroupedArgs& a, const CUtensorMap& mA, const CUtensorMap& mB,
+                               cudaStream_t st) {
+  using S = GroupedShape<TN, STAGES>;
+  auto kern = grouped_kernel<DIR, TN, STAGES, F32>;
+  const cudaError_t err = ensure_smem_limit(reinterpret_cast<const void*>(kern), S::SMEM);
+  if (err != cudaSuccess) return err;
+  return launch_kernel(kern, dim3(sm_count() & ~1), dim3(GroupedThreads<F32>::kAll), S::SMEM, st, false, a,
+                       mA, mB);
+}
+
+// N tile of fwd and dx: the smallest that takes a group's mean rows, so that a batch of few rows
+// spends its shared memory on weight stages.
+int row_tile(const moe_group_cfg& c) {
+  const int live = c.E < c.rows ? c.E : c.rows;
+  const long long mean = (c.rows + live - 1) / live;
+  return mean <= 32 ? 32 : mean <= 64 ? 64 : mean <= 128 ? 128 : 256;
+}
+
+template <int DIR>
+cudaError_t run_rows(int tn, const GroupedArgs& a, const CUtensorMap& mA, const CUtensorMap& mB,
+                     cudaStream_t st) {
+  switch (tn) {
+    case 32: return run_grouped_kernel<DIR, 32, 10, false>(a, mA, mB, st);
+    case 64: return run_grouped_kernel<DIR, 64, 9, false>(a, mA, mB, st);
+    case 128: return run_grouped_kernel<DIR, 128, 8, false>(a, mA, mB, st);
+    default: return run_grouped_kernel<DIR, 256, 6, false>(a, mA, mB, st);
+  }
 }
 
 }  // namespace
@@ -136,18 +512,40 @@ size_t grouped_ws_bytes(const moe_group_cfg&) { return 256; }
 cudaError_t launch_grouped(const moe_group_cfg& c, GroupedDir dir, const void* in0, const void* in1,
                            const int32_t* counts, void* out, bool out_f32, bool accumulate,
                            void* ws, cudaStream_t st) {
-  auto t = [](int v) { return static_cast<unsigned>((v + kTile - 1) / kTile); };
-  const unsigned row_tiles = t(c.rows) + c.E;
-  const dim3 grid = dir == kGroupedFwd  ? dim3(t(c.n), row_tiles)
-                    : dir == kGroupedDx ? dim3(t(c.k), row_tiles)
-                                        : dim3(t(c.k), t(c.n), c.E);
-  auto kern = dir == kGroupedFwd  ? grouped_kernel<kGroupedFwd>
-              : dir == kGroupedDx ? grouped_kernel<kGroupedDx>
-                                  : grouped_kernel<kGroupedDw>;
-  return launch_kernel(kern, grid, dim3(256), 0, st, false,
-                       static_cast<const __nv_bfloat16*>(in0),
-                       static_cast<const __nv_bfloat16*>(in1), counts, out, c.rows, c.E, c.n, c.k,
-                       out_f32 ? 1 : 0, accumulate ? 1 : 0, static_cast<uint32_t*>(ws));
+  if (c.rows == 0) {   // dw without rows: zeros, or nothing to add
+    if (accumulate) return cudaSuccess;
+    return cudaMemsetAsync(out, 0, (size_t)c.E * c.n * c.k * (out_f32 ? 4 : 2), st);
+  }
+  GroupedArgs a{};
+  a.counts = counts;
+  a.out = out;
+  a.status = static_cast<uint32_t*>(ws);
+  a.rows = c.rows;
+  a.E = c.E;
+  a.n = c.n;
+  a.k = c.k;
+  a.cols = dir == kGroupedFwd ? c.n : c.k;
+  a.red = dir == kGroupedFwd ? c.k : c.n;
+  a.mt = (a.cols + 255) / 256;
+  a.accumulate = accumulate ? 1 : 0;
+  CUtensorMap mA, mB;
+  bool ok;
+  const int tn = dir == kGroupedDw ? 256 : row_tile(c);
+  if (dir == kGroupedDw) {
+    ok = make_tensor_map_2d(&mA, in1, 2, c.k, c.rows, 64) &&
+         make_tensor_map_2d(&mB, in0, 2, c.n, c.rows, 64);
+  } else {
+    ok = make_tensor_map_3d_bf16(&mA, in1, c.k, c.n, c.E, dir == kGroupedFwd ? 128 : 64) &&
+         make_tensor_map_2d(&mB, in0, 2, a.red, c.rows, tn / 2);
+  }
+  if (!ok) return cudaErrorInvalidValue;
+  switch (dir) {
+    case kGroupedFwd: return run_rows<kGroupedFwd>(tn, a, mA, mB, st);
+    case kGroupedDx: return run_rows<kGroupedDx>(tn, a, mA, mB, st);
+    default:
+      return out_f32 ? run_grouped_kernel<kGroupedDw, 256, 6, true>(a, mA, mB, st)
+                     : run_grouped_kernel<kGroupedDw, 256, 6, false>(a, mA, mB, st);
+  }
 }
 
 }  // namespace moe
