@@ -23,8 +23,8 @@
 // tile through L2. The tables of the units are built by every CTA from the counts itself: one
 // launch, no schedule kernel.
 //
-// Roles in a CTA (320 threads, one CTA per SM): warp 0 TMA producer, warp 1 MMA issuer (leader
-// CTA; in the peer it relays dw's zeroed tails), warps 2..9 epilogue. Loads of both CTAs count on
+// Roles in a CTA (one CTA per SM): warp 0 TMA producer, warp 1 MMA issuer (leader CTA), warp 2
+// zeroes dw's tails, the others the epilogue. Loads of both CTAs count on
 // the leader's full barriers, its commits free the stages of both. Accumulators are double
 // buffered. Every wait is bounded.
 #include "moe_device.cuh"
@@ -70,18 +70,22 @@ __device__ __forceinline__ void group_offsets(const int32_t* counts, int E, int 
   __syncthreads();
 }
 
-// Epilogue warps: two per tensor-memory quarter, or four where the sums of a tile are held in
-// registers (fp32 weight gradients: 64 columns a thread).
+// Warps 0, 1 and 2 load, issue the MMAs and zero tails; the others are the epilogue: two warps per
+// tensor-memory quarter, or four where the sums of a tile are held in registers (fp32 weight
+// gradients: 64 columns a thread).
 template <bool F32>
 struct GroupedThreads {
   static constexpr int kEpi = F32 ? 16 : 8;
-  static constexpr int kAll = (2 + kEpi) * 32;
+  static constexpr int kAll = (3 + kEpi) * 32;
 };
 // fp32 weight gradients: k-steps per tensor-core sum. The tensor core truncates as it adds, an
 // error that grows with the number of additions (2.1e-6 of the result after 2048 products,
 // 4.4e-6 after 4096, against 4e-7 for rounded fp32 sums); sums of 512 rows are therefore read
 // out and added in registers, rounded.
 constexpr int kSumSteps = 8;
+// bf16 epilogue: a warp turns 32 output rows x 32 columns around in shared memory, rows 80 bytes
+// apart (64 used), which keeps the eight 16-byte rows of a matrix store in different banks.
+constexpr int kTurnPitch = 80, kTurnBytes = 32 * kTurnPitch;
 
 struct GroupedArgs {
   const int32_t* counts;
@@ -94,16 +98,25 @@ struct GroupedArgs {
   int accumulate;
 };
 
-template <int TN, int STAGES>
+template <int TN, int STAGES, bool F32>
 struct GroupedShape {
   static constexpr int A_BYTES = 128 * 128;
   static constexpr int B_BYTES = TN / 2 * 128;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr int TMEM_COLS = 2 * TN;
-  static constexpr int SMEM = STAGES * STAGE_BYTES + 1024 + 512;
+  static constexpr int TURN = F32 ? 0 : GroupedThreads<F32>::kEpi * kTurnBytes;
+  static constexpr int SMEM = STAGES * STAGE_BYTES + TURN + 1024 + 512;
   static_assert(B_BYTES % 1024 == 0 && TMEM_COLS <= 512 && TMEM_COLS >= 32, "");
 };
 
+// The groups with work, in shared memory: fwd and dx list those that have rows.
+struct GroupedTables {
+  int off[kMaxGroups + 1];   // first row of each group
+  int live[kMaxGroups];      // fwd, dx: the groups with rows
+  int n_live;
+};
+
+// One unit of work: 256 output columns (the pair's) x one N tile of one group.
 struct GroupedUnit {
   int g;      // group
   int f0;     // first output column of the pair
@@ -114,50 +127,78 @@ struct GroupedUnit {
   int nt;     // N tiles that read this unit's weight tile
 };
 
+// Walks a pair's units: numbers pair, pair + pairs, ... of the groups' units one group after the
+// other, weight-tile-major (unit m * nt + j of a group: N tile j of its 256 columns number m).
+// fwd, dx: a group of c rows has nt = ceil(c / TN) N tiles of equal size (to 32 rows, the step of
+// an MMA's N) rather than full ones and a rest, which would cost a whole pass over the weight
+// tile for a few rows (16384 rows over 32 experts, about half of them just over 512: forward
+// 796 -> 680 us).
 template <int DIR, int TN>
-__device__ __forceinline__ GroupedUnit grouped_unit(const GroupedArgs& a, const int* off,
-                                                    const int* tcum, int u) {
-  GroupedUnit r;
-  int m;
-  if (DIR == kGroupedDw) {
-    r.nt = (a.n + TN - 1) / TN;
-    const int per = a.mt * r.nt;
-    r.g = u / per;
-    const int local = u - r.g * per;
-    m = local / r.nt;
-    r.n0 = (local - m * r.nt) * TN;
-    r.nlen = min(TN, a.n - r.n0);
-    r.r0 = off[r.g];
-    r.red = off[r.g + 1] - r.r0;
-  } else {
-    const int t = u / a.mt;
-    int lo = 0, hi = a.E - 1;   // last group whose first tile is <= t (empty groups share it)
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (tcum[mid] <= t) lo = mid;
-      else hi = mid - 1;
-    }
-    r.g = lo;
-    r.nt = tcum[lo + 1] - tcum[lo];
-    const int local = u - tcum[lo] * a.mt;
-    m = local / r.nt;
-    r.n0 = off[lo] + (local - m * r.nt) * TN;
-    r.nlen = min(TN, off[lo + 1] - r.n0);
-    r.r0 = 0;
-    r.red = a.red;
+struct GroupedWalk {
+  const GroupedArgs& a;
+  const GroupedTables& tab;
+  int i, local, step, nt, w, base, len;
+
+  __device__ __forceinline__ GroupedWalk(const GroupedArgs& a_, const GroupedTables& t_, int pair,
+                                         int pairs)
+      : a(a_), tab(t_), i(0), local(pair), step(pairs) {
+    load();
+    settle();
   }
-  r.f0 = m * 256;
-  return r;
-}
+  __device__ __forceinline__ int groups() const {
+    return DIR == kGroupedDw ? a.E : tab.n_live;
+  }
+  __device__ __forceinline__ bool more() const { return i < groups(); }
+  __device__ __forceinline__ void load() {   // the group at position i
+    if (DIR == kGroupedDw) {
+      nt = (a.n + TN - 1) / TN;
+      w = TN;
+    } else if (i < tab.n_live) {
+      const int g = tab.live[i];
+      base = tab.off[g];
+      len = tab.off[g + 1] - base;
+      nt = (len + TN - 1) / TN;
+      w = nt == 1 ? TN : ((len + nt - 1) / nt + 31) & ~31;
+    }
+  }
+  __device__ __forceinline__ void settle() {
+    while (more() && local >= nt * a.mt) {
+      local -= nt * a.mt;
+      ++i;
+      load();
+    }
+  }
+  __device__ __forceinline__ void next() {
+    local += step;
+    settle();
+  }
+  __device__ __forceinline__ GroupedUnit unit() const {
+    GroupedUnit r;
+    const int m = nt == 1 ? local : local / nt;
+    const int j = local - m * nt;
+    r.f0 = m * 256;
+    r.nt = nt;
+    if (DIR == kGroupedDw) {
+      r.g = i;
+      r.n0 = j * TN;
+      r.nlen = min(TN, a.n - r.n0);
+      r.r0 = tab.off[i];
+      r.red = tab.off[i + 1] - r.r0;
+    } else {
+      r.g = tab.live[i];
+      r.n0 = base + j * w;
+      r.nlen = min(w, len - j * w);
+      r.r0 = 0;
+      r.red = a.red;
+    }
+    return r;
+  }
+};
 
 // A whole warp's wait: every lane gets the same answer, so the warp leaves its loop together.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
                                           uint32_t* status, uint64_t limit_ns = kWaitLimitNs) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status, limit_ns));
-}
-__device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity,
-                                                  volatile int* abort, uint32_t* status) {
-  return __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity, abort, status));
 }
 
 // Zeroes the reduction rows [from, to) of a stage's MN-major boxes (128-byte rows; the swizzle
@@ -176,22 +217,25 @@ template <int DIR, int TN, int STAGES, bool F32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>::kAll, 1)
     grouped_kernel(const GroupedArgs a, const __grid_constant__ CUtensorMap mapA,
                    const __grid_constant__ CUtensorMap mapB) {
-  using S = GroupedShape<TN, STAGES>;
+  using S = GroupedShape<TN, STAGES, F32>;
   constexpr bool kDw = DIR == kGroupedDw;
   constexpr int kEpiWarps = GroupedThreads<F32>::kEpi;
   constexpr int kBoxesB = kDw ? TN / 128 : 0;
   static_assert(!kDw || TN >= 128, "dw: whole 64-column boxes");
   extern __shared__ uint8_t smem_raw[];
-  __shared__ int off[kMaxGroups + 1];
-  __shared__ int tcum[kDw ? 1 : kMaxGroups + 1];
+  __shared__ GroupedTables tab;
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + STAGES * S::STAGE_BYTES);
+  uint8_t* turn = smem + STAGES * S::STAGE_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(turn + S::TURN);
   uint64_t* empty = full + STAGES;
   uint64_t* tfull = empty + STAGES;
   uint64_t* tempty = tfull + 2;
-  uint64_t* tail = tempty + 2;       // dw, peer: its own loads of a step whose tail it zeroes
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tail + STAGES);
+  // dw, steps whose tail is zeroed: each CTA's loads count on its own tail barrier; the leader's
+  // ptail says that the peer has zeroed its part
+  uint64_t* tail = tempty + 2;
+  uint64_t* ptail = tail + STAGES;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ptail + STAGES);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -200,9 +244,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES; ++i) {
-      mbar_init(&full[i], kDw ? 2 : 1);   // the leader's expect_tx; dw: and the peer
+      mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
       mbar_init(&tail[i], 1);
+      mbar_init(&ptail[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tfull[i], 1);
@@ -213,23 +258,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
     tma_prefetch_map(&mapA);
     tma_prefetch_map(&mapB);
   }
-  group_offsets(a.counts, a.E, a.rows, off, a.status);
-  if (!kDw && warp == 0) {   // token tiles before each group
-    const int per = (a.E + 31) / 32, e0 = min(a.E, lane * per), e1 = min(a.E, e0 + per);
-    int sum = 0;
-    for (int e = e0; e < e1; ++e) sum += (off[e + 1] - off[e] + TN - 1) / TN;
-    int incl = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
+  group_offsets(a.counts, a.E, a.rows, tab.off, a.status);
+  if (!kDw && warp == 0) {
+    int at = 0;
+    for (int e0 = 0; e0 < a.E; e0 += 32) {
+      const int e = e0 + lane;
+      const bool has = e < a.E && tab.off[e + 1] > tab.off[e];
+      const uint32_t m = __ballot_sync(0xffffffffu, has);
+      if (has) tab.live[at + __popc(m & ((1u << lane) - 1u))] = e;
+      at += __popc(m);
     }
-    int at = incl - sum;
-    for (int e = e0; e < e1; ++e) {
-      tcum[e] = at;
-      at += (off[e + 1] - off[e] + TN - 1) / TN;
-    }
-    if (lane == 31) tcum[a.E] = incl;
+    if (lane == 0) tab.n_live = at;
   }
   if (warp == 1) tmem_alloc_pair(tmem_slot, S::TMEM_COLS);
   tc_fence_before();
@@ -238,8 +277,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  const int units = kDw ? a.E * a.mt * ((a.n + TN - 1) / TN) : tcum[a.E] * a.mt;
+  GroupedWalk<DIR, TN> walk(a, tab, blockIdx.x >> 1, gridDim.x >> 1);
   constexpr int kNever = 1 << 30;
   constexpr int kSum = F32 ? kSumSteps : kNever;   // k-steps per tensor-core sum
 
@@ -250,8 +288,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int u = pair; u < units && ok; u += pairs) {
-        const GroupedUnit t = grouped_unit<DIR, TN>(a, off, tcum, u);
+      for (; walk.more() && ok; walk.next()) {
+        const GroupedUnit t = walk.unit();
         // each CTA's half of the N tile, a multiple of 16 rows (an MMA takes N in steps of 32)
         const int half = ((t.nlen + 31) & ~31) >> 1;
         const int steps = (t.red + 63) >> 6;
@@ -266,16 +304,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
           uint8_t* sa = smem + stage * S::STAGE_BYTES;
           uint8_t* sb = sa + S::A_BYTES;
           const bool cut = kDw && (t.red - ks * 64 < 64) && (t.red & 15);
-          uint32_t bar = cluster_addr(&full[stage], 0);
-          if (leader) {
-            mbar_arrive_expect_tx(&full[stage], (cut ? 1 : 2) * S::STAGE_BYTES);
-          } else if (kDw) {
-            if (cut) {
-              mbar_arrive_expect_tx(&tail[stage], S::STAGE_BYTES);
-              bar = cluster_addr(&tail[stage], rank);
-            } else {
-              mbar_arrive_cluster(bar);
-            }
+          uint32_t bar;
+          if (cut) {
+            mbar_arrive_expect_tx(&tail[stage], S::STAGE_BYTES);
+            bar = cluster_addr(&tail[stage], rank);
+          } else {
+            if (leader) mbar_arrive_expect_tx(&full[stage], 2 * S::STAGE_BYTES);
+            bar = cluster_addr(&full[stage], 0);
           }
           if (DIR == kGroupedFwd) {
             tma_load_3d_pair(sa, &mapA, bar, ks * 64, f, t.g, pol_a);
@@ -301,94 +336,112 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
       }
     }
     __syncwarp();
-  } else if (warp == 1 && leader) {
-    // ------------------------------ MMA issuer ------------------------------
-    int stage = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    int it = 0;
-    for (int u = pair; u < units && ok; u += pairs) {
-      const GroupedUnit t = grouped_unit<DIR, TN>(a, off, tcum, u);
-      const uint32_t n_mma = static_cast<uint32_t>((t.nlen + 31) & ~31);
-      const uint32_t idesc = idesc_bf16(256, n_mma) | (DIR != kGroupedFwd ? kIdescAmn : 0u) |
-                             (kDw ? kIdescBmn : 0u);
-      const int steps = (t.red + 63) >> 6;
-      for (int k0 = 0; k0 < steps && ok; k0 += kSum) {
-        const int k1 = min(steps, k0 + kSum);
-        const int b = it & 1;
-        if (!warp_wait_cluster(&tempty[b], ((it >> 1) & 1) ^ 1u, abort_flag, a.status)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t d = tmem + b * TN;
-        for (int ks = k0; ks < k1; ++ks) {
-          if (!warp_wait_cluster(&full[stage], phase, abort_flag, a.status)) {
+  } else if (warp == 1) {
+    // ------------------------------ MMA issuer (leader) ------------------------------
+    // Issuing blocks while the tensor pipe is busy and only about one instruction is queued
+    // behind the running one, so what this thread does between two MMAs must be short: the next
+    // stage's barrier is tested before the last MMA of a stage is issued (forward of 8 x 2048
+    // rows: tensor pipe active 65 -> 80 % of the cycles).
+    if (leader && lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true, ready = false;
+      int it = 0;
+      for (; walk.more() && ok; walk.next()) {
+        const GroupedUnit t = walk.unit();
+        const uint32_t n_mma = static_cast<uint32_t>((t.nlen + 31) & ~31);
+        const uint32_t idesc = idesc_bf16(256, n_mma) | (DIR != kGroupedFwd ? kIdescAmn : 0u) |
+                               (kDw ? kIdescBmn : 0u);
+        const int steps = (t.red + 63) >> 6;
+        for (int k0 = 0; k0 < steps && ok; k0 += kSum) {
+          const int k1 = min(steps, k0 + kSum);
+          const int b = it & 1;
+          if (!mbar_wait_cluster(&tempty[b], ((it >> 1) & 1) ^ 1u, abort_flag, a.status)) {
             ok = false;
             break;
           }
-          uint8_t* st = smem + stage * S::STAGE_BYTES;
-          const int left = t.red - ks * 64;
-          const int slices = left >= 64 ? 4 : (left + 15) >> 4;
-          if (kDw && left < 64 && (left & 15)) zero_rows(st, 2 + kBoxesB, left, slices * 16, lane);
           tc_fence_after();
-          if (lane == 0) {
-            const uint32_t sa = smem_addr(st), sb = sa + S::A_BYTES;
-            for (int kk = 0; kk < slices; ++kk) {
+          const uint32_t d = tmem + b * TN;
+          for (int ks = k0; ks < k1; ++ks) {
+            if (!ready && !mbar_wait_cluster(&full[stage], phase, abort_flag, a.status)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t sa = smem_addr(smem + stage * S::STAGE_BYTES);
+            const uint32_t sb = sa + S::A_BYTES;
+            auto issue = [&](int kk) {
               const uint64_t da = DIR == kGroupedFwd ? smem_desc_sw128(sa + kk * 32)
                                                      : smem_desc_sw128_mn(sa + kk * 2048);
               const uint64_t db = kDw ? smem_desc_sw128_mn(sb + kk * 2048)
                                       : smem_desc_sw128(sb + kk * 32);
               mma_f16_pair(d, da, db, idesc, (ks != k0 || kk != 0) ? 1u : 0u);
+            };
+            uint64_t* done = &empty[stage];
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1u;
             }
-            mma_commit_pair(&empty[stage]);
+            const int left = t.red - ks * 64;
+            if (left >= 64) {
+              issue(0);
+              issue(1);
+              issue(2);
+              ready = mbar_peek_cluster(&full[stage], phase);
+              issue(3);
+            } else {
+              ready = false;
+              for (int kk = 0; kk < (left + 15) >> 4; ++kk) issue(kk);
+            }
+            mma_commit_pair(done);
           }
-          __syncwarp();
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          if (ok) mma_commit_pair(&tfull[b]);
+          ++it;
         }
-        if (ok && lane == 0) mma_commit_pair(&tfull[b]);
-        __syncwarp();
-        ++it;
       }
     }
-  } else if (warp == 1) {
-    // ------------------------------ dw, peer: tails ------------------------------
-    // The peer's loads of a step that ends inside a 16-row slice count on its own barrier; it
-    // zeroes what follows the group's rows in its shared memory, then arrives for the step.
+    __syncwarp();
+  } else if (warp == 2) {
+    // ------------------------------ dw: tails ------------------------------
+    // For a step that ends inside a 16-row slice: wait for this CTA's own loads, zero what follows
+    // the group's rows, tell the leader; the leader then completes the stage's full barrier.
     if (kDw) {
-      uint32_t phases = 0;   // bit s: parity of the next use of tail[s]
+      uint32_t phases = 0;   // bit s: parity of the next use of tail[s] (and ptail[s])
       int stage = 0;
-      for (int u = pair; u < units; u += pairs) {
-        const GroupedUnit t = grouped_unit<DIR, TN>(a, off, tcum, u);
+      for (; walk.more(); walk.next()) {
+        const GroupedUnit t = walk.unit();
         const int steps = (t.red + 63) >> 6;
         stage = (stage + steps) % STAGES;
         if ((t.red & 15) == 0) continue;
         const int last = (stage + STAGES - 1) % STAGES;   // stage of the unit's last step
         // (many units may pass between two tails; an abort of another role ends the wait)
-        if (!warp_wait(&tail[last], (phases >> last) & 1u, abort_flag, a.status,
-                       30 * kWaitLimitNs))
-          break;
+        const uint32_t parity = (phases >> last) & 1u;
+        if (!warp_wait(&tail[last], parity, abort_flag, a.status, 30 * kWaitLimitNs)) break;
         phases ^= 1u << last;
         const int left = t.red - (steps - 1) * 64;
         zero_rows(smem + last * S::STAGE_BYTES, 2 + kBoxesB, left, (left + 15) & ~15, lane);
-        if (lane == 0) mbar_arrive_cluster(cluster_addr(&full[last], 0));
-        __syncwarp();
+        bool ok = true;
+        if (lane == 0) {
+          if (!leader) {
+            mbar_arrive_cluster(cluster_addr(&ptail[last], 0));
+          } else {
+            ok = mbar_wait_cluster(&ptail[last], parity, abort_flag, a.status);
+            if (ok) mbar_arrive_cluster(cluster_addr(&full[last], 0));
+          }
+        }
+        if (!__all_sync(0xffffffffu, ok)) break;
       }
     }
   } else {
     // ------------------------------ epilogue ------------------------------
     // Warp w reads lanes 32 (w % 4) .. +31 (output columns) of its part of the tile's N columns.
-    const int quarter = warp & 3, part = (warp - 2) >> 2;
+    const int quarter = warp & 3, part = (warp - 3) >> 2;
     int it = 0;
     bool ok = true;
-    for (int u = pair; u < units && ok; u += pairs) {
-      const GroupedUnit t = grouped_unit<DIR, TN>(a, off, tcum, u);
+    for (; walk.more() && ok; walk.next()) {
+      const GroupedUnit t = walk.unit();
       const int steps = (t.red + 63) >> 6;
-      const int f = t.f0 + static_cast<int>(rank) * 128 + quarter * 32 + lane;
-      const bool in = f < a.cols;
+      const int fw = t.f0 + static_cast<int>(rank) * 128 + quarter * 32;   // the warp's columns
       const size_t row0 = (kDw ? (size_t)t.g * a.n : 0) + t.n0;
       if constexpr (F32) {
         constexpr int kCols = TN / (kEpiWarps / 4);   // of this warp, in registers
@@ -418,8 +471,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
           ++it;
         }
         if (!ok) break;
-        if (!in || (a.accumulate && steps == 0)) continue;
-        float* out = static_cast<float*>(a.out) + (row0 + part * kCols) * a.cols + f;
+        if (fw + lane >= a.cols || (a.accumulate && steps == 0)) continue;
+        float* out = static_cast<float*>(a.out) + (row0 + part * kCols) * a.cols + fw + lane;
         const int mine = t.nlen - part * kCols;   // rows of this warp's part that exist
 #pragma unroll
         for (int c = 0; c < kCols; c += 16) {
@@ -437,29 +490,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
             if (c + j < mine) o[(size_t)j * a.cols] = acc[c + j];
         }
       } else {
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + row0 * a.cols + f;
-        if (steps == 0) {   // dw of an empty group
-          for (int p = part; p < t.nlen; p += kEpiWarps / 4)
-            if (in) out[(size_t)p * a.cols] = __float2bfloat16_rn(0.0f);
-          continue;
-        }
+        // 32 rows x 32 columns at a time: accumulator fragments to bf16, turned around through
+        // shared memory, stored as 16-byte pieces (four lanes a row)
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
+        uint8_t* mine = turn + (warp - 3) * kTurnBytes;
+        const uint32_t put = smem_addr(mine) + (lane & 7) * kTurnPitch + (lane >> 3) * 16;
+        const uint8_t* get = mine + (lane >> 2) * kTurnPitch + (lane & 3) * 16;
+        const int fl = fw + (lane & 3) * 8;   // this lane's first column when it stores
+        const bool in = fl < a.cols;          // (cols is a multiple of 8)
         const int b = it & 1;
-        if (!warp_wait(&tfull[b], (it >> 1) & 1, abort_flag, a.status)) break;
-        tc_fence_after();
-        const uint32_t tb = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + b * TN;
-        for (int c = part * 16; c < t.nlen; c += kEpiWarps * 4) {
-          uint32_t v[16];
-          tmem_ld16(tb + c, v);
-          tmem_ld_wait();
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (in && c + j < t.nlen)
-              out[(size_t)(c + j) * a.cols] = __float2bfloat16_rn(__uint_as_float(v[j]));
+        if (steps > 0) {
+          if (!warp_wait(&tfull[b], (it >> 1) & 1, abort_flag, a.status)) break;
+          tc_fence_after();
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(cluster_addr(&tempty[b], 0));
-        ++it;
+        const uint32_t tb = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + b * TN;
+        for (int c = part * 32; c < t.nlen; c += kEpiWarps * 8) {
+          uint4 v[4];
+          if (steps > 0) {
+            uint32_t lo[16], hi[16];   // lanes 0-15 and 16-31
+            tmem_ld_16x256_x4(tb + c, lo);
+            tmem_ld_16x256_x4(tb + (16u << 16) + c, hi);
+            tmem_ld_wait();
+            auto pack = [](uint32_t x, uint32_t y) {
+              return pack_bf16x2(__uint_as_float(x), __uint_as_float(y));
+            };
+            __syncwarp();   // the previous rows have been read
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t m[4] = {
+                  pack(lo[4 * i], lo[4 * i + 1]), pack(lo[4 * i + 2], lo[4 * i + 3]),
+                  pack(hi[4 * i], hi[4 * i + 1]), pack(hi[4 * i + 2], hi[4 * i + 3])};
+              stmatrix_x4_trans(put + i * 8 * kTurnPitch, m);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              v[q] = *reinterpret_cast<const uint4*>(get + q * 8 * kTurnPitch);
+          } else {   // dw of an empty group
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = make_uint4(0, 0, 0, 0);
+          }
+          const int p = c + (lane >> 2);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (in && p + 8 * q < t.nlen)
+              *reinterpret_cast<uint4*>(out + (row0 + p + 8 * q) * a.cols + fl) = v[q];
+        }
+        if (steps > 0) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(cluster_addr(&tempty[b], 0));
+          ++it;
+        }
       }
     }
   }
@@ -478,7 +560,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
 template <int DIR, int TN, int STAGES, bool F32>
 cudaError_t run_grouped_kernel(const GroupedArgs& a, const CUtensorMap& mA, const CUtensorMap& mB,
                                cudaStream_t st) {
-  using S = GroupedShape<TN, STAGES>;
+  using S = GroupedShape<TN, STAGES, F32>;
   auto kern = grouped_kernel<DIR, TN, STAGES, F32>;
   const cudaError_t err = ensure_smem_limit(reinterpret_cast<const void*>(kern), S::SMEM);
   if (err != cudaSuccess) return err;
