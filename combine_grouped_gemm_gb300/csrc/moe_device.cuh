@@ -30,6 +30,20 @@ __device__ __forceinline__ uint64_t global_timer_ns() {
   return t;
 }
 
+// True in one lane of a converged warp. A role of one thread is entered through this rather than
+// by lane number: the compiler then knows that one thread runs it and keeps the operands of MMA
+// and TMA instructions in uniform registers (by lane number each MMA took about 70 cycles to
+// issue in the grouped products).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(yes));
+  return yes != 0;
+}
+
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }

@@ -238,7 +238,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ptail + STAGES);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);   // uniform
+  const int lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
 
@@ -283,7 +284,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
 
   if (warp == 0) {
     // ------------------------------ TMA producer ------------------------------
-    if (lane == 0) {
+    if (elect_one()) {
       const uint64_t pol_once = l2_policy_evict_first(), pol_keep = l2_policy_evict_last();
       int stage = 0;
       uint32_t phase = 0;
@@ -338,11 +339,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------ MMA issuer (leader) ------------------------------
-    // Issuing blocks while the tensor pipe is busy and only about one instruction is queued
-    // behind the running one, so what this thread does between two MMAs must be short: the next
-    // stage's barrier is tested before the last MMA of a stage is issued (forward of 8 x 2048
-    // rows: tensor pipe active 65 -> 80 % of the cycles).
-    if (leader && lane == 0) {
+    // The next stage's barrier is tested before the last MMA of a stage is issued, so that the
+    // tensor pipe has work while this thread moves on.
+    if (leader && elect_one()) {
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true, ready = false;
