@@ -334,6 +334,14 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
                : "memory");
 }
 
+// The same without ordering earlier memory accesses: for an arrival that hands over tensor memory
+// only (tcgen05.wait::ld and tcgen05.fence::before_thread_sync come before it). The release above
+// waits for the thread's outstanding global stores, about 1600 cycles in an epilogue.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+               : "memory");
+}
+
 __device__ __forceinline__ bool mbar_test_cluster(uint64_t* bar, uint32_t parity) {
   uint32_t done;
   asm volatile(

@@ -204,11 +204,10 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
 // Zeroes the reduction rows [from, to) of a stage's MN-major boxes (128-byte rows; the swizzle
 // permutes bytes inside a row only) and orders the writes before the tensor core's reads.
 __device__ __forceinline__ void zero_rows(uint8_t* stage, int boxes, int from, int to, int lane) {
-  const int per = (to - from) * 8;   // 16-byte pieces per box
-  for (int i = lane; i < boxes * per; i += 32) {
-    const int b = i / per, j = i - b * per;
-    *reinterpret_cast<uint4*>(stage + b * 8192 + from * 128 + j * 16) = make_uint4(0, 0, 0, 0);
-  }
+  for (int b = lane >> 3; b < boxes; b += 4)   // eight lanes a row
+    for (int p = from; p < to; ++p)
+      *reinterpret_cast<uint4*>(stage + b * 8192 + p * 128 + (lane & 7) * 16) =
+          make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
   __syncwarp();
 }
@@ -466,7 +465,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(cluster_addr(&tempty[b], 0));
+          if (lane == 0) mbar_arrive_cluster_relaxed(cluster_addr(&tempty[b], 0));
           ++it;
         }
         if (!ok) break;
@@ -538,7 +537,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
         if (steps > 0) {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(cluster_addr(&tempty[b], 0));
+          if (lane == 0) mbar_arrive_cluster_relaxed(cluster_addr(&tempty[b], 0));
           ++it;
         }
       }
