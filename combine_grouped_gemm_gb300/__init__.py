@@ -162,8 +162,14 @@ def _p(t):
     return t.data_ptr()
 
 
+# The handle of a device's current stream without building a Stream object (3 us a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _s(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -319,6 +325,9 @@ def expert_ffn_gather(cfg, x, counts, src_tok, weights: dict, ebuf, shared_out, 
 def _need(fn, name, t, dtype, *shape):
     """_p(t), for a tensor that must have this element type and shape. int8 and e4m3 tensors
     count as bytes."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda
+            and t.is_contiguous()):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{fn}: {name} must be a CUDA tensor")
     if t.dtype is not dtype and not (dtype is torch.uint8 and t.dtype in
@@ -327,6 +336,9 @@ def _need(fn, name, t, dtype, *shape):
     if t.shape != shape:
         raise ValueError(f"{fn}: {name} must have shape {shape}, got {tuple(t.shape)}")
     return _p(t)
+
+
+_ws_need = {}   # (rows, E, n, k) -> bytes: a host-side size, asked for once per shape
 
 
 def grouped_ws_bytes(g: GroupCfg) -> int:
@@ -338,7 +350,11 @@ def grouped_ws_bytes(g: GroupCfg) -> int:
 
 
 def _need_ws(fn, g, ws):
-    if not isinstance(ws, torch.Tensor) or ws.numel() * ws.element_size() < grouped_ws_bytes(g):
+    shape = (g.rows, g.E, g.n, g.k)
+    need = _ws_need.get(shape)
+    if need is None:
+        need = _ws_need[shape] = grouped_ws_bytes(g)
+    if not isinstance(ws, torch.Tensor) or ws.nbytes < need:
         raise ValueError(f"{fn}: ws must be a CUDA tensor of grouped_ws_bytes(cfg) bytes")
     return _p(ws)
 

@@ -628,7 +628,7 @@ bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) !
 
 int check_rows(int32_t rows, int32_t cols) {
   if (rows < 0 || cols < 1) return MOE_ERR_INVALID_ARG;
-  return cols % 128 ? MOE_ERR_UNSUPPORTED : MOE_OK;
+  return cols % 128 || (long long)rows * cols >= 1ll << 38 ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 }  // namespace
 
@@ -666,7 +666,7 @@ int moe_act_save(int32_t rows, int32_t d, const void* x, void* q, float* scales,
   MOE_NEED(x);
   MOE_NEED(q);
   MOE_NEED(scales);
-  const cudaError_t e = launch_quant_rows_e4m3(x, rows, d, q, scales, stream);
+  const cudaError_t e = launch_act_save(rows, d, x, q, scales, stream);
   return e == cudaSuccess ? MOE_OK : cuda_fail(e);
 }
 

@@ -163,6 +163,27 @@ __device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
+// Tensor maps edited on the device: a 128-byte copy in shared memory whose extent in dimension 1
+// is replaced (one thread), then written to global memory by the whole warp for loads of any later
+// kernel or thread that acquires it.
+__device__ __forceinline__ void tensor_map_set_rows(uint32_t smem_map, uint32_t rows) {
+  asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 1, %1;" ::"r"(smem_map),
+               "r"(rows)
+               : "memory");
+}
+__device__ __forceinline__ void tensor_map_publish(void* global_map, uint32_t smem_map) {
+  asm volatile(
+      "tensormap.cp_fenceproxy.global.shared::cta.tensormap::generic.release.gpu.sync.aligned "
+      "[%0], [%1], 128;" ::"l"(reinterpret_cast<uint64_t>(global_map)),
+      "r"(smem_map)
+      : "memory");
+}
+__device__ __forceinline__ void tensor_map_acquire(const CUtensorMap* map) {
+  asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(
+                   reinterpret_cast<uint64_t>(map))
+               : "memory");
+}
+
 __device__ __forceinline__ uint64_t l2_policy_evict_first() {
   uint64_t p;
   asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));

@@ -15,16 +15,19 @@
 //   dw   columns of dW  rows of dW              the rows     x, MN-major        dy, MN-major
 // Weights come through 3-D tensor maps, so what a tile reads past a group's own matrix is zero.
 // In fwd and dx, rows past a group's end only feed accumulator columns that are not stored. In
-// dw they would be summed: the last k-step of a group zeroes what follows its rows in shared
-// memory before the MMA reads it (0 x NaN is not 0, so both operands are).
+// dw they would be summed, and 0 x NaN is not 0, so both operands have to end with the group: a
+// first small kernel writes for every group the two tensor maps whose extent ends at its last
+// row, and the loads fill the rest of the last k-step with zeros. (Zeroing the stage in shared
+// memory after the load cost a round trip between the two CTAs in every unit: 32 groups of 520
+// rows, 7168 x 2048, 456 us that way.)
 //
 // Each pair walks the units (group, 256 output columns, N tile) from its number in steps of the
 // pairs; a group's units are weight-tile-major, so pairs that run side by side share a weight
-// tile through L2. The tables of the units are built by every CTA from the counts itself: one
-// launch, no schedule kernel.
+// tile through L2. The tables of the units are built by every CTA from the counts itself, without
+// a schedule kernel.
 //
-// Roles in a CTA (one CTA per SM): warp 0 TMA producer, warp 1 MMA issuer (leader CTA), warp 2
-// zeroes dw's tails, the others the epilogue. Loads of both CTAs count on
+// Roles in a CTA (one CTA per SM): warp 0 TMA producer, warp 1 MMA issuer (leader CTA), the others
+// the epilogue. Loads of both CTAs count on
 // the leader's full barriers, its commits free the stages of both. Accumulators are double
 // buffered. Every wait is bounded.
 #include "moe_device.cuh"
@@ -70,13 +73,13 @@ __device__ __forceinline__ void group_offsets(const int32_t* counts, int E, int 
   __syncthreads();
 }
 
-// Warps 0, 1 and 2 load, issue the MMAs and zero tails; the others are the epilogue: two warps per
-// tensor-memory quarter, or four where the sums of a tile are held in registers (fp32 weight
-// gradients: 64 columns a thread).
+// Warps 0 and 1 load and issue the MMAs; the others are the epilogue: two warps per tensor-memory
+// quarter, or four where the sums of a tile are held in registers (fp32 weight gradients: 64
+// columns a thread).
 template <bool F32>
 struct GroupedThreads {
   static constexpr int kEpi = F32 ? 16 : 8;
-  static constexpr int kAll = (3 + kEpi) * 32;
+  static constexpr int kAll = (2 + kEpi) * 32;
 };
 // fp32 weight gradients: k-steps per tensor-core sum. The tensor core truncates as it adds, an
 // error that grows with the number of additions (2.1e-6 of the result after 2048 products,
@@ -95,7 +98,6 @@ struct GroupedArgs {
   int cols;       // output columns (M)
   int red;        // fwd, dx: length of the reduction
   int mt;         // ceil(cols / 256)
-  int accumulate;
 };
 
 template <int TN, int STAGES, bool F32>
@@ -128,7 +130,10 @@ struct GroupedUnit {
 };
 
 // Walks a pair's units: numbers pair, pair + pairs, ... of the groups' units one group after the
-// other, weight-tile-major (unit m * nt + j of a group: N tile j of its 256 columns number m).
+// other. fwd, dx: weight-tile-major (unit m * nt + j of a group: N tile j of its 256 columns
+// number m), so that neighbours share a weight tile. dw: by rows of the output (unit j * mt + m),
+// so that neighbours write adjacent columns (fp32, 32 groups of 128 rows, 4096 x 7168: 680 us the
+// other way, 644 us so with streaming stores).
 // fwd, dx: a group of c rows has nt = ceil(c / TN) N tiles of equal size (to 32 rows, the step of
 // an MMA's N) rather than full ones and a rest, which would cost a whole pass over the weight
 // tile for a few rows (16384 rows over 32 experts, about half of them just over 512: forward
@@ -137,13 +142,17 @@ template <int DIR, int TN>
 struct GroupedWalk {
   const GroupedArgs& a;
   const GroupedTables& tab;
-  int i, local, step, nt, w, base, len;
+  int i, q, p;          // position of the group; unit q * inner + p of it
+  int step, dq, dp;     // pairs, in units of this group
+  int inner, outer;     // its units: outer x inner
+  int w, base, len;
 
   __device__ __forceinline__ GroupedWalk(const GroupedArgs& a_, const GroupedTables& t_, int pair,
                                          int pairs)
-      : a(a_), tab(t_), i(0), local(pair), step(pairs) {
+      : a(a_), tab(t_), i(0), q(0), p(0), step(pairs), dq(0), dp(0), inner(1), outer(1), w(TN),
+        base(0), len(0) {
     load();
-    settle();
+    settle(pair);
   }
   __device__ __forceinline__ int groups() const {
     return DIR == kGroupedDw ? a.E : tab.n_live;
@@ -151,45 +160,62 @@ struct GroupedWalk {
   __device__ __forceinline__ bool more() const { return i < groups(); }
   __device__ __forceinline__ void load() {   // the group at position i
     if (DIR == kGroupedDw) {
-      nt = (a.n + TN - 1) / TN;
-      w = TN;
+      inner = a.mt;
+      outer = (a.n + TN - 1) / TN;
     } else if (i < tab.n_live) {
       const int g = tab.live[i];
       base = tab.off[g];
       len = tab.off[g + 1] - base;
-      nt = (len + TN - 1) / TN;
-      w = nt == 1 ? TN : ((len + nt - 1) / nt + 31) & ~31;
+      inner = (len + TN - 1) / TN;
+      outer = a.mt;
+      w = inner == 1 ? TN : ((len + inner - 1) / inner + 31) & ~31;
+    }
+    if (DIR != kGroupedDw || i == 0) {
+      dq = step / inner;
+      dp = step - dq * inner;
     }
   }
-  __device__ __forceinline__ void settle() {
-    while (more() && local >= nt * a.mt) {
-      local -= nt * a.mt;
+  // To unit `local` of group i or, past its units, of the groups after it.
+  __device__ __forceinline__ void settle(int local) {
+    while (more() && local >= inner * outer) {
+      local -= inner * outer;
       ++i;
       load();
     }
+    q = local / inner;
+    p = local - q * inner;
   }
-  __device__ __forceinline__ void next() {
-    local += step;
-    settle();
+  __device__ __forceinline__ void next() {   // (no division while the group lasts)
+    q += dq;
+    p += dp;
+    if (p >= inner) {
+      p -= inner;
+      ++q;
+    }
+    if (q < outer) return;
+    const int local = (q - outer) * inner + p;
+    ++i;
+    load();
+    settle(local);
   }
   __device__ __forceinline__ GroupedUnit unit() const {
     GroupedUnit r;
-    const int m = nt == 1 ? local : local / nt;
-    const int j = local - m * nt;
-    r.f0 = m * 256;
-    r.nt = nt;
     if (DIR == kGroupedDw) {
       r.g = i;
-      r.n0 = j * TN;
+      r.f0 = p * 256;
+      r.n0 = q * TN;
       r.nlen = min(TN, a.n - r.n0);
       r.r0 = tab.off[i];
       r.red = tab.off[i + 1] - r.r0;
+      r.nt = outer;
     } else {
       r.g = tab.live[i];
-      r.n0 = base + j * w;
-      r.nlen = min(w, len - j * w);
+      r.f0 = q * 256;
+      r.n0 = base + p * w;
+      r.nlen = min(w, len - p * w);
       r.r0 = 0;
       r.red = a.red;
+      r.nt = inner;
     }
     return r;
   }
@@ -201,20 +227,38 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status, limit_ns));
 }
 
-// Zeroes the reduction rows [from, to) of a stage's MN-major boxes (128-byte rows; the swizzle
-// permutes bytes inside a row only) and orders the writes before the tensor core's reads.
-__device__ __forceinline__ void zero_rows(uint8_t* stage, int boxes, int from, int to, int lane) {
-  for (int b = lane >> 3; b < boxes; b += 4)   // eight lanes a row
-    for (int p = from; p < to; ++p)
-      *reinterpret_cast<uint4*>(stage + b * 8192 + p * 128 + (lane & 7) * 16) =
-          make_uint4(0, 0, 0, 0);
-  fence_proxy_async_smem();
+// dw: the tensor maps of x and dy for every group, ending at the group's last row; one warp a
+// group. map_a, map_b: the whole tensors' maps.
+constexpr int kMapWarps = 4;
+__global__ void __launch_bounds__(kMapWarps * 32)
+    group_maps_kernel(const int32_t* __restrict__ counts, CUtensorMap* maps, int rows, int E,
+                      uint32_t* status, const __grid_constant__ CUtensorMap map_a,
+                      const __grid_constant__ CUtensorMap map_b) {
+  __shared__ int off[kMaxGroups + 1];
+  __shared__ alignas(128) uint32_t copy[kMapWarps][2][32];
+  pdl_trigger();
+  group_offsets(counts, E, rows, off, status);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = blockIdx.x * kMapWarps + warp;
+  if (g >= E) return;
+  copy[warp][0][lane] = reinterpret_cast<const uint32_t*>(&map_a)[lane];
+  copy[warp][1][lane] = reinterpret_cast<const uint32_t*>(&map_b)[lane];
   __syncwarp();
+  const uint32_t sa = smem_addr(copy[warp][0]), sb = smem_addr(copy[warp][1]);
+  if (lane == 0) {
+    const uint32_t end = static_cast<uint32_t>(max(1, off[g + 1]));   // (an extent is at least 1)
+    tensor_map_set_rows(sa, end);
+    tensor_map_set_rows(sb, end);
+  }
+  __syncwarp();
+  tensor_map_publish(maps + 2 * g, sa);
+  tensor_map_publish(maps + 2 * g + 1, sb);
 }
 
-template <int DIR, int TN, int STAGES, bool F32>
+template <int DIR, int TN, int STAGES, bool F32, bool ACC>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>::kAll, 1)
-    grouped_kernel(const GroupedArgs a, const __grid_constant__ CUtensorMap mapA,
+    grouped_kernel(const GroupedArgs a, const CUtensorMap* __restrict__ maps,
+                   const __grid_constant__ CUtensorMap mapA,
                    const __grid_constant__ CUtensorMap mapB) {
   using S = GroupedShape<TN, STAGES, F32>;
   constexpr bool kDw = DIR == kGroupedDw;
@@ -230,11 +274,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
   uint64_t* empty = full + STAGES;
   uint64_t* tfull = empty + STAGES;
   uint64_t* tempty = tfull + 2;
-  // dw, steps whose tail is zeroed: each CTA's loads count on its own tail barrier; the leader's
-  // ptail says that the peer has zeroed its part
-  uint64_t* tail = tempty + 2;
-  uint64_t* ptail = tail + STAGES;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(ptail + STAGES);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);   // uniform
@@ -246,8 +286,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
     for (int i = 0; i < STAGES; ++i) {
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], 1);
-      mbar_init(&tail[i], 1);
-      mbar_init(&ptail[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&tfull[i], 1);
@@ -255,8 +293,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
     }
     *abort_flag = 0;
     mbar_fence_init();
-    tma_prefetch_map(&mapA);
-    tma_prefetch_map(&mapB);
+    if (!kDw) {
+      tma_prefetch_map(&mapA);
+      tma_prefetch_map(&mapB);
+    }
   }
   group_offsets(a.counts, a.E, a.rows, tab.off, a.status);
   if (!kDw && warp == 0) {
@@ -275,6 +315,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
   __syncthreads();
   cluster_sync();   // the peer's barriers and tensor memory are ready
   tc_fence_after();
+  if (kDw) pdl_wait();   // the groups' tensor maps are written
   const uint32_t tmem = *tmem_slot;
 
   GroupedWalk<DIR, TN> walk(a, tab, blockIdx.x >> 1, gridDim.x >> 1);
@@ -288,8 +329,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
+      int acquired = -1;   // dw: the group whose maps this thread has acquired
       for (; walk.more() && ok; walk.next()) {
         const GroupedUnit t = walk.unit();
+        const CUtensorMap *ma = &mapA, *mb = &mapB;
+        if (kDw) {
+          ma = maps + 2 * t.g;
+          mb = ma + 1;
+          if (t.g != acquired) {
+            tensor_map_acquire(ma);
+            tensor_map_acquire(mb);
+            acquired = t.g;
+          }
+        }
         // each CTA's half of the N tile, a multiple of 16 rows (an MMA takes N in steps of 32)
         const int half = ((t.nlen + 31) & ~31) >> 1;
         const int steps = (t.red + 63) >> 6;
@@ -303,30 +355,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
           }
           uint8_t* sa = smem + stage * S::STAGE_BYTES;
           uint8_t* sb = sa + S::A_BYTES;
-          const bool cut = kDw && (t.red - ks * 64 < 64) && (t.red & 15);
-          uint32_t bar;
-          if (cut) {
-            mbar_arrive_expect_tx(&tail[stage], S::STAGE_BYTES);
-            bar = cluster_addr(&tail[stage], rank);
-          } else {
-            if (leader) mbar_arrive_expect_tx(&full[stage], 2 * S::STAGE_BYTES);
-            bar = cluster_addr(&full[stage], 0);
-          }
+          if (leader) mbar_arrive_expect_tx(&full[stage], 2 * S::STAGE_BYTES);
+          const uint32_t bar = cluster_addr(&full[stage], 0);
           if (DIR == kGroupedFwd) {
-            tma_load_3d_pair(sa, &mapA, bar, ks * 64, f, t.g, pol_a);
+            tma_load_3d_pair(sa, ma, bar, ks * 64, f, t.g, pol_a);
           } else if (DIR == kGroupedDx) {
-            tma_load_3d_pair(sa, &mapA, bar, f, ks * 64, t.g, pol_a);
-            tma_load_3d_pair(sa + 8192, &mapA, bar, f + 64, ks * 64, t.g, pol_a);
+            tma_load_3d_pair(sa, ma, bar, f, ks * 64, t.g, pol_a);
+            tma_load_3d_pair(sa + 8192, ma, bar, f + 64, ks * 64, t.g, pol_a);
           } else {
-            tma_load_2d_pair(sa, &mapA, bar, f, t.r0 + ks * 64, pol_a);
-            tma_load_2d_pair(sa + 8192, &mapA, bar, f + 64, t.r0 + ks * 64, pol_a);
+            tma_load_2d_pair(sa, ma, bar, f, t.r0 + ks * 64, pol_a);
+            tma_load_2d_pair(sa + 8192, ma, bar, f + 64, t.r0 + ks * 64, pol_a);
           }
           if (kDw) {
 #pragma unroll
             for (int j = 0; j < kBoxesB; ++j)
-              tma_load_2d_pair(sb + j * 8192, &mapB, bar, nb + 64 * j, t.r0 + ks * 64, pol_keep);
+              tma_load_2d_pair(sb + j * 8192, mb, bar, nb + 64 * j, t.r0 + ks * 64, pol_keep);
           } else {
-            tma_load_2d_pair(sb, &mapB, bar, ks * 64, nb, pol_keep);
+            tma_load_2d_pair(sb, mb, bar, ks * 64, nb, pol_keep);
           }
           if (++stage == STAGES) {
             stage = 0;
@@ -399,54 +444,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
       }
     }
     __syncwarp();
-  } else if (warp == 2) {
-    // ------------------------------ dw: tails ------------------------------
-    // For a step that ends inside a 16-row slice: wait for this CTA's own loads, zero what follows
-    // the group's rows, tell the leader; the leader then completes the stage's full barrier.
-    if (kDw) {
-      uint32_t phases = 0;   // bit s: parity of the next use of tail[s] (and ptail[s])
-      int stage = 0;
-      for (; walk.more(); walk.next()) {
-        const GroupedUnit t = walk.unit();
-        const int steps = (t.red + 63) >> 6;
-        stage = (stage + steps) % STAGES;
-        if ((t.red & 15) == 0) continue;
-        const int last = (stage + STAGES - 1) % STAGES;   // stage of the unit's last step
-        // (many units may pass between two tails; an abort of another role ends the wait)
-        const uint32_t parity = (phases >> last) & 1u;
-        if (!warp_wait(&tail[last], parity, abort_flag, a.status, 30 * kWaitLimitNs)) break;
-        phases ^= 1u << last;
-        const int left = t.red - (steps - 1) * 64;
-        zero_rows(smem + last * S::STAGE_BYTES, 2 + kBoxesB, left, (left + 15) & ~15, lane);
-        bool ok = true;
-        if (lane == 0) {
-          if (!leader) {
-            mbar_arrive_cluster(cluster_addr(&ptail[last], 0));
-          } else {
-            ok = mbar_wait_cluster(&ptail[last], parity, abort_flag, a.status);
-            if (ok) mbar_arrive_cluster(cluster_addr(&full[last], 0));
-          }
-        }
-        if (!__all_sync(0xffffffffu, ok)) break;
-      }
-    }
   } else {
     // ------------------------------ epilogue ------------------------------
     // Warp w reads lanes 32 (w % 4) .. +31 (output columns) of its part of the tile's N columns.
-    const int quarter = warp & 3, part = (warp - 3) >> 2;
+    const int quarter = warp & 3, part = (warp - 2) >> 2;
     int it = 0;
     bool ok = true;
     for (; walk.more() && ok; walk.next()) {
       const GroupedUnit t = walk.unit();
       const int steps = (t.red + 63) >> 6;
       const int fw = t.f0 + static_cast<int>(rank) * 128 + quarter * 32;   // the warp's columns
-      const size_t row0 = (kDw ? (size_t)t.g * a.n : 0) + t.n0;
       if constexpr (F32) {
-        constexpr int kCols = TN / (kEpiWarps / 4);   // of this warp, in registers
+        // All sums but the last are added up in registers; the last goes straight to memory with
+        // them, 128 bytes of a row per warp store. (Tile stores through shared memory were no
+        // faster: 654 us for 32 groups of 128 rows, 4096 x 7168.)
+        constexpr int kCols = TN / (kEpiWarps / 4);   // of this warp
         float acc[kCols];
 #pragma unroll
         for (int j = 0; j < kCols; ++j) acc[j] = 0.0f;
-        for (int k0 = 0; k0 < steps; k0 += kSum) {
+        int k0 = 0;
+        for (; k0 + kSum < steps; k0 += kSum) {
           const int b = it & 1;
           if (!warp_wait(&tfull[b], (it >> 1) & 1, abort_flag, a.status)) {
             ok = false;
@@ -469,29 +486,61 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
           ++it;
         }
         if (!ok) break;
-        if (fw + lane >= a.cols || (a.accumulate && steps == 0)) continue;
-        float* out = static_cast<float*>(a.out) + (row0 + part * kCols) * a.cols + fw + lane;
-        const int mine = t.nlen - part * kCols;   // rows of this warp's part that exist
+        if (ACC && steps == 0) continue;
+        if (steps > 0) {
+          const int b = it & 1;
+          if (!warp_wait(&tfull[b], (it >> 1) & 1, abort_flag, a.status)) break;
+          tc_fence_after();
+          const uint32_t tb =
+              tmem + (static_cast<uint32_t>(quarter * 32) << 16) + b * TN + part * kCols;
 #pragma unroll
-        for (int c = 0; c < kCols; c += 16) {
-          float* o = out + (size_t)c * a.cols;
-          if (a.accumulate) {
-            float old[16];
+          for (int c = 0; c < kCols; c += 16) {
+            uint32_t v[16];
+            tmem_ld16(tb + c, v);
+            tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              old[j] = c + j < mine ? o[(size_t)j * a.cols] : 0.0f;
-#pragma unroll
-            for (int j = 0; j < 16; ++j) acc[c + j] += old[j];
+            for (int j = 0; j < 16; ++j) acc[c + j] += __uint_as_float(v[j]);
           }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster_relaxed(cluster_addr(&tempty[b], 0));
+          ++it;
+        }
+        if (fw + lane >= a.cols) continue;
+        const int first = t.n0 + part * kCols;   // this warp's first row of dW_g
+        float* o = static_cast<float*>(a.out) + ((size_t)t.g * a.n + first) * a.cols + fw + lane;
+        const int mine = a.n - first;            // rows from there to the last
+        if constexpr (ACC) {
+          const float* old = o;
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            if (c + j < mine) o[(size_t)j * a.cols] = acc[c + j];
+          for (int c = 0; c < kCols; c += 16) {
+            float was[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) was[j] = c + j < mine ? old[(size_t)j * a.cols] : 0.0f;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) acc[c + j] += was[j];
+            old += 16 * (size_t)a.cols;
+          }
+        }
+        if (mine >= kCols) {   // (the test in every store costs 5 %)
+#pragma unroll
+          for (int j = 0; j < kCols; ++j) {
+            __stcs(o, acc[j]);
+            o += a.cols;
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < kCols; ++j) {
+            if (j < mine) __stcs(o, acc[j]);
+            o += a.cols;
+          }
         }
       } else {
         // 32 rows x 32 columns at a time: accumulator fragments to bf16, turned around through
         // shared memory, stored as 16-byte pieces (four lanes a row)
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
-        uint8_t* mine = turn + (warp - 3) * kTurnBytes;
+        const size_t row0 = (kDw ? (size_t)t.g * a.n : 0) + t.n0;
+        uint8_t* mine = turn + (warp - 2) * kTurnBytes;
         const uint32_t put = smem_addr(mine) + (lane & 7) * kTurnPitch + (lane >> 3) * 16;
         const uint8_t* get = mine + (lane >> 2) * kTurnPitch + (lane & 3) * 16;
         const int fl = fw + (lane & 3) * 8;   // this lane's first column when it stores
@@ -555,15 +604,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
   }
 }
 
-template <int DIR, int TN, int STAGES, bool F32>
+template <int DIR, int TN, int STAGES, bool F32 = false, bool ACC = false>
 cudaError_t run_grouped_kernel(const GroupedArgs& a, const CUtensorMap& mA, const CUtensorMap& mB,
-                               cudaStream_t st) {
+                               cudaStream_t st, const CUtensorMap* maps = nullptr) {
   using S = GroupedShape<TN, STAGES, F32>;
-  auto kern = grouped_kernel<DIR, TN, STAGES, F32>;
+  auto kern = grouped_kernel<DIR, TN, STAGES, F32, ACC>;
   const cudaError_t err = ensure_smem_limit(reinterpret_cast<const void*>(kern), S::SMEM);
   if (err != cudaSuccess) return err;
-  return launch_kernel(kern, dim3(sm_count() & ~1), dim3(GroupedThreads<F32>::kAll), S::SMEM, st, false, a,
-                       mA, mB);
+  return launch_kernel(kern, dim3(sm_count() & ~1), dim3(GroupedThreads<F32>::kAll), S::SMEM, st,
+                       maps != nullptr, a, maps, mA, mB);
 }
 
 // N tile of fwd and dx: the smallest that takes a group's mean rows, so that a batch of few rows
@@ -578,16 +627,19 @@ template <int DIR>
 cudaError_t run_rows(int tn, const GroupedArgs& a, const CUtensorMap& mA, const CUtensorMap& mB,
                      cudaStream_t st) {
   switch (tn) {
-    case 32: return run_grouped_kernel<DIR, 32, 10, false>(a, mA, mB, st);
-    case 64: return run_grouped_kernel<DIR, 64, 9, false>(a, mA, mB, st);
-    case 128: return run_grouped_kernel<DIR, 128, 8, false>(a, mA, mB, st);
-    default: return run_grouped_kernel<DIR, 256, 6, false>(a, mA, mB, st);
+    case 32: return run_grouped_kernel<DIR, 32, 10>(a, mA, mB, st);
+    case 64: return run_grouped_kernel<DIR, 64, 9>(a, mA, mB, st);
+    case 128: return run_grouped_kernel<DIR, 128, 8>(a, mA, mB, st);
+    default: return run_grouped_kernel<DIR, 256, 6>(a, mA, mB, st);
   }
 }
 
 }  // namespace
 
-size_t grouped_ws_bytes(const moe_group_cfg&) { return 256; }
+// status word; then, from the next 128-byte boundary after 256 bytes, dw's tensor maps
+size_t grouped_ws_bytes(const moe_group_cfg& c) {
+  return 256 + 128 + 2 * sizeof(CUtensorMap) * (size_t)c.E;
+}
 
 cudaError_t launch_grouped(const moe_group_cfg& c, GroupedDir dir, const void* in0, const void* in1,
                            const int32_t* counts, void* out, bool out_f32, bool accumulate,
@@ -607,7 +659,6 @@ cudaError_t launch_grouped(const moe_group_cfg& c, GroupedDir dir, const void* i
   a.cols = dir == kGroupedFwd ? c.n : c.k;
   a.red = dir == kGroupedFwd ? c.k : c.n;
   a.mt = (a.cols + 255) / 256;
-  a.accumulate = accumulate ? 1 : 0;
   CUtensorMap mA, mB;
   bool ok;
   const int tn = dir == kGroupedDw ? 256 : row_tile(c);
@@ -622,10 +673,17 @@ cudaError_t launch_grouped(const moe_group_cfg& c, GroupedDir dir, const void* i
   switch (dir) {
     case kGroupedFwd: return run_rows<kGroupedFwd>(tn, a, mA, mB, st);
     case kGroupedDx: return run_rows<kGroupedDx>(tn, a, mA, mB, st);
-    default:
-      return out_f32 ? run_grouped_kernel<kGroupedDw, 256, 6, true>(a, mA, mB, st)
-                     : run_grouped_kernel<kGroupedDw, 256, 6, false>(a, mA, mB, st);
+    default: break;
   }
+  auto* maps = reinterpret_cast<CUtensorMap*>(
+      (reinterpret_cast<uintptr_t>(ws) + 256 + 127) & ~static_cast<uintptr_t>(127));
+  const cudaError_t err = launch_kernel(
+      group_maps_kernel, dim3((c.E + kMapWarps - 1) / kMapWarps), dim3(kMapWarps * 32), 0, st,
+      false, counts, maps, c.rows, c.E, static_cast<uint32_t*>(ws), mA, mB);
+  if (err != cudaSuccess) return err;
+  if (!out_f32) return run_grouped_kernel<kGroupedDw, 256, 6>(a, mA, mB, st, maps);
+  return accumulate ? run_grouped_kernel<kGroupedDw, 256, 6, true, true>(a, mA, mB, st, maps)
+                    : run_grouped_kernel<kGroupedDw, 256, 6, true>(a, mA, mB, st, maps);
 }
 
 }  // namespace moe

@@ -192,6 +192,8 @@ cudaError_t launch_grouped(const moe_group_cfg& c, GroupedDir dir, const void* i
                            const int32_t* counts, void* out, bool out_f32, bool accumulate,
                            void* ws, cudaStream_t st);
 
+cudaError_t launch_act_save(int rows, int d, const void* x, void* q, float* scales,
+                            cudaStream_t st);
 cudaError_t launch_act_load(int rows, int src_rows, int d, const void* q, const float* scales,
                             const int32_t* index, void* out, uint32_t* status, cudaStream_t st);
 cudaError_t launch_swiglu_save(int rows, int f, const void* gu, void* a, void* q, float* scales,

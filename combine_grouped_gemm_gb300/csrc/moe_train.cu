@@ -34,113 +34,176 @@ __device__ __forceinline__ void codes8(const uint2& c, float s, float (&f)[8]) {
   codes4(c.y, s, f + 4);
 }
 
-// A 128-column block of one row over 16 lanes, 8 values each: the block's scale (the dispatch's
-// rule, with IEEE divisions so that the codes are the dispatch's) and this lane's codes.
-__device__ __forceinline__ uint2 quantise8(const float (&f)[8], float* scale_out) {
-  float amax = 0.0f;
+__device__ __forceinline__ float sigmoid(float g) {   // 0 where exp(-g) passes the fp32 range
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(1.0f + __expf(-g)));   // 1 ulp
+  return r;
+}
+
+// Largest magnitude of 8 bf16 values (a NaN does not count), in the low half of the result.
+__device__ __forceinline__ __nv_bfloat162 amax8(const uint4& v) {
+  const auto h = [](uint32_t w) { return __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w)); };
+  const __nv_bfloat162 m = __hmax2(__hmax2(h(v.x), h(v.y)), __hmax2(h(v.z), h(v.w)));
+  return __hmax2(m, __lowhigh2highlow(m));
+}
+
+// Largest over the 16 lanes of a half-warp, both halves of the register at once.
+__device__ __forceinline__ __nv_bfloat162 half_warp_max2(__nv_bfloat162 m) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(f[j]));
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  const float scale = amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
-  uint32_t w[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    w[h] = 0;
-#pragma unroll
-    for (int j = 0; j < 4; j += 2)
-      w[h] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(
-                  make_float2(__fdiv_rn(f[4 * h + j], scale), __fdiv_rn(f[4 * h + j + 1], scale)),
-                  __NV_SATFINITE, __NV_E4M3))
-              << (8 * j);
+  for (int o = 8; o > 0; o >>= 1) {
+    const uint32_t other =
+        __shfl_xor_sync(0xffffffffu, *reinterpret_cast<const uint32_t*>(&m), o);
+    m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162*>(&other));
   }
-  *scale_out = scale;
+  return m;
+}
+
+// The dispatch's rule: scale = amax / 448 (1 if amax is 0), codes e4m3(x / scale), both IEEE
+// divisions, so that the codes are the dispatch's bit for bit. The quotients x / scale come from
+// the correctly rounded reciprocal by one correction step (P. Markstein, "Computation of
+// elementary functions on the IBM RISC System/6000 processor", 1990): q = x r, then q + r (x - q
+// scale) with fused multiply-adds is the correctly rounded quotient as long as nothing underflows
+// or overflows. Scales outside 2^-60 .. 2^100 (infinities among them) take the divisions.
+__device__ __forceinline__ float block_scale(float amax) {
+  return amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
+}
+__device__ __forceinline__ uint2 codes_of8(const float (&f)[8], float scale) {
+  float q[8];
+  if (scale > 0x1p-60f && scale < 0x1p100f) {
+    const float r = __frcp_rn(scale);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float q0 = f[j] * r;
+      // (the correction of a -0 gives +0: the sign is the dividend's)
+      q[j] = copysignf(__fmaf_rn(__fmaf_rn(-q0, scale, f[j]), r, q0), f[j]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) q[j] = __fdiv_rn(f[j], scale);
+  }
+  uint32_t w[2] = {0, 0};
+#pragma unroll
+  for (int j = 0; j < 8; j += 2)
+    w[j >> 2] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(q[j], q[j + 1]),
+                                                                __NV_SATFINITE, __NV_E4M3))
+                 << (8 * (j & 3));
   return make_uint2(w[0], w[1]);
 }
 
-// One thread: 8 columns of one output row. A row is d / 8 threads.
+// The kernels that read or write scales take tiles of 16 rows x 128 columns a CTA: a half-warp is
+// one row's block (8 columns a lane), so a CTA's scales are 16 consecutive floats. CTA c: column
+// block c % nb of row group c / nb.
+constexpr int kTileRows = kThreads / 16;
+
+__global__ void __launch_bounds__(kThreads) act_save_kernel(const uint4* __restrict__ x,
+                                                            uint2* __restrict__ q,
+                                                            float* __restrict__ scales, int rows,
+                                                            int nb) {
+  const int rg = blockIdx.x / nb, b = blockIdx.x - rg * nb;
+  const int r = rg * kTileRows + (threadIdx.x >> 4), l = threadIdx.x & 15;
+  const bool in = r < rows;
+  const size_t at = ((size_t)r * nb + b) * 16 + l;
+  uint4 v = make_uint4(0, 0, 0, 0);
+  if (in) v = x[at];
+  const float scale = block_scale(__low2float(half_warp_max2(amax8(v))));
+  float f[8];
+  unpack8(v, f);
+  if (!in) return;
+  q[at] = codes_of8(f, scale);
+  if (l == 0) scales[(size_t)b * rows + r] = scale;
+}
+
+// One warp: up to 8 column blocks of one output row, two at a time. part: ceil(nb / 8).
+constexpr int kLoadBlocks = 8;
 __global__ void __launch_bounds__(kThreads) act_load_kernel(
     const uint2* __restrict__ q, const float* __restrict__ scales,
-    const int32_t* __restrict__ index, uint4* __restrict__ out, int rows, int src_rows, int vpr,
-    uint32_t* status) {
-  const long long total = (long long)rows * vpr;
-  for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < total;
-       i += (long long)gridDim.x * kThreads) {
-    const int r = static_cast<int>(i / vpr), v = static_cast<int>(i % vpr);
-    int src = index ? index[r] : r;
-    if (src < -1 || src >= src_rows) {
-      if (v == 0) raise_status(status, MOE_DEV_BOUNDS);
-      src = -1;
-    }
-    uint4 o = make_uint4(0, 0, 0, 0);
-    if (src >= 0) {
-      float f[8];
-      codes8(q[(long long)src * vpr + v], scales[(long long)(v / 16) * src_rows + src], f);
-      o = pack8(f);
-    }
-    out[i] = o;
+    const int32_t* __restrict__ index, uint4* __restrict__ out, int rows, int src_rows, int nb,
+    int parts, uint32_t* status) {
+  const unsigned item = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  const unsigned r = item / parts, part = item - r * parts;
+  if (r >= static_cast<unsigned>(rows)) return;
+  int src = index ? index[r] : static_cast<int>(r);
+  if (src < -1 || src >= src_rows) {
+    if (lane == 0 && part == 0) raise_status(status, MOE_DEV_BOUNDS);
+    src = -1;
+  }
+  const int b0 = part * kLoadBlocks + (lane >> 4);
+  uint2 c[kLoadBlocks / 2];
+  float s[kLoadBlocks / 2];
+#pragma unroll
+  for (int i = 0; i < kLoadBlocks / 2; ++i) {
+    const int b = b0 + 2 * i;
+    const bool in = src >= 0 && b < nb;
+    c[i] = in ? q[((size_t)src * nb + b) * 16 + (lane & 15)] : make_uint2(0, 0);
+    s[i] = in ? scales[(size_t)b * src_rows + src] : 0.0f;
+  }
+#pragma unroll
+  for (int i = 0; i < kLoadBlocks / 2; ++i) {
+    const int b = b0 + 2 * i;
+    float f[8];
+    codes8(c[i], s[i], f);
+    if (b < nb) __stcs(out + ((size_t)r * nb + b) * 16 + (lane & 15), pack8(f));
   }
 }
 
-// One thread: 8 columns of one row's gate and of its up half. The 16 lanes of a 128-column block
-// are in one half-warp (f / 8 is a multiple of 16), and whole half-warps leave the loop together.
 __global__ void __launch_bounds__(kThreads) swiglu_save_kernel(const uint4* __restrict__ gu,
                                                                uint4* __restrict__ a,
                                                                uint2* __restrict__ q,
                                                                float* __restrict__ scales,
-                                                               int rows, int vpr) {
-  const long long total = (long long)rows * vpr;
-  const long long step = (long long)gridDim.x * kThreads;
-  // every lane of a warp runs the same number of iterations (the shuffles take whole warps)
-  for (long long i0 = (long long)blockIdx.x * kThreads; i0 < total; i0 += step) {
-    const long long i = i0 + threadIdx.x;
-    const bool in = i < total;
-    const long long r = in ? i / vpr : 0;
-    const int v = in ? static_cast<int>(i % vpr) : 0;
-    float g[8] = {}, u[8] = {}, o[8];
-    if (in) {
-      unpack8(gu[r * 2 * vpr + v], g);
-      unpack8(gu[r * 2 * vpr + vpr + v], u);
-    }
-    float sg, su;
-    const uint2 cg = quantise8(g, &sg), cu = quantise8(u, &su);
+                                                               int rows, int nb) {
+  const int rg = blockIdx.x / nb, b = blockIdx.x - rg * nb;
+  const int r = rg * kTileRows + (threadIdx.x >> 4), l = threadIdx.x & 15;
+  const bool in = r < rows;
+  const size_t ga = ((size_t)r * 2 * nb + b) * 16 + l, ua = ga + (size_t)nb * 16;
+  uint4 gv = make_uint4(0, 0, 0, 0), uv = gv;
+  if (in) {
+    gv = gu[ga];
+    uv = gu[ua];
+  }
+  // both halves' largest values through the same shuffles: gate low, up high
+  const __nv_bfloat162 m = half_warp_max2(__lows2bfloat162(amax8(gv), amax8(uv)));
+  const float sg = block_scale(__low2float(m)), su = block_scale(__high2float(m));
+  if (!in) return;
+  float g[8], u[8], o[8];
+  unpack8(gv, g);
+  unpack8(uv, u);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) o[j] = silu(g[j]) * u[j];
-    if (!in) continue;
-    a[i] = pack8(o);
-    q[r * 2 * vpr + v] = cg;
-    q[r * 2 * vpr + vpr + v] = cu;
-    if ((v & 15) == 0) {
-      scales[(long long)(v / 16) * rows + r] = sg;
-      scales[(long long)((vpr + v) / 16) * rows + r] = su;
-    }
+  for (int j = 0; j < 8; ++j) o[j] = g[j] * sigmoid(g[j]) * u[j];
+  a[((size_t)r * nb + b) * 16 + l] = pack8(o);
+  q[ga] = codes_of8(g, sg);
+  q[ua] = codes_of8(u, su);
+  if (l == 0) {
+    scales[(size_t)b * rows + r] = sg;
+    scales[(size_t)(nb + b) * rows + r] = su;
   }
 }
 
 __global__ void __launch_bounds__(kThreads) swiglu_grad_kernel(
     const uint2* __restrict__ q, const float* __restrict__ scales, const uint4* __restrict__ da,
-    uint4* __restrict__ dgu, uint4* __restrict__ a, int rows, int vpr) {
-  const long long total = (long long)rows * vpr;
-  for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < total;
-       i += (long long)gridDim.x * kThreads) {
-    const long long r = i / vpr;
-    const int v = static_cast<int>(i % vpr);
-    float g[8], u[8], d[8], dg[8], du[8], o[8];
-    codes8(q[r * 2 * vpr + v], scales[(long long)(v / 16) * rows + r], g);
-    codes8(q[r * 2 * vpr + vpr + v], scales[(long long)((vpr + v) / 16) * rows + r], u);
-    unpack8(da[i], d);
+    uint4* __restrict__ dgu, uint4* __restrict__ a, int rows, int nb) {
+  const int rg = blockIdx.x / nb, b = blockIdx.x - rg * nb;
+  const int r = rg * kTileRows + (threadIdx.x >> 4), l = threadIdx.x & 15;
+  if (r >= rows) return;
+  const size_t ga = ((size_t)r * 2 * nb + b) * 16 + l, ua = ga + (size_t)nb * 16;
+  const size_t at = ((size_t)r * nb + b) * 16 + l;
+  float g[8], u[8], d[8], dg[8], du[8], o[8];
+  const uint2 cg = q[ga], cu = q[ua];
+  const uint4 dv = da[at];
+  codes8(cg, scales[(size_t)b * rows + r], g);
+  codes8(cu, scales[(size_t)(nb + b) * rows + r], u);
+  unpack8(dv, d);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float s = 1.0f / (1.0f + __expf(-g[j]));
-      const float gs = g[j] * s;
-      dg[j] = d[j] * u[j] * (s + gs * (1.0f - s));
-      du[j] = d[j] * gs;
-      o[j] = gs * u[j];
-    }
-    dgu[r * 2 * vpr + v] = pack8(dg);
-    dgu[r * 2 * vpr + vpr + v] = pack8(du);
-    if (a) a[i] = pack8(o);
+  for (int j = 0; j < 8; ++j) {
+    const float s = sigmoid(g[j]);
+    const float gs = g[j] * s;
+    dg[j] = d[j] * u[j] * (s + gs * (1.0f - s));
+    du[j] = d[j] * gs;
+    o[j] = gs * u[j];
   }
+  __stcs(dgu + ga, pack8(dg));
+  __stcs(dgu + ua, pack8(du));
+  if (a) __stcs(a + at, pack8(o));
 }
 
 // One CTA per (token, choice): dy's row times the weight, and its dot product with the row.
@@ -183,33 +246,41 @@ __global__ void __launch_bounds__(kThreads) combine_grad_kernel(
   }
 }
 
-unsigned blocks_for(long long threads) {
-  const long long b = (threads + kThreads - 1) / kThreads;
-  return static_cast<unsigned>(b < (1 << 20) ? b : 1 << 20);
+// CTAs of the 16-row tiles. (The callers keep rows * cols below 2^38: the grid fits.)
+unsigned tiles_of(int rows, int nb) {
+  return static_cast<unsigned>(((long long)rows + kTileRows - 1) / kTileRows * nb);
 }
 
 }  // namespace
 
+cudaError_t launch_act_save(int rows, int d, const void* x, void* q, float* scales,
+                            cudaStream_t st) {
+  return launch_kernel(act_save_kernel, dim3(tiles_of(rows, d / 128)), dim3(kThreads), 0, st, false,
+                       static_cast<const uint4*>(x), static_cast<uint2*>(q), scales, rows,
+                       d / 128);
+}
+
 cudaError_t launch_act_load(int rows, int src_rows, int d, const void* q, const float* scales,
                             const int32_t* index, void* out, uint32_t* status, cudaStream_t st) {
-  return launch_kernel(act_load_kernel, dim3(blocks_for((long long)rows * (d / 8))),
+  const int nb = d / 128, parts = (nb + kLoadBlocks - 1) / kLoadBlocks;
+  const long long warps = (long long)rows * parts;
+  return launch_kernel(act_load_kernel, dim3((unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32))),
                        dim3(kThreads), 0, st, false, static_cast<const uint2*>(q), scales, index,
-                       static_cast<uint4*>(out), rows, src_rows, d / 8, status);
+                       static_cast<uint4*>(out), rows, src_rows, nb, parts, status);
 }
 
 cudaError_t launch_swiglu_save(int rows, int f, const void* gu, void* a, void* q, float* scales,
                                cudaStream_t st) {
-  return launch_kernel(swiglu_save_kernel, dim3(blocks_for((long long)rows * (f / 8))),
-                       dim3(kThreads), 0, st, false, static_cast<const uint4*>(gu),
-                       static_cast<uint4*>(a), static_cast<uint2*>(q), scales, rows, f / 8);
+  return launch_kernel(swiglu_save_kernel, dim3(tiles_of(rows, f / 128)), dim3(kThreads), 0, st,
+                       false, static_cast<const uint4*>(gu), static_cast<uint4*>(a),
+                       static_cast<uint2*>(q), scales, rows, f / 128);
 }
 
 cudaError_t launch_swiglu_grad(int rows, int f, const void* q, const float* scales,
                                const void* da, void* dgu, void* a, cudaStream_t st) {
-  return launch_kernel(swiglu_grad_kernel, dim3(blocks_for((long long)rows * (f / 8))),
-                       dim3(kThreads), 0, st, false, static_cast<const uint2*>(q), scales,
-                       static_cast<const uint4*>(da), static_cast<uint4*>(dgu),
-                       static_cast<uint4*>(a), rows, f / 8);
+  return launch_kernel(swiglu_grad_kernel, dim3(tiles_of(rows, f / 128)), dim3(kThreads), 0, st,
+                       false, static_cast<const uint2*>(q), scales, static_cast<const uint4*>(da),
+                       static_cast<uint4*>(dgu), static_cast<uint4*>(a), rows, f / 128);
 }
 
 cudaError_t launch_combine_grad(int T, int k, int d, int rows, const void* ebuf,
