@@ -21,13 +21,15 @@
 // memory after the load cost a round trip between the two CTAs in every unit: 32 groups of 520
 // rows, 7168 x 2048, 456 us that way.)
 //
-// Each pair walks the units (group, 256 output columns, N tile) from its number in steps of the
-// pairs; a group's units are weight-tile-major, so pairs that run side by side share a weight
-// tile through L2. The tables of the units are built by every CTA from the counts itself, without
-// a schedule kernel.
+// The units (group, 256 output columns, N tile) are numbered group after group; a pair starts with
+// its own number and takes further ones from a counter in the workspace as it gets free, since
+// the groups' units differ in size (fixed shares left 6 to 11 % of the time to the slowest pair
+// with uneven groups). Which pair computes a unit does not change its result. The tables are
+// built by every CTA from the counts itself, without a schedule kernel.
 //
-// Roles in a CTA (one CTA per SM): warp 0 TMA producer, warp 1 MMA issuer (leader CTA), the others
-// the epilogue. Loads of both CTAs count on
+// Roles in a CTA (one CTA per SM): warp 0 TMA producer, warp 1 MMA issuer (leader CTA), warp 2
+// scheduler (leader CTA: hands decoded units to the roles of both CTAs through a small ring), the
+// others the epilogue. Loads of both CTAs count on
 // the leader's full barriers, its commits free the stages of both. Accumulators are double
 // buffered. Every wait is bounded.
 #include "moe_device.cuh"
@@ -73,13 +75,13 @@ __device__ __forceinline__ void group_offsets(const int32_t* counts, int E, int 
   __syncthreads();
 }
 
-// Warps 0 and 1 load and issue the MMAs; the others are the epilogue: two warps per tensor-memory
+// Warps 0, 1 and 2 load, issue the MMAs and schedule; the others are the epilogue: two warps per tensor-memory
 // quarter, or four where the sums of a tile are held in registers (fp32 weight gradients: 64
 // columns a thread).
 template <bool F32>
 struct GroupedThreads {
   static constexpr int kEpi = F32 ? 16 : 8;
-  static constexpr int kAll = (2 + kEpi) * 32;
+  static constexpr int kAll = (3 + kEpi) * 32;
 };
 // fp32 weight gradients: k-steps per tensor-core sum. The tensor core truncates as it adds, an
 // error that grows with the number of additions (2.1e-6 of the result after 2048 products,
@@ -90,10 +92,15 @@ constexpr int kSumSteps = 8;
 // apart (64 used), which keeps the eight 16-byte rows of a matrix store in different banks.
 constexpr int kTurnPitch = 80, kTurnBytes = 32 * kTurnPitch;
 
+// Units on their way from the scheduler to the roles. A role frees its slot once it has read it:
+// one slot ahead of the producer, which is itself a unit or two ahead of the epilogue.
+constexpr int kRing = 3;
+
 struct GroupedArgs {
   const int32_t* counts;
   void* out;
   uint32_t* status;
+  uint32_t* counter;   // units taken, 0 before and after a launch
   int rows, E, n, k;
   int cols;       // output columns (M)
   int red;        // fwd, dx: length of the reduction
@@ -116,48 +123,44 @@ struct GroupedTables {
   int off[kMaxGroups + 1];   // first row of each group
   int live[kMaxGroups];      // fwd, dx: the groups with rows
   int n_live;
+  int n_units;
 };
 
 // One unit of work: 256 output columns (the pair's) x one N tile of one group.
-struct GroupedUnit {
-  int g;      // group
+struct alignas(16) GroupedUnit {
+  int g;      // group, or -1: no more units
   int f0;     // first output column of the pair
   int n0;     // fwd, dx: first row; dw: first row of dW_g
   int nlen;   // rows of the tile
   int r0;     // dw: the group's first row
   int red;    // length of the reduction
   int nt;     // N tiles that read this unit's weight tile
+  int pad;
 };
 
-// Walks a pair's units: numbers pair, pair + pairs, ... of the groups' units one group after the
-// other. fwd, dx: weight-tile-major (unit m * nt + j of a group: N tile j of its 256 columns
-// number m), so that neighbours share a weight tile. dw: by rows of the output (unit j * mt + m),
-// so that neighbours write adjacent columns (fp32, 32 groups of 128 rows, 4096 x 7168: 680 us the
-// other way, 644 us so with streaming stores).
+// The units by ascending number. fwd, dx: weight-tile-major (unit m * nt + j of a group: N tile j
+// of its 256 columns number m), so that pairs at work on neighbouring units share a weight tile
+// through L2. dw: by rows of the output (unit j * mt + m), so that they write adjacent columns
+// (fp32, 32 groups of 128 rows, 4096 x 7168: 680 us the other way, 644 us so with streaming
+// stores).
 // fwd, dx: a group of c rows has nt = ceil(c / TN) N tiles of equal size (to 32 rows, the step of
 // an MMA's N) rather than full ones and a rest, which would cost a whole pass over the weight
-// tile for a few rows (16384 rows over 32 experts, about half of them just over 512: forward
-// 796 -> 680 us).
+// tile for a few rows.
 template <int DIR, int TN>
 struct GroupedWalk {
   const GroupedArgs& a;
   const GroupedTables& tab;
-  int i, q, p;          // position of the group; unit q * inner + p of it
-  int step, dq, dp;     // pairs, in units of this group
+  int i, local;         // position of the group, unit of it
   int inner, outer;     // its units: outer x inner
   int w, base, len;
 
-  __device__ __forceinline__ GroupedWalk(const GroupedArgs& a_, const GroupedTables& t_, int pair,
-                                         int pairs)
-      : a(a_), tab(t_), i(0), q(0), p(0), step(pairs), dq(0), dp(0), inner(1), outer(1), w(TN),
-        base(0), len(0) {
+  __device__ __forceinline__ GroupedWalk(const GroupedArgs& a_, const GroupedTables& t_)
+      : a(a_), tab(t_), i(0), local(0), inner(1), outer(1), w(TN), base(0), len(0) {
     load();
-    settle(pair);
   }
-  __device__ __forceinline__ int groups() const {
-    return DIR == kGroupedDw ? a.E : tab.n_live;
+  __device__ __forceinline__ bool more() const {
+    return i < (DIR == kGroupedDw ? a.E : tab.n_live);
   }
-  __device__ __forceinline__ bool more() const { return i < groups(); }
   __device__ __forceinline__ void load() {   // the group at position i
     if (DIR == kGroupedDw) {
       inner = a.mt;
@@ -170,36 +173,22 @@ struct GroupedWalk {
       outer = a.mt;
       w = inner == 1 ? TN : ((len + inner - 1) / inner + 31) & ~31;
     }
-    if (DIR != kGroupedDw || i == 0) {
-      dq = step / inner;
-      dp = step - dq * inner;
-    }
   }
-  // To unit `local` of group i or, past its units, of the groups after it.
-  __device__ __forceinline__ void settle(int local) {
+  __device__ __forceinline__ void advance(int units) {
+    local += units;
     while (more() && local >= inner * outer) {
       local -= inner * outer;
       ++i;
       load();
     }
-    q = local / inner;
-    p = local - q * inner;
-  }
-  __device__ __forceinline__ void next() {   // (no division while the group lasts)
-    q += dq;
-    p += dp;
-    if (p >= inner) {
-      p -= inner;
-      ++q;
-    }
-    if (q < outer) return;
-    const int local = (q - outer) * inner + p;
-    ++i;
-    load();
-    settle(local);
   }
   __device__ __forceinline__ GroupedUnit unit() const {
-    GroupedUnit r;
+    GroupedUnit r{};
+    if (!more()) {
+      r.g = -1;
+      return r;
+    }
+    const int q = local / inner, p = local - q * inner;
     if (DIR == kGroupedDw) {
       r.g = i;
       r.f0 = p * 256;
@@ -218,6 +207,33 @@ struct GroupedWalk {
       r.nt = inner;
     }
     return r;
+  }
+};
+
+// A role's end of the ring. next(): waits for the next unit and frees its slot; false at the end
+// or after an abort. One thread (kWarp false) or a whole warp calls it.
+template <bool kWarp>
+struct UnitReader {
+  const GroupedUnit* ring;
+  uint64_t* full;
+  uint64_t* empty;   // of the leader
+  volatile int* abort;
+  uint32_t* status;
+  int slot = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ bool next(GroupedUnit* u) {
+    bool ok = mbar_wait_cluster(&full[slot], phase, abort, status);
+    if (kWarp) ok = __all_sync(0xffffffffu, ok);
+    if (!ok) return false;
+    *u = ring[slot];
+    if (kWarp) __syncwarp();   // every lane has read it
+    if (u->g < 0) return false;
+    if (!kWarp || (threadIdx.x & 31) == 0) mbar_arrive_cluster_relaxed(cluster_addr(&empty[slot], 0));
+    if (++slot == kRing) {
+      slot = 0;
+      phase ^= 1u;
+    }
+    return true;
   }
 };
 
@@ -267,6 +283,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
   static_assert(!kDw || TN >= 128, "dw: whole 64-column boxes");
   extern __shared__ uint8_t smem_raw[];
   __shared__ GroupedTables tab;
+  __shared__ GroupedUnit ring[kRing];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* turn = smem + STAGES * S::STAGE_BYTES;
@@ -274,7 +291,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
   uint64_t* empty = full + STAGES;
   uint64_t* tfull = empty + STAGES;
   uint64_t* tempty = tfull + 2;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
+  uint64_t* rfull = tempty + 2;
+  uint64_t* rempty = rfull + kRing;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rempty + kRing);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);   // uniform
@@ -291,6 +310,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
       mbar_init(&tfull[i], 1);
       mbar_init(&tempty[i], 2 * kEpiWarps);
     }
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&rfull[i], 1);
+      mbar_init(&rempty[i], 2 * kEpiWarps + 3);   // both epilogues and producers, the MMA thread
+    }
     *abort_flag = 0;
     mbar_fence_init();
     if (!kDw) {
@@ -300,15 +323,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
   }
   group_offsets(a.counts, a.E, a.rows, tab.off, a.status);
   if (!kDw && warp == 0) {
-    int at = 0;
+    int at = 0, tiles = 0;
     for (int e0 = 0; e0 < a.E; e0 += 32) {
       const int e = e0 + lane;
-      const bool has = e < a.E && tab.off[e + 1] > tab.off[e];
+      const int c = e < a.E ? tab.off[e + 1] - tab.off[e] : 0;
+      const bool has = c > 0;
+      tiles += (c + TN - 1) / TN;
       const uint32_t m = __ballot_sync(0xffffffffu, has);
       if (has) tab.live[at + __popc(m & ((1u << lane) - 1u))] = e;
       at += __popc(m);
     }
-    if (lane == 0) tab.n_live = at;
+    tiles = __reduce_add_sync(0xffffffffu, tiles);
+    if (lane == 0) {
+      tab.n_live = at;
+      tab.n_units = tiles * a.mt;
+    }
+  } else if (kDw && threadIdx.x == 0) {
+    tab.n_units = a.E * a.mt * ((a.n + TN - 1) / TN);
   }
   if (warp == 1) tmem_alloc_pair(tmem_slot, S::TMEM_COLS);
   tc_fence_before();
@@ -318,7 +349,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
   if (kDw) pdl_wait();   // the groups' tensor maps are written
   const uint32_t tmem = *tmem_slot;
 
-  GroupedWalk<DIR, TN> walk(a, tab, blockIdx.x >> 1, gridDim.x >> 1);
   constexpr int kNever = 1 << 30;
   constexpr int kSum = F32 ? kSumSteps : kNever;   // k-steps per tensor-core sum
 
@@ -330,8 +360,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
       uint32_t phase = 0;
       bool ok = true;
       int acquired = -1;   // dw: the group whose maps this thread has acquired
-      for (; walk.more() && ok; walk.next()) {
-        const GroupedUnit t = walk.unit();
+      UnitReader<false> units{ring, rfull, rempty, abort_flag, a.status};
+      GroupedUnit t;
+      while (ok && units.next(&t)) {
         const CUtensorMap *ma = &mapA, *mb = &mapB;
         if (kDw) {
           ma = maps + 2 * t.g;
@@ -390,8 +421,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
       uint32_t phase = 0;
       bool ok = true, ready = false;
       int it = 0;
-      for (; walk.more() && ok; walk.next()) {
-        const GroupedUnit t = walk.unit();
+      UnitReader<false> units{ring, rfull, rempty, abort_flag, a.status};
+      GroupedUnit t;
+      while (ok && units.next(&t)) {
         const uint32_t n_mma = static_cast<uint32_t>((t.nlen + 31) & ~31);
         const uint32_t idesc = idesc_bf16(256, n_mma) | (DIR != kGroupedFwd ? kIdescAmn : 0u) |
                                (kDw ? kIdescBmn : 0u);
@@ -444,14 +476,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
       }
     }
     __syncwarp();
+  } else if (warp == 2) {
+    // ------------------------------ scheduler (leader) ------------------------------
+    if (leader && elect_one()) {
+      GroupedWalk<DIR, TN> walk(a, tab);
+      const uint32_t pairs = gridDim.x >> 1;
+      uint32_t at = blockIdx.x >> 1;   // number of the unit the walk stands at
+      walk.advance(static_cast<int>(at));
+      uint32_t last = 0;               // value of this pair's last fetch
+      int slot = 0;
+      uint32_t phase = 0;
+      while (true) {
+        const GroupedUnit u = walk.unit();
+        // the next number, while this unit's slot gets free: one is taken for every unit, and
+        // whoever takes the last leaves the counter as it was
+        if (u.g >= 0) {
+          last = atomicAdd(a.counter, 1u);
+          if (last + 1 == static_cast<uint32_t>(tab.n_units)) *a.counter = 0;
+        }
+        if (!mbar_wait_cluster(&rempty[slot], phase ^ 1u, abort_flag, a.status)) break;
+        const int4* v = reinterpret_cast<const int4*>(&u);
+        for (uint32_t cta = 0; cta < 2; ++cta) {
+          const uint32_t to = cluster_addr(&ring[slot], cta);
+          st_cluster16(to, v[0]);
+          st_cluster16(to + 16, v[1]);
+          mbar_arrive_cluster(cluster_addr(&rfull[slot], cta));
+        }
+        if (u.g < 0) break;
+        if (++slot == kRing) {
+          slot = 0;
+          phase ^= 1u;
+        }
+        walk.advance(static_cast<int>(pairs + last - at));
+        at = pairs + last;
+      }
+    }
+    __syncwarp();
   } else {
     // ------------------------------ epilogue ------------------------------
     // Warp w reads lanes 32 (w % 4) .. +31 (output columns) of its part of the tile's N columns.
-    const int quarter = warp & 3, part = (warp - 2) >> 2;
+    const int quarter = warp & 3, part = (warp - 3) >> 2;
     int it = 0;
     bool ok = true;
-    for (; walk.more() && ok; walk.next()) {
-      const GroupedUnit t = walk.unit();
+    UnitReader<true> units{ring, rfull, rempty, abort_flag, a.status};
+    GroupedUnit t;
+    while (ok && units.next(&t)) {
       const int steps = (t.red + 63) >> 6;
       const int fw = t.f0 + static_cast<int>(rank) * 128 + quarter * 32;   // the warp's columns
       if constexpr (F32) {
@@ -540,7 +609,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
         // shared memory, stored as 16-byte pieces (four lanes a row)
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
         const size_t row0 = (kDw ? (size_t)t.g * a.n : 0) + t.n0;
-        uint8_t* mine = turn + (warp - 2) * kTurnBytes;
+        uint8_t* mine = turn + (warp - 3) * kTurnBytes;
         const uint32_t put = smem_addr(mine) + (lane & 7) * kTurnPitch + (lane >> 3) * 16;
         const uint8_t* get = mine + (lane >> 2) * kTurnPitch + (lane & 3) * 16;
         const int fl = fw + (lane & 3) * 8;   // this lane's first column when it stores
@@ -636,7 +705,8 @@ cudaError_t run_rows(int tn, const GroupedArgs& a, const CUtensorMap& mA, const 
 
 }  // namespace
 
-// status word; then, from the next 128-byte boundary after 256 bytes, dw's tensor maps
+// status word; at byte 128 the unit counter; from the next 128-byte boundary after 256 bytes on,
+// dw's tensor maps
 size_t grouped_ws_bytes(const moe_group_cfg& c) {
   return 256 + 128 + 2 * sizeof(CUtensorMap) * (size_t)c.E;
 }
@@ -652,6 +722,7 @@ cudaError_t launch_grouped(const moe_group_cfg& c, GroupedDir dir, const void* i
   a.counts = counts;
   a.out = out;
   a.status = static_cast<uint32_t*>(ws);
+  a.counter = static_cast<uint32_t*>(ws) + 32;
   a.rows = c.rows;
   a.E = c.E;
   a.n = c.n;

@@ -367,7 +367,8 @@ typedef struct moe_group_cfg {
 
 /* Bytes of the workspace that the grouped products of this shape take. The first word of the
  * workspace is its status word (moe_clear_status, moe_read_status); the caller zeroes the
- * workspace once, before its first use, and every call leaves it ready for the next. Calls that
+ * workspace once, before its first use, and every call leaves it ready for the next (after a
+ * call that reported MOE_DEV_TIMEOUT, zero it again). Calls that
  * may overlap on the GPU need workspaces of their own. MOE_ERR_INVALID_ARG for a negative or
  * zero size, MOE_ERR_UNSUPPORTED for n or k not a multiple of 8 or E > 1024. */
 int moe_grouped_query(const moe_group_cfg* cfg, size_t* ws_bytes);
