@@ -350,6 +350,11 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
   return a;
 }
 
+// Makes this thread's earlier accesses visible in the cluster before its later relaxed arrivals.
+__device__ __forceinline__ void fence_release_cluster() {
+  asm volatile("fence.acq_rel.cluster;" ::: "memory");
+}
+
 // 16 bytes to an address of the cluster's shared-memory window (cluster_addr).
 __device__ __forceinline__ void st_cluster16(uint32_t addr, const int4& v) {
   asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y),

@@ -122,6 +122,7 @@ struct GroupedShape {
 struct GroupedTables {
   int off[kMaxGroups + 1];   // first row of each group
   int live[kMaxGroups];      // fwd, dx: the groups with rows
+  int first[kMaxGroups];     // and the N tiles before each of them
   int n_live;
   int n_units;
 };
@@ -138,77 +139,52 @@ struct alignas(16) GroupedUnit {
   int pad;
 };
 
-// The units by ascending number. fwd, dx: weight-tile-major (unit m * nt + j of a group: N tile j
-// of its 256 columns number m), so that pairs at work on neighbouring units share a weight tile
-// through L2. dw: by rows of the output (unit j * mt + m), so that they write adjacent columns
-// (fp32, 32 groups of 128 rows, 4096 x 7168: 680 us the other way, 644 us so with streaming
-// stores).
+// Unit number u. fwd, dx: weight-tile-major (unit m * nt + j of a group: N tile j of its 256
+// columns number m), so that pairs at work on neighbouring units share a weight tile through L2.
+// dw: by rows of the output (unit j * mt + m), so that they write adjacent columns (fp32, 32 groups
+// of 128 rows, 4096 x 7168: 680 us the other way, 644 us so with streaming stores).
 // fwd, dx: a group of c rows has nt = ceil(c / TN) N tiles of equal size (to 32 rows, the step of
 // an MMA's N) rather than full ones and a rest, which would cost a whole pass over the weight
-// tile for a few rows.
+// tile for a few rows. The group is found by binary search over the tiles before each: walking
+// there from the unit before took several thousand cycles where groups are many and small.
 template <int DIR, int TN>
-struct GroupedWalk {
-  const GroupedArgs& a;
-  const GroupedTables& tab;
-  int i, local;         // position of the group, unit of it
-  int inner, outer;     // its units: outer x inner
-  int w, base, len;
-
-  __device__ __forceinline__ GroupedWalk(const GroupedArgs& a_, const GroupedTables& t_)
-      : a(a_), tab(t_), i(0), local(0), inner(1), outer(1), w(TN), base(0), len(0) {
-    load();
-  }
-  __device__ __forceinline__ bool more() const {
-    return i < (DIR == kGroupedDw ? a.E : tab.n_live);
-  }
-  __device__ __forceinline__ void load() {   // the group at position i
-    if (DIR == kGroupedDw) {
-      inner = a.mt;
-      outer = (a.n + TN - 1) / TN;
-    } else if (i < tab.n_live) {
-      const int g = tab.live[i];
-      base = tab.off[g];
-      len = tab.off[g + 1] - base;
-      inner = (len + TN - 1) / TN;
-      outer = a.mt;
-      w = inner == 1 ? TN : ((len + inner - 1) / inner + 31) & ~31;
-    }
-  }
-  __device__ __forceinline__ void advance(int units) {
-    local += units;
-    while (more() && local >= inner * outer) {
-      local -= inner * outer;
-      ++i;
-      load();
-    }
-  }
-  __device__ __forceinline__ GroupedUnit unit() const {
-    GroupedUnit r{};
-    if (!more()) {
-      r.g = -1;
-      return r;
-    }
-    const int q = local / inner, p = local - q * inner;
-    if (DIR == kGroupedDw) {
-      r.g = i;
-      r.f0 = p * 256;
-      r.n0 = q * TN;
-      r.nlen = min(TN, a.n - r.n0);
-      r.r0 = tab.off[i];
-      r.red = tab.off[i + 1] - r.r0;
-      r.nt = outer;
-    } else {
-      r.g = tab.live[i];
-      r.f0 = q * 256;
-      r.n0 = base + p * w;
-      r.nlen = min(w, len - p * w);
-      r.r0 = 0;
-      r.red = a.red;
-      r.nt = inner;
-    }
+__device__ __forceinline__ GroupedUnit grouped_unit(const GroupedArgs& a, const GroupedTables& tab,
+                                                    int u) {
+  GroupedUnit r{};
+  if (u >= tab.n_units) {
+    r.g = -1;
     return r;
   }
-};
+  if (DIR == kGroupedDw) {
+    const int row = u / a.mt;   // of the N tiles of all groups
+    r.nt = (a.n + TN - 1) / TN;
+    r.f0 = (u - row * a.mt) * 256;
+    r.g = row / r.nt;
+    r.n0 = (row - r.g * r.nt) * TN;
+    r.nlen = min(TN, a.n - r.n0);
+    r.r0 = tab.off[r.g];
+    r.red = tab.off[r.g + 1] - r.r0;
+  } else {
+    const int t = u / a.mt;
+    int lo = 0, hi = tab.n_live - 1;   // last group whose first tile is <= t
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (tab.first[mid] <= t) lo = mid;
+      else hi = mid - 1;
+    }
+    r.g = tab.live[lo];
+    const int base = tab.off[r.g], len = tab.off[r.g + 1] - base;
+    const int local = u - tab.first[lo] * a.mt;
+    r.nt = (len + TN - 1) / TN;
+    const int m = local / r.nt, j = local - m * r.nt;
+    const int w = r.nt == 1 ? TN : ((len + r.nt - 1) / r.nt + 31) & ~31;
+    r.f0 = m * 256;
+    r.n0 = base + j * w;
+    r.nlen = min(w, len - j * w);
+    r.red = a.red;
+  }
+  return r;
+}
 
 // A role's end of the ring. next(): waits for the next unit and frees its slot; false at the end
 // or after an abort. One thread (kWarp false) or a whole warp calls it.
@@ -328,12 +304,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
       const int e = e0 + lane;
       const int c = e < a.E ? tab.off[e + 1] - tab.off[e] : 0;
       const bool has = c > 0;
-      tiles += (c + TN - 1) / TN;
+      const int nt = (c + TN - 1) / TN;
+      int incl = nt;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
       const uint32_t m = __ballot_sync(0xffffffffu, has);
-      if (has) tab.live[at + __popc(m & ((1u << lane) - 1u))] = e;
+      if (has) {
+        const int i = at + __popc(m & ((1u << lane) - 1u));
+        tab.live[i] = e;
+        tab.first[i] = tiles + incl - nt;
+      }
       at += __popc(m);
+      tiles += __shfl_sync(0xffffffffu, incl, 31);
     }
-    tiles = __reduce_add_sync(0xffffffffu, tiles);
     if (lane == 0) {
       tab.n_live = at;
       tab.n_units = tiles * a.mt;
@@ -479,36 +465,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
   } else if (warp == 2) {
     // ------------------------------ scheduler (leader) ------------------------------
     if (leader && elect_one()) {
-      GroupedWalk<DIR, TN> walk(a, tab);
       const uint32_t pairs = gridDim.x >> 1;
-      uint32_t at = blockIdx.x >> 1;   // number of the unit the walk stands at
-      walk.advance(static_cast<int>(at));
-      uint32_t last = 0;               // value of this pair's last fetch
+      int at = blockIdx.x >> 1;   // number of the unit at hand
       int slot = 0;
       uint32_t phase = 0;
       while (true) {
-        const GroupedUnit u = walk.unit();
-        // the next number, while this unit's slot gets free: one is taken for every unit, and
-        // whoever takes the last leaves the counter as it was
-        if (u.g >= 0) {
-          last = atomicAdd(a.counter, 1u);
-          if (last + 1 == static_cast<uint32_t>(tab.n_units)) *a.counter = 0;
-        }
+        const GroupedUnit u = grouped_unit<DIR, TN>(a, tab, at);
+        // one number is taken for every unit; whoever takes the last leaves the counter as it was
+        uint32_t taken = 0;
+        if (u.g >= 0) taken = atomicAdd(a.counter, 1u);
         if (!mbar_wait_cluster(&rempty[slot], phase ^ 1u, abort_flag, a.status)) break;
         const int4* v = reinterpret_cast<const int4*>(&u);
         for (uint32_t cta = 0; cta < 2; ++cta) {
           const uint32_t to = cluster_addr(&ring[slot], cta);
           st_cluster16(to, v[0]);
           st_cluster16(to + 16, v[1]);
-          mbar_arrive_cluster(cluster_addr(&rfull[slot], cta));
         }
+        fence_release_cluster();
+        mbar_arrive_cluster_relaxed(cluster_addr(&rfull[slot], 0));
+        mbar_arrive_cluster_relaxed(cluster_addr(&rfull[slot], 1));
         if (u.g < 0) break;
         if (++slot == kRing) {
           slot = 0;
           phase ^= 1u;
         }
-        walk.advance(static_cast<int>(pairs + last - at));
-        at = pairs + last;
+        if (taken + 1 == static_cast<uint32_t>(tab.n_units)) *a.counter = 0;
+        at = static_cast<int>(pairs + taken);
       }
     }
     __syncwarp();
