@@ -88,9 +88,11 @@ struct GroupedThreads {
 // 4.4e-6 after 4096, against 4e-7 for rounded fp32 sums); sums of 512 rows are therefore read
 // out and added in registers, rounded.
 constexpr int kSumSteps = 8;
-// bf16 epilogue: a warp turns 32 output rows x 32 columns around in shared memory, rows 80 bytes
-// apart (64 used), which keeps the eight 16-byte rows of a matrix store in different banks.
-constexpr int kTurnPitch = 80, kTurnBytes = 32 * kTurnPitch;
+// bf16 epilogue: two warps turn 32 output rows x 64 columns around in shared memory, rows 144 bytes
+// apart (128 used), which keeps the eight 16-byte rows of a matrix store in different banks.
+// Together they store whole 128-byte lines: the store path takes about one segment every four
+// cycles, of 64 bytes or of 128.
+constexpr int kTurnPitch = 144, kTurnBytes = 32 * kTurnPitch;
 
 // Units on their way from the scheduler to the roles. A role frees its slot once it has read it:
 // one slot ahead of the producer, which is itself a unit or two ahead of the epilogue.
@@ -113,7 +115,7 @@ struct GroupedShape {
   static constexpr int B_BYTES = TN / 2 * 128;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr int TMEM_COLS = 2 * TN;
-  static constexpr int TURN = F32 ? 0 : GroupedThreads<F32>::kEpi * kTurnBytes;
+  static constexpr int TURN = F32 ? 0 : GroupedThreads<F32>::kEpi / 2 * kTurnBytes;
   static constexpr int SMEM = STAGES * STAGE_BYTES + TURN + 1024 + 512;
   static_assert(B_BYTES % 1024 == 0 && TMEM_COLS <= 512 && TMEM_COLS >= 32, "");
 };
@@ -184,6 +186,23 @@ __device__ __forceinline__ GroupedUnit grouped_unit(const GroupedArgs& a, const 
     r.red = a.red;
   }
   return r;
+}
+
+// Barrier of the 64 threads of two warps, and whether both said yes.
+__device__ __forceinline__ void pair_sync(int id) {
+  asm volatile("barrier.cta.sync %0, 64;" ::"r"(id) : "memory");
+}
+__device__ __forceinline__ bool pair_agree(int id, bool yes) {
+  uint32_t all;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 q, %2, 0;\n\t"
+      "barrier.cta.red.and.pred p, %1, 64, q;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(all)
+      : "r"(id), "r"(static_cast<uint32_t>(yes))
+      : "memory");
+  return all != 0;
 }
 
 // A role's end of the ring. next(): waits for the next unit and frees its slot; false at the end
@@ -501,8 +520,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
     int it = 0;
     bool ok = true;
     UnitReader<true> units{ring, rfull, rempty, abort_flag, a.status};
-    GroupedUnit t;
-    while (ok && units.next(&t)) {
+    GroupedUnit t{};
+    while (ok) {
+      ok = units.next(&t);
+      if (F32 && !ok) break;   // (bf16: the two warps of a pair leave together, below)
       const int steps = (t.red + 63) >> 6;
       const int fw = t.f0 + static_cast<int>(rank) * 128 + quarter * 32;   // the warp's columns
       if constexpr (F32) {
@@ -587,20 +608,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
           }
         }
       } else {
-        // 32 rows x 32 columns at a time: accumulator fragments to bf16, turned around through
-        // shared memory, stored as 16-byte pieces (four lanes a row)
+        // 32 rows x 64 columns of two warps at a time: accumulator fragments to bf16, turned around
+        // through shared memory, stored as 16-byte pieces, eight lanes a row
+        const int b = it & 1, duo = quarter >> 1;
+        const int id = 1 + 2 * part + duo;
+        if (ok && steps > 0) ok = warp_wait(&tfull[b], (it >> 1) & 1, abort_flag, a.status);
+        if (!pair_agree(id, ok)) break;
+        tc_fence_after();
         __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
         const size_t row0 = (kDw ? (size_t)t.g * a.n : 0) + t.n0;
-        uint8_t* mine = turn + (warp - 3) * kTurnBytes;
-        const uint32_t put = smem_addr(mine) + (lane & 7) * kTurnPitch + (lane >> 3) * 16;
-        const uint8_t* get = mine + (lane >> 2) * kTurnPitch + (lane & 3) * 16;
-        const int fl = fw + (lane & 3) * 8;   // this lane's first column when it stores
-        const bool in = fl < a.cols;          // (cols is a multiple of 8)
-        const int b = it & 1;
-        if (steps > 0) {
-          if (!warp_wait(&tfull[b], (it >> 1) & 1, abort_flag, a.status)) break;
-          tc_fence_after();
-        }
+        uint8_t* mine = turn + (2 * part + duo) * kTurnBytes;
+        const uint32_t put = smem_addr(mine) + (lane & 7) * kTurnPitch + (quarter & 1) * 64 +
+                             (lane >> 3) * 16;
+        const int first = (quarter & 1) * 16 + (lane >> 3);   // of the rows this lane stores
+        const uint8_t* get = mine + first * kTurnPitch + (lane & 7) * 16;
+        const int fl = fw - (quarter & 1) * 32 + (lane & 7) * 8;   // and their columns
+        const bool in = fl < a.cols;                               // (cols is a multiple of 8)
         const uint32_t tb = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + b * TN;
         for (int c = part * 32; c < t.nlen; c += kEpiWarps * 8) {
           uint4 v[4];
@@ -612,7 +635,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
             auto pack = [](uint32_t x, uint32_t y) {
               return pack_bf16x2(__uint_as_float(x), __uint_as_float(y));
             };
-            __syncwarp();   // the previous rows have been read
+            pair_sync(id);   // the previous rows have been read
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const uint32_t m[4] = {
@@ -620,19 +643,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
                   pack(hi[4 * i], hi[4 * i + 1]), pack(hi[4 * i + 2], hi[4 * i + 3])};
               stmatrix_x4_trans(put + i * 8 * kTurnPitch, m);
             }
-            __syncwarp();
+            pair_sync(id);
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-              v[q] = *reinterpret_cast<const uint4*>(get + q * 8 * kTurnPitch);
+              v[q] = *reinterpret_cast<const uint4*>(get + q * 4 * kTurnPitch);
           } else {   // dw of an empty group
 #pragma unroll
             for (int q = 0; q < 4; ++q) v[q] = make_uint4(0, 0, 0, 0);
           }
-          const int p = c + (lane >> 2);
+          const int p = c + first;
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            if (in && p + 8 * q < t.nlen)
-              *reinterpret_cast<uint4*>(out + (row0 + p + 8 * q) * a.cols + fl) = v[q];
+            if (in && p + 4 * q < t.nlen)
+              *reinterpret_cast<uint4*>(out + (row0 + p + 4 * q) * a.cols + fl) = v[q];
         }
         if (steps > 0) {
           tc_fence_before();
