@@ -381,6 +381,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
         // each CTA's half of the N tile, a multiple of 16 rows (an MMA takes N in steps of 32)
         const int half = ((t.nlen + 31) & ~31) >> 1;
         const int steps = (t.red + 63) >> 6;
+        // bytes of a step in both CTAs (dw: of B only the 64-column boxes that the tile has)
+        const uint32_t bytes =
+            2 * (S::A_BYTES + (kDw ? (half + 63) / 64 * 8192 : S::B_BYTES));
         const uint64_t pol_a = kDw || t.nt > 1 ? pol_keep : pol_once;
         const int f = t.f0 + static_cast<int>(rank) * 128;
         const int nb = t.n0 + static_cast<int>(rank) * half;
@@ -391,7 +394,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
           }
           uint8_t* sa = smem + stage * S::STAGE_BYTES;
           uint8_t* sb = sa + S::A_BYTES;
-          if (leader) mbar_arrive_expect_tx(&full[stage], 2 * S::STAGE_BYTES);
+          if (leader) mbar_arrive_expect_tx(&full[stage], bytes);
           const uint32_t bar = cluster_addr(&full[stage], 0);
           if (DIR == kGroupedFwd) {
             tma_load_3d_pair(sa, ma, bar, ks * 64, f, t.g, pol_a);
@@ -405,7 +408,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
           if (kDw) {
 #pragma unroll
             for (int j = 0; j < kBoxesB; ++j)
-              tma_load_2d_pair(sb + j * 8192, mb, bar, nb + 64 * j, t.r0 + ks * 64, pol_keep);
+              if (64 * j < half)
+                tma_load_2d_pair(sb + j * 8192, mb, bar, nb + 64 * j, t.r0 + ks * 64, pol_keep);
           } else {
             tma_load_2d_pair(sb, mb, bar, ks * 64, nb, pol_keep);
           }
@@ -680,12 +684,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
 
 template <int DIR, int TN, int STAGES, bool F32 = false, bool ACC = false>
 cudaError_t run_grouped_kernel(const GroupedArgs& a, const CUtensorMap& mA, const CUtensorMap& mB,
-                               cudaStream_t st, const CUtensorMap* maps = nullptr) {
+                               long long units, cudaStream_t st,
+                               const CUtensorMap* maps = nullptr) {
   using S = GroupedShape<TN, STAGES, F32>;
   auto kern = grouped_kernel<DIR, TN, STAGES, F32, ACC>;
   const cudaError_t err = ensure_smem_limit(reinterpret_cast<const void*>(kern), S::SMEM);
   if (err != cudaSuccess) return err;
-  return launch_kernel(kern, dim3(sm_count() & ~1), dim3(GroupedThreads<F32>::kAll), S::SMEM, st,
+  // one pair for every two SMs, or for every unit there can be
+  const long long pairs = sm_count() / 2;
+  return launch_kernel(kern, dim3(2 * (unsigned)(units < pairs ? units : pairs)), dim3(GroupedThreads<F32>::kAll), S::SMEM, st,
                        maps != nullptr, a, maps, mA, mB);
 }
 
@@ -700,11 +707,12 @@ int row_tile(const moe_group_cfg& c) {
 template <int DIR>
 cudaError_t run_rows(int tn, const GroupedArgs& a, const CUtensorMap& mA, const CUtensorMap& mB,
                      cudaStream_t st) {
+  const long long units = ((long long)a.rows / tn + (a.E < a.rows ? a.E : a.rows)) * a.mt;
   switch (tn) {
-    case 32: return run_grouped_kernel<DIR, 32, 10>(a, mA, mB, st);
-    case 64: return run_grouped_kernel<DIR, 64, 9>(a, mA, mB, st);
-    case 128: return run_grouped_kernel<DIR, 128, 8>(a, mA, mB, st);
-    default: return run_grouped_kernel<DIR, 256, 6>(a, mA, mB, st);
+    case 32: return run_grouped_kernel<DIR, 32, 10>(a, mA, mB, units, st);
+    case 64: return run_grouped_kernel<DIR, 64, 9>(a, mA, mB, units, st);
+    case 128: return run_grouped_kernel<DIR, 128, 8>(a, mA, mB, units, st);
+    default: return run_grouped_kernel<DIR, 256, 6>(a, mA, mB, units, st);
   }
 }
 
@@ -757,9 +765,11 @@ cudaError_t launch_grouped(const moe_group_cfg& c, GroupedDir dir, const void* i
       group_maps_kernel, dim3((c.E + kMapWarps - 1) / kMapWarps), dim3(kMapWarps * 32), 0, st,
       false, counts, maps, c.rows, c.E, static_cast<uint32_t*>(ws), mA, mB);
   if (err != cudaSuccess) return err;
-  if (!out_f32) return run_grouped_kernel<kGroupedDw, 256, 6>(a, mA, mB, st, maps);
-  return accumulate ? run_grouped_kernel<kGroupedDw, 256, 6, true, true>(a, mA, mB, st, maps)
-                    : run_grouped_kernel<kGroupedDw, 256, 6, true>(a, mA, mB, st, maps);
+  const long long units = (long long)c.E * a.mt * ((c.n + 255) / 256);
+  if (!out_f32) return run_grouped_kernel<kGroupedDw, 256, 6>(a, mA, mB, units, st, maps);
+  return accumulate
+             ? run_grouped_kernel<kGroupedDw, 256, 6, true, true>(a, mA, mB, units, st, maps)
+             : run_grouped_kernel<kGroupedDw, 256, 6, true>(a, mA, mB, units, st, maps);
 }
 
 }  // namespace moe
