@@ -27,6 +27,11 @@
 // with uneven groups). Which pair computes a unit does not change its result. The tables are
 // built by every CTA from the counts itself, without a schedule kernel.
 //
+// Where there are fewer units than pairs, the reduction of each is split: every part leaves its
+// fp32 sums in the workspace, and for each warp's piece of the tile whichever part comes last adds
+// them up in the order of the parts and stores the result (one group of 64 rows, 4096 x 7168: 27.5
+// us unsplit; weight gradient of 30000 rows, 512 x 512: 133 us).
+//
 // Roles in a CTA (one CTA per SM): warp 0 TMA producer, warp 1 MMA issuer (leader CTA), warp 2
 // scheduler (leader CTA: hands decoded units to the roles of both CTAs through a small ring), the
 // others the epilogue. Loads of both CTAs count on
@@ -98,6 +103,10 @@ constexpr int kTurnPitch = 144, kTurnBytes = 32 * kTurnPitch;
 // one slot ahead of the producer, which is itself a unit or two ahead of the epilogue.
 constexpr int kRing = 3;
 
+// Split reductions: at most kPairs parts in all, of at least kMinSteps k-steps each; a counter of
+// arrivals per unit and epilogue warp of the pair.
+constexpr int kPairs = 76, kMinSteps = 4, kSplitSlots = 32;
+
 struct GroupedArgs {
   const int32_t* counts;
   void* out;
@@ -107,6 +116,9 @@ struct GroupedArgs {
   int cols;       // output columns (M)
   int red;        // fwd, dx: length of the reduction
   int mt;         // ceil(cols / 256)
+  int splits;     // parts of a unit's reduction, at most
+  uint32_t* arrived;   // [units][kSplitSlots], 0 before and after a launch
+  float* parts;        // [units][splits][TN][256]
 };
 
 template <int TN, int STAGES, bool F32>
@@ -135,10 +147,10 @@ struct alignas(16) GroupedUnit {
   int f0;     // first output column of the pair
   int n0;     // fwd, dx: first row; dw: first row of dW_g
   int nlen;   // rows of the tile
-  int r0;     // dw: the group's first row
-  int red;    // length of the reduction
+  int r0;     // where the reduction starts: a column, dw: a row
+  int red;    // its length
   int nt;     // N tiles that read this unit's weight tile
-  int pad;
+  int split;  // unit | part << 8 | parts << 16 where the reduction is split, else 0
 };
 
 // Unit number u. fwd, dx: weight-tile-major (unit m * nt + j of a group: N tile j of its 256
@@ -156,6 +168,12 @@ __device__ __forceinline__ GroupedUnit grouped_unit(const GroupedArgs& a, const 
   if (u >= tab.n_units) {
     r.g = -1;
     return r;
+  }
+  int part = 0;
+  const int number = u / a.splits;
+  if (a.splits > 1) {
+    part = u - number * a.splits;
+    u = number;
   }
   if (DIR == kGroupedDw) {
     const int row = u / a.mt;   // of the N tiles of all groups
@@ -185,6 +203,19 @@ __device__ __forceinline__ GroupedUnit grouped_unit(const GroupedArgs& a, const 
     r.nlen = min(w, len - j * w);
     r.red = a.red;
   }
+  if (a.splits > 1) {   // parts of equal length, as many as have kMinSteps; red < 0: no such part
+    const int steps = (r.red + 63) >> 6;
+    const int want = max(1, min(a.splits, steps / kMinSteps));
+    const int per = (steps + want - 1) / want;
+    const int have = steps ? (steps + per - 1) / per : 1;
+    if (part >= have) {
+      r.red = -1;
+    } else if (have > 1) {
+      r.r0 += part * per * 64;
+      r.red = min(r.red - part * per * 64, per * 64);
+      r.split = number | part << 8 | have << 16;
+    }
+  }
   return r;
 }
 
@@ -203,6 +234,22 @@ __device__ __forceinline__ bool pair_agree(int id, bool yes) {
       : "r"(id), "r"(static_cast<uint32_t>(yes))
       : "memory");
   return all != 0;
+}
+
+// One epilogue warp's arrival for its piece of a split unit, after its sums are in the workspace:
+// true for the part that comes last, which then sees all the others' sums.
+__device__ __forceinline__ bool last_part(const GroupedArgs& a, int split, int slot, int lane) {
+  __threadfence();
+  __syncwarp();
+  uint32_t before = 0;
+  if (lane == 0) {
+    uint32_t* n = a.arrived + (split & 255) * kSplitSlots + slot;
+    before = atomicAdd(n, 1u);
+    if (before + 1 == static_cast<uint32_t>(split >> 16)) *n = 0;   // ready for the next launch
+  }
+  before = __shfl_sync(0xffffffffu, before, 0);
+  __threadfence();
+  return before + 1 == static_cast<uint32_t>(split >> 16);
 }
 
 // A role's end of the ring. next(): waits for the next unit and frees its slot; false at the end
@@ -341,10 +388,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
     }
     if (lane == 0) {
       tab.n_live = at;
-      tab.n_units = tiles * a.mt;
+      tab.n_units = tiles * a.mt * a.splits;
     }
   } else if (kDw && threadIdx.x == 0) {
-    tab.n_units = a.E * a.mt * ((a.n + TN - 1) / TN);
+    tab.n_units = a.E * a.mt * ((a.n + TN - 1) / TN) * a.splits;
   }
   if (warp == 1) tmem_alloc_pair(tmem_slot, S::TMEM_COLS);
   tc_fence_before();
@@ -397,10 +444,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
           if (leader) mbar_arrive_expect_tx(&full[stage], bytes);
           const uint32_t bar = cluster_addr(&full[stage], 0);
           if (DIR == kGroupedFwd) {
-            tma_load_3d_pair(sa, ma, bar, ks * 64, f, t.g, pol_a);
+            tma_load_3d_pair(sa, ma, bar, t.r0 + ks * 64, f, t.g, pol_a);
           } else if (DIR == kGroupedDx) {
-            tma_load_3d_pair(sa, ma, bar, f, ks * 64, t.g, pol_a);
-            tma_load_3d_pair(sa + 8192, ma, bar, f + 64, ks * 64, t.g, pol_a);
+            tma_load_3d_pair(sa, ma, bar, f, t.r0 + ks * 64, t.g, pol_a);
+            tma_load_3d_pair(sa + 8192, ma, bar, f + 64, t.r0 + ks * 64, t.g, pol_a);
           } else {
             tma_load_2d_pair(sa, ma, bar, f, t.r0 + ks * 64, pol_a);
             tma_load_2d_pair(sa + 8192, ma, bar, f + 64, t.r0 + ks * 64, pol_a);
@@ -411,7 +458,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
               if (64 * j < half)
                 tma_load_2d_pair(sb + j * 8192, mb, bar, nb + 64 * j, t.r0 + ks * 64, pol_keep);
           } else {
-            tma_load_2d_pair(sb, mb, bar, ks * 64, nb, pol_keep);
+            tma_load_2d_pair(sb, mb, bar, t.r0 + ks * 64, nb, pol_keep);
           }
           if (++stage == STAGES) {
             stage = 0;
@@ -497,6 +544,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
         // one number is taken for every unit; whoever takes the last leaves the counter as it was
         uint32_t taken = 0;
         if (u.g >= 0) taken = atomicAdd(a.counter, 1u);
+        if (u.red < 0) {   // a part that this unit does not have
+          if (taken + 1 == static_cast<uint32_t>(tab.n_units)) *a.counter = 0;
+          at = static_cast<int>(pairs + taken);
+          continue;
+        }
         if (!mbar_wait_cluster(&rempty[slot], phase ^ 1u, abort_flag, a.status)) break;
         const int4* v = reinterpret_cast<const int4*>(&u);
         for (uint32_t cta = 0; cta < 2; ++cta) {
@@ -582,6 +634,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
           if (lane == 0) mbar_arrive_cluster_relaxed(cluster_addr(&tempty[b], 0));
           ++it;
         }
+        if (t.split) {
+          const int uid = t.split & 255, part_k = (t.split >> 8) & 255, have = t.split >> 16;
+          const size_t hop = (size_t)TN * 256;   // floats of one part's sums
+          float* sums = a.parts + (size_t)uid * a.splits * hop + (size_t)(part * kCols) * 256 +
+                        rank * 128 + quarter * 32 + lane;
+#pragma unroll
+          for (int j = 0; j < kCols; ++j) __stcg(sums + part_k * hop + j * 256, acc[j]);
+          if (!last_part(a, t.split, rank * 16 + warp - 3, lane)) continue;
+#pragma unroll
+          for (int j = 0; j < kCols; ++j) acc[j] = 0.0f;
+          for (int s = 0; s < have; ++s)
+#pragma unroll
+            for (int j = 0; j < kCols; ++j) acc[j] += __ldcg(sums + s * hop + j * 256);
+        }
         if (fw + lane >= a.cols) continue;
         const int first = t.n0 + part * kCols;   // this warp's first row of dW_g
         float* o = static_cast<float*>(a.out) + ((size_t)t.g * a.n + first) * a.cols + fw + lane;
@@ -629,6 +695,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
         const int fl = fw - (quarter & 1) * 32 + (lane & 7) * 8;   // and their columns
         const bool in = fl < a.cols;                               // (cols is a multiple of 8)
         const uint32_t tb = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + b * TN;
+        if (t.split) {   // (few units: this warp's columns alone, 64 bytes a row)
+          const int uid = t.split & 255, part_k = (t.split >> 8) & 255, have = t.split >> 16;
+          const size_t hop = (size_t)TN * 256;   // floats of one part's sums
+          float* sums = a.parts + (size_t)uid * a.splits * hop + rank * 128 + quarter * 32 + lane;
+          for (int c = part * 16; c < t.nlen; c += kEpiWarps * 4) {
+            uint32_t x[16];
+            tmem_ld16(tb + c, x);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              __stcg(sums + part_k * hop + (c + j) * 256, __uint_as_float(x[j]));
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster_relaxed(cluster_addr(&tempty[b], 0));
+          ++it;
+          if (!last_part(a, t.split, rank * 16 + warp - 3, lane) || fw + lane >= a.cols) continue;
+          for (int c = part * 16; c < t.nlen; c += kEpiWarps * 4) {
+            float x[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) x[j] = 0.0f;
+            for (int s = 0; s < have; s += 4) {   // four parts' loads at a time, added in order
+              float v[4][16];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                  v[i][j] = s + i < have ? __ldcg(sums + (s + i) * hop + (c + j) * 256) : 0.0f;
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) x[j] += v[i][j];
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              if (c + j < t.nlen)
+                out[(row0 + c + j) * a.cols + fw + lane] = __float2bfloat16_rn(x[j]);
+          }
+          continue;
+        }
         for (int c = part * 32; c < t.nlen; c += kEpiWarps * 8) {
           uint4 v[4];
           if (steps > 0) {
@@ -690,25 +796,74 @@ cudaError_t run_grouped_kernel(const GroupedArgs& a, const CUtensorMap& mA, cons
   auto kern = grouped_kernel<DIR, TN, STAGES, F32, ACC>;
   const cudaError_t err = ensure_smem_limit(reinterpret_cast<const void*>(kern), S::SMEM);
   if (err != cudaSuccess) return err;
-  // one pair for every two SMs, or for every unit there can be
+  // one pair for every two SMs, or for every part of a unit there can be
   const long long pairs = sm_count() / 2;
+  units *= a.splits;
   return launch_kernel(kern, dim3(2 * (unsigned)(units < pairs ? units : pairs)), dim3(GroupedThreads<F32>::kAll), S::SMEM, st,
                        maps != nullptr, a, maps, mA, mB);
 }
 
-// N tile of fwd and dx: the smallest that takes a group's mean rows, so that a batch of few rows
-// spends its shared memory on weight stages.
-int row_tile(const moe_group_cfg& c) {
-  const int live = c.E < c.rows ? c.E : c.rows;
-  const long long mean = (c.rows + live - 1) / live;
-  return mean <= 32 ? 32 : mean <= 64 ? 64 : mean <= 128 ? 128 : 256;
+// The launch plan of a shape and direction, from host sizes alone.
+struct GroupedPlan {
+  int tn;            // N tile
+  long long units;   // the most there can be
+  int splits;
+};
+GroupedPlan grouped_plan(const moe_group_cfg& c, GroupedDir dir) {
+  GroupedPlan p{};
+  const long long live = c.E < c.rows ? c.E : c.rows;   // groups that can have rows
+  const long long mt = ((dir == kGroupedFwd ? c.n : c.k) + 255ll) / 256;
+  long long steps;
+  if (dir == kGroupedDw) {
+    p.tn = 256;
+    p.units = c.E * mt * ((c.n + 255ll) / 256);
+    steps = (c.rows + 63ll) / 64;   // of a group that has all the rows
+  } else {
+    // the smallest tile that takes a group's mean rows, so that a batch of few rows spends its
+    // shared memory on weight stages; ceil(c / tn) of each group is at most (c - 1) / tn + 1
+    const long long mean = live ? (c.rows + live - 1) / live : 0;
+    p.tn = mean <= 32 ? 32 : mean <= 64 ? 64 : mean <= 128 ? 128 : 256;
+    auto units = [&](int tn) { return ((c.rows - live) / tn + live) * mt; };
+    // and smaller ones still while they leave half of the pairs idle (a group of 300 rows, 512 x
+    // 4096: 19 us with tiles of 256)
+    while (p.tn > 32 && units(p.tn) < kPairs / 2) p.tn /= 2;
+    p.units = units(p.tn);
+    steps = ((dir == kGroupedFwd ? c.k : c.n) + 63ll) / 64;
+  }
+  long long splits = p.units ? kPairs / p.units : 1;
+  if (splits > steps / kMinSteps) splits = steps / kMinSteps;
+  // the time of a part falls with their number and that of the joining grows with it: the join of
+  // one part's sums of a 256-row tile costs about as much as four k-steps, in proportion to tn
+  while (splits > 1 && splits * splits * p.tn > steps * 64) --splits;
+  p.splits = splits > 1 ? static_cast<int>(splits) : 1;
+  return p;
+}
+
+// Workspace: status word; at byte 128 the unit counter; from the next 128-byte boundary after 256
+// bytes on dw's tensor maps; then the split reductions' counters and sums.
+struct GroupedWs {
+  size_t maps, arrived, parts, total;
+};
+GroupedWs grouped_ws(const moe_group_cfg& c) {
+  GroupedWs w{};
+  w.maps = 256;
+  w.arrived = w.maps + 2 * sizeof(CUtensorMap) * (size_t)c.E;
+  w.parts = w.arrived + sizeof(uint32_t) * kPairs * kSplitSlots;
+  size_t floats = 0;
+  for (int d = 0; d < 3; ++d) {
+    const GroupedPlan p = grouped_plan(c, static_cast<GroupedDir>(d));
+    const size_t f = p.splits > 1 ? (size_t)p.units * p.splits * p.tn * 256 : 0;
+    if (f > floats) floats = f;
+  }
+  w.total = w.parts + sizeof(float) * floats + 128;   // (128: ws is 16-byte aligned only)
+  return w;
 }
 
 template <int DIR>
-cudaError_t run_rows(int tn, const GroupedArgs& a, const CUtensorMap& mA, const CUtensorMap& mB,
-                     cudaStream_t st) {
-  const long long units = ((long long)a.rows / tn + (a.E < a.rows ? a.E : a.rows)) * a.mt;
-  switch (tn) {
+cudaError_t run_rows(const GroupedPlan& p, const GroupedArgs& a, const CUtensorMap& mA,
+                     const CUtensorMap& mB, cudaStream_t st) {
+  const long long units = p.units;
+  switch (p.tn) {
     case 32: return run_grouped_kernel<DIR, 32, 10>(a, mA, mB, units, st);
     case 64: return run_grouped_kernel<DIR, 64, 9>(a, mA, mB, units, st);
     case 128: return run_grouped_kernel<DIR, 128, 8>(a, mA, mB, units, st);
@@ -718,11 +873,7 @@ cudaError_t run_rows(int tn, const GroupedArgs& a, const CUtensorMap& mA, const 
 
 }  // namespace
 
-// status word; at byte 128 the unit counter; from the next 128-byte boundary after 256 bytes on,
-// dw's tensor maps
-size_t grouped_ws_bytes(const moe_group_cfg& c) {
-  return 256 + 128 + 2 * sizeof(CUtensorMap) * (size_t)c.E;
-}
+size_t grouped_ws_bytes(const moe_group_cfg& c) { return grouped_ws(c).total; }
 
 cudaError_t launch_grouped(const moe_group_cfg& c, GroupedDir dir, const void* in0, const void* in1,
                            const int32_t* counts, void* out, bool out_f32, bool accumulate,
@@ -736,6 +887,13 @@ cudaError_t launch_grouped(const moe_group_cfg& c, GroupedDir dir, const void* i
   a.out = out;
   a.status = static_cast<uint32_t*>(ws);
   a.counter = static_cast<uint32_t*>(ws) + 32;
+  const GroupedPlan plan = grouped_plan(c, dir);
+  const GroupedWs L = grouped_ws(c);
+  char* base = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(ws) + 127) &
+                                       ~static_cast<uintptr_t>(127));
+  a.splits = plan.splits;
+  a.arrived = reinterpret_cast<uint32_t*>(base + L.arrived);
+  a.parts = reinterpret_cast<float*>(base + L.parts);
   a.rows = c.rows;
   a.E = c.E;
   a.n = c.n;
@@ -745,27 +903,25 @@ cudaError_t launch_grouped(const moe_group_cfg& c, GroupedDir dir, const void* i
   a.mt = (a.cols + 255) / 256;
   CUtensorMap mA, mB;
   bool ok;
-  const int tn = dir == kGroupedDw ? 256 : row_tile(c);
   if (dir == kGroupedDw) {
     ok = make_tensor_map_2d(&mA, in1, 2, c.k, c.rows, 64) &&
          make_tensor_map_2d(&mB, in0, 2, c.n, c.rows, 64);
   } else {
     ok = make_tensor_map_3d_bf16(&mA, in1, c.k, c.n, c.E, dir == kGroupedFwd ? 128 : 64) &&
-         make_tensor_map_2d(&mB, in0, 2, a.red, c.rows, tn / 2);
+         make_tensor_map_2d(&mB, in0, 2, a.red, c.rows, plan.tn / 2);
   }
   if (!ok) return cudaErrorInvalidValue;
   switch (dir) {
-    case kGroupedFwd: return run_rows<kGroupedFwd>(tn, a, mA, mB, st);
-    case kGroupedDx: return run_rows<kGroupedDx>(tn, a, mA, mB, st);
+    case kGroupedFwd: return run_rows<kGroupedFwd>(plan, a, mA, mB, st);
+    case kGroupedDx: return run_rows<kGroupedDx>(plan, a, mA, mB, st);
     default: break;
   }
-  auto* maps = reinterpret_cast<CUtensorMap*>(
-      (reinterpret_cast<uintptr_t>(ws) + 256 + 127) & ~static_cast<uintptr_t>(127));
+  auto* maps = reinterpret_cast<CUtensorMap*>(base + L.maps);
   const cudaError_t err = launch_kernel(
       group_maps_kernel, dim3((c.E + kMapWarps - 1) / kMapWarps), dim3(kMapWarps * 32), 0, st,
       false, counts, maps, c.rows, c.E, static_cast<uint32_t*>(ws), mA, mB);
   if (err != cudaSuccess) return err;
-  const long long units = (long long)c.E * a.mt * ((c.n + 255) / 256);
+  const long long units = plan.units;
   if (!out_f32) return run_grouped_kernel<kGroupedDw, 256, 6>(a, mA, mB, units, st, maps);
   return accumulate
              ? run_grouped_kernel<kGroupedDw, 256, 6, true, true>(a, mA, mB, units, st, maps)

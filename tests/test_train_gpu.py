@@ -89,6 +89,9 @@ SHAPES = [
     (300, 5, 520, 328, "gaps"), (257, 1, 1032, 136, "one"), (513, 2, 264, 1000, "random"),
     (2000, 7, 384, 256, "random"), (96, 1024, 64, 64, "random"), (8, 256, 512, 1024, "random"),
     (700, 1, 8, 2048, "one"), (777, 2, 2048, 16, "even"), (4100, 3, 256, 192, "gaps"),
+    # few units and long reductions: split, with parts of unequal length and groups without any
+    (64, 1, 512, 4096, "one"), (2, 2, 1096, 3272, "even"), (40, 5, 264, 2056, "gaps"),
+    (9000, 1, 256, 264, "one"), (3001, 4, 128, 512, "random"),
 ]
 
 
