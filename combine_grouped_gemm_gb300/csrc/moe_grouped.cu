@@ -27,10 +27,10 @@
 // with uneven groups). Which pair computes a unit does not change its result. The tables are
 // built by every CTA from the counts itself, without a schedule kernel.
 //
-// Where there are fewer units than pairs, the reduction of each is split: every part leaves its
-// fp32 sums in the workspace, and for each warp's piece of the tile whichever part comes last adds
-// them up in the order of the parts and stores the result (one group of 64 rows, 4096 x 7168: 27.5
-// us unsplit; weight gradient of 30000 rows, 512 x 512: 133 us).
+// Where there are far fewer units than pairs, the reduction of each is split: every part leaves its
+// fp32 sums in the workspace, and a second kernel over the whole GPU adds them up in the order of
+// the parts and stores the results. (Joining in whichever part came last instead, by a counter,
+// took 29 us for ten parts of a 256 x 256 tile: one pair cannot keep enough loads in flight.)
 //
 // Roles in a CTA (one CTA per SM): warp 0 TMA producer, warp 1 MMA issuer (leader CTA), warp 2
 // scheduler (leader CTA: hands decoded units to the roles of both CTAs through a small ring), the
@@ -103,9 +103,8 @@ constexpr int kTurnPitch = 144, kTurnBytes = 32 * kTurnPitch;
 // one slot ahead of the producer, which is itself a unit or two ahead of the epilogue.
 constexpr int kRing = 3;
 
-// Split reductions: at most kPairs parts in all, of at least kMinSteps k-steps each; a counter of
-// arrivals per unit and epilogue warp of the pair.
-constexpr int kPairs = 76, kMinSteps = 4, kSplitSlots = 32;
+// Split reductions: at most kPairs parts in all, of at least kMinSteps k-steps each.
+constexpr int kPairs = 76, kMinSteps = 8;
 
 struct GroupedArgs {
   const int32_t* counts;
@@ -117,8 +116,7 @@ struct GroupedArgs {
   int red;        // fwd, dx: length of the reduction
   int mt;         // ceil(cols / 256)
   int splits;     // parts of a unit's reduction, at most
-  uint32_t* arrived;   // [units][kSplitSlots], 0 before and after a launch
-  float* parts;        // [units][splits][TN][256]
+  float* parts;   // [units][splits][TN][256]: their sums
 };
 
 template <int TN, int STAGES, bool F32>
@@ -152,6 +150,41 @@ struct alignas(16) GroupedUnit {
   int nt;     // N tiles that read this unit's weight tile
   int split;  // unit | part << 8 | parts << 16 where the reduction is split, else 0
 };
+
+// The rest of the tables, after group_offsets; the caller puts a block barrier behind it.
+template <int DIR, int TN>
+__device__ __forceinline__ void list_units(const GroupedArgs& a, GroupedTables& tab) {
+  const int lane = threadIdx.x & 31;
+  if (DIR == kGroupedDw) {
+    if (threadIdx.x == 0) tab.n_units = a.E * a.mt * ((a.n + TN - 1) / TN) * a.splits;
+  } else if (threadIdx.x < 32) {
+    int at = 0, tiles = 0;
+    for (int e0 = 0; e0 < a.E; e0 += 32) {
+      const int e = e0 + lane;
+      const int c = e < a.E ? tab.off[e + 1] - tab.off[e] : 0;
+      const bool has = c > 0;
+      const int nt = (c + TN - 1) / TN;
+      int incl = nt;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      const uint32_t m = __ballot_sync(0xffffffffu, has);
+      if (has) {
+        const int i = at + __popc(m & ((1u << lane) - 1u));
+        tab.live[i] = e;
+        tab.first[i] = tiles + incl - nt;
+      }
+      at += __popc(m);
+      tiles += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) {
+      tab.n_live = at;
+      tab.n_units = tiles * a.mt * a.splits;
+    }
+  }
+}
 
 // Unit number u. fwd, dx: weight-tile-major (unit m * nt + j of a group: N tile j of its 256
 // columns number m), so that pairs at work on neighbouring units share a weight tile through L2.
@@ -219,6 +252,12 @@ __device__ __forceinline__ GroupedUnit grouped_unit(const GroupedArgs& a, const 
   return r;
 }
 
+// Where a part of a split unit leaves its sums.
+template <int TN>
+__device__ __forceinline__ float* part_sums(const GroupedArgs& a, const GroupedUnit& t) {
+  return a.parts + ((size_t)(t.split & 255) * a.splits + ((t.split >> 8) & 255)) * (TN * 256);
+}
+
 // Barrier of the 64 threads of two warps, and whether both said yes.
 __device__ __forceinline__ void pair_sync(int id) {
   asm volatile("barrier.cta.sync %0, 64;" ::"r"(id) : "memory");
@@ -234,22 +273,6 @@ __device__ __forceinline__ bool pair_agree(int id, bool yes) {
       : "r"(id), "r"(static_cast<uint32_t>(yes))
       : "memory");
   return all != 0;
-}
-
-// One epilogue warp's arrival for its piece of a split unit, after its sums are in the workspace:
-// true for the part that comes last, which then sees all the others' sums.
-__device__ __forceinline__ bool last_part(const GroupedArgs& a, int split, int slot, int lane) {
-  __threadfence();
-  __syncwarp();
-  uint32_t before = 0;
-  if (lane == 0) {
-    uint32_t* n = a.arrived + (split & 255) * kSplitSlots + slot;
-    before = atomicAdd(n, 1u);
-    if (before + 1 == static_cast<uint32_t>(split >> 16)) *n = 0;   // ready for the next launch
-  }
-  before = __shfl_sync(0xffffffffu, before, 0);
-  __threadfence();
-  return before + 1 == static_cast<uint32_t>(split >> 16);
 }
 
 // A role's end of the ring. next(): waits for the next unit and frees its slot; false at the end
@@ -364,41 +387,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
     }
   }
   group_offsets(a.counts, a.E, a.rows, tab.off, a.status);
-  if (!kDw && warp == 0) {
-    int at = 0, tiles = 0;
-    for (int e0 = 0; e0 < a.E; e0 += 32) {
-      const int e = e0 + lane;
-      const int c = e < a.E ? tab.off[e + 1] - tab.off[e] : 0;
-      const bool has = c > 0;
-      const int nt = (c + TN - 1) / TN;
-      int incl = nt;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-      }
-      const uint32_t m = __ballot_sync(0xffffffffu, has);
-      if (has) {
-        const int i = at + __popc(m & ((1u << lane) - 1u));
-        tab.live[i] = e;
-        tab.first[i] = tiles + incl - nt;
-      }
-      at += __popc(m);
-      tiles += __shfl_sync(0xffffffffu, incl, 31);
-    }
-    if (lane == 0) {
-      tab.n_live = at;
-      tab.n_units = tiles * a.mt * a.splits;
-    }
-  } else if (kDw && threadIdx.x == 0) {
-    tab.n_units = a.E * a.mt * ((a.n + TN - 1) / TN) * a.splits;
-  }
+  list_units<DIR, TN>(a, tab);
   if (warp == 1) tmem_alloc_pair(tmem_slot, S::TMEM_COLS);
   tc_fence_before();
   __syncthreads();
   cluster_sync();   // the peer's barriers and tensor memory are ready
   tc_fence_after();
   if (kDw) pdl_wait();   // the groups' tensor maps are written
+  if (a.splits > 1) pdl_trigger();   // the joining kernel may come up and wait
   const uint32_t tmem = *tmem_slot;
 
   constexpr int kNever = 1 << 30;
@@ -635,18 +631,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
           ++it;
         }
         if (t.split) {
-          const int uid = t.split & 255, part_k = (t.split >> 8) & 255, have = t.split >> 16;
-          const size_t hop = (size_t)TN * 256;   // floats of one part's sums
-          float* sums = a.parts + (size_t)uid * a.splits * hop + (size_t)(part * kCols) * 256 +
-                        rank * 128 + quarter * 32 + lane;
+          float* sums = part_sums<TN>(a, t) + part * kCols * 256 + rank * 128 + quarter * 32 + lane;
 #pragma unroll
-          for (int j = 0; j < kCols; ++j) __stcg(sums + part_k * hop + j * 256, acc[j]);
-          if (!last_part(a, t.split, rank * 16 + warp - 3, lane)) continue;
-#pragma unroll
-          for (int j = 0; j < kCols; ++j) acc[j] = 0.0f;
-          for (int s = 0; s < have; ++s)
-#pragma unroll
-            for (int j = 0; j < kCols; ++j) acc[j] += __ldcg(sums + s * hop + j * 256);
+          for (int j = 0; j < kCols; ++j) sums[j * 256] = acc[j];
+          continue;
         }
         if (fw + lane >= a.cols) continue;
         const int first = t.n0 + part * kCols;   // this warp's first row of dW_g
@@ -695,44 +683,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
         const int fl = fw - (quarter & 1) * 32 + (lane & 7) * 8;   // and their columns
         const bool in = fl < a.cols;                               // (cols is a multiple of 8)
         const uint32_t tb = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + b * TN;
-        if (t.split) {   // (few units: this warp's columns alone, 64 bytes a row)
-          const int uid = t.split & 255, part_k = (t.split >> 8) & 255, have = t.split >> 16;
-          const size_t hop = (size_t)TN * 256;   // floats of one part's sums
-          float* sums = a.parts + (size_t)uid * a.splits * hop + rank * 128 + quarter * 32 + lane;
+        if (t.split) {
+          float* sums = part_sums<TN>(a, t) + rank * 128 + quarter * 32 + lane;
           for (int c = part * 16; c < t.nlen; c += kEpiWarps * 4) {
             uint32_t x[16];
             tmem_ld16(tb + c, x);
             tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              __stcg(sums + part_k * hop + (c + j) * 256, __uint_as_float(x[j]));
+            for (int j = 0; j < 16; ++j) sums[(c + j) * 256] = __uint_as_float(x[j]);
           }
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster_relaxed(cluster_addr(&tempty[b], 0));
           ++it;
-          if (!last_part(a, t.split, rank * 16 + warp - 3, lane) || fw + lane >= a.cols) continue;
-          for (int c = part * 16; c < t.nlen; c += kEpiWarps * 4) {
-            float x[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) x[j] = 0.0f;
-            for (int s = 0; s < have; s += 4) {   // four parts' loads at a time, added in order
-              float v[4][16];
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                  v[i][j] = s + i < have ? __ldcg(sums + (s + i) * hop + (c + j) * 256) : 0.0f;
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 16; ++j) x[j] += v[i][j];
-            }
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              if (c + j < t.nlen)
-                out[(row0 + c + j) * a.cols + fw + lane] = __float2bfloat16_rn(x[j]);
-          }
           continue;
         }
         for (int c = part * 32; c < t.nlen; c += kEpiWarps * 8) {
@@ -788,19 +751,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
   }
 }
 
+// Adds the parts of split units. CTA: kJoinRows rows of one unit's tile, a thread a column.
+constexpr int kJoinRows = 8;
+template <int DIR, int TN>
+__global__ void __launch_bounds__(256) join_kernel(const GroupedArgs a, int out_f32, int accumulate) {
+  __shared__ GroupedTables tab;
+  // counts and offsets are those that the products read: nothing before this has changed them
+  group_offsets(a.counts, a.E, a.rows, tab.off, nullptr);
+  list_units<DIR, TN>(a, tab);
+  __syncthreads();
+  constexpr int kSets = TN / kJoinRows;
+  const int unit = blockIdx.x / kSets, j0 = (blockIdx.x - unit * kSets) * kJoinRows;
+  const GroupedUnit t = grouped_unit<DIR, TN>(a, tab, unit * a.splits);   // its first part
+  pdl_wait();
+  const int f = t.f0 + threadIdx.x;
+  if (t.g < 0 || !t.split || j0 >= t.nlen || f >= a.cols) return;
+  const int have = t.split >> 16;
+  const float* sums = part_sums<TN>(a, t) + j0 * 256 + threadIdx.x;
+  float x[kJoinRows] = {};
+#pragma unroll 4
+  for (int s = 0; s < have; ++s)
+#pragma unroll
+    for (int j = 0; j < kJoinRows; ++j) x[j] += sums[((size_t)s * TN + j) * 256];
+  const size_t row0 = (DIR == kGroupedDw ? (size_t)t.g * a.n : 0) + t.n0 + j0;
+#pragma unroll
+  for (int j = 0; j < kJoinRows; ++j) {
+    if (j0 + j >= t.nlen) break;
+    const size_t o = (row0 + j) * a.cols + f;
+    if (out_f32) {
+      float* out = static_cast<float*>(a.out) + o;
+      *out = accumulate ? *out + x[j] : x[j];
+    } else {
+      static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(x[j]);
+    }
+  }
+}
+
 template <int DIR, int TN, int STAGES, bool F32 = false, bool ACC = false>
 cudaError_t run_grouped_kernel(const GroupedArgs& a, const CUtensorMap& mA, const CUtensorMap& mB,
                                long long units, cudaStream_t st,
                                const CUtensorMap* maps = nullptr) {
   using S = GroupedShape<TN, STAGES, F32>;
   auto kern = grouped_kernel<DIR, TN, STAGES, F32, ACC>;
-  const cudaError_t err = ensure_smem_limit(reinterpret_cast<const void*>(kern), S::SMEM);
+  cudaError_t err = ensure_smem_limit(reinterpret_cast<const void*>(kern), S::SMEM);
   if (err != cudaSuccess) return err;
   // one pair for every two SMs, or for every part of a unit there can be
-  const long long pairs = sm_count() / 2;
-  units *= a.splits;
-  return launch_kernel(kern, dim3(2 * (unsigned)(units < pairs ? units : pairs)), dim3(GroupedThreads<F32>::kAll), S::SMEM, st,
-                       maps != nullptr, a, maps, mA, mB);
+  const long long pairs = sm_count() / 2, parts = units * a.splits;
+  err = launch_kernel(kern, dim3(2 * (unsigned)(parts < pairs ? parts : pairs)),
+                      dim3(GroupedThreads<F32>::kAll), S::SMEM, st, maps != nullptr, a, maps, mA,
+                      mB);
+  if (err != cudaSuccess || a.splits == 1) return err;
+  return launch_kernel(join_kernel<DIR, TN>, dim3((unsigned)(units * (TN / kJoinRows))), dim3(256),
+                       0, st, true, a, F32 ? 1 : 0, ACC ? 1 : 0);
 }
 
 // The launch plan of a shape and direction, from host sizes alone.
@@ -819,36 +821,38 @@ GroupedPlan grouped_plan(const moe_group_cfg& c, GroupedDir dir) {
     p.units = c.E * mt * ((c.n + 255ll) / 256);
     steps = (c.rows + 63ll) / 64;   // of a group that has all the rows
   } else {
-    // the smallest tile that takes a group's mean rows, so that a batch of few rows spends its
-    // shared memory on weight stages; ceil(c / tn) of each group is at most (c - 1) / tn + 1
-    const long long mean = live ? (c.rows + live - 1) / live : 0;
-    p.tn = mean <= 32 ? 32 : mean <= 64 ? 64 : mean <= 128 ? 128 : 256;
+    // ceil(c / tn) tiles of a group of c rows are at most (c - 1) / tn + 1
     auto units = [&](int tn) { return ((c.rows - live) / tn + live) * mt; };
-    // and smaller ones still while they leave half of the pairs idle (a group of 300 rows, 512 x
-    // 4096: 19 us with tiles of 256)
-    while (p.tn > 32 && units(p.tn) < kPairs / 2) p.tn /= 2;
+    // Tiles of 128 rows up to that mean (64 groups, 2048 x 2048: of 100 rows 91 us, with tiles of
+    // 256 95 us; of 200 rows 117 and 108 us); of 64 for a few rows, whose smaller stages leave room
+    // for more weights in flight (4096 x 7168: 8 groups of a row 76 us, with 128 85 us; 32 uneven
+    // groups of 25 rows on average 288 and 280 us), and while they leave half of the pairs idle
+    // (one group of 512 rows, 4096 x 7168: 31 us, with 256 34 us).
+    const long long mean = live ? (c.rows + live - 1) / live : 0;
+    p.tn = mean <= 16 ? 64 : mean <= 128 ? 128 : 256;
+    while (p.tn > 64 && units(p.tn) < kPairs / 2) p.tn /= 2;
     p.units = units(p.tn);
     steps = ((dir == kGroupedFwd ? c.k : c.n) + 63ll) / 64;
   }
   long long splits = p.units ? kPairs / p.units : 1;
   if (splits > steps / kMinSteps) splits = steps / kMinSteps;
-  // the time of a part falls with their number and that of the joining grows with it: the join of
-  // one part's sums of a 256-row tile costs about as much as four k-steps, in proportion to tn
-  while (splits > 1 && splits * splits * p.tn > steps * 64) --splits;
+  // A part saves the k-steps of the others, about a quarter of a microsecond each, and the second
+  // kernel takes about four: split from 24 saved steps on. Weight gradient, 512 x 512: 30000 rows
+  // 134 us unsplit and 37 split, 2000 rows 20 and 17; forward of 64 rows, 4096 x 7168: 29 and 19.
+  if (splits > 1 && steps - steps / splits < 24) splits = 1;
   p.splits = splits > 1 ? static_cast<int>(splits) : 1;
   return p;
 }
 
 // Workspace: status word; at byte 128 the unit counter; from the next 128-byte boundary after 256
-// bytes on dw's tensor maps; then the split reductions' counters and sums.
+// bytes on dw's tensor maps; then the split reductions' sums.
 struct GroupedWs {
-  size_t maps, arrived, parts, total;
+  size_t maps, parts, total;
 };
 GroupedWs grouped_ws(const moe_group_cfg& c) {
   GroupedWs w{};
   w.maps = 256;
-  w.arrived = w.maps + 2 * sizeof(CUtensorMap) * (size_t)c.E;
-  w.parts = w.arrived + sizeof(uint32_t) * kPairs * kSplitSlots;
+  w.parts = w.maps + 2 * sizeof(CUtensorMap) * (size_t)c.E;
   size_t floats = 0;
   for (int d = 0; d < 3; ++d) {
     const GroupedPlan p = grouped_plan(c, static_cast<GroupedDir>(d));
@@ -864,7 +868,6 @@ cudaError_t run_rows(const GroupedPlan& p, const GroupedArgs& a, const CUtensorM
                      const CUtensorMap& mB, cudaStream_t st) {
   const long long units = p.units;
   switch (p.tn) {
-    case 32: return run_grouped_kernel<DIR, 32, 10>(a, mA, mB, units, st);
     case 64: return run_grouped_kernel<DIR, 64, 9>(a, mA, mB, units, st);
     case 128: return run_grouped_kernel<DIR, 128, 8>(a, mA, mB, units, st);
     default: return run_grouped_kernel<DIR, 256, 6>(a, mA, mB, units, st);
@@ -892,7 +895,6 @@ cudaError_t launch_grouped(const moe_group_cfg& c, GroupedDir dir, const void* i
   char* base = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(ws) + 127) &
                                        ~static_cast<uintptr_t>(127));
   a.splits = plan.splits;
-  a.arrived = reinterpret_cast<uint32_t*>(base + L.arrived);
   a.parts = reinterpret_cast<float*>(base + L.parts);
   a.rows = c.rows;
   a.E = c.E;
