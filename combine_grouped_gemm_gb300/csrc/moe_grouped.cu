@@ -19,13 +19,13 @@
 // first small kernel writes for every group the two tensor maps whose extent ends at its last
 // row, and the loads fill the rest of the last k-step with zeros. (Zeroing the stage in shared
 // memory after the load cost a round trip between the two CTAs in every unit: 32 groups of 520
-// rows, 7168 x 2048, 456 us that way.)
+// rows, 7168 x 2048, 456 us that way, 322 us so.)
 //
 // The units (group, 256 output columns, N tile) are numbered group after group; a pair starts with
 // its own number and takes further ones from a counter in the workspace as it gets free, since
-// the groups' units differ in size (fixed shares left 6 to 11 % of the time to the slowest pair
-// with uneven groups). Which pair computes a unit does not change its result. The tables are
-// built by every CTA from the counts itself, without a schedule kernel.
+// the groups' units differ in size (16384 rows dealt over 32 groups, forward 4096 x 7168: 620 us
+// with fixed shares, 588 us so). Which pair computes a unit does not change its result. The tables
+// are built by every CTA from the counts itself, without a schedule kernel.
 //
 // Where there are far fewer units than pairs, the reduction of each is split: every part leaves its
 // fp32 sums in the workspace, and a second kernel over the whole GPU adds them up in the order of
@@ -34,9 +34,16 @@
 //
 // Roles in a CTA (one CTA per SM): warp 0 TMA producer, warp 1 MMA issuer (leader CTA), warp 2
 // scheduler (leader CTA: hands decoded units to the roles of both CTAs through a small ring), the
-// others the epilogue. Loads of both CTAs count on
-// the leader's full barriers, its commits free the stages of both. Accumulators are double
-// buffered. Every wait is bounded.
+// others the epilogue. Loads of both CTAs count on the leader's full barriers, its commits free the
+// stages of both. Accumulators are double buffered. Every wait is bounded.
+//
+// What bounds it. Full tiles keep the tensor pipe busy for 512 of 523 cycles a k-step (clock
+// counters in the MMA thread): 8 groups of 2048 rows, 4096 x 7168, 488 us forward (1.97 PFLOP/s),
+// and in long runs the power cap sets the clock. A k-step brings 32 KB into each SM, 64 bytes a
+// cycle, which is why narrower tiles (a group's rows spread over its tiles, 160 to 256 each) fall
+// below that rate: 32 groups of about 512 rows 588 us, unevenly loaded ones 317 us (7168 x 2048).
+// Few rows a group: HBM, 64 tokens through 256 experts 1.83 ms (7.2 TB/s of weights). Weight
+// gradients of few rows a group: the stores, fp32 of 4096 rows 578 us (6.7 TB/s).
 #include "moe_device.cuh"
 
 namespace moe {
@@ -80,9 +87,9 @@ __device__ __forceinline__ void group_offsets(const int32_t* counts, int E, int 
   __syncthreads();
 }
 
-// Warps 0, 1 and 2 load, issue the MMAs and schedule; the others are the epilogue: two warps per tensor-memory
-// quarter, or four where the sums of a tile are held in registers (fp32 weight gradients: 64
-// columns a thread).
+// Warps 0, 1 and 2 load, issue the MMAs and schedule; the others are the epilogue: two warps per
+// tensor-memory quarter, or four where the sums of a tile are held in registers (fp32 weight
+// gradients: 64 columns a thread).
 template <bool F32>
 struct GroupedThreads {
   static constexpr int kEpi = F32 ? 16 : 8;
