@@ -628,7 +628,7 @@ bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) !
 
 int check_rows(int32_t rows, int32_t cols) {
   if (rows < 0 || cols < 1) return MOE_ERR_INVALID_ARG;
-  return cols % 128 || (long long)rows * cols >= 1ll << 38 ? MOE_ERR_UNSUPPORTED : MOE_OK;
+  return cols % 128 || (long long)rows * cols >= 1ll << 37 ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 }  // namespace
 

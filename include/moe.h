@@ -399,7 +399,7 @@ int moe_grouped_mm_dw(const moe_group_cfg* cfg, const void* dy, const void* x,
  * = e4m3(x/scale), nearest even, saturating; the amax is over the block's numbers). Scales are
  * block-major: the scale of block b of row r at scales[b * rows + r]. A NaN stays a NaN; an
  * infinity makes its block read back as NaN. Here and in the two calls below, rows times columns
- * (d or f) at or past 2^38 is MOE_ERR_UNSUPPORTED.
+ * (d or f) at or past 2^37 is MOE_ERR_UNSUPPORTED.
  * moe_act_save: x bf16 [rows][d] -> q [rows][d] bytes, scales [d/128][rows]. d % 128 == 0.
  * moe_act_load: out[i] = bf16(code * scale) of saved row index[i] (index int32 [rows], NULL: row
  *   i), out bf16 [rows][d]; src_rows: the saved rows. An index of -1 gives a row of zeros; any

@@ -261,6 +261,52 @@ def test_no_rows_zero_the_weight_gradient(moe):
     assert float(b.float().abs().sum()) == 0.0
 
 
+def test_groups_without_any_row(moe):
+    """Rows that no group owns at all: nothing is written, and the weight gradient is zero."""
+    g = moe.GroupCfg(rows=50, E=5, n=264, k=136)
+    c = torch.zeros(5, dtype=torch.int32, device="cuda")
+    ws = workspace(moe, g)
+    x = torch.full((50, 136), float("nan"), dtype=BF, device="cuda")
+    dy = torch.full((50, 264), float("nan"), dtype=BF, device="cuda")
+    w = normal(1, 5, 264, 136)
+    y = torch.full((50, 264), 3.0, dtype=BF, device="cuda")
+    dx = torch.full((50, 136), 3.0, dtype=BF, device="cuda")
+    moe.grouped_mm(g, x, c, w, y, ws)
+    moe.grouped_mm_dx(g, dy, c, w, dx, ws)
+    assert bool((y == 3.0).all()) and bool((dx == 3.0).all())
+    for dtype in (torch.float32, BF):
+        dw = torch.full((5, 264, 136), float("nan"), dtype=dtype, device="cuda")
+        moe.grouped_mm_dw(g, dy, x, c, dw, ws)
+        assert float(dw.float().abs().sum()) == 0.0
+    dw = torch.full((5, 264, 136), 3.0, device="cuda")
+    moe.grouped_mm_dw(g, dy, x, c, dw, ws, accumulate=True)
+    assert bool((dw == 3.0).all())
+    assert moe.read_status(ws) == 0
+
+
+def test_one_workspace_for_many_shapes(moe):
+    """Calls of several shapes and directions one after the other in the largest one's workspace:
+    each leaves it as the next needs it."""
+    shapes = [(300, 3, 264, 520), (64, 1, 512, 4096), (9000, 1, 256, 264), (5, 40, 64, 64)]
+    cfgs = [moe.GroupCfg(rows=r, E=E, n=n, k=k) for r, E, n, k in shapes]
+    ws = torch.zeros(max(moe.grouped_ws_bytes(g) for g in cfgs), dtype=torch.uint8, device="cuda")
+    for turn in range(2):
+        for g in cfgs:
+            counts = spread(g.rows, g.E, "random", turn)
+            c = torch.tensor(counts, dtype=torch.int32, device="cuda")
+            x, w, dy = normal(turn, g.rows, g.k), normal(2, g.E, g.n, g.k), normal(3, g.rows, g.n)
+            y, dx = torch.empty_like(dy), torch.empty_like(x)
+            dw = torch.empty((g.E, g.n, g.k), device="cuda")
+            moe.grouped_mm(g, x, c, w, y, ws)
+            moe.grouped_mm_dw(g, dy, x, c, dw, ws)
+            moe.grouped_mm_dx(g, dy, c, w, dx, ws)
+            for out, kind, a, b, m, t in ((y, "mm", x, w, g.k, "bf16"), (dx, "dx", dy, w, g.n, "bf16"),
+                                          (dw, "dw", dy, x, max(counts), "fp32")):
+                ref, mag = grouped_reference(kind, a, b, counts)
+                check(out, ref, m * 2.0 ** -23 * mag, t)
+    assert moe.read_status(ws) == 0
+
+
 def test_offsets_past_32_bits(moe):
     """The last group's weights and gradient start past 2^31 elements."""
     g = moe.GroupCfg(rows=40, E=75, n=4096, k=7168)
@@ -373,6 +419,22 @@ def test_act_save_and_load(moe, rows, d):
     assert int(st[0]) == 0
 
 
+@pytest.mark.parametrize("amax", [1.0, 1.9921875, 448.0, 0.0131, 3.3e38, 3.1e-20, 1e-37])
+def test_codes_of_every_bf16_value(moe, amax):
+    """Every finite bf16 value up to the block's largest against the IEEE quotient."""
+    v = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(BF)
+    top = torch.tensor(amax).to(BF)
+    v = v[v.float().isfinite() & (v.float().abs() <= top.float())]
+    pad = -v.numel() % 127
+    v = torch.cat([v, torch.zeros(pad, dtype=BF)]).view(-1, 127)
+    x = torch.cat([v, top.expand(v.shape[0], 1)], 1).contiguous().cuda()
+    q = torch.empty(x.shape, dtype=torch.uint8, device="cuda")
+    s = torch.empty((1, x.shape[0]), device="cuda")
+    moe.act_save(x, q, s)
+    rq, rs = quantise(x)
+    assert torch.equal(q.cpu(), rq) and torch.equal(s.cpu(), rs)
+
+
 def test_act_load_reports_wrong_rows(moe):
     x = normal(1, 4, 128)
     q, s = torch.empty((4, 128), dtype=torch.uint8, device="cuda"), torch.empty((1, 4), device="cuda")
@@ -447,7 +509,7 @@ def test_swiglu_grad(moe, rows, f):
 
 # ------------------------------------- the combine's gradient -------------------------------------
 @pytest.mark.parametrize("T,k,d", [(1, 1, 128), (1, 8, 7168), (3, 32, 256), (37, 5, 640),
-                                   (64, 8, 7168), (500, 2, 1024)])
+                                   (64, 8, 7168), (500, 2, 1024), (5000, 2, 1152)])
 def test_combine_grad(moe, T, k, d):
     rows = T * k + 9                                   # rows that no choice names
     gen = torch.Generator(device="cuda")

@@ -71,7 +71,8 @@ def test_no_rows_is_no_work(moe):
     assert L.moe_combine_grad(0, 2, 128, 0, None, None, None, None, None, None, None, None) == 0
 
 
-@pytest.mark.parametrize("rows,cols,code", [(-1, 128, 1), (4, 0, 1), (4, 64, 2), (4, 200, 2)])
+@pytest.mark.parametrize("rows,cols,code", [(-1, 128, 1), (4, 0, 1), (4, 64, 2), (4, 200, 2),
+                                            (2 ** 30, 128, 2)])
 def test_row_shapes(moe, rows, cols, code):
     L = moe._lib
     assert L.moe_act_save(rows, cols, OK, OK, OK, None) == code
@@ -79,6 +80,7 @@ def test_row_shapes(moe, rows, cols, code):
     assert L.moe_swiglu_save(rows, cols, OK, OK, OK, OK, None) == code
     assert L.moe_swiglu_grad(rows, cols, OK, OK, OK, OK, OK, None) == code
     assert L.moe_combine_grad(rows, 2, cols, 8, OK, OK, OK, OK, OK + 16, OK, None, None) == code
+    assert L.moe_combine_grad(4, 2, 128, -1, OK, OK, OK, OK, OK + 16, OK, None, None) == 1
 
 
 def test_row_pointers(moe):
