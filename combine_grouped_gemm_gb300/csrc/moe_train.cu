@@ -1,6 +1,6 @@
 // The element-wise operators of the expert path's training step: activation checkpoints in 8
 // bits (loading them, the SwiGLU that saves its input and its gradient from the saved codes) and
-// the gradient of the combine. Each reads its inputs once and writes its outputs once.
+// the gradient of the combine. Each reads its inputs from HBM once and writes its outputs once.
 #include "moe_device.cuh"
 
 namespace moe {

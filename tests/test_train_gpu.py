@@ -538,6 +538,32 @@ def test_combine_grad(moe, T, k, d):
     assert torch.equal(dw, dw2)
 
 
+def test_combine_grad_against_differences(moe):
+    """The combine y[t] = sum_i w[t][i] e[row_of[t][i]] is linear in w and in e, so its central
+    difference in 64 bits is the derivative itself; dtopk_w is off by the fp32 sum (d 2^-24 of the
+    products' magnitudes), debuf by its rounding to bf16."""
+    T, k, d, rows = 9, 3, 256, 40
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(5)
+    row_of = torch.randperm(rows, generator=gen, device="cuda")[:T * k].to(torch.int32).view(T, k)
+    w = torch.rand((T, k), generator=gen, device="cuda")
+    ebuf, dy = normal(1, rows, d), normal(2, T, d)
+    de, dw = torch.zeros_like(ebuf), torch.empty((T, k), device="cuda")
+    moe.combine_grad(ebuf, row_of, w, dy, de, dw)
+
+    def loss(ww, ee):
+        return ((ww.unsqueeze(-1) * ee[row_of.long()]).sum(1) * dy.double()).sum()
+    W, E, h = w.double(), ebuf.double(), 1e-3
+    for seed in range(3):
+        v = torch.randn((T, k), generator=gen, device="cuda", dtype=torch.float64)
+        u = torch.randn((rows, d), generator=gen, device="cuda", dtype=torch.float64)
+        diff = float((loss(W + h * v, E) - loss(W - h * v, E)) / (2 * h))
+        mag = (dy.double().unsqueeze(1) * E[row_of.long()]).abs().sum(-1)
+        assert abs(diff - float((dw.double() * v).sum())) <= d * 2.0 ** -24 * float((mag * v.abs()).sum()) + 1e-9
+        diff = float((loss(W, E + h * u) - loss(W, E - h * u)) / (2 * h))
+        assert abs(diff - float((de.double() * u).sum())) <= 2.0 ** -8 * float((de.double() * u).abs().sum())
+
+
 def test_combine_grad_reports_wrong_rows(moe):
     ebuf, dy = normal(1, 6, 256), normal(2, 2, 256)
     row_of = torch.tensor([[0, 6], [-5, 2 ** 31 - 1]], dtype=torch.int32, device="cuda")
