@@ -362,14 +362,11 @@ __device__ __forceinline__ void st_cluster16(uint32_t addr, const int4& v) {
                : "memory");
 }
 
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
-               : "memory");
-}
-
-// The same without ordering earlier memory accesses: for an arrival that hands over tensor memory
-// only (tcgen05.wait::ld and tcgen05.fence::before_thread_sync come before it). The release above
-// waits for the thread's outstanding global stores, about 1600 cycles in an epilogue.
+// Arrival on a barrier of either CTA, by itself not ordered after earlier memory accesses: after
+// fence_release_cluster for what it publishes, or alone where it hands over tensor memory
+// (tcgen05.wait::ld and tcgen05.fence::before_thread_sync come before it) or something the thread
+// has finished reading. A releasing arrival would wait for the thread's outstanding global stores,
+// about 1600 cycles in an epilogue.
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
                : "memory");

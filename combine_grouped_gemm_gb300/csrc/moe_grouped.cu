@@ -300,7 +300,8 @@ struct UnitReader {
     *u = ring[slot];
     if (kWarp) __syncwarp();   // every lane has read it
     if (u->g < 0) return false;
-    if (!kWarp || (threadIdx.x & 31) == 0) mbar_arrive_cluster_relaxed(cluster_addr(&empty[slot], 0));
+    if (!kWarp || (threadIdx.x & 31) == 0)
+      mbar_arrive_cluster_relaxed(cluster_addr(&empty[slot], 0));
     if (++slot == kRing) {
       slot = 0;
       phase ^= 1u;
@@ -311,8 +312,8 @@ struct UnitReader {
 
 // A whole warp's wait: every lane gets the same answer, so the warp leaves its loop together.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                          uint32_t* status, uint64_t limit_ns = kWaitLimitNs) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status, limit_ns));
+                                          uint32_t* status) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status));
 }
 
 // dw: the tensor maps of x and dy for every group, ending at the group's last row; one warp a
@@ -761,7 +762,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
 // Adds the parts of split units. CTA: kJoinRows rows of one unit's tile, a thread a column.
 constexpr int kJoinRows = 8;
 template <int DIR, int TN>
-__global__ void __launch_bounds__(256) join_kernel(const GroupedArgs a, int out_f32, int accumulate) {
+__global__ void __launch_bounds__(256)
+    join_kernel(const GroupedArgs a, int out_f32, int accumulate) {
   __shared__ GroupedTables tab;
   // counts and offsets are those that the products read: nothing before this has changed them
   group_offsets(a.counts, a.E, a.rows, tab.off, nullptr);

@@ -116,9 +116,9 @@ __device__ __forceinline__ uint2 codes_of8(const float (&f)[8], float scale) {
   return make_uint2(w[0], w[1]);
 }
 
-// What these kernels measured (whole calls replayed from a graph, copy rate 6.7 TB/s): swiglu_save of
-// 16384 rows of 2048 45 us (6.0 TB/s, instruction issue 79 % busy), its gradient 50 us (6.7 TB/s),
-// 2048 rows of 7168 saved and loaded 8-fold 46 us (6.4 TB/s); 8 rows about 2 us, a launch.
+// What these kernels measured (whole calls replayed from a graph, copy rate 6.7 TB/s): swiglu_save
+// of 16384 rows of 2048 45 us (6.0 TB/s, instruction issue 79 % busy), its gradient 50 us (6.7
+// TB/s), 2048 rows of 7168 saved and loaded 8-fold 46 us (6.4 TB/s); 8 rows about 2 us, a launch.
 //
 // The kernels that read or write scales take tiles of 16 rows x 128 columns a CTA: a half-warp is
 // one row's block (8 columns a lane), so a CTA's scales are 16 consecutive floats. CTA c: column
@@ -305,7 +305,8 @@ __global__ void __launch_bounds__(kThreads) combine_grad_kernel(
   }
 }
 
-// CTAs of the 16-row tiles. (The callers keep rows * cols below 2^37: grids and row numbers fit 32 bits.)
+// CTAs of the 16-row tiles. (The callers keep rows * cols below 2^37: grids and row numbers fit 32
+// bits.)
 unsigned tiles_of(int rows, int nb) {
   return static_cast<unsigned>(((long long)rows + kTileRows - 1) / kTileRows * nb);
 }
@@ -323,7 +324,8 @@ cudaError_t launch_act_load(int rows, int src_rows, int d, const void* q, const 
                             const int32_t* index, void* out, uint32_t* status, cudaStream_t st) {
   const int nb = d / 128, parts = (nb + kLoadBlocks - 1) / kLoadBlocks;
   const long long warps = (long long)rows * parts;
-  return launch_kernel(act_load_kernel, dim3((unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32))),
+  constexpr int kWarps = kThreads / 32;
+  return launch_kernel(act_load_kernel, dim3((unsigned)((warps + kWarps - 1) / kWarps)),
                        dim3(kThreads), 0, st, false, static_cast<const uint2*>(q), scales, index,
                        static_cast<uint4*>(out), rows, src_rows, nb, parts, status);
 }
@@ -352,8 +354,8 @@ cudaError_t launch_combine_grad(int T, int k, int d, int rows, const void* ebuf,
   const bool warps = d <= 1024 || choices >= 64 * 152;
   const unsigned per = warps ? kThreads / 32 : 1;
   auto kern = warps ? combine_grad_kernel<32> : combine_grad_kernel<kThreads>;
-  return launch_kernel(kern, dim3(((unsigned)choices + per - 1) / per), dim3(kThreads), 0, st, false,
-                       static_cast<const uint4*>(ebuf), row_of, topk_w,
+  return launch_kernel(kern, dim3(((unsigned)choices + per - 1) / per), dim3(kThreads), 0, st,
+                       false, static_cast<const uint4*>(ebuf), row_of, topk_w,
                        static_cast<const uint4*>(dy), static_cast<uint4*>(debuf), dtopk_w, choices,
                        k, d / 8, rows, status);
 }
