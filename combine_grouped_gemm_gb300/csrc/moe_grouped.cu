@@ -394,9 +394,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
       tma_prefetch_map(&mapB);
     }
   }
+  if (warp == 1) tmem_alloc_pair(tmem_slot, S::TMEM_COLS);
   group_offsets(a.counts, a.E, a.rows, tab.off, a.status);
   list_units<DIR, TN>(a, tab);
-  if (warp == 1) tmem_alloc_pair(tmem_slot, S::TMEM_COLS);
   tc_fence_before();
   __syncthreads();
   cluster_sync();   // the peer's barriers and tensor memory are ready
@@ -405,6 +405,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
   if (a.splits > 1) pdl_trigger();   // the joining kernel may come up and wait
   const uint32_t tmem = *tmem_slot;
 
+  // every role finds the pair's first unit itself (a microsecond sooner than through the ring); the
+  // further ones come through the ring
+  const int first = blockIdx.x >> 1;
+  const bool any = first < tab.n_units;
   constexpr int kNever = 1 << 30;
   constexpr int kSum = F32 ? kSumSteps : kNever;   // k-steps per tensor-core sum
 
@@ -417,8 +421,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
       bool ok = true;
       int acquired = -1;   // dw: the group whose maps this thread has acquired
       UnitReader<false> units{ring, rfull, rempty, abort_flag, a.status};
-      GroupedUnit t;
-      while (ok && units.next(&t)) {
+      GroupedUnit t = grouped_unit<DIR, TN>(a, tab, first);
+      for (bool more = any && (t.red >= 0 || units.next(&t)); more; more = ok && units.next(&t)) {
         const CUtensorMap *ma = &mapA, *mb = &mapB;
         if (kDw) {
           ma = maps + 2 * t.g;
@@ -482,8 +486,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
       bool ok = true, ready = false;
       int it = 0;
       UnitReader<false> units{ring, rfull, rempty, abort_flag, a.status};
-      GroupedUnit t;
-      while (ok && units.next(&t)) {
+      GroupedUnit t = grouped_unit<DIR, TN>(a, tab, first);
+      for (bool more = any && (t.red >= 0 || units.next(&t)); more; more = ok && units.next(&t)) {
         const uint32_t n_mma = static_cast<uint32_t>((t.nlen + 31) & ~31);
         const uint32_t idesc = idesc_bf16(256, n_mma) | (DIR != kGroupedFwd ? kIdescAmn : 0u) |
                                (kDw ? kIdescBmn : 0u);
@@ -540,36 +544,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
     // ------------------------------ scheduler (leader) ------------------------------
     if (leader && elect_one()) {
       const uint32_t pairs = gridDim.x >> 1;
-      int at = blockIdx.x >> 1;   // number of the unit at hand
       int slot = 0;
       uint32_t phase = 0;
-      while (true) {
-        const GroupedUnit u = grouped_unit<DIR, TN>(a, tab, at);
-        // one number is taken for every unit; whoever takes the last leaves the counter as it was
-        uint32_t taken = 0;
-        if (u.g >= 0) taken = atomicAdd(a.counter, 1u);
-        if (u.red < 0) {   // a part that this unit does not have
-          if (taken + 1 == static_cast<uint32_t>(tab.n_units)) *a.counter = 0;
-          at = static_cast<int>(pairs + taken);
-          continue;
+      // One number is taken for every unit, that of a unit while the one before is handed over;
+      // whoever takes the last leaves the counter as it was.
+      auto take = [&]() { return atomicAdd(a.counter, 1u); };
+      uint32_t taken = any ? take() : 0;
+      for (bool more = any; more;) {
+        const uint32_t last = taken;
+        const GroupedUnit u = grouped_unit<DIR, TN>(a, tab, static_cast<int>(pairs + taken));
+        more = u.g >= 0;
+        if (more) taken = take();
+        if (u.red >= 0) {   // (below 0: a part that its unit does not have)
+          if (!mbar_wait_cluster(&rempty[slot], phase ^ 1u, abort_flag, a.status)) break;
+          const int4* v = reinterpret_cast<const int4*>(&u);
+          for (uint32_t cta = 0; cta < 2; ++cta) {
+            const uint32_t to = cluster_addr(&ring[slot], cta);
+            st_cluster16(to, v[0]);
+            st_cluster16(to + 16, v[1]);
+          }
+          fence_release_cluster();
+          mbar_arrive_cluster_relaxed(cluster_addr(&rfull[slot], 0));
+          mbar_arrive_cluster_relaxed(cluster_addr(&rfull[slot], 1));
+          if (++slot == kRing) {
+            slot = 0;
+            phase ^= 1u;
+          }
         }
-        if (!mbar_wait_cluster(&rempty[slot], phase ^ 1u, abort_flag, a.status)) break;
-        const int4* v = reinterpret_cast<const int4*>(&u);
-        for (uint32_t cta = 0; cta < 2; ++cta) {
-          const uint32_t to = cluster_addr(&ring[slot], cta);
-          st_cluster16(to, v[0]);
-          st_cluster16(to + 16, v[1]);
-        }
-        fence_release_cluster();
-        mbar_arrive_cluster_relaxed(cluster_addr(&rfull[slot], 0));
-        mbar_arrive_cluster_relaxed(cluster_addr(&rfull[slot], 1));
-        if (u.g < 0) break;
-        if (++slot == kRing) {
-          slot = 0;
-          phase ^= 1u;
-        }
-        if (taken + 1 == static_cast<uint32_t>(tab.n_units)) *a.counter = 0;
-        at = static_cast<int>(pairs + taken);
+        if (last + 1 == static_cast<uint32_t>(tab.n_units)) *a.counter = 0;
       }
     }
     __syncwarp();
@@ -580,9 +582,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
     int it = 0;
     bool ok = true;
     UnitReader<true> units{ring, rfull, rempty, abort_flag, a.status};
-    GroupedUnit t{};
-    while (ok) {
-      ok = units.next(&t);
+    GroupedUnit t = grouped_unit<DIR, TN>(a, tab, first);
+    for (bool have = t.red >= 0; any && ok; have = false) {
+      ok = have || units.next(&t);
       if (F32 && !ok) break;   // (bf16: the two warps of a pair leave together, below)
       const int steps = (t.red + 63) >> 6;
       const int fw = t.f0 + static_cast<int>(rank) * 128 + quarter * 32;   // the warp's columns
