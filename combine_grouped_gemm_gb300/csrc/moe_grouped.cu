@@ -51,38 +51,87 @@ namespace {
 
 constexpr int kMaxGroups = 1024;
 
-// First rows of the groups, off[0..E], from counts, in shared memory: warp 0 scans, each lane
-// over ceil(E / 32) consecutive groups. A negative count is 0 and the offsets stop at `rows`;
-// either is reported. Ends with a block barrier.
-__device__ __forceinline__ void group_offsets(const int32_t* counts, int E, int rows, int* off,
-                                              uint32_t* status) {
-  for (int e = threadIdx.x; e < E; e += blockDim.x) off[e + 1] = counts[e];
+// The groups in shared memory, at most LIVE of them with rows.
+template <int LIVE>
+struct GroupedTables {
+  int off[kMaxGroups + 1];   // first row of each group
+  int live[LIVE];            // fwd, dx: the groups with rows
+  int first[LIVE];           // and the N tiles before each of them
+  int n_live;
+  int n_tiles;
+};
+
+// The tables from the counts: warp 0, each lane over ceil(E / 32) consecutive groups. A negative
+// count is 0 and the offsets stop at `rows` (sums saturate there, so none overflows); either is
+// reported. TN: the N tile, or 0: offsets only. Ends with a block barrier.
+template <int TN, int LIVE>
+__device__ __forceinline__ void group_tables(const int32_t* counts, int E, int rows,
+                                             GroupedTables<LIVE>& tab, uint32_t* status) {
+  for (int e = threadIdx.x; e < E; e += blockDim.x) tab.off[e + 1] = counts[e];
   __syncthreads();
   if (threadIdx.x < 32) {
     const int lane = threadIdx.x, per = (E + 31) / 32;
     const int e0 = min(E, lane * per), e1 = min(E, e0 + per);
+    const uint32_t most = static_cast<uint32_t>(rows);
     bool bad = false;
-    long long sum = 0;
+    auto add = [&](uint32_t x, uint32_t y) {
+      const uint32_t s = x + y;   // (both below 2^31)
+      bad |= s > most;
+      return min(s, most);
+    };
+    uint32_t incl = 0;
     for (int e = e0; e < e1; ++e) {
-      const int c = off[e + 1];
+      const int c = tab.off[e + 1];
       bad |= c < 0;
-      sum += max(c, 0);
+      incl = add(incl, static_cast<uint32_t>(max(c, 0)));
     }
-    long long incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
+      const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl = add(incl, v);
     }
-    bad |= incl > rows;
-    long long at = incl - sum;
+    const uint32_t before = __shfl_up_sync(0xffffffffu, incl, 1);
+    const uint32_t start = lane == 0 ? 0u : before;
+    int live = 0, tiles = 0;   // of this lane's groups
+    uint32_t at = start;
     for (int e = e0; e < e1; ++e) {
-      at += max(off[e + 1], 0);
-      off[e + 1] = static_cast<int>(at < rows ? at : rows);
+      const uint32_t end = min(at + static_cast<uint32_t>(max(tab.off[e + 1], 0)), most);
+      tab.off[e + 1] = static_cast<int>(end);
+      if (TN > 0) {
+        live += end > at;
+        tiles += static_cast<int>(end - at + TN - 1) / (TN > 0 ? TN : 1);
+      }
+      at = end;
     }
-    if (lane == 0) off[0] = 0;
-    if (bad && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
-      raise_status(status, MOE_DEV_BOUNDS);
+    if (lane == 0) tab.off[0] = 0;
+    if (TN > 0) {
+      int live_incl = live, tiles_incl = tiles;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, live_incl, o);
+        const int w = __shfl_up_sync(0xffffffffu, tiles_incl, o);
+        if (lane >= o) {
+          live_incl += v;
+          tiles_incl += w;
+        }
+      }
+      int i = live_incl - live, t = tiles_incl - tiles;
+      at = start;
+      for (int e = e0; e < e1; ++e) {
+        const uint32_t end = static_cast<uint32_t>(tab.off[e + 1]);
+        if (end > at) {
+          tab.live[i] = e;
+          tab.first[i++] = t;
+          t += static_cast<int>(end - at + TN - 1) / (TN > 0 ? TN : 1);
+        }
+        at = end;
+      }
+      if (lane == 31) {
+        tab.n_live = live_incl;
+        tab.n_tiles = tiles_incl;
+      }
+    }
+    if (bad && blockIdx.x == 0) raise_status(status, MOE_DEV_BOUNDS);
   }
   __syncthreads();
 }
@@ -137,15 +186,6 @@ struct GroupedShape {
   static_assert(B_BYTES % 1024 == 0 && TMEM_COLS <= 512 && TMEM_COLS >= 32, "");
 };
 
-// The groups with work, in shared memory: fwd and dx list those that have rows.
-struct GroupedTables {
-  int off[kMaxGroups + 1];   // first row of each group
-  int live[kMaxGroups];      // fwd, dx: the groups with rows
-  int first[kMaxGroups];     // and the N tiles before each of them
-  int n_live;
-  int n_units;
-};
-
 // One unit of work: 256 output columns (the pair's) x one N tile of one group.
 struct alignas(16) GroupedUnit {
   int g;      // group, or -1: no more units
@@ -158,39 +198,11 @@ struct alignas(16) GroupedUnit {
   int split;  // unit | part << 8 | parts << 16 where the reduction is split, else 0
 };
 
-// The rest of the tables, after group_offsets; the caller puts a block barrier behind it.
-template <int DIR, int TN>
-__device__ __forceinline__ void list_units(const GroupedArgs& a, GroupedTables& tab) {
-  const int lane = threadIdx.x & 31;
-  if (DIR == kGroupedDw) {
-    if (threadIdx.x == 0) tab.n_units = a.E * a.mt * ((a.n + TN - 1) / TN) * a.splits;
-  } else if (threadIdx.x < 32) {
-    int at = 0, tiles = 0;
-    for (int e0 = 0; e0 < a.E; e0 += 32) {
-      const int e = e0 + lane;
-      const int c = e < a.E ? tab.off[e + 1] - tab.off[e] : 0;
-      const bool has = c > 0;
-      const int nt = (c + TN - 1) / TN;
-      int incl = nt;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-      }
-      const uint32_t m = __ballot_sync(0xffffffffu, has);
-      if (has) {
-        const int i = at + __popc(m & ((1u << lane) - 1u));
-        tab.live[i] = e;
-        tab.first[i] = tiles + incl - nt;
-      }
-      at += __popc(m);
-      tiles += __shfl_sync(0xffffffffu, incl, 31);
-    }
-    if (lane == 0) {
-      tab.n_live = at;
-      tab.n_units = tiles * a.mt * a.splits;
-    }
-  }
+// Units of all groups, in parts.
+template <int DIR, int TN, typename Tables>
+__device__ __forceinline__ int unit_count(const GroupedArgs& a, const Tables& tab) {
+  const int tiles = DIR == kGroupedDw ? a.E * ((a.n + TN - 1) / TN) : tab.n_tiles;
+  return tiles * a.mt * a.splits;
 }
 
 // Unit number u. fwd, dx: weight-tile-major (unit m * nt + j of a group: N tile j of its 256
@@ -201,17 +213,16 @@ __device__ __forceinline__ void list_units(const GroupedArgs& a, GroupedTables& 
 // an MMA's N) rather than full ones and a rest, which would cost a whole pass over the weight
 // tile for a few rows. The group is found by binary search over the tiles before each: walking
 // there from the unit before took several thousand cycles where groups are many and small.
-template <int DIR, int TN>
-__device__ __forceinline__ GroupedUnit grouped_unit(const GroupedArgs& a, const GroupedTables& tab,
-                                                    int u) {
+template <int DIR, int TN, typename Tables>
+__device__ __forceinline__ GroupedUnit grouped_unit(const GroupedArgs& a, const Tables& tab, int u) {
   GroupedUnit r{};
-  if (u >= tab.n_units) {
+  if (u >= unit_count<DIR, TN>(a, tab)) {
     r.g = -1;
     return r;
   }
-  int part = 0;
-  const int number = u / a.splits;
+  int part = 0, number = 0;
   if (a.splits > 1) {
+    number = u / a.splits;
     part = u - number * a.splits;
     u = number;
   }
@@ -236,7 +247,7 @@ __device__ __forceinline__ GroupedUnit grouped_unit(const GroupedArgs& a, const 
     const int base = tab.off[r.g], len = tab.off[r.g + 1] - base;
     const int local = u - tab.first[lo] * a.mt;
     r.nt = (len + TN - 1) / TN;
-    const int m = local / r.nt, j = local - m * r.nt;
+    const int m = r.nt == 1 ? local : local / r.nt, j = local - m * r.nt;
     const int w = r.nt == 1 ? TN : ((len + r.nt - 1) / r.nt + 31) & ~31;
     r.f0 = m * 256;
     r.n0 = base + j * w;
@@ -323,10 +334,10 @@ __global__ void __launch_bounds__(kMapWarps * 32)
     group_maps_kernel(const int32_t* __restrict__ counts, CUtensorMap* maps, int rows, int E,
                       uint32_t* status, const __grid_constant__ CUtensorMap map_a,
                       const __grid_constant__ CUtensorMap map_b) {
-  __shared__ int off[kMaxGroups + 1];
+  __shared__ GroupedTables<1> tab;
   __shared__ alignas(128) uint32_t copy[kMapWarps][2][32];
   pdl_trigger();
-  group_offsets(counts, E, rows, off, status);
+  group_tables<0>(counts, E, rows, tab, status);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = blockIdx.x * kMapWarps + warp;
   if (g >= E) return;
@@ -335,7 +346,7 @@ __global__ void __launch_bounds__(kMapWarps * 32)
   __syncwarp();
   const uint32_t sa = smem_addr(copy[warp][0]), sb = smem_addr(copy[warp][1]);
   if (lane == 0) {
-    const uint32_t end = static_cast<uint32_t>(max(1, off[g + 1]));   // (an extent is at least 1)
+    const uint32_t end = static_cast<uint32_t>(max(1, tab.off[g + 1]));   // (an extent is at least 1)
     tensor_map_set_rows(sa, end);
     tensor_map_set_rows(sb, end);
   }
@@ -355,7 +366,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
   constexpr int kBoxesB = kDw ? TN / 128 : 0;
   static_assert(!kDw || TN >= 128, "dw: whole 64-column boxes");
   extern __shared__ uint8_t smem_raw[];
-  __shared__ GroupedTables tab;
+  __shared__ GroupedTables<kDw ? 1 : kMaxGroups> tab;
   __shared__ GroupedUnit ring[kRing];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -395,11 +406,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
     }
   }
   if (warp == 1) tmem_alloc_pair(tmem_slot, S::TMEM_COLS);
-  group_offsets(a.counts, a.E, a.rows, tab.off, a.status);
-  list_units<DIR, TN>(a, tab);
   tc_fence_before();
-  __syncthreads();
-  cluster_sync();   // the peer's barriers and tensor memory are ready
+  __syncwarp();
+  cluster_arrive();
+  group_tables<kDw ? 0 : TN>(a.counts, a.E, a.rows, tab, a.status);
+  cluster_wait();   // the peer's barriers and tensor memory are ready
   tc_fence_after();
   if (kDw) pdl_wait();   // the groups' tensor maps are written
   if (a.splits > 1) pdl_trigger();   // the joining kernel may come up and wait
@@ -408,7 +419,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
   // every role finds the pair's first unit itself (a microsecond sooner than through the ring); the
   // further ones come through the ring
   const int first = blockIdx.x >> 1;
-  const bool any = first < tab.n_units;
+  const int n_units = unit_count<DIR, TN>(a, tab);
+  const bool any = first < n_units;
   constexpr int kNever = 1 << 30;
   constexpr int kSum = F32 ? kSumSteps : kNever;   // k-steps per tensor-core sum
 
@@ -571,7 +583,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
             phase ^= 1u;
           }
         }
-        if (last + 1 == static_cast<uint32_t>(tab.n_units)) *a.counter = 0;
+        if (last + 1 == static_cast<uint32_t>(n_units)) *a.counter = 0;
       }
     }
     __syncwarp();
@@ -754,7 +766,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GroupedThreads<F32>:
   if (*abort_flag) __nanosleep(1000000);
   tc_fence_before();
   __syncthreads();
-  cluster_sync();   // neither CTA leaves while the other still reads or signals it
+  cluster_arrive();   // neither CTA leaves while the other still reads or signals it
+  cluster_wait();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, S::TMEM_COLS);
@@ -766,11 +779,9 @@ constexpr int kJoinRows = 8;
 template <int DIR, int TN>
 __global__ void __launch_bounds__(256)
     join_kernel(const GroupedArgs a, int out_f32, int accumulate) {
-  __shared__ GroupedTables tab;
-  // counts and offsets are those that the products read: nothing before this has changed them
-  group_offsets(a.counts, a.E, a.rows, tab.off, nullptr);
-  list_units<DIR, TN>(a, tab);
-  __syncthreads();
+  __shared__ GroupedTables<DIR == kGroupedDw ? 1 : kMaxGroups> tab;
+  // counts are those that the products read: nothing before this has changed them
+  group_tables<DIR == kGroupedDw ? 0 : TN>(a.counts, a.E, a.rows, tab, nullptr);
   constexpr int kSets = TN / kJoinRows;
   const int unit = blockIdx.x / kSets, j0 = (blockIdx.x - unit * kSets) * kJoinRows;
   const GroupedUnit t = grouped_unit<DIR, TN>(a, tab, unit * a.splits);   // its first part
