@@ -349,8 +349,7 @@ def grouped_ws_bytes(g: GroupCfg) -> int:
     return n.value
 
 
-def _need_ws(fn, g, ws):
-    shape = (g.rows, g.E, g.n, g.k)
+def _need_ws(fn, g, shape, ws):
     need = _ws_need.get(shape)
     if need is None:
         need = _ws_need[shape] = grouped_ws_bytes(g)
@@ -362,35 +361,37 @@ def _need_ws(fn, g, ws):
 def grouped_mm(g: GroupCfg, x, counts, w, y, ws, stream=None):
     """y[r] = x[r] . w[e]^T for every row r of group e (counts rows each, in group order)."""
     fn, bf = "moe_grouped_mm", torch.bfloat16
-    _check(fn, _lib.moe_grouped_mm(ctypes.byref(g), _need(fn, "x", x, bf, g.rows, g.k),
-                                   _need(fn, "counts", counts, torch.int32, g.E),
-                                   _need(fn, "w", w, bf, g.E, g.n, g.k),
-                                   _need(fn, "y", y, bf, g.rows, g.n), _need_ws(fn, g, ws),
+    rows, E, n, k = shape = g.rows, g.E, g.n, g.k
+    _check(fn, _lib.moe_grouped_mm(ctypes.byref(g), _need(fn, "x", x, bf, rows, k),
+                                   _need(fn, "counts", counts, torch.int32, E),
+                                   _need(fn, "w", w, bf, E, n, k),
+                                   _need(fn, "y", y, bf, rows, n), _need_ws(fn, g, shape, ws),
                                    _s(stream)))
 
 
 def grouped_mm_dx(g: GroupCfg, dy, counts, w, dx, ws, stream=None):
     """dx[r] = dy[r] . w[e]: the gradient of grouped_mm's rows."""
     fn, bf = "moe_grouped_mm_dx", torch.bfloat16
-    _check(fn, _lib.moe_grouped_mm_dx(ctypes.byref(g), _need(fn, "dy", dy, bf, g.rows, g.n),
-                                      _need(fn, "counts", counts, torch.int32, g.E),
-                                      _need(fn, "w", w, bf, g.E, g.n, g.k),
-                                      _need(fn, "dx", dx, bf, g.rows, g.k), _need_ws(fn, g, ws),
-                                      _s(stream)))
+    rows, E, n, k = shape = g.rows, g.E, g.n, g.k
+    _check(fn, _lib.moe_grouped_mm_dx(ctypes.byref(g), _need(fn, "dy", dy, bf, rows, n),
+                                      _need(fn, "counts", counts, torch.int32, E),
+                                      _need(fn, "w", w, bf, E, n, k),
+                                      _need(fn, "dx", dx, bf, rows, k),
+                                      _need_ws(fn, g, shape, ws), _s(stream)))
 
 
 def grouped_mm_dw(g: GroupCfg, dy, x, counts, dw, ws, accumulate=False, stream=None):
     """dw[e] = sum of dy[r]^T x[r] over group e's rows (accumulate: added to dw, fp32 only): the
     gradient of grouped_mm's weights. dw bf16 or fp32."""
     fn, bf = "moe_grouped_mm_dw", torch.bfloat16
+    rows, E, n, k = shape = g.rows, g.E, g.n, g.k
     f32 = isinstance(dw, torch.Tensor) and dw.dtype is torch.float32
-    _check(fn, _lib.moe_grouped_mm_dw(ctypes.byref(g), _need(fn, "dy", dy, bf, g.rows, g.n),
-                                      _need(fn, "x", x, bf, g.rows, g.k),
-                                      _need(fn, "counts", counts, torch.int32, g.E),
-                                      _need(fn, "dw", dw, torch.float32 if f32 else bf, g.E, g.n,
-                                            g.k),
-                                      MOE_F32 if f32 else MOE_BF16, int(bool(accumulate)),
-                                      _need_ws(fn, g, ws), _s(stream)))
+    _check(fn, _lib.moe_grouped_mm_dw(ctypes.byref(g), _need(fn, "dy", dy, bf, rows, n),
+                                      _need(fn, "x", x, bf, rows, k),
+                                      _need(fn, "counts", counts, torch.int32, E),
+                                      _need(fn, "dw", dw, torch.float32 if f32 else bf, E, n, k),
+                                      MOE_F32 if f32 else MOE_BF16, 1 if accumulate else 0,
+                                      _need_ws(fn, g, shape, ws), _s(stream)))
 
 
 def _rows_cols(fn, name, t):
