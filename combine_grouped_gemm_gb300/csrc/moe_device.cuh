@@ -365,10 +365,10 @@ __device__ __forceinline__ void st_cluster16(uint32_t addr, const int4& v) {
 }
 
 // Arrival on a barrier of either CTA, by itself not ordered after earlier memory accesses: after
-// fence_release_cluster for what it publishes, or alone where it hands over tensor memory
-// (tcgen05.wait::ld and tcgen05.fence::before_thread_sync come before it) or something the thread
-// has finished reading. A releasing arrival would wait for the thread's outstanding global stores,
-// about 1600 cycles in an epilogue.
+// fence_release_cluster for what it publishes, alone where it hands over tensor memory
+// (tcgen05.wait::ld and tcgen05.fence::before_thread_sync come before it), or conditional on the
+// values of loads that have to come first. A releasing arrival would wait for the thread's
+// outstanding global stores, about 1600 cycles in an epilogue.
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
                : "memory");
