@@ -603,6 +603,9 @@ namespace {
 int check_group(const moe_group_cfg* c) {
   if (!c || c->rows < 0 || c->E < 1 || c->n < 1 || c->k < 1) return MOE_ERR_INVALID_ARG;
   if (c->E > 1024 || c->n % 8 || c->k % 8) return MOE_ERR_UNSUPPORTED;
+  // the kernels round sizes up to tiles and k-steps in 32 bits
+  constexpr int32_t kMost = INT32_MAX - 512;
+  if (c->rows > kMost || c->n > kMost || c->k > kMost) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 

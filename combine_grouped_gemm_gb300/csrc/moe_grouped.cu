@@ -99,7 +99,7 @@ __device__ __forceinline__ void group_tables(const int32_t* counts, int E, int r
       tab.off[e + 1] = static_cast<int>(end);
       if (TN > 0) {
         live += end > at;
-        tiles += static_cast<int>(end - at + TN - 1) / (TN > 0 ? TN : 1);
+        tiles += static_cast<int>((end - at + TN - 1) / (TN > 0 ? TN : 1));
       }
       at = end;
     }
@@ -122,7 +122,7 @@ __device__ __forceinline__ void group_tables(const int32_t* counts, int E, int r
         if (end > at) {
           tab.live[i] = e;
           tab.first[i++] = t;
-          t += static_cast<int>(end - at + TN - 1) / (TN > 0 ? TN : 1);
+          t += static_cast<int>((end - at + TN - 1) / (TN > 0 ? TN : 1));
         }
         at = end;
       }
@@ -248,7 +248,7 @@ __device__ __forceinline__ GroupedUnit grouped_unit(const GroupedArgs& a, const 
     const int local = u - tab.first[lo] * a.mt;
     r.nt = (len + TN - 1) / TN;
     const int m = r.nt == 1 ? local : local / r.nt, j = local - m * r.nt;
-    const int w = r.nt == 1 ? TN : ((len + r.nt - 1) / r.nt + 31) & ~31;
+    const int w = r.nt == 1 ? TN : ((len - 1) / r.nt + 32) & ~31;   // ceil(len / nt), to 32
     r.f0 = m * 256;
     r.n0 = base + j * w;
     r.nlen = min(w, len - j * w);

@@ -357,7 +357,8 @@ int moe_expert_ffn_gather(const moe_cfg* cfg, const void* x, const int32_t* coun
  * ------------------------------------------------------------------------------------- */
 
 /* Shape of one grouped product. The row tensors hold the rows of the E groups one group after
- * another: group e owns rows [s_e, s_e + counts[e]), s_e = counts[0] + ... + counts[e-1]. */
+ * another: group e owns rows [s_e, s_e + counts[e]), s_e = counts[0] + ... + counts[e-1]. rows, n
+ * and k are at most 2^31 - 513. */
 typedef struct moe_group_cfg {
   int32_t rows;  /* rows of the row tensors, >= 0; the groups own the first sum(counts) of them */
   int32_t E;     /* groups (experts), 1 <= E <= 1024 */
@@ -370,7 +371,8 @@ typedef struct moe_group_cfg {
  * workspace once, before its first use, and every call leaves it ready for the next (after a
  * call that reported MOE_DEV_TIMEOUT, zero it again). Calls that
  * may overlap on the GPU need workspaces of their own. MOE_ERR_INVALID_ARG for a negative or
- * zero size, MOE_ERR_UNSUPPORTED for n or k not a multiple of 8 or E > 1024. */
+ * zero size, MOE_ERR_UNSUPPORTED for n or k not a multiple of 8, E > 1024 or a size past
+ * 2^31 - 513. */
 int moe_grouped_query(const moe_group_cfg* cfg, size_t* ws_bytes);
 
 /* Matrix products grouped by expert, rows of any number per group (0 included). bf16 operands,

@@ -116,3 +116,43 @@ def test_weight_gradients_over_many_units_a_pair(moe, rows, E, n, k, empty):
             moe.grouped_mm_dw(g, dy, x, c, again, ws, accumulate=True)
             assert torch.equal(again, 2 * dw)
     assert moe.read_status(ws) == 0
+
+
+def test_groups_near_the_end_of_the_row_range(moe):
+    """One group of nearly 2^31 rows: all rows are written and read, and the weight gradient's sum
+    keeps its precision. It adds 2^31 products in parts of at most 512; each addition of those sums
+    rounds by at most 2^-24 of a partial sum no larger than the result, with random signs, 2^25
+    additions in all: 2^-24 2^12.5 of it, at most."""
+    g = moe.GroupCfg(rows=2 ** 31 - 520, E=2, n=8, k=8)
+    counts = [g.rows - 3, 3]
+    c = torch.tensor(counts, dtype=torch.int32, device="cuda")
+    ws = torch.zeros(moe.grouped_ws_bytes(g), dtype=torch.uint8, device="cuda")
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(1)
+    x = torch.empty((g.rows, 8), dtype=BF, device="cuda").normal_(0.25, 1.0, generator=gen)
+    w = normal(2, 2, 8, 8)
+    y = torch.full((g.rows, 8), float("nan"), dtype=BF, device="cuda")
+    moe.grouped_mm(g, x, c, w, y, ws)
+    at = torch.randint(0, counts[0], (200000,), generator=gen, device="cuda")
+    at[:3] = torch.tensor([0, 2 ** 30, counts[0] - 1])
+
+    def check(out, src, mats):
+        for first in range(0, g.rows, 1 << 27):
+            assert bool(torch.isfinite(out[first:first + (1 << 27)]).all())
+        for s, o, m in ((src[at], out[at], mats[0]), (src[-3:], out[-3:], mats[1])):
+            within(o, s.double() @ m, s.double().abs() @ m.abs(), 8)
+    check(y, x, [w[e].double().t() for e in range(2)])
+    dx = torch.full((g.rows, 8), float("nan"), dtype=BF, device="cuda")
+    moe.grouped_mm_dx(g, y, c, w, dx, ws)
+    check(dx, y, [w[e].double() for e in range(2)])
+    del dx
+    dw = torch.empty((2, 8, 8), device="cuda")
+    moe.grouped_mm_dw(g, y, x, c, dw, ws)
+    ref = torch.zeros((8, 8), dtype=torch.float64, device="cuda")
+    for first in range(0, counts[0], 1 << 25):
+        r = slice(first, min(first + (1 << 25), counts[0]))
+        ref += y[r].double().t() @ x[r].double()
+    assert float((dw[0].double() - ref).norm() / ref.norm()) < 2.0 ** -11.5
+    last = y[-3:].double().t(), x[-3:].double()
+    within(dw[1], last[0] @ last[1], last[0].abs() @ last[1].abs(), 3)
+    assert moe.read_status(ws) == 0
