@@ -6,6 +6,7 @@
 #include <stdlib.h>
 
 #include <algorithm>
+#include <initializer_list>
 
 #include "moe_internal.h"
 
@@ -609,7 +610,24 @@ int check_group(const moe_group_cfg* c) {
   return MOE_OK;
 }
 
-// in0, in1, out, with how many of the three are row tensors (NULL allowed when rows == 0)
+// A call's array in bytes; n is 0 for one that is not there.
+struct Span {
+  const void* p;
+  size_t n;
+};
+
+// Whether an output meets any of these arrays. The calls' blocks run in any order, so a result
+// written over an input would change what other blocks read.
+bool meets(const Span& out, std::initializer_list<Span> others) {
+  const auto o = reinterpret_cast<uintptr_t>(out.p);
+  for (const Span& s : others) {
+    const auto b = reinterpret_cast<uintptr_t>(s.p);
+    if (out.p && s.p && out.n && s.n && o < b + s.n && b < o + out.n) return true;
+  }
+  return false;
+}
+
+// (row tensors may be NULL when rows == 0)
 int run_grouped(const moe_group_cfg* cfg, GroupedDir dir, const void* in0, const void* in1,
                 const int32_t* counts, void* out, bool f32, bool accumulate, void* ws,
                 cudaStream_t stream) {
@@ -622,6 +640,14 @@ int run_grouped(const moe_group_cfg* cfg, GroupedDir dir, const void* in0, const
   if (!(empty && !out && dir != kGroupedDw)) MOE_NEED(out);
   MOE_NEED(ws);
   if (empty && dir != kGroupedDw) return MOE_OK;
+  const size_t rows = cfg->rows, xs = 2 * rows * cfg->k, ys = 2 * rows * cfg->n;
+  const size_t weights = (size_t)cfg->E * cfg->n * cfg->k;
+  const Span a{in0, dir == kGroupedFwd ? xs : ys}, b{in1, dir == kGroupedDw ? xs : 2 * weights};
+  const Span c{counts, sizeof(int32_t) * cfg->E}, work{ws, grouped_ws_bytes(*cfg)};
+  const Span o{out, dir == kGroupedFwd  ? ys
+                    : dir == kGroupedDx ? xs
+                                        : weights * (f32 ? 4 : 2)};
+  if (meets(o, {a, b, c, work}) || meets(work, {a, b, c})) return MOE_ERR_INVALID_ARG;
   const cudaError_t e =
       launch_grouped(*cfg, dir, in0, in1, counts, out, f32, accumulate, ws, stream);
   return e == cudaSuccess ? MOE_OK : cuda_fail(e);
@@ -669,6 +695,9 @@ int moe_act_save(int32_t rows, int32_t d, const void* x, void* q, float* scales,
   MOE_NEED(x);
   MOE_NEED(q);
   MOE_NEED(scales);
+  const size_t n = (size_t)rows * d;
+  const Span in{x, 2 * n}, codes{q, n}, sc{scales, n / 32};
+  if (meets(codes, {in, sc}) || meets(sc, {in})) return MOE_ERR_INVALID_ARG;
   const cudaError_t e = launch_act_save(rows, d, x, q, scales, stream);
   return e == cudaSuccess ? MOE_OK : cuda_fail(e);
 }
@@ -686,6 +715,10 @@ int moe_act_load(int32_t rows, int32_t src_rows, int32_t d, const void* q, const
   MOE_OPT(index);
   MOE_NEED(out);
   if (status && misaligned4(status)) return MOE_ERR_MISALIGNED;
+  const size_t n = (size_t)src_rows * d;
+  if (meets({out, 2 * (size_t)rows * d},
+            {{q, n}, {scales, n / 32}, {index, sizeof(int32_t) * (size_t)rows}}))
+    return MOE_ERR_INVALID_ARG;
   const cudaError_t e =
       launch_act_load(rows, src_rows, d, q, scales, index, out, status, stream);
   return e == cudaSuccess ? MOE_OK : cuda_fail(e);
@@ -699,6 +732,10 @@ int moe_swiglu_save(int32_t rows, int32_t f, const void* gu, void* a, void* q, f
   MOE_NEED(a);
   MOE_NEED(q);
   MOE_NEED(scales);
+  const size_t n = (size_t)rows * f;
+  const Span in{gu, 4 * n}, act{a, 2 * n}, codes{q, 2 * n}, sc{scales, n / 16};
+  if (meets(act, {in, codes, sc}) || meets(codes, {in, sc}) || meets(sc, {in}))
+    return MOE_ERR_INVALID_ARG;
   const cudaError_t e = launch_swiglu_save(rows, f, gu, a, q, scales, stream);
   return e == cudaSuccess ? MOE_OK : cuda_fail(e);
 }
@@ -712,6 +749,10 @@ int moe_swiglu_grad(int32_t rows, int32_t f, const void* q, const float* scales,
   MOE_NEED(da);
   MOE_NEED(dgu);
   MOE_OPT(a);
+  const size_t n = (size_t)rows * f;
+  const Span codes{q, 2 * n}, sc{scales, n / 16}, in{da, 2 * n}, g{dgu, 4 * n}, act{a, 2 * n};
+  if (meets(g, {codes, sc, in, act}) || meets(act, {codes, sc}) || (a != da && meets(act, {in})))
+    return MOE_ERR_INVALID_ARG;
   const cudaError_t e = launch_swiglu_grad(rows, f, q, scales, da, dgu, a, stream);
   return e == cudaSuccess ? MOE_OK : cuda_fail(e);
 }
@@ -725,13 +766,18 @@ int moe_combine_grad(int32_t T, int32_t k, int32_t d, int32_t rows, const void* 
   if (rows > 0) {
     MOE_NEED(ebuf);
     MOE_NEED(debuf);
-    if (ebuf == debuf) return MOE_ERR_INVALID_ARG;
   }
   MOE_NEED(row_of);
   MOE_NEED(topk_w);
   MOE_NEED(dy);
   MOE_NEED(dtopk_w);
   if (status && misaligned4(status)) return MOE_ERR_MISALIGNED;
+  const size_t n = (size_t)rows * d, tk = sizeof(int32_t) * (size_t)T * k;
+  const Span e0{ebuf, 2 * n}, de{debuf, 2 * n}, at{row_of, tk}, w{topk_w, tk}, dw{dtopk_w, tk};
+  const Span in{dy, 2 * (size_t)T * d};
+  if (meets(de, {e0, at, w, in, dw}) || meets(dw, {e0, at, in}) ||
+      (dtopk_w != topk_w && meets(dw, {w})))
+    return MOE_ERR_INVALID_ARG;
   const cudaError_t e = launch_combine_grad(T, k, d, rows, ebuf, row_of, topk_w, dy, debuf,
                                             dtopk_w, status, stream);
   return e == cudaSuccess ? MOE_OK : cuda_fail(e);

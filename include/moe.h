@@ -354,6 +354,10 @@ int moe_expert_ffn_gather(const moe_cfg* cfg, const void* x, const int32_t* coun
  *             -> moe_act_load (x's rows) -> moe_grouped_mm_dw (gate/up)
  *             -> moe_combine with weights of one (dx: the dispatch's gradient)
  * The pages cover inference only and have no counterpart to these calls.
+ *
+ * An output (the workspace of a grouped product too) may not overlap an input or another output:
+ * MOE_ERR_INVALID_ARG. Two may be the very array they take the place of: moe_swiglu_grad's a that
+ * of da, moe_combine_grad's dtopk_w that of topk_w.
  * ------------------------------------------------------------------------------------- */
 
 /* Shape of one grouped product. The row tensors hold the rows of the E groups one group after
@@ -431,8 +435,7 @@ int moe_swiglu_grad(int32_t rows, int32_t f, const void* q, const float* scales,
  * (summed in fp32 in a fixed order). Rows of debuf that no choice names are not written. A
  * negative row_of is a choice that the dispatch skipped: its dtopk_w is 0. One at or past rows is
  * treated so too and reported (MOE_DEV_BOUNDS in status, NULL or a device uint32). The shared
- * expert's rows have dy itself as gradient. d % 128 == 0, 1 <= k <= 32,
- * T * k < 2^31. debuf may not be ebuf. */
+ * expert's rows have dy itself as gradient. d % 128 == 0, 1 <= k <= 32, T * k < 2^31. */
 int moe_combine_grad(int32_t T, int32_t k, int32_t d, int32_t rows, const void* ebuf,
                      const int32_t* row_of, const float* topk_w, const void* dy, void* debuf,
                      float* dtopk_w, uint32_t* status, cudaStream_t stream);

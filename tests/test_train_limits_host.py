@@ -3,6 +3,10 @@ launches GPU work."""
 import ctypes
 
 import pytest
+import torch
+
+# the addresses are made up, so a check that let one through must not find a device
+pytestmark = pytest.mark.skipif(torch.cuda.is_available(), reason="host checks, run without a GPU")
 
 OK = 1 << 20   # an aligned address that the checks never dereference
 
@@ -30,3 +34,69 @@ def test_sizes_that_leave_no_room_for_a_tile(moe, dim, size, code):
         assert L.moe_grouped_mm(g, OK, OK, OK, OK, OK, None) == code
         assert L.moe_grouped_mm_dx(g, OK, OK, OK, OK, OK, None) == code
         assert L.moe_grouped_mm_dw(g, OK, OK, OK, OK, 0, 0, OK, None) == code
+
+
+def refuses_overlap(call, sizes, out, allowed=()):
+    """Each way in which array `out` can meet another one is an invalid argument. sizes: name ->
+    bytes, of arrays at fake addresses 1 TB apart."""
+    base = {n: (i + 1) << 40 for i, n in enumerate(sizes)}
+    for other in sizes:
+        if other == out:
+            continue
+        meets = [base[other] + sizes[other] - 16, base[other] - sizes[out] + 16]
+        if other not in allowed:
+            meets.append(base[other])
+        for at in meets:
+            assert call(**{**base, out: at}) == 1, (out, other, at)
+
+
+def test_outputs_that_meet_an_input_are_refused(moe):
+    """Every call's blocks run in any order: a result over an input would change what other blocks
+    read. (sizes: whole multiples of 16 bytes, at least 32)"""
+    L = moe._lib
+    rows, E, n, k = 16, 8, 64, 128
+    g = ctypes.byref(moe.GroupCfg(rows=rows, E=E, n=n, k=k))
+    x, w, y = 2 * rows * k, 2 * E * n * k, 2 * rows * n
+    ws = moe.grouped_ws_bytes(moe.GroupCfg(rows=rows, E=E, n=n, k=k)) // 16 * 16
+
+    def mm(a, counts, w, out, ws):
+        return L.moe_grouped_mm(g, a, counts, w, out, ws, None)
+
+    def dx(a, counts, w, out, ws):
+        return L.moe_grouped_mm_dx(g, a, counts, w, out, ws, None)
+
+    def dw(a, counts, w, out, ws, dtype=moe.MOE_F32):
+        return L.moe_grouped_mm_dw(g, a, w, counts, out, dtype, 0, ws, None)
+    refuses_overlap(mm, dict(a=x, counts=4 * E, w=w, out=y, ws=ws), "out")
+    refuses_overlap(dx, dict(a=y, counts=4 * E, w=w, out=x, ws=ws), "out")
+    refuses_overlap(dw, dict(a=y, counts=4 * E, w=x, out=2 * w, ws=ws), "out")
+    refuses_overlap(lambda **p: dw(dtype=moe.MOE_BF16, **p),
+                    dict(a=y, counts=4 * E, w=x, out=w, ws=ws), "out")
+    for f, s in ((mm, dict(a=x, counts=4 * E, w=w, out=y, ws=ws)),
+                 (dx, dict(a=y, counts=4 * E, w=w, out=x, ws=ws)),
+                 (dw, dict(a=y, counts=4 * E, w=x, out=2 * w, ws=ws))):
+        refuses_overlap(f, s, "ws")
+
+    rows, d = 16, 256
+    save = dict(x=2 * rows * d, q=rows * d, scales=rows * d // 32)
+    for out in ("q", "scales"):
+        refuses_overlap(lambda x, q, scales: L.moe_act_save(rows, d, x, q, scales, None), save, out)
+    load = dict(q=8 * d, scales=8 * d // 32, index=4 * rows, out=2 * rows * d)
+    refuses_overlap(lambda q, scales, index, out: L.moe_act_load(
+        rows, 8, d, q, scales, index, out, None, None), load, "out")
+    swi = dict(gu=4 * rows * d, a=2 * rows * d, q=2 * rows * d, scales=rows * d // 16)
+    for out in ("a", "q", "scales"):
+        refuses_overlap(lambda gu, a, q, scales: L.moe_swiglu_save(rows, d, gu, a, q, scales, None),
+                        swi, out)
+    grad = dict(q=2 * rows * d, scales=rows * d // 16, da=2 * rows * d, dgu=4 * rows * d,
+                a=2 * rows * d)
+    for out in ("dgu", "a"):   # a may be da itself: one thread reads and writes an element
+        refuses_overlap(lambda q, scales, da, dgu, a: L.moe_swiglu_grad(
+            rows, d, q, scales, da, dgu, a, None), grad, out, ("da",) if out == "a" else ())
+    T, k = 8, 4
+    comb = dict(ebuf=2 * rows * d, row_of=4 * T * k, topk_w=4 * T * k, dy=2 * T * d,
+                debuf=2 * rows * d, dtopk_w=4 * T * k)
+    for out in ("debuf", "dtopk_w"):   # dtopk_w may be topk_w itself, likewise
+        refuses_overlap(lambda ebuf, row_of, topk_w, dy, debuf, dtopk_w: L.moe_combine_grad(
+            T, k, d, rows, ebuf, row_of, topk_w, dy, debuf, dtopk_w, None, None),
+            comb, out, ("topk_w",) if out == "dtopk_w" else ())
