@@ -320,13 +320,37 @@ def expert_ffn_gather(cfg, x, counts, src_tok, weights: dict, ebuf, shared_out, 
 
 # ---------------------------------------------------------------------------------------------
 # Training of the expert path (see include/moe.h). Row counts and widths are taken from the
-# tensors; a tensor of another type or size than the call needs is a ValueError.
+# tensors; a tensor of another type or size than the call needs, or of another device than the
+# current one, is a ValueError.
 # ---------------------------------------------------------------------------------------------
-def _need(fn, name, t, dtype, *shape):
-    """_p(t), for a tensor that must have this element type and shape. int8 and e4m3 tensors
-    count as bytes."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_cuda
-            and t.is_contiguous()):
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _device():
+    """The number of the current device, which no tensor has where there is none."""
+    try:
+        return _get_device()
+    except (RuntimeError, AssertionError):
+        return -2
+
+
+def _here(fn, dev, name, t):
+    """_p(t), for a tensor that must be device dev's."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() != dev:
+        raise ValueError(f"{fn}: {name} must be on the current device, cuda:{dev}")
+    return _p(t)
+
+
+def _stream(stream, dev):
+    """_s(stream), where the current device's number is known."""
+    return _raw_stream(dev) if stream is None and _raw_stream is not None else _s(stream)
+
+
+def _need(fn, dev, name, t, dtype, *shape):
+    """_p(t), for a tensor of device dev that must have this element type and shape. int8 and
+    e4m3 tensors count as bytes."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.get_device() == dev and t.is_contiguous()):
         return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{fn}: {name} must be a CUDA tensor")
@@ -335,7 +359,7 @@ def _need(fn, name, t, dtype, *shape):
         raise ValueError(f"{fn}: {name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{fn}: {name} must have shape {shape}, got {tuple(t.shape)}")
-    return _p(t)
+    return _here(fn, dev, name, t)
 
 
 _ws_need = {}   # (rows, E, n, k) -> bytes: a host-side size, asked for once per shape
@@ -349,49 +373,50 @@ def grouped_ws_bytes(g: GroupCfg) -> int:
     return n.value
 
 
-def _need_ws(fn, g, shape, ws):
+def _need_ws(fn, dev, g, shape, ws):
     need = _ws_need.get(shape)
     if need is None:
         need = _ws_need[shape] = grouped_ws_bytes(g)
     if not isinstance(ws, torch.Tensor) or ws.nbytes < need:
         raise ValueError(f"{fn}: ws must be a CUDA tensor of grouped_ws_bytes(cfg) bytes")
-    return _p(ws)
+    return _here(fn, dev, "ws", ws)
 
 
 def grouped_mm(g: GroupCfg, x, counts, w, y, ws, stream=None):
     """y[r] = x[r] . w[e]^T for every row r of group e (counts rows each, in group order)."""
-    fn, bf = "moe_grouped_mm", torch.bfloat16
+    fn, bf, dev = "moe_grouped_mm", torch.bfloat16, _device()
     rows, E, n, k = shape = g.rows, g.E, g.n, g.k
-    _check(fn, _lib.moe_grouped_mm(ctypes.byref(g), _need(fn, "x", x, bf, rows, k),
-                                   _need(fn, "counts", counts, torch.int32, E),
-                                   _need(fn, "w", w, bf, E, n, k),
-                                   _need(fn, "y", y, bf, rows, n), _need_ws(fn, g, shape, ws),
-                                   _s(stream)))
+    _check(fn, _lib.moe_grouped_mm(ctypes.byref(g), _need(fn, dev, "x", x, bf, rows, k),
+                                   _need(fn, dev, "counts", counts, torch.int32, E),
+                                   _need(fn, dev, "w", w, bf, E, n, k),
+                                   _need(fn, dev, "y", y, bf, rows, n),
+                                   _need_ws(fn, dev, g, shape, ws), _stream(stream, dev)))
 
 
 def grouped_mm_dx(g: GroupCfg, dy, counts, w, dx, ws, stream=None):
     """dx[r] = dy[r] . w[e]: the gradient of grouped_mm's rows."""
-    fn, bf = "moe_grouped_mm_dx", torch.bfloat16
+    fn, bf, dev = "moe_grouped_mm_dx", torch.bfloat16, _device()
     rows, E, n, k = shape = g.rows, g.E, g.n, g.k
-    _check(fn, _lib.moe_grouped_mm_dx(ctypes.byref(g), _need(fn, "dy", dy, bf, rows, n),
-                                      _need(fn, "counts", counts, torch.int32, E),
-                                      _need(fn, "w", w, bf, E, n, k),
-                                      _need(fn, "dx", dx, bf, rows, k),
-                                      _need_ws(fn, g, shape, ws), _s(stream)))
+    _check(fn, _lib.moe_grouped_mm_dx(ctypes.byref(g), _need(fn, dev, "dy", dy, bf, rows, n),
+                                      _need(fn, dev, "counts", counts, torch.int32, E),
+                                      _need(fn, dev, "w", w, bf, E, n, k),
+                                      _need(fn, dev, "dx", dx, bf, rows, k),
+                                      _need_ws(fn, dev, g, shape, ws), _stream(stream, dev)))
 
 
 def grouped_mm_dw(g: GroupCfg, dy, x, counts, dw, ws, accumulate=False, stream=None):
     """dw[e] = sum of dy[r]^T x[r] over group e's rows (accumulate: added to dw, fp32 only): the
     gradient of grouped_mm's weights. dw bf16 or fp32."""
-    fn, bf = "moe_grouped_mm_dw", torch.bfloat16
+    fn, bf, dev = "moe_grouped_mm_dw", torch.bfloat16, _device()
     rows, E, n, k = shape = g.rows, g.E, g.n, g.k
     f32 = isinstance(dw, torch.Tensor) and dw.dtype is torch.float32
-    _check(fn, _lib.moe_grouped_mm_dw(ctypes.byref(g), _need(fn, "dy", dy, bf, rows, n),
-                                      _need(fn, "x", x, bf, rows, k),
-                                      _need(fn, "counts", counts, torch.int32, E),
-                                      _need(fn, "dw", dw, torch.float32 if f32 else bf, E, n, k),
+    _check(fn, _lib.moe_grouped_mm_dw(ctypes.byref(g), _need(fn, dev, "dy", dy, bf, rows, n),
+                                      _need(fn, dev, "x", x, bf, rows, k),
+                                      _need(fn, dev, "counts", counts, torch.int32, E),
+                                      _need(fn, dev, "dw", dw, torch.float32 if f32 else bf,
+                                            E, n, k),
                                       MOE_F32 if f32 else MOE_BF16, 1 if accumulate else 0,
-                                      _need_ws(fn, g, shape, ws), _s(stream)))
+                                      _need_ws(fn, dev, g, shape, ws), _stream(stream, dev)))
 
 
 def _rows_cols(fn, name, t):
@@ -403,64 +428,67 @@ def _rows_cols(fn, name, t):
 def act_save(x, q, scales, stream=None):
     """Keeps bf16 rows x [rows][d] as e4m3 codes q (bytes [rows][d]) and fp32 scales
     [d/128][rows]."""
-    fn = "moe_act_save"
+    fn, dev = "moe_act_save", _device()
     rows, d = _rows_cols(fn, "x", x)
-    _check(fn, _lib.moe_act_save(rows, d, _need(fn, "x", x, torch.bfloat16, rows, d),
-                                 _need(fn, "q", q, torch.uint8, rows, d),
-                                 _need(fn, "scales", scales, torch.float32, d // 128, rows),
-                                 _s(stream)))
+    _check(fn, _lib.moe_act_save(rows, d, _need(fn, dev, "x", x, torch.bfloat16, rows, d),
+                                 _need(fn, dev, "q", q, torch.uint8, rows, d),
+                                 _need(fn, dev, "scales", scales, torch.float32, d // 128, rows),
+                                 _stream(stream, dev)))
 
 
 def act_load(q, scales, index, out, stream=None, status=None):
     """out[i] = the saved row index[i] in bf16 (index None: row i; -1: zeros)."""
-    fn = "moe_act_load"
+    fn, dev = "moe_act_load", _device()
     src, d = _rows_cols(fn, "q", q)
     rows = _rows_cols(fn, "out", out)[0]
-    _check(fn, _lib.moe_act_load(rows, src, d, _need(fn, "q", q, torch.uint8, src, d),
-                                 _need(fn, "scales", scales, torch.float32, d // 128, src),
+    _check(fn, _lib.moe_act_load(rows, src, d, _need(fn, dev, "q", q, torch.uint8, src, d),
+                                 _need(fn, dev, "scales", scales, torch.float32, d // 128, src),
                                  None if index is None else
-                                 _need(fn, "index", index, torch.int32, rows),
-                                 _need(fn, "out", out, torch.bfloat16, rows, d), _p(status),
-                                 _s(stream)))
+                                 _need(fn, dev, "index", index, torch.int32, rows),
+                                 _need(fn, dev, "out", out, torch.bfloat16, rows, d),
+                                 _here(fn, dev, "status", status), _stream(stream, dev)))
 
 
 def swiglu_save(gu, a, q, scales, stream=None):
     """a = silu(g) * u of gu = [g | u] [rows][2f], with gu kept as act_save keeps it."""
-    fn = "moe_swiglu_save"
+    fn, dev = "moe_swiglu_save", _device()
     rows, f2 = _rows_cols(fn, "gu", gu)
     f = f2 // 2
-    _check(fn, _lib.moe_swiglu_save(rows, f, _need(fn, "gu", gu, torch.bfloat16, rows, 2 * f),
-                                    _need(fn, "a", a, torch.bfloat16, rows, f),
-                                    _need(fn, "q", q, torch.uint8, rows, 2 * f),
-                                    _need(fn, "scales", scales, torch.float32, 2 * f // 128, rows),
-                                    _s(stream)))
+    _check(fn, _lib.moe_swiglu_save(rows, f, _need(fn, dev, "gu", gu, torch.bfloat16, rows, 2 * f),
+                                    _need(fn, dev, "a", a, torch.bfloat16, rows, f),
+                                    _need(fn, dev, "q", q, torch.uint8, rows, 2 * f),
+                                    _need(fn, dev, "scales", scales, torch.float32, 2 * f // 128,
+                                          rows),
+                                    _stream(stream, dev)))
 
 
 def swiglu_grad(q, scales, da, dgu, a=None, stream=None):
     """dgu [rows][2f], and a [rows][f] again (None: not wanted), from swiglu_save's codes."""
-    fn = "moe_swiglu_grad"
+    fn, dev = "moe_swiglu_grad", _device()
     rows, f = _rows_cols(fn, "da", da)
-    _check(fn, _lib.moe_swiglu_grad(rows, f, _need(fn, "q", q, torch.uint8, rows, 2 * f),
-                                    _need(fn, "scales", scales, torch.float32, 2 * f // 128, rows),
-                                    _need(fn, "da", da, torch.bfloat16, rows, f),
-                                    _need(fn, "dgu", dgu, torch.bfloat16, rows, 2 * f),
+    _check(fn, _lib.moe_swiglu_grad(rows, f, _need(fn, dev, "q", q, torch.uint8, rows, 2 * f),
+                                    _need(fn, dev, "scales", scales, torch.float32, 2 * f // 128,
+                                          rows),
+                                    _need(fn, dev, "da", da, torch.bfloat16, rows, f),
+                                    _need(fn, dev, "dgu", dgu, torch.bfloat16, rows, 2 * f),
                                     None if a is None else
-                                    _need(fn, "a", a, torch.bfloat16, rows, f), _s(stream)))
+                                    _need(fn, dev, "a", a, torch.bfloat16, rows, f),
+                                    _stream(stream, dev)))
 
 
 def combine_grad(ebuf, row_of, topk_w, dy, debuf, dtopk_w, stream=None, status=None):
     """The gradient of combine: debuf (rows of ebuf) and dtopk_w [T][k] from dy [T][d]."""
-    fn, bf = "moe_combine_grad", torch.bfloat16
+    fn, bf, dev = "moe_combine_grad", torch.bfloat16, _device()
     T, d = _rows_cols(fn, "dy", dy)
     k = _rows_cols(fn, "row_of", row_of)[1]
     rows = _rows_cols(fn, "ebuf", ebuf)[0]
-    _check(fn, _lib.moe_combine_grad(T, k, d, rows, _need(fn, "ebuf", ebuf, bf, rows, d),
-                                     _need(fn, "row_of", row_of, torch.int32, T, k),
-                                     _need(fn, "topk_w", topk_w, torch.float32, T, k),
-                                     _need(fn, "dy", dy, bf, T, d),
-                                     _need(fn, "debuf", debuf, bf, rows, d),
-                                     _need(fn, "dtopk_w", dtopk_w, torch.float32, T, k),
-                                     _p(status), _s(stream)))
+    _check(fn, _lib.moe_combine_grad(T, k, d, rows, _need(fn, dev, "ebuf", ebuf, bf, rows, d),
+                                     _need(fn, dev, "row_of", row_of, torch.int32, T, k),
+                                     _need(fn, dev, "topk_w", topk_w, torch.float32, T, k),
+                                     _need(fn, dev, "dy", dy, bf, T, d),
+                                     _need(fn, dev, "debuf", debuf, bf, rows, d),
+                                     _need(fn, dev, "dtopk_w", dtopk_w, torch.float32, T, k),
+                                     _here(fn, dev, "status", status), _stream(stream, dev)))
 
 
 def clear_status(ws, stream=None):

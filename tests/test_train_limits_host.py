@@ -100,3 +100,41 @@ def test_outputs_that_meet_an_input_are_refused(moe):
         refuses_overlap(lambda ebuf, row_of, topk_w, dy, debuf, dtopk_w: L.moe_combine_grad(
             T, k, d, rows, ebuf, row_of, topk_w, dy, debuf, dtopk_w, None, None),
             comb, out, ("topk_w",) if out == "dtopk_w" else ())
+
+
+class OnDevice(torch.Tensor):
+    """A tensor that says it lies on CUDA device `place`."""
+    place = 0
+    is_cuda = property(lambda self: True)
+
+    def get_device(self):
+        return self.place
+
+
+def test_tensors_of_another_device_are_refused(moe, monkeypatch):
+    """The kernels run on the current device: its streams, its memory."""
+    monkeypatch.setattr(moe, "_device", lambda: 0)
+    bf, i32, f32, u8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
+
+    def make(*shapes):
+        return [torch.zeros(s, dtype=t).as_subclass(OnDevice) for t, *s in shapes]
+    g = moe.GroupCfg(rows=16, E=4, n=64, k=128)
+    x, c, w, y, ws = make((bf, 16, 128), (i32, 4), (bf, 4, 64, 128), (bf, 16, 64), (u8, 1 << 20))
+    dw, = make((f32, 4, 64, 128))
+    r, q, s, i, o = make((bf, 16, 128), (u8, 16, 128), (f32, 1, 16), (i32, 8), (bf, 8, 128))
+    gu, q2, s2, a, dgu = make((bf, 16, 256), (u8, 16, 256), (f32, 2, 16), (bf, 16, 128),
+                              (bf, 16, 256))
+    ro, tw, dy, de, dt = make((i32, 8, 2), (f32, 8, 2), (bf, 8, 128), (bf, 16, 128), (f32, 8, 2))
+    st, = make((i32, 4))
+    calls = [(moe.grouped_mm, (g, x, c, w, y, ws)), (moe.grouped_mm_dx, (g, y, c, w, x, ws)),
+             (moe.grouped_mm_dw, (g, y, x, c, dw, ws)), (moe.act_save, (r, q, s)),
+             (lambda *t: moe.act_load(*t[:4], status=t[4]), (q, s, i, o, st)),
+             (moe.swiglu_save, (gu, a, q2, s2)), (moe.swiglu_grad, (q2, s2, a, dgu, r)),
+             (lambda *t: moe.combine_grad(*t[:6], status=t[6]), (r, ro, tw, dy, de, dt, st))]
+    for fn, args in calls:
+        for t in args:
+            if isinstance(t, torch.Tensor):
+                t.place = 1
+                with pytest.raises(ValueError, match="device"):
+                    fn(*args)
+                t.place = 0
