@@ -53,7 +53,8 @@ class MoETrainLayer:
     shared expert, ws13 and ws2, as MoELayer takes them. grad_dtype: torch.float32 (gradients
     may be summed over micro-batches, ``backward(dy, accumulate=True)``) or torch.bfloat16.
     Between forward and backward the layer keeps x once per token and the gate/up products in 8
-    bits, and the expert outputs (for dtopk_w) in bf16."""
+    bits, and the expert outputs (for dtopk_w) in bf16. backward writes over the latter two, so
+    it runs once for each forward: another one is a RuntimeError."""
 
     def __init__(self, cfg, w_gate, bias, weights: dict, device="cuda",
                  grad_dtype=torch.float32):
@@ -61,6 +62,7 @@ class MoETrainLayer:
         if mc.R != 1 or mc.act_dtype != MOE_BF16:
             raise ValueError("MoETrainLayer takes a bf16 configuration with R == 1")
         self.cfg, self.w_gate, self.bias, self.weights = cfg, w_gate, bias, weights
+        self._saved = False   # whether the buffers hold a forward's values
         T, k, d, E, f, fs = cfg.T, cfg.k, cfg.d, cfg.E, cfg.d_ff, cfg.d_ff_shared
         rows = T * k
         bf = dict(dtype=torch.bfloat16, device=device)
@@ -86,6 +88,7 @@ class MoETrainLayer:
 
     def forward(self, x, y=None, stream=None):
         b, w = self.bufs, self.weights
+        self._saved = False
         if y is None:
             y = torch.empty((self.cfg.T, self.cfg.d), dtype=torch.bfloat16, device=x.device)
         route(self.cfg, x, self.w_gate, self.bias, b["topk_idx"], b["topk_w"], b["ws"], stream)
@@ -98,11 +101,15 @@ class MoETrainLayer:
                                 b["shared_out"], stream)
         combine(self.cfg, b["ebuf"], b["row_of"], b["topk_w"], b["shared_out"], y, stream,
                 status=b["ws"])
+        self._saved = True
         return y
 
     def backward(self, dy, accumulate=False, stream=None):
         """Gradients for the last forward: dx and dtopk_w (replaced), dw13, dw2 and the shared
-        expert's dws13, dws2 (accumulate: added to)."""
+        expert's dws13, dws2 (accumulate: added to). Once for each forward."""
+        if not self._saved:
+            raise RuntimeError("MoETrainLayer.backward: needs a forward of its own")
+        self._saved = False
         b, w, g = self.bufs, self.weights, self.grads
         counts = b["counts"].view(-1)
         de = self.drows
