@@ -109,8 +109,10 @@ class MoETrainLayer:
         expert's dws13, dws2 (accumulate: added to). Once for each forward."""
         if not self._saved:
             raise RuntimeError("MoETrainLayer.backward: needs a forward of its own")
-        self._saved = False
         b, w, g = self.bufs, self.weights, self.grads
+        if accumulate and g["dw13"].dtype is not torch.float32:
+            raise ValueError("MoETrainLayer.backward: accumulate needs grad_dtype torch.float32")
+        self._saved = False
         counts = b["counts"].view(-1)
         de = self.drows
         combine_grad(b["ebuf"], b["row_of"], b["topk_w"], dy, de, g["dtopk_w"], stream=stream,

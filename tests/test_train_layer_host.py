@@ -44,3 +44,14 @@ def test_one_backward_a_forward(layer):
         with pytest.raises(RuntimeError, match="forward"):
             lay.backward(layer.x, accumulate=True)
         assert len(calls) == done
+
+
+def test_sums_need_fp32_gradients(layer):
+    """Refused before the first call, so that the forward's values are still there."""
+    lay, calls = layer(grad_dtype=torch.bfloat16)
+    lay.forward(layer.x)
+    done = len(calls)
+    with pytest.raises(ValueError, match="float32"):
+        lay.backward(layer.x, accumulate=True)
+    assert len(calls) == done
+    lay.backward(layer.x)
