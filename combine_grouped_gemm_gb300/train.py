@@ -51,7 +51,8 @@ class MoETrainLayer:
 
     cfg: a bf16 configuration with R = 1 (expert-contiguous rows). weights: w13, w2 and, with a
     shared expert, ws13 and ws2, as MoELayer takes them. grad_dtype: torch.float32 (gradients
-    may be summed over micro-batches, ``backward(dy, accumulate=True)``) or torch.bfloat16.
+    may be summed over micro-batches, ``backward(dy, accumulate=True)``; they start at zero) or
+    torch.bfloat16.
     Between forward and backward the layer keeps x once per token and the gate/up products in 8
     bits, and the expert outputs (for dtopk_w) in bf16. backward writes over the latter two, so
     it runs once for each forward: another one is a RuntimeError."""
@@ -76,15 +77,15 @@ class MoETrainLayer:
         g = dict(dtype=grad_dtype, device=device)
         self.grads = dict(dx=torch.empty((T, d), **bf),
                           dtopk_w=torch.empty((T, k), dtype=torch.float32, device=device),
-                          dw13=torch.empty((E, 2 * f, d), **g), dw2=torch.empty((E, d, f), **g))
+                          dw13=torch.zeros((E, 2 * f, d), **g), dw2=torch.zeros((E, d, f), **g))
         self.shared = None
         if fs:
             self.shared = _Experts(T, 1, d, fs, device)
             self.all_rows = torch.full((1,), T, dtype=torch.int32, device=device)
             self.xs = torch.empty((T, d), **bf)
             self.dxs = torch.empty((T, d), **bf)
-            self.grads.update(dws13=torch.empty((1, 2 * fs, d), **g),
-                              dws2=torch.empty((1, d, fs), **g))
+            self.grads.update(dws13=torch.zeros((1, 2 * fs, d), **g),
+                              dws2=torch.zeros((1, d, fs), **g))
 
     def forward(self, x, y=None, stream=None):
         b, w = self.bufs, self.weights

@@ -55,3 +55,13 @@ def test_sums_need_fp32_gradients(layer):
         lay.backward(layer.x, accumulate=True)
     assert len(calls) == done
     lay.backward(layer.x)
+
+
+def test_gradients_start_at_zero(layer, monkeypatch):
+    """So that every micro-batch, the first one too, may be added. (The layer's memory comes filled
+    with 7s here, as any bytes may.)"""
+    empty = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: empty(*a, **k).fill_(7))
+    lay, _ = layer()
+    for n in ("dw13", "dw2", "dws13", "dws2"):
+        assert not bool(lay.grads[n].any()), n
