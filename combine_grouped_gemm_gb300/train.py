@@ -89,9 +89,13 @@ class MoETrainLayer:
 
     def forward(self, x, y=None, stream=None):
         b, w = self.bufs, self.weights
+        shape = (self.cfg.T, self.cfg.d)
+        for name, t in (("x", x), ("y", x if y is None else y)):
+            if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.shape != shape:
+                raise ValueError(f"MoETrainLayer.forward: {name} must be a bf16 tensor {shape}")
         self._saved = False
         if y is None:
-            y = torch.empty((self.cfg.T, self.cfg.d), dtype=torch.bfloat16, device=x.device)
+            y = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
         route(self.cfg, x, self.w_gate, self.bias, b["topk_idx"], b["topk_w"], b["ws"], stream)
         dispatch(self.cfg, x, b["topk_idx"], b["recv"], None, b["counts"], b["row_of"],
                  self.src_tok, stream, status=b["ws"])

@@ -65,3 +65,16 @@ def test_gradients_start_at_zero(layer, monkeypatch):
     lay, _ = layer()
     for n in ("dw13", "dw2", "dws13", "dws2"):
         assert not bool(lay.grads[n].any()), n
+
+
+def test_rows_of_another_size_are_refused(layer):
+    """The router and the combine read and write T rows of d whatever they are given."""
+    lay, calls = layer()
+    x = layer.x
+    for bad in (x[:-1], x[:, :-8], x.float(), None):
+        with pytest.raises(ValueError, match="x must be"):
+            lay.forward(bad)
+        if bad is not None:
+            with pytest.raises(ValueError, match="y must be"):
+                lay.forward(x, bad)
+    assert not calls
