@@ -684,21 +684,6 @@ bool make_tensor_map_2d(CUtensorMap* m, const void* base, int elem_bytes, uint64
   return r == CUDA_SUCCESS;
 }
 
-bool make_tensor_map_3d_bf16(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows,
-                             uint64_t depth, uint32_t box_rows) {
-  EncodeTiledFn fn = encode_fn();
-  if (!fn) return false;
-  const cuuint64_t dims[3] = {cols, rows, depth};
-  const cuuint64_t strides[2] = {cols * 2, rows * cols * 2};
-  const cuuint32_t box[3] = {64, box_rows, 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
-                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS;
-}
-
 cudaError_t ensure_smem_limit(const void* kern, size_t bytes) {
   if (bytes <= 48 * 1024) return cudaSuccess;
   int dev = 0;

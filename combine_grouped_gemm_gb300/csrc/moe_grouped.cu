@@ -44,7 +44,7 @@
 // below that rate: 32 groups of about 512 rows 588 us, unevenly loaded ones 317 us (7168 x 2048).
 // Few rows a group: HBM, 64 tokens through 256 experts 1.83 ms (7.2 TB/s of weights). Weight
 // gradients of few rows a group: the stores, fp32 of 4096 rows 578 us (6.7 TB/s).
-#include "moe_device.cuh"
+#include "moe_pair.cuh"
 
 namespace moe {
 namespace {
@@ -889,6 +889,23 @@ GroupedWs grouped_ws(const moe_group_cfg& c) {
   }
   w.total = w.parts + sizeof(float) * floats + 128;   // (128: ws is 16-byte aligned only)
   return w;
+}
+
+// 3-D bf16 tensor map [depth][rows][cols], box of one plane, box_rows x 64 columns, 128-byte
+// swizzle. What a box reads outside its own plane's rows and columns is zero.
+bool make_tensor_map_3d_bf16(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows,
+                             uint64_t depth, uint32_t box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {cols, rows, depth};
+  const cuuint64_t strides[2] = {cols * 2, rows * cols * 2};
+  const cuuint32_t box[3] = {64, box_rows, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
+                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
 }
 
 template <int DIR>

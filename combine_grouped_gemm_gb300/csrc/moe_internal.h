@@ -208,10 +208,12 @@ cudaError_t launch_combine_grad(int T, int k, int d, int rows, const void* ebuf,
 bool make_tensor_map_2d(CUtensorMap* m, const void* base, int elem_bytes, uint64_t cols,
                         uint64_t rows, uint32_t box_rows);
 
-// 3-D bf16 tensor map [depth][rows][cols], box of one plane, box_rows x 64 columns, 128-byte
-// swizzle. What a box reads outside its own plane's rows and columns is zero.
-bool make_tensor_map_3d_bf16(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows,
-                             uint64_t depth, uint32_t box_rows);
+// The driver's tensor-map encoder, or NULL where it has none (moe_ffn.cu).
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn();
 
 // Streaming multiprocessors of the current device.
 int sm_count();
