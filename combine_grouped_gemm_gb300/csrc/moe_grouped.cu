@@ -37,13 +37,17 @@
 // others the epilogue. Loads of both CTAs count on the leader's full barriers, its commits free the
 // stages of both. Accumulators are double buffered. Every wait is bounded.
 //
-// What bounds it. Full tiles keep the tensor pipe busy for 512 of 523 cycles a k-step (clock
-// counters in the MMA thread): 8 groups of 2048 rows, 4096 x 7168, 488 us forward (1.97 PFLOP/s),
-// and in long runs the power cap sets the clock. A k-step brings 32 KB into each SM, 64 bytes a
-// cycle, which is why narrower tiles (a group's rows spread over its tiles, 160 to 256 each) fall
-// below that rate: 32 groups of about 512 rows 588 us, unevenly loaded ones 317 us (7168 x 2048).
-// Few rows a group: HBM, 64 tokens through 256 experts 1.83 ms (7.2 TB/s of weights). Weight
-// gradients of few rows a group: the stores, fp32 of 4096 rows 578 us (6.7 TB/s).
+// What bounds it. (us of ten calls after a pause, then of calls for a second or more, where the
+// power cap sets the clock.) Full tiles keep the tensor pipe busy for 512 of 523 cycles a k-step
+// (clock counters in the MMA thread): 8 groups of 2048 rows, 4096 x 7168, forward 500 (1.92
+// PFLOP/s) and 579. A k-step brings 32 KB into each SM, 64 bytes a cycle, which is why narrower
+// tiles (a group's rows spread over its tiles, 160 to 256 each) fall below that rate: 32 groups of
+// 512 rows 543 and 630, of about 512 rows 582 and 687; row gradient of unevenly loaded ones,
+// 7168 x 2048, 319 and 362; their bf16 weight gradient 318 and 366. Few rows a group: HBM, 64
+// tokens through 256 experts 1840 (7.2 TB/s of weights). fp32 weight gradients of few rows a group:
+// the stores, 4096 rows 577 (6.7 TB/s). Added to what is there 1612 (4.7 TB/s both ways): 64 sums
+// and 16 old values a thread are more than its 96 registers hold, and the old values are asked for
+// 16 at a time.
 #include "moe_pair.cuh"
 
 namespace moe {
@@ -154,6 +158,9 @@ constexpr int kSumSteps = 8;
 // Together they store whole 128-byte lines: the store path takes about one segment every four
 // cycles, of 64 bytes or of 128.
 constexpr int kTurnPitch = 144, kTurnBytes = 32 * kTurnPitch;
+
+// (Results in bf16, and the row products, keep one tensor-core sum: at 1.1e-9 of the result a product
+// its error reaches their own rounding after some two million.)
 
 // Units on their way from the scheduler to the roles. A role frees its slot once it has read it:
 // one slot ahead of the producer, which is itself a unit or two ahead of the epilogue.
@@ -851,11 +858,12 @@ GroupedPlan grouped_plan(const moe_group_cfg& c, GroupedDir dir) {
   } else {
     // ceil(c / tn) tiles of a group of c rows are at most (c - 1) / tn + 1
     auto units = [&](int tn) { return ((c.rows - live) / tn + live) * mt; };
-    // Tiles of 128 rows up to that mean (64 groups, 2048 x 2048: of 100 rows 91 us, with tiles of
-    // 256 95 us; of 200 rows 117 and 108 us); of 64 for a few rows, whose smaller stages leave room
-    // for more weights in flight (4096 x 7168: 8 groups of a row 76 us, with 128 85 us; 32 uneven
-    // groups of 25 rows on average 288 and 280 us), and while they leave half of the pairs idle
-    // (one group of 512 rows, 4096 x 7168: 31 us, with 256 34 us).
+    // The mean is over all groups, of which the host knows no more: one crowded group among many
+    // small ones takes their tile. Tiles of 128 rows up to that mean (64 groups, 2048 x 2048: of
+    // 100 rows 90 us, with tiles of 256 95 us; of 200 rows 117 and 107 us); of 64 for a few rows,
+    // whose smaller stages leave room for more weights in flight (4096 x 7168: 8 groups of a row 76
+    // us, with 128 85 us; 32 uneven groups of 25 rows on average 288 and 279 us), and while they
+    // leave half of the pairs idle (one group of 512 rows, 4096 x 7168: 29 us, with 256 34 us).
     const long long mean = live ? (c.rows + live - 1) / live : 0;
     p.tn = mean <= 16 ? 64 : mean <= 128 ? 128 : 256;
     while (p.tn > 64 && units(p.tn) < kPairs / 2) p.tn /= 2;
@@ -866,7 +874,9 @@ GroupedPlan grouped_plan(const moe_group_cfg& c, GroupedDir dir) {
   if (splits > steps / kMinSteps) splits = steps / kMinSteps;
   // A part saves the k-steps of the others, about a quarter of a microsecond each, and the second
   // kernel takes about four: split from 24 saved steps on. Weight gradient, 512 x 512: 30000 rows
-  // 134 us unsplit and 37 split, 2000 rows 20 and 17; forward of 64 rows, 4096 x 7168: 29 and 19.
+  // 134 us unsplit and 37 split, 2000 rows 20 and 17; forward of 64 rows, 4096 x 7168: 29 and 18.
+  // A weight gradient's groups all count as units, whatever their rows: the 30000 rows in one of 9
+  // groups take 76 us, in one of 10 or more, unsplit, 133 to 139.
   if (splits > 1 && steps - steps / splits < 24) splits = 1;
   p.splits = splits > 1 ? static_cast<int>(splits) : 1;
   return p;

@@ -118,7 +118,7 @@ __device__ __forceinline__ uint2 codes_of8(const float (&f)[8], float scale) {
 
 // What these kernels measured (whole calls replayed from a graph, copy rate 6.7 TB/s): swiglu_save
 // of 16384 rows of 2048 45 us (6.0 TB/s, instruction issue 79 % busy), its gradient 50 us (6.7
-// TB/s), 2048 rows of 7168 saved and loaded 8-fold 46 us (6.4 TB/s); 8 rows about 2 us, a launch.
+// TB/s), 2048 rows of 7168 saved and loaded 8-fold 44 us (6.7 TB/s); 8 rows about 2 us, a launch.
 //
 // The kernels that read or write scales take tiles of 16 rows x 128 columns a CTA: a half-warp is
 // one row's block (8 columns a lane), so a CTA's scales are 16 consecutive floats. CTA c: column

@@ -390,7 +390,7 @@ int moe_grouped_query(const moe_group_cfg* cfg, size_t* ws_bytes);
  * dw_dtype: MOE_BF16 or MOE_F32. accumulate (MOE_F32 only, else MOE_ERR_INVALID_ARG): dW_e is
  * added to dw instead of replacing it. An empty group's dW_e is 0. The results do not depend on
  * the order in which the GPU runs the work (no floating-point atomics). With rows == 0 the row
- * tensors may be NULL. */
+ * tensors may be NULL, and counts are not read. */
 #define MOE_F32 3 /* dw_dtype only */
 int moe_grouped_mm(const moe_group_cfg* cfg, const void* x, const int32_t* counts, const void* w,
                    void* y, void* ws, cudaStream_t stream);
@@ -432,7 +432,8 @@ int moe_swiglu_grad(int32_t rows, int32_t f, const void* q, const float* scales,
 /* Gradient of moe_combine. dy bf16 [T][d]; row_of int32 [T][k] and topk_w fp32 [T][k] as given to
  * the combine; ebuf bf16 [rows][d] its expert rows:
  *   debuf[row_of[t][i]] = bf16(topk_w[t][i] * dy[t]);  dtopk_w[t][i] = dy[t] . ebuf[row_of[t][i]]
- * (summed in fp32 in a fixed order). Rows of debuf that no choice names are not written. A
+ * (summed in fp32 in a fixed order). No two choices may name one row (the dispatch gives each its
+ * own). Rows of debuf that no choice names are not written. A
  * negative row_of is a choice that the dispatch skipped: its dtopk_w is 0. One at or past rows is
  * treated so too and reported (MOE_DEV_BOUNDS in status, NULL or a device uint32). The shared
  * expert's rows have dy itself as gradient. d % 128 == 0, 1 <= k <= 32, T * k < 2^31. */
