@@ -283,8 +283,12 @@ def _framework(s):
     if op == "norm_in":
         moe.norm_in(s["x"], s["w"], s["n"], s["rstd"], eps=_EPS)
         return s["n"], s["rstd"]
+    gate, dgate = s.get("gate"), s.get("dgate")
+    if c.get("gate") == "token":   # [rows][1]: one factor a row, whatever the width
+        gate = gate.view(-1, 1)
+        dgate = None if dgate is None else dgate.view(-1, 1)
     if op == "norm_out":
-        moe.norm_out(s["y"], s["x"], s["w_post"], s["gate"], s["w_next"], s["h"], s["n"],
+        moe.norm_out(s["y"], s["x"], s["w_post"], gate, s["w_next"], s["h"], s["n"],
                      s["rstd_y"], s["rstd_h"], eps=_EPS, res_scale=s["res_scale"],
                      out_scale=s["out_scale"])
         return [t for t in (s["h"], s["n"], s["rstd_y"], s["rstd_h"]) if t is not None]
@@ -296,8 +300,8 @@ def _framework(s):
             moe.norm_in_grad(s["dn"], s["x"], s["w"], s["rstd"], s["dres"], s["dx"], s["dw"],
                              s["ws"])
             return s["dx"], s["dw"]
-        moe.norm_out_grad(s["dh"], s["dn"], s["y"], s["h"], s["w_post"], s["gate"], s["w_next"],
-                          s["rstd_y"], s["rstd_h"], s["dx"], s["dy"], s["dgate"], s["dw_post"],
+        moe.norm_out_grad(s["dh"], s["dn"], s["y"], s["h"], s["w_post"], gate, s["w_next"],
+                          s["rstd_y"], s["rstd_h"], s["dx"], s["dy"], dgate, s["dw_post"],
                           s["dw_next"], s["ws"], res_scale=s["res_scale"],
                           out_scale=s["out_scale"])
         return [t for t in (s["dx"], s["dy"], s["dgate"], s["dw_post"], s["dw_next"])
