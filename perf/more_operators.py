@@ -452,8 +452,21 @@ def _round_e4m3(q, r16):
     return torch.where(small, y - 2.0 ** -6, y)
 
 
-def _plain_hold(x, r16, positive):
-    """A moment x [n] in 8 bits: codes and scales. positive: a value above 0 keeps a code above 0."""
+def _round_root_e4m3(q, r16):
+    """The same for the root of a second moment, with odds that keep the mean of its square:
+    (q^2 - lo^2) / (hi^2 - lo^2) between the neighbours lo and hi."""
+    small = q < 2.0 ** -6
+    y = torch.where(small, q + 2.0 ** -6, q)
+    bits = y.view(torch.int32) & ~0xFFFFF
+    shift = torch.where(small, torch.full_like(q, 2.0 ** -6), torch.zeros_like(q))
+    lo, hi = bits.view(torch.float32) - shift, (bits + 0x100000).view(torch.float32) - shift
+    up = r16.float() * ((hi - lo) * (hi + lo)) < (q - lo) * (q + lo) * 65536.0
+    return torch.where(up, hi, lo)
+
+
+def _plain_hold(x, r16, root):
+    """A moment x [n] in 8 bits: codes and scales. root: x is the root of the second one, which
+    keeps a code above 0 where it is above 0."""
     n = x.numel()
     b = _blocks(x)
     mag = b.abs()
@@ -461,8 +474,8 @@ def _plain_hold(x, r16, positive):
     scale = torch.where(amax > 0, amax / _E4M3_MAX, torch.ones_like(amax))
     q = mag / scale
     q = torch.where(q > _E4M3_MAX, torch.full_like(q, _E4M3_MAX), q)
-    q = _round_e4m3(q, r16)
-    if positive:
+    q = _round_root_e4m3(q, r16) if root else _round_e4m3(q, r16)
+    if root:
         q = torch.where((b > 0) & (q < 2.0 ** -9), torch.full_like(q, 2.0 ** -9), q)
     code = torch.copysign(q, b).to(torch.float8_e4m3fn).view(torch.uint8)
     return code.flatten()[:n], scale.flatten()
