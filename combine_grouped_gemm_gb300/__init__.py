@@ -17,8 +17,10 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libmoe.so")
 
 MOE_BF16, MOE_FP8_E4M3, MOE_FP8_E4M3_POW2 = 0, 1, 2
-MOE_F32 = 3   # dtype of a weight gradient only
-MOE_DEV_TIMEOUT, MOE_DEV_BOUNDS, MOE_DEV_SCALE = 1, 2, 4
+MOE_F32 = 3   # dtype of a weight gradient, the norms' residual stream or an optimiser's gradient
+MOE_DEV_TIMEOUT, MOE_DEV_BOUNDS, MOE_DEV_SCALE, MOE_DEV_NONFINITE = 1, 2, 4, 8
+MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_TOKEN, MOE_GATE_ELEMENT = 0, 1, 2, 3
+MOE_ADAM_TENSORS = 256   # tensors of one moe_adamw or moe_grad_norm call
 MOE_LAYER_EVENTS = 7
 STAGE_NAMES = ["route", "dispatch", "ffn_setup", "ffn_gate_up", "ffn_down", "combine"]
 
@@ -66,6 +68,27 @@ class GroupCfg(ctypes.Structure):
                 ("k", ctypes.c_int32)]
 
 
+class NormCfg(ctypes.Structure):
+    """moe_norm_cfg: rows, width, scales and types of the norms around a block."""
+    _fields_ = [("rows", ctypes.c_int32), ("d", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("res_scale", ctypes.c_float), ("out_scale", ctypes.c_float),
+                ("stream_dtype", ctypes.c_int32), ("gate", ctypes.c_int32)]
+
+
+class AdamTensorC(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("p", "g", "w", "m", "v", "m_scale", "v_scale")] + [
+        ("n", ctypes.c_int64), ("weight_decay", ctypes.c_float), ("seed", ctypes.c_uint32),
+        ("g_dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class AdamCfg(ctypes.Structure):
+    """moe_adam_cfg: an AdamW step's rates. state_bits is set from the tensors' plan."""
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("max_norm", ctypes.c_double),
+                ("lr_dev", ctypes.c_void_p), ("state_bits", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
 class Weights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in
                 ("w13", "w13_scales", "w2", "w2_scales", "ws13", "ws13_scales", "ws2",
@@ -101,6 +124,17 @@ def _load():
         "moe_swiglu_save": [I, I, P, P, P, P, S],
         "moe_swiglu_grad": [I, I, P, P, P, P, P, S],
         "moe_combine_grad": [I, I, I, I, P, P, P, P, P, P, P, S],
+        "moe_norm_query": [I, I, P],
+        "moe_norm_in": [P, P, P, P, P, S],
+        "moe_norm_in_grad": [P, P, P, P, P, P, P, P, I, P, S],
+        "moe_norm_out": [P, P, P, P, P, P, P, P, P, P, S],
+        "moe_norm_out_grad": [P] * 15 + [I, P, S],
+        "moe_route_save": [P, P, P, P, P, P, P, P, S],
+        "moe_route_grad": [P, P, P, P, P, P, P, P, P, I, P, S],
+        "moe_route_grad_query": [P, P],
+        "moe_adamw": [P, P, I, I, P, P, S],
+        "moe_grad_norm": [P, I, I, P, P, S],
+        "moe_adam_query": [P],
         "moe_clear_status": [P, S],
         "moe_read_status": [P, P, S],
         "moe_selftest_wait": [P, ctypes.c_int64, S],
@@ -122,7 +156,10 @@ EXPORTED = ["moe_validate", "moe_query_sizes", "moe_route", "moe_route_noalloc",
             "moe_expert_ffn_gather", "moe_place_experts", "moe_query_sizes_placed",
             "moe_grouped_query", "moe_grouped_mm", "moe_grouped_mm_dx", "moe_grouped_mm_dw",
             "moe_act_save", "moe_act_load", "moe_swiglu_save", "moe_swiglu_grad",
-            "moe_combine_grad", "moe_clear_status", "moe_read_status", "moe_selftest_wait",
+            "moe_combine_grad", "moe_norm_query", "moe_norm_in", "moe_norm_in_grad",
+            "moe_norm_out", "moe_norm_out_grad", "moe_route_save", "moe_route_grad",
+            "moe_route_grad_query", "moe_adamw", "moe_grad_norm", "moe_adam_query",
+            "moe_clear_status", "moe_read_status", "moe_selftest_wait",
             "moe_strerror", "moe_abi_version", "moe_last_cuda_error"]
 
 
@@ -489,6 +526,277 @@ def combine_grad(ebuf, row_of, topk_w, dy, debuf, dtopk_w, stream=None, status=N
                                      _need(fn, dev, "debuf", debuf, bf, rows, d),
                                      _need(fn, dev, "dtopk_w", dtopk_w, torch.float32, T, k),
                                      _here(fn, dev, "status", status), _stream(stream, dev)))
+
+
+# ---------------------------------------------------------------------------------------------
+# The rest of a training step of an MoE block (see include/moe.h): the norms around the layer, the
+# router's gradient and the optimiser. Sizes come from the tensors, checked as above.
+# ---------------------------------------------------------------------------------------------
+def _stream_type(fn, name, t):
+    if not isinstance(t, torch.Tensor) or t.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{fn}: {name} must be a bf16 or fp32 CUDA tensor")
+    return t.dtype
+
+
+def _norm_cfg(rows, d, st, eps=0.0, res=1.0, out=1.0, gate=MOE_GATE_NONE):
+    return ctypes.byref(NormCfg(rows, d, eps, res, out,
+                                MOE_F32 if st is torch.float32 else MOE_BF16, gate))
+
+
+def _gate_of(fn, gate, rows, d):
+    """The kind of a gate, from its type and shape, and that type and shape. fp32 [d] is a channel
+    gate where rows == d: a token gate is then fp32 [rows][1]."""
+    if gate is None:
+        return MOE_GATE_NONE, None, ()
+    if isinstance(gate, torch.Tensor):
+        shape, f32 = tuple(gate.shape), gate.dtype is torch.float32
+        if f32 and shape == (d,):
+            return MOE_GATE_CHANNEL, torch.float32, shape
+        if f32 and shape in ((rows,), (rows, 1)):
+            return MOE_GATE_TOKEN, torch.float32, shape
+        if gate.dtype is torch.bfloat16 and shape == (rows, d):
+            return MOE_GATE_ELEMENT, torch.bfloat16, shape
+    raise ValueError(f"{fn}: gate must be fp32 [d], fp32 [rows] or bf16 [rows][d]")
+
+
+def _opt(fn, dev, name, t, dtype, *shape):
+    return None if t is None else _need(fn, dev, name, t, dtype, *shape)
+
+
+def norm_ws_bytes(rows, d) -> int:
+    """Bytes of the norm gradients' scratch for rows of width d."""
+    n = ctypes.c_size_t(0)
+    _check("moe_norm_query", _lib.moe_norm_query(int(rows), int(d), ctypes.byref(n)))
+    return n.value
+
+
+_norm_need = {}   # (rows, d) -> bytes
+
+
+def _norm_ws(fn, dev, rows, d, ws):
+    need = _norm_need.get((rows, d))
+    if need is None:
+        need = _norm_need[rows, d] = norm_ws_bytes(rows, d)
+    if not isinstance(ws, torch.Tensor) or ws.nbytes < need:
+        raise ValueError(f"{fn}: ws must be a CUDA tensor of norm_ws_bytes(rows, d) bytes")
+    return _here(fn, dev, "ws", ws)
+
+
+def norm_in(x, w, n, rstd=None, eps=1e-6, stream=None):
+    """n = bf16(x r w), r = 1/sqrt(mean x^2 + eps) of each row (kept in rstd if given). x bf16 or
+    fp32 [rows][d], w fp32 [d], n bf16."""
+    fn, dev, f32 = "moe_norm_in", _device(), torch.float32
+    rows, d = _rows_cols(fn, "x", x)
+    st = _stream_type(fn, "x", x)
+    _check(fn, _lib.moe_norm_in(_norm_cfg(rows, d, st, eps), _need(fn, dev, "x", x, st, rows, d),
+                                _need(fn, dev, "w", w, f32, d),
+                                _need(fn, dev, "n", n, torch.bfloat16, rows, d),
+                                _opt(fn, dev, "rstd", rstd, f32, rows), _stream(stream, dev)))
+
+
+def norm_in_grad(dn, x, w, rstd, dres, dx, dw, ws, accumulate=False, stream=None):
+    """dx = dres + the gradient of norm_in's rows (dres None: without it), dw (None: not wanted;
+    accumulate: added to) that of its weight."""
+    fn, dev, f32 = "moe_norm_in_grad", _device(), torch.float32
+    rows, d = _rows_cols(fn, "x", x)
+    st = _stream_type(fn, "x", x)
+    _check(fn, _lib.moe_norm_in_grad(
+        _norm_cfg(rows, d, st), _need(fn, dev, "dn", dn, torch.bfloat16, rows, d),
+        _need(fn, dev, "x", x, st, rows, d), _need(fn, dev, "w", w, f32, d),
+        _need(fn, dev, "rstd", rstd, f32, rows), _opt(fn, dev, "dres", dres, st, rows, d),
+        _need(fn, dev, "dx", dx, st, rows, d), _opt(fn, dev, "dw", dw, f32, d),
+        1 if accumulate else 0, _norm_ws(fn, dev, rows, d, ws), _stream(stream, dev)))
+
+
+def norm_out(y, x, w_post, gate, w_next, h, n, rstd_y=None, rstd_h=None, eps=1e-6, res_scale=1.0,
+             out_scale=1.0, stream=None):
+    """h = res_scale x + out_scale gate s, s the norm of y with weight w_post (None: y itself), and
+    n the norm of h with weight w_next (None: no n). gate: None, fp32 [d], fp32 [rows] or bf16
+    [rows][d]. x, h bf16 or fp32 [rows][d]."""
+    fn, dev, f32, bf = "moe_norm_out", _device(), torch.float32, torch.bfloat16
+    rows, d = _rows_cols(fn, "y", y)
+    st = _stream_type(fn, "x", x)
+    kind, gt, gs = _gate_of(fn, gate, rows, d)
+    _check(fn, _lib.moe_norm_out(
+        _norm_cfg(rows, d, st, eps, res_scale, out_scale, kind),
+        _need(fn, dev, "y", y, bf, rows, d), _need(fn, dev, "x", x, st, rows, d),
+        _opt(fn, dev, "w_post", w_post, f32, d), _opt(fn, dev, "gate", gate, gt, *gs),
+        _opt(fn, dev, "w_next", w_next, f32, d), _need(fn, dev, "h", h, st, rows, d),
+        _opt(fn, dev, "n", n, bf, rows, d), _opt(fn, dev, "rstd_y", rstd_y, f32, rows),
+        _opt(fn, dev, "rstd_h", rstd_h, f32, rows), _stream(stream, dev)))
+
+
+def norm_out_grad(dh, dn, y, h, w_post, gate, w_next, rstd_y, rstd_h, dx, dy, dgate, dw_post,
+                  dw_next, ws, res_scale=1.0, out_scale=1.0, accumulate=False, stream=None):
+    """The gradient of norm_out from dh (None: none) and dn: dy, and dx, dgate, dw_post, dw_next
+    (None: not wanted). y, h, rstd_y, rstd_h, dn: None where norm_out's form does not need them."""
+    fn, dev, f32, bf = "moe_norm_out_grad", _device(), torch.float32, torch.bfloat16
+    rows, d = _rows_cols(fn, "dy", dy)
+    st = next((_stream_type(fn, name, t) for name, t in (("dh", dh), ("h", h), ("dx", dx))
+               if t is not None), bf)
+    kind, gt, gs = _gate_of(fn, gate, rows, d)
+    _check(fn, _lib.moe_norm_out_grad(
+        _norm_cfg(rows, d, st, 0.0, res_scale, out_scale, kind),
+        _opt(fn, dev, "dh", dh, st, rows, d), _opt(fn, dev, "dn", dn, bf, rows, d),
+        _opt(fn, dev, "y", y, bf, rows, d), _opt(fn, dev, "h", h, st, rows, d),
+        _opt(fn, dev, "w_post", w_post, f32, d), _opt(fn, dev, "gate", gate, gt, *gs),
+        _opt(fn, dev, "w_next", w_next, f32, d), _opt(fn, dev, "rstd_y", rstd_y, f32, rows),
+        _opt(fn, dev, "rstd_h", rstd_h, f32, rows), _opt(fn, dev, "dx", dx, st, rows, d),
+        _need(fn, dev, "dy", dy, bf, rows, d), _opt(fn, dev, "dgate", dgate, gt, *gs),
+        _opt(fn, dev, "dw_post", dw_post, f32, d), _opt(fn, dev, "dw_next", dw_next, f32, d),
+        1 if accumulate else 0, _norm_ws(fn, dev, rows, d, ws), _stream(stream, dev)))
+
+
+def route_save(cfg, x, w_gate, bias, topk_idx, topk_w, topk_s, ws, stream=None):
+    """route that also keeps the chosen experts' sigmoid scores topk_s [T][k] for route_grad."""
+    fn, dev, c = "moe_route_save", _device(), make_cfg(cfg)
+    f32 = torch.float32
+    _check(fn, _lib.moe_route_save(
+        ctypes.byref(c), _need(fn, dev, "x", x, torch.bfloat16, c.T, c.d),
+        _need(fn, dev, "w_gate", w_gate, f32, c.E, c.d), _need(fn, dev, "bias", bias, f32, c.E),
+        _need(fn, dev, "topk_idx", topk_idx, torch.int32, c.T, c.k),
+        _need(fn, dev, "topk_w", topk_w, f32, c.T, c.k),
+        _need(fn, dev, "topk_s", topk_s, f32, c.T, c.k), _here(fn, dev, "ws", ws),
+        _stream(stream, dev)))
+
+
+def route_grad_ws_bytes(cfg) -> int:
+    """Bytes of route_grad's workspace; zero its first word once before its first use."""
+    n = ctypes.c_size_t(0)
+    c = cfg if isinstance(cfg, Cfg) else make_cfg(cfg)
+    _check("moe_route_grad_query", _lib.moe_route_grad_query(ctypes.byref(c), ctypes.byref(n)))
+    return n.value
+
+
+_route_need = {}   # (T, E, k, d) -> bytes
+
+
+def route_grad(cfg, x, w_gate, topk_idx, topk_s, dtopk_w, dx_in, dx, dw_gate, ws,
+               accumulate=False, stream=None):
+    """The router's gradient from that of its weights: dx = dx_in (None: 0) + the tokens' part,
+    dw_gate fp32 [E][d] (accumulate: added to)."""
+    fn, dev = "moe_route_grad", _device()
+    c = cfg if isinstance(cfg, Cfg) else make_cfg(cfg)
+    T, d, E, k = c.T, c.d, c.E, c.k
+    f32, bf = torch.float32, torch.bfloat16
+    need = _route_need.get((T, E, k, d))
+    if need is None:
+        need = _route_need[T, E, k, d] = route_grad_ws_bytes(c)
+    if not isinstance(ws, torch.Tensor) or ws.nbytes < need:
+        raise ValueError(f"{fn}: ws must be a CUDA tensor of route_grad_ws_bytes(cfg) bytes")
+    _check(fn, _lib.moe_route_grad(
+        ctypes.byref(c), _need(fn, dev, "x", x, bf, T, d),
+        _need(fn, dev, "w_gate", w_gate, f32, E, d),
+        _need(fn, dev, "topk_idx", topk_idx, torch.int32, T, k),
+        _need(fn, dev, "topk_s", topk_s, f32, T, k), _need(fn, dev, "dtopk_w", dtopk_w, f32, T, k),
+        _opt(fn, dev, "dx_in", dx_in, bf, T, d), _need(fn, dev, "dx", dx, bf, T, d),
+        _need(fn, dev, "dw_gate", dw_gate, f32, E, d), 1 if accumulate else 0,
+        _here(fn, dev, "ws", ws), _stream(stream, dev)))
+
+
+class AdamTensors:
+    """The tensors of an AdamW step, checked once and held: a list of dicts with p (fp32), g (fp32
+    or bf16), w (bf16 copy of p, or None), m, v (fp32; 8 bits: bytes) and, with state_bits 8,
+    m_scale and v_scale (fp32, one per 128 elements); optional weight_decay (0) and seed (the
+    tensor's place in the list). All contiguous, on one device; step by step, the same storage."""
+
+    def __init__(self, tensors, state_bits=32):
+        fn, dev = "AdamTensors", _device()
+        if state_bits not in (32, 8):
+            raise ValueError(f"{fn}: state_bits must be 32 or 8")
+        self.state_bits, self.device, self.tensors = state_bits, dev, list(tensors)
+        f32, n = torch.float32, len(self.tensors)
+        self.array = (AdamTensorC * n)()
+        for i, (t, c) in enumerate(zip(self.tensors, self.array)):
+            p, g = t["p"], t["g"]
+            gt = _stream_type(fn, "g", g)
+            if not isinstance(p, torch.Tensor):
+                raise ValueError(f"{fn}: p must be a CUDA tensor")
+            shape, c.n = tuple(p.shape), p.numel()
+            held = state_bits == 8
+            st = torch.uint8 if held else f32
+            c.p = _need(fn, dev, "p", p, f32, *shape)
+            c.g = _need(fn, dev, "g", g, gt, *shape)
+            c.w = _opt(fn, dev, "w", t.get("w"), torch.bfloat16, *shape)
+            c.m = _need(fn, dev, "m", t["m"], st, *shape)
+            c.v = _need(fn, dev, "v", t["v"], st, *shape)
+            if held:
+                blocks = (c.n + 127) // 128
+                c.m_scale = _need(fn, dev, "m_scale", t["m_scale"], f32, blocks)
+                c.v_scale = _need(fn, dev, "v_scale", t["v_scale"], f32, blocks)
+            c.weight_decay = float(t.get("weight_decay", 0.0))
+            c.seed = int(t.get("seed", i)) & 0xFFFFFFFF
+            c.g_dtype = MOE_F32 if gt is f32 else MOE_BF16
+        # the calls a step is made of: (first tensor, tensors, whether another call follows)
+        size = ctypes.sizeof(AdamTensorC)
+        base = ctypes.addressof(self.array)
+        self.parts = [(base + i * size, min(MOE_ADAM_TENSORS, n - i), i + MOE_ADAM_TENSORS < n)
+                      for i in range(0, max(n, 1), MOE_ADAM_TENSORS)]
+
+
+_adam_bytes = []
+
+
+def _adam_state(fn, dev, state):
+    if not _adam_bytes:
+        n = ctypes.c_size_t(0)
+        _check("moe_adam_query", _lib.moe_adam_query(ctypes.byref(n)))
+        _adam_bytes.append(n.value)
+    if not isinstance(state, torch.Tensor) or state.nbytes < _adam_bytes[0]:
+        raise ValueError(f"{fn}: state must be a tensor of adam_state")
+    return _here(fn, dev, "state", state)
+
+
+def adam_state(step=0, beta1=0.9, beta2=0.999, device="cuda"):
+    """The state of an optimiser that has made `step` steps with these betas."""
+    n = ctypes.c_size_t(0)
+    _check("moe_adam_query", _lib.moe_adam_query(ctypes.byref(n)))
+    host = torch.zeros(n.value, dtype=torch.uint8)
+    host[8:16].view(torch.int64)[0] = step
+    host[16:32].view(torch.float64).copy_(
+        torch.tensor([1.0 - beta1 ** step, 1.0 - beta2 ** step], dtype=torch.float64))
+    return host.to(device)
+
+
+def adam_step(state) -> int:
+    """The number of steps that a state counts (synchronises)."""
+    return int(state[8:16].cpu().view(torch.int64))
+
+
+def _same_device(fn, plan):
+    dev = _device()
+    if plan.device != dev:
+        raise ValueError(f"{fn}: the tensors must be on the current device, cuda:{dev}")
+    return dev
+
+
+def grad_norm(plan: AdamTensors, state, norm, stream=None):
+    """norm (fp32, one element) = the root of the sum of all gradients' squares."""
+    fn = "moe_grad_norm"
+    dev = _same_device(fn, plan)
+    if not isinstance(norm, torch.Tensor) or norm.dtype is not torch.float32 or norm.numel() != 1:
+        raise ValueError(f"{fn}: norm must be an fp32 CUDA tensor of one element")
+    st, out, s = _adam_state(fn, dev, state), _here(fn, dev, "norm", norm), _stream(stream, dev)
+    for at, n, more in plan.parts:
+        _check(fn, _lib.moe_grad_norm(at, n, more, st, out, s))
+
+
+def adamw(cfg: AdamCfg, plan: AdamTensors, state, norm=None, stream=None, lr=None):
+    """One AdamW step over the plan's tensors. norm: grad_norm's result (needed where the cfg clips;
+    a norm that is not finite leaves the step out). lr: None, or an fp32 CUDA tensor of one element
+    that is read in place of cfg.lr."""
+    fn = "moe_adamw"
+    dev = _same_device(fn, plan)
+    for name, t in (("norm", norm), ("lr", lr)):
+        if t is not None and (not isinstance(t, torch.Tensor) or t.dtype is not torch.float32
+                              or t.numel() != 1):
+            raise ValueError(f"{fn}: {name} must be an fp32 CUDA tensor of one element")
+    cfg.state_bits = plan.state_bits
+    cfg.lr_dev = None if lr is None else _here(fn, dev, "lr", lr)
+    st, s = _adam_state(fn, dev, state), _stream(stream, dev)
+    nm = None if norm is None else _here(fn, dev, "norm", norm)
+    for at, n, more in plan.parts:
+        _check(fn, _lib.moe_adamw(ctypes.byref(cfg), at, n, more, st, nm, s))
 
 
 def clear_status(ws, stream=None):

@@ -6,9 +6,8 @@
 #include <stdlib.h>
 
 #include <algorithm>
-#include <initializer_list>
 
-#include "moe_internal.h"
+#include "moe_check.h"
 
 // NVTX ranges around the layer's stages, so a profiler's timeline (or `ncu --nvtx`) can tell
 // them apart. NVTX is header-only: without a profiler attached a range costs a pointer check.
@@ -31,8 +30,6 @@ int cuda_fail(cudaError_t e) {
 }
 
 namespace {
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 size_t up256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 
 // one NVTX range for the lifetime of the object (no-op without the NVTX header)
@@ -128,24 +125,6 @@ WsLayout ws_layout(const moe_cfg& c) {
 }  // namespace moe
 
 using namespace moe;
-
-#define MOE_CHECK_CFG(cfg)                      \
-  do {                                          \
-    if (!(cfg)) return MOE_ERR_INVALID_ARG;     \
-    const int rc_ = validate(*(cfg));           \
-    if (rc_ != MOE_OK) return rc_;              \
-  } while (0)
-
-#define MOE_NEED(p)                              \
-  do {                                           \
-    if (!(p)) return MOE_ERR_INVALID_ARG;        \
-    if (!aligned16(p)) return MOE_ERR_MISALIGNED; \
-  } while (0)
-
-#define MOE_OPT(p)                                      \
-  do {                                                  \
-    if ((p) && !aligned16(p)) return MOE_ERR_MISALIGNED; \
-  } while (0)
 
 extern "C" {
 
@@ -285,6 +264,34 @@ int moe_route(const moe_cfg* cfg, const void* x, const float* w_gate, const floa
   cudaError_t e = launch_route(*cfg, x, w_gate, bias, topk_idx, topk_w,
                                reinterpret_cast<float*>(w + L.partials),
                                reinterpret_cast<uint32_t*>(w + L.status), stream);
+  return e == cudaSuccess ? MOE_OK : cuda_fail(e);
+}
+
+int moe_route_save(const moe_cfg* cfg, const void* x, const float* w_gate, const float* bias,
+                   int32_t* topk_idx, float* topk_w, float* topk_s, void* ws,
+                   cudaStream_t stream) {
+  MOE_CHECK_CFG(cfg);
+  MOE_NEED(x);
+  MOE_NEED(w_gate);
+  MOE_NEED(bias);
+  MOE_NEED(topk_idx);
+  MOE_NEED(topk_w);
+  MOE_NEED(topk_s);
+  MOE_NEED(ws);
+  const WsLayout L = ws_layout(*cfg);
+  const size_t tk = 4 * (size_t)cfg->T * cfg->k, E = cfg->E, d = cfg->d;
+  const Span in[] = {{x, 2 * cfg->T * d}, {w_gate, 4 * E * d}, {bias, 4 * E}};
+  const Span out[] = {{topk_idx, tk}, {topk_w, tk}, {topk_s, tk}, {ws, L.total}};
+  for (int i = 0; i < 4; ++i) {
+    if (meets(out[i], {in[0], in[1], in[2]})) return MOE_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (meets(out[i], {out[j]})) return MOE_ERR_INVALID_ARG;
+  }
+  char* w = static_cast<char*>(ws);
+  const cudaError_t e = launch_route(*cfg, x, w_gate, bias, topk_idx, topk_w,
+                                     reinterpret_cast<float*>(w + L.partials),
+                                     reinterpret_cast<uint32_t*>(w + L.status), stream, false,
+                                     nullptr, 0, topk_s);
   return e == cudaSuccess ? MOE_OK : cuda_fail(e);
 }
 
@@ -610,23 +617,6 @@ int check_group(const moe_group_cfg* c) {
   return MOE_OK;
 }
 
-// A call's array in bytes; n is 0 for one that is not there.
-struct Span {
-  const void* p;
-  size_t n;
-};
-
-// Whether an output meets any of these arrays. The calls' blocks run in any order, so a result
-// written over an input would change what other blocks read.
-bool meets(const Span& out, std::initializer_list<Span> others) {
-  const auto o = reinterpret_cast<uintptr_t>(out.p);
-  for (const Span& s : others) {
-    const auto b = reinterpret_cast<uintptr_t>(s.p);
-    if (out.p && s.p && out.n && s.n && o < b + s.n && b < o + out.n) return true;
-  }
-  return false;
-}
-
 // (row tensors may be NULL when rows == 0)
 int run_grouped(const moe_group_cfg* cfg, GroupedDir dir, const void* in0, const void* in1,
                 const int32_t* counts, void* out, bool f32, bool accumulate, void* ws,
@@ -652,8 +642,6 @@ int run_grouped(const moe_group_cfg* cfg, GroupedDir dir, const void* in0, const
       launch_grouped(*cfg, dir, in0, in1, counts, out, f32, accumulate, ws, stream);
   return e == cudaSuccess ? MOE_OK : cuda_fail(e);
 }
-
-bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
 
 int check_rows(int32_t rows, int32_t cols) {
   if (rows < 0 || cols < 1) return MOE_ERR_INVALID_ARG;

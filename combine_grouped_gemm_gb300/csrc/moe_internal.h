@@ -101,11 +101,11 @@ inline moe_cfg slot_cfg(const moe_cfg& c, const moe_placement* p) {
 // launcher's kernels are launched programmatically: each may become resident while the
 // previous kernel in the stream is still running, and waits for it before touching memory
 // (launch_route's first kernel, which follows the caller's own work, is always launched as
-// usual).
+// usual). topk_s: NULL, or where the chosen experts' scores go.
 cudaError_t launch_route(const moe_cfg& c, const void* x, const float* w_gate, const float* bias,
                          int32_t* topk_idx, float* topk_w, float* partials, uint32_t* status,
                          cudaStream_t st, bool pdl = false, const void* warm = nullptr,
-                         size_t warm_bytes = 0);
+                         size_t warm_bytes = 0, float* topk_s = nullptr);
 
 // With recv == nullptr only the index pass runs (counts, row_of, src_tok): the gather mode,
 // whose expert GEMMs read token rows straight from x. clear_src_tok: fill src_tok with -1
@@ -203,6 +203,41 @@ cudaError_t launch_swiglu_grad(int rows, int f, const void* q, const float* scal
 cudaError_t launch_combine_grad(int T, int k, int d, int rows, const void* ebuf,
                                 const int32_t* row_of, const float* topk_w, const void* dy,
                                 void* debuf, float* dtopk_w, uint32_t* status, cudaStream_t st);
+
+// Norms around a block. The shapes are checked by the callers (moe_step_api.cu).
+size_t norm_ws_bytes(int rows, int d);
+struct NormFwd {
+  const void *y, *x;   // y: NULL for the norm before a block
+  const float *w_post, *w_next;
+  const void* gate;
+  void *h, *n;
+  float *rstd_y, *rstd_h;
+};
+cudaError_t launch_norm(const moe_norm_cfg& c, const NormFwd& a, cudaStream_t st);
+struct NormGrad {
+  const void *dh, *dn, *y, *h;
+  const float *w_post, *w_next;
+  const void* gate;
+  const float *rstd_y, *rstd_h;
+  void *dx, *dy, *dgate;
+  float *dw_post, *dw_next;
+};
+cudaError_t launch_norm_grad(const moe_norm_cfg& c, const NormGrad& a, bool accumulate, void* ws,
+                             cudaStream_t st);
+
+// The router's gradient.
+size_t route_grad_ws_bytes(const moe_cfg& c);
+cudaError_t launch_route_grad(const moe_cfg& c, const void* x, const float* w_gate,
+                              const int32_t* topk_idx, const float* topk_s, const float* dtopk_w,
+                              const void* dx_in, void* dx, float* dw_gate, bool accumulate,
+                              void* ws, cudaStream_t st);
+
+// AdamW over a list of tensors, and the norm of their gradients.
+size_t adam_state_bytes();
+cudaError_t launch_grad_norm(const moe_adam_tensor* t, int n, bool more, void* state, float* norm,
+                             cudaStream_t st);
+cudaError_t launch_adamw(const moe_adam_cfg& c, const moe_adam_tensor* t, int n, bool more,
+                         void* state, const float* norm, cudaStream_t st);
 
 // 2-D row-major tensor map [rows][cols] with a box of box_rows x 128 bytes, 128-byte swizzle.
 bool make_tensor_map_2d(CUtensorMap* m, const void* base, int elem_bytes, uint64_t cols,

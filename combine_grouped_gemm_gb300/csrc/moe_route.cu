@@ -608,6 +608,7 @@ __device__ __forceinline__ int warp_topk(const float* v, const int* keep, int E,
 //     took with them);
 //  5. threads i < k: the weights from the raw sigmoid scores in selection order (each forms the
 //     same sequential sum).
+// This kernel and the two below write the chosen experts' raw scores to topk_s too, unless NULL.
 // ---------------------------------------------------------------------------------------
 constexpr int kSelThreads = 256;
 __host__ __device__ constexpr int sel_cta_scratch_floats(int E) { return 2 * E + 64 + 64 + 32 + 32; }
@@ -615,8 +616,8 @@ constexpr int kWarmCtas = 64;   // CTAs that issue the L2 warm-up (about 1 MB ea
 
 __global__ void __launch_bounds__(kSelThreads) route_select_cta_kernel(
     const float* __restrict__ partials, const float* __restrict__ bias,
-    int32_t* __restrict__ topk_idx, float* __restrict__ topk_w, int T, int E, int k,
-    int n_group, int topk_group, float route_scale, const void* warm, size_t warm_bytes,
+    int32_t* __restrict__ topk_idx, float* __restrict__ topk_w, float* __restrict__ topk_s,
+    int T, int E, int k, int n_group, int topk_group, float route_scale, const void* warm, size_t warm_bytes,
     int warm_ctas) {
   extern __shared__ float sm[];
   float* s = sm;                 // [E] sigmoid scores
@@ -712,6 +713,7 @@ __global__ void __launch_bounds__(kSelThreads) route_select_cta_kernel(
     for (int i = 0; i < k; ++i) sum = __fadd_rn(sum, sel_s[i]);
     topk_idx[(size_t)t * k + lane] = sel_e;
     topk_w[(size_t)t * k + lane] = __fmul_rn(__fdiv_rn(sel_s[lane], sum), route_scale);
+    if (topk_s) topk_s[(size_t)t * k + lane] = sel_s[lane];
   }
 }
 
@@ -730,8 +732,8 @@ __host__ __device__ constexpr int sel_scratch_floats(int E) { return 2 * E + 64 
 
 __global__ void __launch_bounds__(256) route_select_kernel(
     const float* __restrict__ partials, const float* __restrict__ bias,
-    int32_t* __restrict__ topk_idx, float* __restrict__ topk_w, int T, int E, int k,
-    int n_group, int topk_group, float route_scale, const void* warm, size_t warm_bytes,
+    int32_t* __restrict__ topk_idx, float* __restrict__ topk_w, float* __restrict__ topk_s,
+    int T, int E, int k, int n_group, int topk_group, float route_scale, const void* warm, size_t warm_bytes,
     int warm_ctas) {
   extern __shared__ float sm[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -795,7 +797,10 @@ __global__ void __launch_bounds__(256) route_select_kernel(
   __syncwarp();
 
   const int sel_e = warp_topk(v, keep, E, gs, k, lane);
-  if (lane < k) sel_s[lane] = s[sel_e];
+  if (lane < k) {
+    sel_s[lane] = s[sel_e];
+    if (topk_s) topk_s[(size_t)t * k + lane] = s[sel_e];
+  }
   __syncwarp();
   if (lane == 0) {
     float sum = 0.0f;
@@ -831,8 +836,8 @@ constexpr int kSegE = 256, kSegGroups = 8;
 
 __global__ void __launch_bounds__(kSegThreads) route_select_seg_kernel(
     const float* __restrict__ partials, const float* __restrict__ bias,
-    int32_t* __restrict__ topk_idx, float* __restrict__ topk_w, int T, int k, int topk_group,
-    float route_scale, const void* warm, size_t warm_bytes, int warm_ctas) {
+    int32_t* __restrict__ topk_idx, float* __restrict__ topk_w, float* __restrict__ topk_s,
+    int T, int k, int topk_group, float route_scale, const void* warm, size_t warm_bytes, int warm_ctas) {
   constexpr int E = kSegE;
   extern __shared__ float s_all[];   // [16 tokens][E] sigmoid scores
   pdl_wait();
@@ -965,6 +970,7 @@ __global__ void __launch_bounds__(kSegThreads) route_select_seg_kernel(
   if (tok && q < k) {
     topk_idx[(size_t)t * k + q] = sel_e;
     topk_w[(size_t)t * k + q] = __fmul_rn(__fdiv_rn(si, sum), route_scale);
+    if (topk_s) topk_s[(size_t)t * k + q] = si;
   }
 }
 
@@ -972,7 +978,8 @@ __global__ void __launch_bounds__(kSegThreads) route_select_seg_kernel(
 
 cudaError_t launch_route(const moe_cfg& c, const void* x, const float* w_gate, const float* bias,
                          int32_t* topk_idx, float* topk_w, float* partials, uint32_t* status,
-                         cudaStream_t st, bool pdl, const void* warm, size_t warm_bytes) {
+                         cudaStream_t st, bool pdl, const void* warm, size_t warm_bytes,
+                         float* topk_s) {
   (void)status;
   const __nv_bfloat16* xb = static_cast<const __nv_bfloat16*>(x);
   if (reinterpret_cast<uintptr_t>(warm) & 15) warm = nullptr;   // bulk prefetches need 16 bytes
@@ -1010,8 +1017,8 @@ cudaError_t launch_route(const moe_cfg& c, const void* x, const float* w_gate, c
   if (c.T < 1024) {   // a CTA per token keeps every expert's loads in flight at once
     const size_t smem1 = (size_t)sel_cta_scratch_floats(c.E) * sizeof(float);
     return launch_kernel(route_select_cta_kernel, dim3(warm_ctas + c.T), dim3(kSelThreads), smem1,
-                         st, pdl, partials, bias, topk_idx, topk_w, c.T, c.E, c.k, c.n_group,
-                         c.topk_group, c.route_scale, warm, warm_bytes, warm_ctas);
+                         st, pdl, partials, bias, topk_idx, topk_w, topk_s, c.T, c.E, c.k,
+                         c.n_group, c.topk_group, c.route_scale, warm, warm_bytes, warm_ctas);
   }
   // the DeepSeek-V3 router shape from 2048 tokens: 8 lanes per token (1024 tokens: 106 us
   // against 99 us with a warp per token, whose CTAs spread over more SMs; 4096 / 16384 tokens:
@@ -1021,8 +1028,8 @@ cudaError_t launch_route(const moe_cfg& c, const void* x, const float* w_gate, c
     const int per_cta = kSegThreads / 8;
     return launch_kernel(route_select_seg_kernel, dim3(warm_ctas + (c.T + per_cta - 1) / per_cta),
                          dim3(kSegThreads), (size_t)per_cta * kSegE * sizeof(float), st, pdl,
-                         partials, bias, topk_idx, topk_w, c.T, c.k, c.topk_group, c.route_scale,
-                         warm, warm_bytes, warm_ctas);
+                         partials, bias, topk_idx, topk_w, topk_s, c.T, c.k, c.topk_group,
+                         c.route_scale, warm, warm_bytes, warm_ctas);
   }
   // one warp per token; CTAs of up to 8 warps, fewer when T is small so the tokens still spread
   // over the SMs
@@ -1031,8 +1038,8 @@ cudaError_t launch_route(const moe_cfg& c, const void* x, const float* w_gate, c
   err = ensure_smem_limit(reinterpret_cast<const void*>(route_select_kernel), smem);
   if (err != cudaSuccess) return err;
   return launch_kernel(route_select_kernel, dim3(warm_ctas + (c.T + wpc - 1) / wpc),
-                       dim3(32 * wpc), smem, st, pdl, partials, bias, topk_idx, topk_w, c.T, c.E,
-                       c.k, c.n_group, c.topk_group, c.route_scale, warm, warm_bytes, warm_ctas);
+                       dim3(32 * wpc), smem, st, pdl, partials, bias, topk_idx, topk_w, topk_s,
+                       c.T, c.E, c.k, c.n_group, c.topk_group, c.route_scale, warm, warm_bytes, warm_ctas);
 }
 
 }  // namespace moe

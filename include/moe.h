@@ -53,6 +53,8 @@ extern "C" {
                                   (not positive, not finite, or with mantissa bits); the GEMM
                                   applied 2^(its exponent field - 127) in its place */
 
+#define MOE_DEV_NONFINITE 8u   /* moe_adamw: the gradients' norm is not finite; step left out */
+
 /* Element formats */
 #define MOE_BF16 0
 #define MOE_FP8_E4M3 1       /* e4m3 with fp32 block scales: 1x128 for activations (scale =
@@ -391,7 +393,7 @@ int moe_grouped_query(const moe_group_cfg* cfg, size_t* ws_bytes);
  * added to dw instead of replacing it. An empty group's dW_e is 0. The results do not depend on
  * the order in which the GPU runs the work (no floating-point atomics). With rows == 0 the row
  * tensors may be NULL, and counts are not read. */
-#define MOE_F32 3 /* dw_dtype only */
+#define MOE_F32 3 /* dw_dtype, the residual stream of the norms, gradients of the optimiser */
 int moe_grouped_mm(const moe_group_cfg* cfg, const void* x, const int32_t* counts, const void* w,
                    void* y, void* ws, cudaStream_t stream);
 int moe_grouped_mm_dx(const moe_group_cfg* cfg, const void* dy, const int32_t* counts,
@@ -440,6 +442,161 @@ int moe_swiglu_grad(int32_t rows, int32_t f, const void* q, const float* scales,
 int moe_combine_grad(int32_t T, int32_t k, int32_t d, int32_t rows, const void* ebuf,
                      const int32_t* row_of, const float* topk_w, const void* dy, void* debuf,
                      float* dtopk_w, uint32_t* status, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------------------
+ * The rest of a training step of an MoE block: the norms around the layer, the router's gradient,
+ * the optimiser. A block is
+ *   n = norm(x) w  ->  y = moe_layer(n)  ->  h = res x + out gate norm(y) w_post (-> next n)
+ * The pages cover neither training nor the norms and have no counterpart to these calls. As in the
+ * section above, an output may not overlap an input or another output (MOE_ERR_INVALID_ARG) except
+ * where a call says that it may take an input's place (the very array).
+ * ------------------------------------------------------------------------------------- */
+
+#define MOE_GATE_NONE 0
+#define MOE_GATE_CHANNEL 1   /* fp32 [d]: one factor a column (a learned layer scale) */
+#define MOE_GATE_TOKEN 2     /* fp32 [rows]: one factor a row */
+#define MOE_GATE_ELEMENT 3   /* bf16 [rows][d] */
+
+typedef struct moe_norm_cfg {
+  int32_t rows;           /* >= 0 */
+  int32_t d;              /* d % 8 == 0, d <= 16384; rows * d < 2^37 */
+  float eps;              /* finite, >= 0 */
+  float res_scale;        /* res: factor of the residual stream (norm_out) */
+  float out_scale;        /* out: factor of the block's gated output (norm_out) */
+  int32_t stream_dtype;   /* MOE_BF16 or MOE_F32: type of the residual stream (x, h, dh, dx) */
+  int32_t gate;           /* MOE_GATE_* (norm_out) */
+} moe_norm_cfg;
+
+/* RMS norm before a block: r = 1/sqrt(mean_j x_j^2 + eps) of each row, n = bf16(x r w).
+ * x [rows][d] of the stream's type, w fp32 [d], n bf16 [rows][d] (may take the place of a bf16 x),
+ * rstd fp32 [rows]: r, kept for the gradient (NULL: not wanted). Sums in fp32 here and below. */
+int moe_norm_in(const moe_norm_cfg* cfg, const void* x, const float* w, void* n, float* rstd,
+                cudaStream_t stream);
+
+/* Its gradient: dx = dres + r (dn w - xh mean(dn w xh)), xh = x r; dw = sum over rows of dn xh
+ * (fp32 [d]; accumulate: added to dw; NULL: not wanted). dn bf16; dres (the gradient that reaches x
+ * by the residual, NULL: none) and dx of the stream's type; dx may take dres's place. ws: scratch
+ * of moe_norm_query bytes (no initial value; calls that may overlap on the GPU need their own). */
+int moe_norm_in_grad(const moe_norm_cfg* cfg, const void* dn, const void* x, const float* w,
+                     const float* rstd, const void* dres, void* dx, float* dw, int32_t accumulate,
+                     void* ws, cudaStream_t stream);
+
+/* Norm after a block, gate, residual and the norm before the next block in one pass:
+ *   s = y r_y w_post (w_post NULL: s = y)      r_y as above, from y
+ *   h = res x + out gate s                     in fp32, stored in the stream's type
+ *   n = bf16(h r_h w_next) (w_next NULL: none) r_h and n from h before its rounding
+ * y bf16 [rows][d], the block's output; x the residual stream; gate by cfg->gate (NULL for NONE);
+ * h may take x's place, n that of y. rstd_y, rstd_h fp32 [rows] (NULL: not wanted). */
+int moe_norm_out(const moe_norm_cfg* cfg, const void* y, const void* x, const float* w_post,
+                 const void* gate, const float* w_next, void* h, void* n, float* rstd_y,
+                 float* rstd_h, cudaStream_t stream);
+
+/* Its gradient, from dh (NULL: none) and dn (with w_next), from y (needed with w_post or a gate),
+ * from h as stored and rstd_h (with w_next), and rstd_y (with w_post). With hh = h r_h, yh = y r_y:
+ *   G  = dh + r_h (dn w_next - hh mean(dn w_next hh))
+ *   dx = res G                        ds = out gate G        dgate = out G s, summed to the
+ *   dy = r_y (ds w_post - yh mean(ds w_post yh)) (or ds)     gate's shape, in the gate's type
+ *   dw_post = sum over rows of ds yh  dw_next = sum over rows of dn hh
+ * dx (may take dh's place), dgate, dw_post, dw_next: NULL where not wanted; dy may take dn's place.
+ * accumulate: dw_post, dw_next and a CHANNEL gate's dgate are added to. The sums do not depend on
+ * the order in which the GPU runs the work. ws as in moe_norm_in_grad. */
+int moe_norm_out_grad(const moe_norm_cfg* cfg, const void* dh, const void* dn, const void* y,
+                      const void* h, const float* w_post, const void* gate, const float* w_next,
+                      const float* rstd_y, const float* rstd_h, void* dx, void* dy, void* dgate,
+                      float* dw_post, float* dw_next, int32_t accumulate, void* ws,
+                      cudaStream_t stream);
+
+/* Bytes of the scratch of the two gradients. MOE_ERR_INVALID_ARG for rows < 0 or d < 1,
+ * MOE_ERR_UNSUPPORTED for a d or a size that the calls do not take. */
+int moe_norm_query(int32_t rows, int32_t d, size_t* ws_bytes);
+
+/* moe_route that also keeps the raw sigmoid scores of the chosen experts, topk_s fp32 [T][k], for
+ * moe_route_grad. topk_idx and topk_w are moe_route's, bit for bit. */
+int moe_route_save(const moe_cfg* cfg, const void* x, const float* w_gate, const float* bias,
+                   int32_t* topk_idx, float* topk_w, float* topk_s, void* ws,
+                   cudaStream_t stream);
+
+/* Gradient of the router, from that of its weights (dtopk_w fp32 [T][k], as moe_combine_grad gives
+ * it). The choice has no gradient (nor has the bias, which steers it alone). With s = topk_s and
+ * p_i = s_i / (s_0 + ... + s_{k-1}), so that topk_w_i = route_scale p_i:
+ *   dz_i = route_scale p_i (1 - s_i) (dtopk_w_i - sum_j p_j dtopk_w_j)
+ *   dx[t] = bf16(dx_in[t] + sum_i dz_i w_gate[e_i])          e_i = topk_idx[t][i]
+ *   dw_gate[e] = sum of dz x[t] over the choices of e        fp32 [E][d]; accumulate: added to
+ * x, dx_in (NULL: none), dx bf16 [T][d]; dx may take dx_in's place. Sums in fp32 in a fixed order.
+ * A choice outside [0, E) gets no gradient and gives none (its p counts) and is reported
+ * (MOE_DEV_BOUNDS in the first word of ws; -1, a choice that was dropped, is not reported). Of cfg,
+ * T, d, E, k and route_scale count; d <= 65536 and T * d < 2^37 (else MOE_ERR_UNSUPPORTED). ws:
+ * moe_route_grad_query bytes; zero its first word once. Calls that may overlap on the GPU need
+ * workspaces of their own. */
+int moe_route_grad(const moe_cfg* cfg, const void* x, const float* w_gate, const int32_t* topk_idx,
+                   const float* topk_s, const float* dtopk_w, const void* dx_in, void* dx,
+                   float* dw_gate, int32_t accumulate, void* ws, cudaStream_t stream);
+int moe_route_grad_query(const moe_cfg* cfg, size_t* ws_bytes);
+
+/* One tensor of an optimiser's step (an entry of a HOST array; the pointers are device pointers).
+ * With moments in 32 bits m and v are fp32 [n], m_scale and v_scale are NULL. In 8 bits m and v are
+ * e4m3 codes [n] of m and of sqrt(v), each block of 128 consecutive elements with an fp32 scale
+ * (m_scale, v_scale [ceil(n/128)]). Moments and scales start at zero. */
+typedef struct moe_adam_tensor {
+  float* p;             /* parameters, fp32 [n] */
+  const void* g;        /* their gradient, fp32 or bf16 [n] */
+  void* w;              /* bf16 copy of p that the step refreshes; NULL: none */
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  int64_t n;            /* elements, 0 <= n < 2^39 */
+  float weight_decay;   /* finite, >= 0 */
+  uint32_t seed;        /* 8 bits: of the tensor's random numbers; another one for each tensor */
+  int32_t g_dtype;      /* MOE_F32 or MOE_BF16 */
+  int32_t reserved;     /* 0 */
+} moe_adam_tensor;
+
+typedef struct moe_adam_cfg {
+  double lr;            /* finite, >= 0 */
+  double beta1, beta2;  /* in [0, 1) */
+  double eps;           /* > 0, in fp32 too */
+  double max_norm;      /* largest norm of all gradients; 0: they are not clipped */
+  const float* lr_dev;  /* NULL, or a device scalar that is read in lr's place (for a captured step
+                           whose rate changes between replays) */
+  int32_t state_bits;   /* 32 or 8 */
+  int32_t reserved;     /* 0 */
+} moe_adam_cfg;
+
+/* Tensors a call takes at most. A step over more of them is made of several calls, all but the last
+ * with `more` set. */
+#define MOE_ADAM_TENSORS 256
+
+/* AdamW (I. Loshchilov and F. Hutter, "Decoupled weight decay regularization", 2019), step t, over
+ * n tensors in one launch:
+ *   g' = g min(1, max_norm / *norm)          (max_norm 0 or norm NULL: g' = g)
+ *   m  = b1 m + (1 - b1) g'                  v = b2 v + (1 - b2) g'^2
+ *   p  = p - lr weight_decay p - lr/(1 - b1^t) m / (sqrt(v/(1 - b2^t)) + eps);   w = bf16(p)
+ * p moves by the new moments in fp32, before they are put into 8 bits. There, q = |m| / scale or
+ * q = sqrt(v) / scale (scale = amax/448 of the block, 1 if amax is 0; IEEE divisions and roots, each
+ * of the products and sums above rounded by itself) is rounded to a neighbouring code at random, by
+ * 16 random bits an element from (seed, t, element), with odds that keep the mean of m and of v:
+ * with nearest rounding a v with b2 near 1 would not move. A code of v is never 0 where v is not.
+ * A NaN or an infinity spoils its block.
+ * state: moe_adam_query bytes, zeroed once (step 0); it holds the status word, t, the bias
+ * corrections and the partial sums of moe_grad_norm. The last call of a step advances t.
+ * norm: NULL, or the device scalar of moe_grad_norm (needed with max_norm > 0). Where it is not
+ * finite the step is left out (nothing is written, t stays) and MOE_DEV_NONFINITE is reported.
+ * Results do not depend on the order in which the GPU runs the work. p, w, m, v and the scales are
+ * read and written in place; no two of the call's arrays may overlap. */
+int moe_adamw(const moe_adam_cfg* cfg, const moe_adam_tensor* tensors, int32_t n, int32_t more,
+              void* state, const float* norm, cudaStream_t stream);
+
+/* norm = sqrt of the sum of all g^2 (device fp32 scalar; squares in fp32, so that a gradient past
+ * 1e19 counts as infinite). Of the tensors, g, g_dtype and n count. With `more` the sum goes on in
+ * the next call and norm is not written. */
+int moe_grad_norm(const moe_adam_tensor* tensors, int32_t n, int32_t more, void* state,
+                  float* norm, cudaStream_t stream);
+
+/* Bytes of the state. Its layout, for saving and loading: uint32 status, uint32 (scratch, 0), int64
+ * t, double 1 - b1^t, double 1 - b2^t, then scratch that is 0 between steps or written before it is
+ * read. */
+int moe_adam_query(size_t* state_bytes);
 
 /* Sets the device status word in ws to 0 (enqueued on stream). */
 int moe_clear_status(void* ws, cudaStream_t stream);
