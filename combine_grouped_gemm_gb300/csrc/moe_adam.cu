@@ -217,9 +217,10 @@ __device__ __forceinline__ Scalars scalars(const Hyper& h, const State* state, c
     sc.step = static_cast<uint32_t>(state->step + 1);
     const float total = norm ? *norm : 0.0f;
     sc.skip = !(fabsf(total) < INFINITY);
-    const float most = static_cast<float>(h.max_norm);
-    sc.clip = h.max_norm > 0.0 && total > most;
-    sc.factor = sc.clip ? __fdiv_rn(most, total) : 1.0f;
+    sc.factor = h.max_norm > 0.0
+                    ? fminf(__fmul_rn(static_cast<float>(h.max_norm), __frcp_rn(total)), 1.0f)
+                    : 1.0f;
+    sc.clip = sc.factor < 1.0f;
   }
   __syncthreads();
   return sc;
@@ -302,7 +303,7 @@ __device__ __forceinline__ void codes4(uint32_t c, float s, float (&f)[4]) {
   }
 }
 __device__ __forceinline__ float block_scale(float amax) {
-  return amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
+  return amax > 0.0f ? __fmul_rn(amax, 1.0f / 448.0f) : 1.0f;
 }
 
 template <int CAP, int BITS>

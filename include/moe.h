@@ -573,8 +573,9 @@ typedef struct moe_adam_cfg {
  *   m  = b1 m + (1 - b1) g'                  v = b2 v + (1 - b2) g'^2
  *   p  = p - lr weight_decay p - lr/(1 - b1^t) m / (sqrt(v/(1 - b2^t)) + eps);   w = bf16(p)
  * p moves by the new moments in fp32, before they are put into 8 bits. There, q = |m| / scale or
- * q = sqrt(v) / scale (scale = amax/448 of the block, 1 if amax is 0; IEEE divisions and roots, each
- * of the products and sums above rounded by itself) is rounded to a neighbouring code at random, by
+ * q = sqrt(v) / scale (scale = amax * fp32(1/448) of the block, 1 if amax is 0; max_norm / norm is
+ * max_norm * (1/norm); IEEE operations, each of these and of m and v above rounded by itself) is
+ * rounded to a neighbouring code at random, by
  * 16 random bits an element from (seed, t, element), with odds that keep the mean of m and of v:
  * with nearest rounding a v with b2 near 1 would not move. A code of v is never 0 where v is not.
  * A NaN or an infinity spoils its block.

@@ -479,7 +479,7 @@ def hold_reference(x, r16, root):
     b = b.reshape(nb, 128)
     mag = np.abs(b)
     amax = mag.max(1, keepdims=True)
-    scale = np.where(amax > 0, amax / f(448), f(1)).astype(f)
+    scale = np.where(amax > 0, amax * (f(1) / f(448)), f(1)).astype(f)
     q = np.minimum((mag / scale).astype(f), f(448))
     r = r16.reshape(nb, 128).astype(np.int64)
     tab = np.concatenate([e4m3_table(), [f(480)]]).astype(f)
