@@ -68,24 +68,25 @@ __device__ __forceinline__ float4 load4(const float* p, int cnt) {
   if (cnt == 4) return __ldcs(reinterpret_cast<const float4*>(p));
   return make_float4(cnt > 0 ? p[0] : 0.0f, cnt > 1 ? p[1] : 0.0f, cnt > 2 ? p[2] : 0.0f, 0.0f);
 }
-__device__ __forceinline__ void store4(float* p, const float (&v)[4], int cnt) {
+__device__ __forceinline__ void store4(float* p, const float2 (&v)[2], int cnt) {
   if (cnt == 4) {
-    __stcs(reinterpret_cast<float4*>(p), make_float4(v[0], v[1], v[2], v[3]));
+    __stcs(reinterpret_cast<float4*>(p), make_float4(v[0].x, v[0].y, v[1].x, v[1].y));
     return;
   }
-#pragma unroll
-  for (int j = 0; j < 3; ++j)
-    if (j < cnt) p[j] = v[j];
+  if (cnt > 0) p[0] = v[0].x;
+  if (cnt > 1) p[1] = v[0].y;
+  if (cnt > 2) p[2] = v[1].x;
 }
-__device__ __forceinline__ void store4_bf16(void* w, long long i, const float (&v)[4], int cnt) {
+__device__ __forceinline__ void store4_bf16(void* w, long long i, const float2 (&v)[2], int cnt) {
   __nv_bfloat16* p = static_cast<__nv_bfloat16*>(w) + i;
   if (cnt == 4) {
-    __stcs(reinterpret_cast<uint2*>(p), make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])));
+    __stcs(reinterpret_cast<uint2*>(p),
+           make_uint2(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y)));
     return;
   }
-#pragma unroll
-  for (int j = 0; j < 3; ++j)
-    if (j < cnt) p[j] = __float2bfloat16_rn(v[j]);
+  if (cnt > 0) p[0] = __float2bfloat16_rn(v[0].x);
+  if (cnt > 1) p[1] = __float2bfloat16_rn(v[0].y);
+  if (cnt > 2) p[2] = __float2bfloat16_rn(v[1].x);
 }
 __device__ __forceinline__ uint32_t load_codes(const void* q, long long i, int cnt) {
   const uint8_t* p = static_cast<const uint8_t*>(q) + i;
@@ -226,17 +227,61 @@ __device__ __forceinline__ Scalars scalars(const Hyper& h, const State* state, c
   return sc;
 }
 
-// One element: the new moments and the parameter. Each product and sum of the moments is rounded by
-// itself (no fused multiply-add), so that 8-bit moments can be checked code by code.
-__device__ __forceinline__ void update(const Scalars& sc, float decay, float g, float& p, float& m,
-                                       float& v, float& root) {
-  if (sc.clip) g = __fmul_rn(g, sc.factor);
-  m = __fadd_rn(__fmul_rn(sc.b1, m), __fmul_rn(sc.n1, g));
-  v = __fadd_rn(__fmul_rn(sc.b2, v), __fmul_rn(sc.n2, __fmul_rn(g, g)));
-  root = __fsqrt_rn(v);
-  const float den = __fmaf_rn(root, sc.root, sc.eps);
-  p = __fmaf_rn(-decay, p, p);
-  p = __fmaf_rn(-sc.move, __fdividef(m, den), p);
+// Two fp32 operations in one instruction. (The assembler joins a mul2 and an add2 of its result into
+// one operation of one rounding, .rn or not: sums of products that have to be rounded twice are
+// written one by one, which it leaves as they are.)
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 minus(float2 v) { return make_float2(-v.x, -v.y); }
+
+// A pair of elements: the new moments and the parameters. Each product and sum of the moments is
+// rounded by itself, so that 8-bit moments can be checked code by code; the parameter's quotient
+// takes the hardware's reciprocal (1 ulp).
+__device__ __forceinline__ float recip(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ void update(const Scalars& sc, float decay, float2 g, float2& p, float2& m,
+                                       float2& v, float2& root) {
+  if (sc.clip) g = mul2(g, both(sc.factor));
+  const auto mean = [](float b, float old, float n, float now) {
+    return __fadd_rn(__fmul_rn(b, old), __fmul_rn(n, now));
+  };
+  const float2 gg = mul2(g, g);
+  m = make_float2(mean(sc.b1, m.x, sc.n1, g.x), mean(sc.b1, m.y, sc.n1, g.y));
+  v = make_float2(mean(sc.b2, v.x, sc.n2, gg.x), mean(sc.b2, v.y, sc.n2, gg.y));
+  root = make_float2(__fsqrt_rn(v.x), __fsqrt_rn(v.y));
+  const float2 den = fma2(root, both(sc.root), both(sc.eps));
+  const float2 quot = mul2(m, make_float2(recip(den.x), recip(den.y)));
+  p = fma2(both(-decay), p, p);
+  p = fma2(both(-sc.move), quot, p);
 }
 
 // The largest of a warp's non-negative numbers (their order is that of their bits).
@@ -244,66 +289,140 @@ __device__ __forceinline__ float warp_max(float v) {
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
 }
 
-// e4m3 codes of four values of a block, rounded up or down by 16 random bits each: with the random
-// bits added below the code's last bit, cutting off what is below it rounds up with odds of the
-// distance from the lower code. Below 2^-6 the steps are 2^-9: with 2^-6 added they lie at the same
-// bits.
-__device__ __forceinline__ float round_e4m3(float q, uint32_t r16) {
-  const bool small = q < 0x1p-6f;
-  float y = small ? __fadd_rn(q, 0x1p-6f) : q;
-  y = __uint_as_float((__float_as_uint(y) + (r16 << 4)) & 0xfff00000u);
-  return small ? __fadd_rn(y, -0x1p-6f) : y;
-}
-// The same for the root of a second moment, with odds that keep the mean of its square, (q^2 - lo^2)
-// / (hi^2 - lo^2): odds linear in q would add the rounding's variance to v each step, several
-// percent of v in the long run.
-__device__ __forceinline__ float round_root_e4m3(float q, uint32_t r16) {
-  const float shift = q < 0x1p-6f ? 0x1p-6f : 0.0f;
-  const uint32_t bits = __float_as_uint(__fadd_rn(q, shift)) & 0xfff00000u;
-  const float lo = __fadd_rn(__uint_as_float(bits), -shift);   // exact, as are hi, hi - lo, hi + lo
-  const float hi = __fadd_rn(__uint_as_float(bits + 0x100000u), -shift);
-  const float odds = __fmul_rn(__fadd_rn(q, -lo), __fadd_rn(q, lo));
-  const float whole = __fmul_rn(__fadd_rn(hi, -lo), __fadd_rn(hi, lo));
-  return __fmul_rn(static_cast<float>(r16), whole) < __fmul_rn(odds, 65536.0f) ? hi : lo;
-}
-template <bool ROOT>
-__device__ __forceinline__ uint32_t hold4(const float (&x)[4], float scale, const uint32_t (&r)[4],
-                                          int shift) {
-  uint32_t code = 0;
-#pragma unroll
-  for (int j = 0; j < 4; j += 2) {
-    float q[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float a = fabsf(x[j + i]);
-      const uint32_t r16 = (r[j + i] >> shift) & 0xffffu;
-      q[i] = __fdiv_rn(a, scale);
-      q[i] = q[i] > 448.0f ? 448.0f : q[i];
-      if (ROOT) {
-        q[i] = round_root_e4m3(q[i], r16);
-        q[i] = a > 0.0f && q[i] < 0x1p-9f ? 0x1p-9f : q[i];
-      } else {
-        q[i] = copysignf(round_e4m3(q[i], r16), x[j + i]);
-      }
-    }
-    code |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(q[0], q[1]), __NV_SATFINITE,
-                                                           __NV_E4M3))
-            << (8 * j);
+// |x| / scale, the IEEE quotients, at most 448. By the correctly rounded reciprocal and one
+// correction step (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990) where nothing of it can leave the fp32 range, by division otherwise.
+__device__ __forceinline__ float2 quotients(float2 x, float scale, float r, bool plain) {
+  float2 a = make_float2(fabsf(x.x), fabsf(x.y)), q;
+  if (plain) {
+    const float2 q0 = mul2(a, both(r));
+    q = fma2(fma2(q0, both(scale), minus(a)), both(-r), q0);
+  } else {
+    q = make_float2(__fdiv_rn(a.x, scale), __fdiv_rn(a.y, scale));
   }
-  return code;
+  return make_float2(q.x > 448.0f ? 448.0f : q.x, q.y > 448.0f ? 448.0f : q.y);
 }
-__device__ __forceinline__ void codes4(uint32_t c, float s, float (&f)[4]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
-        static_cast<__nv_fp8x2_storage_t>((c >> (16 * i)) & 0xffffu), __NV_E4M3);
-    const float2 v = __half22float2(__half2(h));
-    f[2 * i] = __fmul_rn(v.x, s);
-    f[2 * i + 1] = __fmul_rn(v.y, s);
-  }
+
+// A pair of quotients rounded up or down to e4m3 by 16 random bits each (the upper half of r). With
+// the random bits added below the code's last bit, cutting off what is below it rounds up with odds
+// of the distance from the lower code. Below 2^-6 the steps are 2^-9: with 2^-6 added they lie at the
+// same bits.
+__device__ __forceinline__ float2 shift_of(float2 q) {
+  return make_float2(q.x < 0x1p-6f ? 0x1p-6f : 0.0f, q.y < 0x1p-6f ? 0x1p-6f : 0.0f);
+}
+__device__ __forceinline__ float cut(float v, uint32_t more = 0) {
+  return __uint_as_float((__float_as_uint(v) + more) & 0xfff00000u);
+}
+__device__ __forceinline__ float2 round_e4m3(float2 q, uint32_t r0, uint32_t r1) {
+  const float2 shift = shift_of(q), y = add2(q, shift);
+  return add2(make_float2(cut(y.x, (r0 >> 12) & 0xffff0u), cut(y.y, (r1 >> 12) & 0xffff0u)),
+              minus(shift));
+}
+// The same for the root of a second moment (by the lower half of r), with odds that keep the mean of
+// its square, (q^2 - lo^2) / (hi^2 - lo^2): odds linear in q would add the rounding's variance to v
+// each step, several percent of v in the long run.
+__device__ __forceinline__ float2 round_root_e4m3(float2 q, uint32_t r0, uint32_t r1) {
+  const float2 shift = shift_of(q), y = add2(q, shift);
+  const float2 cx = make_float2(cut(y.x), cut(y.y));
+  const float2 cy = make_float2(__uint_as_float(__float_as_uint(cx.x) + 0x100000u),
+                                __uint_as_float(__float_as_uint(cx.y) + 0x100000u));
+  const float2 lo = add2(cx, minus(shift)), hi = add2(cy, minus(shift));   // exact, and so are
+  const float2 odds = mul2(add2(q, minus(lo)), add2(q, lo));
+  const float2 whole = mul2(add2(hi, minus(lo)), add2(hi, lo));            // hi - lo and hi + lo
+  // r / 2^16 as the fraction of a number between 1 and 2
+  const float2 r = add2(make_float2(__uint_as_float(0x3f800000u | ((r0 << 7) & 0x7fff80u)),
+                                    __uint_as_float(0x3f800000u | ((r1 << 7) & 0x7fff80u))),
+                        both(-1.0f));
+  const float2 at = mul2(r, whole);
+  return make_float2(at.x < odds.x ? hi.x : lo.x, at.y < odds.y ? hi.y : lo.y);
+}
+__device__ __forceinline__ uint32_t pack_codes(float2 a, float2 b) {
+  return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3)) |
+         static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3)) << 16;
+}
+__device__ __forceinline__ float2 codes2(uint32_t c, float s) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+      static_cast<__nv_fp8x2_storage_t>(c & 0xffffu), __NV_E4M3);
+  return mul2(__half22float2(__half2(h)), both(s));
 }
 __device__ __forceinline__ float block_scale(float amax) {
   return amax > 0.0f ? __fmul_rn(amax, 1.0f / 448.0f) : 1.0f;
+}
+__device__ __forceinline__ bool plain_scale(float s) { return s > 0x1p-60f && s < 0x1p100f; }
+
+// What a lane has loaded of its four elements of a block.
+template <int BITS>
+struct Loaded {
+  float4 g, p, m, v;
+  uint32_t qm, qv;
+  float sm, sv;
+};
+template <int BITS>
+__device__ __forceinline__ Loaded<BITS> load_block(const moe_adam_tensor& e, bool f32,
+                                                   long long block, int lane, int cnt) {
+  const long long at = block * kBlock + lane * 4;
+  Loaded<BITS> l;
+  l.g = load_grad(e.g, f32, at, cnt);
+  l.p = load4(e.p + at, cnt);
+  if (BITS == 32) {
+    l.m = load4(static_cast<const float*>(e.m) + at, cnt);
+    l.v = load4(static_cast<const float*>(e.v) + at, cnt);
+  } else {
+    l.qm = load_codes(e.m, at, cnt);
+    l.qv = load_codes(e.v, at, cnt);
+    l.sm = __ldcs(e.m_scale + block);
+    l.sv = __ldcs(e.v_scale + block);
+  }
+  return l;
+}
+template <int BITS>
+__device__ __forceinline__ void step_block(const Scalars& sc, const moe_adam_tensor& e, float decay,
+                                           uint32_t key, long long block, int lane, int cnt,
+                                           const Loaded<BITS>& l) {
+  const long long at = block * kBlock + lane * 4;
+  float2 p[2] = {make_float2(l.p.x, l.p.y), make_float2(l.p.z, l.p.w)}, m[2], v[2], root[2];
+  if (BITS == 32) {
+    m[0] = make_float2(l.m.x, l.m.y), m[1] = make_float2(l.m.z, l.m.w);
+    v[0] = make_float2(l.v.x, l.v.y), v[1] = make_float2(l.v.z, l.v.w);
+  } else {
+    m[0] = codes2(l.qm, l.sm), m[1] = codes2(l.qm >> 16, l.sm);
+    v[0] = codes2(l.qv, l.sv), v[1] = codes2(l.qv >> 16, l.sv);
+    v[0] = mul2(v[0], v[0]), v[1] = mul2(v[1], v[1]);
+  }
+  update(sc, decay, make_float2(l.g.x, l.g.y), p[0], m[0], v[0], root[0]);
+  update(sc, decay, make_float2(l.g.z, l.g.w), p[1], m[1], v[1], root[1]);
+  store4(e.p + at, p, cnt);
+  if (e.w) store4_bf16(e.w, at, p, cnt);
+  if (BITS == 32) {
+    store4(static_cast<float*>(e.m) + at, m, cnt);
+    store4(static_cast<float*>(e.v) + at, v, cnt);
+    return;
+  }
+  // (fmaxf leaves a NaN out)
+  const float am = warp_max(fmaxf(fmaxf(fabsf(m[0].x), fabsf(m[0].y)),
+                                  fmaxf(fabsf(m[1].x), fabsf(m[1].y))));
+  const float av = warp_max(fmaxf(fmaxf(root[0].x, root[0].y), fmaxf(root[1].x, root[1].y)));
+  const float sm = block_scale(am), sv = block_scale(av);
+  const float rm = __frcp_rn(sm), rv = __frcp_rn(sv);
+  const bool pm = plain_scale(sm), pv = plain_scale(sv);
+  const uint32_t from = mix(key ^ static_cast<uint32_t>(block)) + lane * 4 * kGolden;
+  float2 cm[2], cv[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const uint32_t r0 = mix(from + 2 * j * kGolden), r1 = mix(from + (2 * j + 1) * kGolden);
+    const float2 q = round_e4m3(quotients(m[j], sm, rm, pm), r0, r1);
+    cm[j] = make_float2(copysignf(q.x, m[j].x), copysignf(q.y, m[j].y));
+    const float2 u = round_root_e4m3(quotients(root[j], sv, rv, pv), r0, r1);
+    // a second moment above 0 stays above 0 (its place in the quotient m / sqrt(v) must not)
+    cv[j] = make_float2(root[j].x > 0.0f && u.x < 0x1p-9f ? 0x1p-9f : u.x,
+                        root[j].y > 0.0f && u.y < 0x1p-9f ? 0x1p-9f : u.y);
+  }
+  store_codes(e.m, at, pack_codes(cm[0], cm[1]), cnt);
+  store_codes(e.v, at, pack_codes(cv[0], cv[1]), cnt);
+  if (lane == 0) {
+    e.m_scale[block] = sm;
+    e.v_scale[block] = sv;
+  }
 }
 
 template <int CAP, int BITS>
@@ -316,62 +435,33 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     if (blockIdx.x == 0 && threadIdx.x == 0) raise_status(&state->status, MOE_DEV_NONFINITE);
     return;
   }
+  constexpr int kWarps = kThreads / 32, kSteps = kChunk / (4 * kThreads);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
     const int t = tensor_of(tab, c);
     const moe_adam_tensor& e = tab.t[t];
-    const long long base = (long long)(c - tab.first[t]) * kChunk;
+    const long long chunk = c - tab.first[t];
     const bool f32 = e.g_dtype == MOE_F32;
     const float decay = sc.lr * e.weight_decay;
     const uint32_t key = BITS == 8 ? mix(e.seed ^ (sc.step * kGolden)) : 0;
     // a warp's four elements a lane are one block of 128
-#pragma unroll 2
-    for (int i = 0; i < kChunk / (4 * kThreads); ++i) {
-      const long long block = base / kBlock + i * (kThreads / 32) + warp;
-      const long long at = block * kBlock + lane * 4;
-      const long long left = e.n - at;
+    const long long first = chunk * (kChunk / kBlock) + warp;
+    if ((chunk + 1) * kChunk <= e.n) {
+      Loaded<BITS> next = load_block<BITS>(e, f32, first, lane, 4);
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        const Loaded<BITS> now = next;
+        if (i + 1 < kSteps) next = load_block<BITS>(e, f32, first + (i + 1) * kWarps, lane, 4);
+        step_block<BITS>(sc, e, decay, key, first + i * kWarps, lane, 4, now);
+      }
+      continue;
+    }
+    for (int i = 0; i < kSteps; ++i) {
+      const long long block = first + i * kWarps, left = e.n - block * kBlock - lane * 4;
       if (e.n <= block * kBlock) break;   // whole warps
       const int cnt = left >= 4 ? 4 : left > 0 ? (int)left : 0;
-      const float4 g4 = load_grad(e.g, f32, at, cnt);
-      const float4 p4 = load4(e.p + at, cnt);
-      float g[4] = {g4.x, g4.y, g4.z, g4.w}, p[4] = {p4.x, p4.y, p4.z, p4.w};
-      float m[4], v[4], root[4];
-      if (BITS == 32) {
-        const float4 m4 = load4(static_cast<const float*>(e.m) + at, cnt);
-        const float4 v4 = load4(static_cast<const float*>(e.v) + at, cnt);
-        m[0] = m4.x, m[1] = m4.y, m[2] = m4.z, m[3] = m4.w;
-        v[0] = v4.x, v[1] = v4.y, v[2] = v4.z, v[3] = v4.w;
-      } else {
-        const uint32_t qm = load_codes(e.m, at, cnt), qv = load_codes(e.v, at, cnt);
-        codes4(qm, e.m_scale[block], m);
-        codes4(qv, e.v_scale[block], v);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = __fmul_rn(v[j], v[j]);
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) update(sc, decay, g[j], p[j], m[j], v[j], root[j]);
-      store4(e.p + at, p, cnt);
-      if (e.w) store4_bf16(e.w, at, p, cnt);
-      if (BITS == 32) {
-        store4(static_cast<float*>(e.m) + at, m, cnt);
-        store4(static_cast<float*>(e.v) + at, v, cnt);
-      } else {
-        // (fmaxf leaves a NaN out)
-        const float am = warp_max(fmaxf(fmaxf(fabsf(m[0]), fabsf(m[1])),
-                                        fmaxf(fabsf(m[2]), fabsf(m[3]))));
-        const float av = warp_max(fmaxf(fmaxf(root[0], root[1]), fmaxf(root[2], root[3])));
-        const float sm = block_scale(am), sv = block_scale(av);
-        const uint32_t bkey = mix(key ^ static_cast<uint32_t>(block));
-        uint32_t r[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) r[j] = mix(bkey + (lane * 4 + j) * kGolden);
-        store_codes(e.m, at, hold4<false>(m, sm, r, 16), cnt);
-        store_codes(e.v, at, hold4<true>(root, sv, r, 0), cnt);
-        if (lane == 0) {
-          e.m_scale[block] = sm;
-          e.v_scale[block] = sv;
-        }
-      }
+      step_block<BITS>(sc, e, decay, key, block, lane, cnt,
+                       load_block<BITS>(e, f32, block, lane, cnt));
     }
   }
   if (more || !last_cta(&state->ticket) || threadIdx.x != 0) return;

@@ -11,9 +11,8 @@
 namespace moe {
 namespace {
 
-constexpr int kGpuSms = 152;       // grids are sized for GB300
-constexpr int kMaxThreads = 1024;  // a CTA; also the threads that a grid puts on one SM
-constexpr int kWsHead = 256;       // the status word's place at the head of the scratch
+constexpr int kGpuSms = 152;   // grids are sized for GB300
+constexpr int kWsHead = 256;   // the status word's place at the head of the scratch
 
 struct Shape {
   int rows, d, vecs;   // vecs = d / 8
@@ -21,47 +20,97 @@ struct Shape {
   int gate;
 };
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
-  f[0] = bf16_lo(v.x), f[1] = bf16_hi(v.x), f[2] = bf16_lo(v.y), f[3] = bf16_hi(v.y);
-  f[4] = bf16_lo(v.z), f[5] = bf16_hi(v.z), f[6] = bf16_lo(v.w), f[7] = bf16_hi(v.w);
+// 8 columns as fp32 pairs, whose operations are one instruction a pair.
+struct F8 {
+  float2 p[4];
+};
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
 }
-__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                    pack_bf16x2(f[6], f[7]));
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
 }
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ F8 operator*(const F8& a, const F8& b) {
+  F8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.p[i] = mul2(a.p[i], b.p[i]);
+  return r;
+}
+__device__ __forceinline__ F8 operator*(const F8& a, float b) {
+  F8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.p[i] = mul2(a.p[i], both(b));
+  return r;
+}
+__device__ __forceinline__ F8 fma(const F8& a, const F8& b, const F8& c) {
+  F8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.p[i] = fma2(a.p[i], b.p[i], c.p[i]);
+  return r;
+}
+__device__ __forceinline__ F8 fma(const F8& a, float b, const F8& c) {
+  F8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.p[i] = fma2(a.p[i], both(b), c.p[i]);
+  return r;
+}
+// adds the products of the columns to a pair of sums
+__device__ __forceinline__ void dot(const F8& a, const F8& b, float2& sum) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) sum = fma2(a.p[i], b.p[i], sum);
+}
+__device__ __forceinline__ F8 all(float v) { return F8{{both(v), both(v), both(v), both(v)}}; }
 
-// 8 consecutive values of the residual stream: 16 bytes of bf16 or 32 of fp32.
+// 8 columns of bf16 (16 bytes) or, F32, of fp32 (32 bytes).
 template <bool F32>
-__device__ __forceinline__ void read8(const char* at, float (&f)[8]) {
+__device__ __forceinline__ F8 read8(const char* at) {
   if (F32) {
     const float4 a = *reinterpret_cast<const float4*>(at);
     const float4 b = *reinterpret_cast<const float4*>(at + 16);
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-  } else {
-    unpack8(*reinterpret_cast<const uint4*>(at), f);
+    return F8{{make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y),
+               make_float2(b.z, b.w)}};
   }
+  const uint4 v = *reinterpret_cast<const uint4*>(at);
+  return F8{{make_float2(bf16_lo(v.x), bf16_hi(v.x)), make_float2(bf16_lo(v.y), bf16_hi(v.y)),
+             make_float2(bf16_lo(v.z), bf16_hi(v.z)), make_float2(bf16_lo(v.w), bf16_hi(v.w))}};
 }
 template <bool F32>
-__device__ __forceinline__ void write8(char* at, const float (&f)[8]) {
+__device__ __forceinline__ void write8(char* at, const F8& f) {
   if (F32) {
-    *reinterpret_cast<float4*>(at) = make_float4(f[0], f[1], f[2], f[3]);
-    *reinterpret_cast<float4*>(at + 16) = make_float4(f[4], f[5], f[6], f[7]);
+    *reinterpret_cast<float4*>(at) = make_float4(f.p[0].x, f.p[0].y, f.p[1].x, f.p[1].y);
+    *reinterpret_cast<float4*>(at + 16) = make_float4(f.p[2].x, f.p[2].y, f.p[3].x, f.p[3].y);
   } else {
-    *reinterpret_cast<uint4*>(at) = pack8(f);
+    *reinterpret_cast<uint4*>(at) =
+        make_uint4(pack_bf16x2(f.p[0].x, f.p[0].y), pack_bf16x2(f.p[1].x, f.p[1].y),
+                   pack_bf16x2(f.p[2].x, f.p[2].y), pack_bf16x2(f.p[3].x, f.p[3].y));
   }
 }
-__device__ __forceinline__ void load_weights(const float* w, int vec, bool in, float (&f)[8],
-                                             float none) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) f[j] = none;
-  if (w && in) read8<true>(reinterpret_cast<const char*>(w) + (size_t)vec * 32, f);
+// 8 columns of a weight, `none` where there is no weight or no column.
+__device__ __forceinline__ F8 weights(const float* w, int vec, bool in, float none) {
+  if (!w || !in) return all(none);
+  return read8<true>(reinterpret_cast<const char*>(w) + (size_t)vec * 32);
 }
 
 __device__ __forceinline__ void copy16(char* smem, const char* gmem) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(smem)), "l"(gmem)
                : "memory");
 }
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copies_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
 template <int N>
 __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
@@ -92,8 +141,9 @@ __device__ __forceinline__ void cta_sum(float (&v)[K], float* buf, int& flip) {
     for (int i = 0; i < K; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
 }
 
-__device__ __forceinline__ float inv_root(float sum, const Shape& s) {
-  return 1.0f / sqrtf(sum / static_cast<float>(s.d) + s.eps);
+// 1/sqrt(mean + eps). rsqrtf is off by 2^-22 at most, a sixteenth of what the sum may be.
+__device__ __forceinline__ float inv_root(float sum, float inv_d, float eps) {
+  return rsqrtf(__fmaf_rn(sum, inv_d, eps));
 }
 
 // The arrays of a row in the ring: slot(array, vec) of a stage. Sizes in bytes a vector.
@@ -123,8 +173,13 @@ __device__ __forceinline__ void fetch_row(const Arrays& a, char* stage, long lon
   }
 }
 
+// Most threads of a CTA that takes VPT vectors a thread, and the CTAs of that size an SM holds.
+constexpr int most_threads(int vpt) { return vpt == 1 ? 256 : 512; }
+constexpr int most_ctas(int vpt) { return vpt == 1 ? 3 : 1; }
+
 template <bool F32, int VPT, int STAGES>
-__global__ void __launch_bounds__(kMaxThreads, 1) norm_kernel(Shape s, NormFwd a, int stage_bytes) {
+__global__ void __launch_bounds__(most_threads(VPT), most_ctas(VPT))
+    norm_kernel(Shape s, NormFwd a, int stage_bytes) {
   extern __shared__ __align__(16) char ring[];
   __shared__ float sums[2 * 32];
   constexpr int kSt = F32 ? 32 : 16;
@@ -135,29 +190,25 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_kernel(Shape s, NormFwd a
   in.p[1] = static_cast<const char*>(a.y), in.bytes[1] = has_y ? 16 : 0;
   in.p[2] = static_cast<const char*>(a.gate), in.bytes[2] = elem ? 16 : 0;
   const int off_y = s.vecs * kSt, off_g = off_y + (has_y ? s.vecs * 16 : 0);
-
-  // what a column's normed output is multiplied by: out, the channel gate and the weight; and the
-  // next norm's weight
-  float gw[VPT][8], wn[VPT][8];
-#pragma unroll
-  for (int k = 0; k < VPT; ++k) {
-    const int v = threadIdx.x + k * blockDim.x;
-    const bool col = v < s.vecs;
-    float g[8];
-    load_weights(a.w_post, v, col, gw[k], 1.0f);
-    load_weights(s.gate == MOE_GATE_CHANNEL ? static_cast<const float*>(a.gate) : nullptr, v, col, g,
-                 1.0f);
-    load_weights(a.w_next, v, col, wn[k], 0.0f);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) gw[k][j] *= s.out * g[j];
-  }
   const int step = gridDim.x;
+  const float inv_d = 1.0f / static_cast<float>(s.d);
   int flip = 0, slot = 0;
 #pragma unroll
   for (int i = 0; i < STAGES - 1; ++i) {
     const long long r = blockIdx.x + (long long)i * step;
     if (r < s.rows) fetch_row<3, VPT>(in, ring + (size_t)i * stage_bytes, r, s.vecs);
     copies_commit();
+  }
+  // what a column's normed output is multiplied by: out, the channel gate and the weight; and the
+  // next norm's weight
+  F8 gw[VPT], wn[VPT];
+#pragma unroll
+  for (int k = 0; k < VPT; ++k) {
+    const int v = threadIdx.x + k * blockDim.x;
+    const bool col = v < s.vecs;
+    const float* g = s.gate == MOE_GATE_CHANNEL ? static_cast<const float*>(a.gate) : nullptr;
+    gw[k] = weights(a.w_post, v, col, 1.0f) * weights(g, v, col, 1.0f) * s.out;
+    wn[k] = weights(a.w_next, v, col, 0.0f);
   }
   for (long long row = blockIdx.x; row < s.rows; row += step) {
     {
@@ -166,60 +217,51 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_kernel(Shape s, NormFwd a
       if (ahead < s.rows) fetch_row<3, VPT>(in, ring + (size_t)to * stage_bytes, ahead, s.vecs);
       copies_commit();
     }
+    float factor = 1.0f;   // of this row's y
+    if (s.gate == MOE_GATE_TOKEN) factor = static_cast<const float*>(a.gate)[row];
     copies_wait<STAGES - 1>();
     const char* st = ring + (size_t)slot * stage_bytes;
     slot = slot + 1 == STAGES ? 0 : slot + 1;
-    float h[VPT][8];
-    float factor = 1.0f;   // of this row's y
     if (post) {
-      float q[1] = {0.0f};
+      float2 q = both(0.0f);
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
         const int v = threadIdx.x + k * blockDim.x;
         if (v >= s.vecs) continue;
-        float y[8];
-        read8<false>(st + off_y + (size_t)v * 16, y);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) q[0] = __fmaf_rn(y[j], y[j], q[0]);
+        const F8 y = read8<false>(st + off_y + (size_t)v * 16);
+        dot(y, y, q);
       }
-      cta_sum<1>(q, sums, flip);
-      factor = inv_root(q[0], s);
-      if (threadIdx.x == 0 && a.rstd_y) a.rstd_y[row] = factor;
+      float sum[1] = {q.x + q.y};
+      cta_sum<1>(sum, sums, flip);
+      const float r = inv_root(sum[0], inv_d, s.eps);
+      if (threadIdx.x == 0 && a.rstd_y) a.rstd_y[row] = r;
+      factor *= r;
     }
-    if (s.gate == MOE_GATE_TOKEN) factor *= static_cast<const float*>(a.gate)[row];
-    float q[1] = {0.0f};
+    F8 h[VPT];
+    float2 q = both(0.0f);
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       const int v = threadIdx.x + k * blockDim.x;
       if (v >= s.vecs) continue;
-      read8<F32>(st + (size_t)v * kSt, h[k]);
+      h[k] = read8<F32>(st + (size_t)v * kSt);
       if (has_y) {
-        float y[8], g[8];
-        read8<false>(st + off_y + (size_t)v * 16, y);
-        if (elem) {
-          read8<false>(st + off_g + (size_t)v * 16, g);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) y[j] *= g[j];
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) h[k][j] = __fmaf_rn(y[j] * factor, gw[k][j], s.res * h[k][j]);
+        F8 y = read8<false>(st + off_y + (size_t)v * 16);
+        if (elem) y = y * read8<false>(st + off_g + (size_t)v * 16);
+        h[k] = fma(y * factor, gw[k], h[k] * s.res);
         write8<F32>(static_cast<char*>(a.h) + ((size_t)row * s.vecs + v) * kSt, h[k]);
       }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) q[0] = __fmaf_rn(h[k][j], h[k][j], q[0]);
+      dot(h[k], h[k], q);
     }
     if (!next) continue;
-    cta_sum<1>(q, sums, flip);
-    const float r = inv_root(q[0], s);
+    float sum[1] = {q.x + q.y};
+    cta_sum<1>(sum, sums, flip);
+    const float r = inv_root(sum[0], inv_d, s.eps);
     if (threadIdx.x == 0 && a.rstd_h) a.rstd_h[row] = r;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       const int v = threadIdx.x + k * blockDim.x;
       if (v >= s.vecs) continue;
-      float o[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = h[k][j] * r * wn[k][j];
-      write8<false>(static_cast<char*>(a.n) + ((size_t)row * s.vecs + v) * 16, o);
+      write8<false>(static_cast<char*>(a.n) + ((size_t)row * s.vecs + v) * 16, h[k] * r * wn[k]);
     }
   }
 }
@@ -229,18 +271,21 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_kernel(Shape s, NormFwd a
 //   sum u G = sum u (dh + r_h a) - r_h mean(a hh) sum u hh.
 // The second pass reads the row again from the ring. Column sums: acc_y = sum out G gate yh (without
 // a channel gate, which like w_post is the same in all rows: dw_post = gate acc_y, dgate = w_post
-// acc_y) and acc_n = sum dn hh.
+// acc_y) and acc_n = sum dn hh. With 4 vectors a thread the weights do not fit the registers beside
+// those: they are read again for each row, from L2.
 template <bool F32, int VPT, int STAGES>
-__global__ void __launch_bounds__(kMaxThreads, 1)
+__global__ void __launch_bounds__(most_threads(VPT), most_ctas(VPT))
     norm_grad_kernel(Shape s, NormGrad a, int stage_bytes, float* partial) {
   extern __shared__ __align__(16) char ring[];
   __shared__ float sums[2 * 32 * 3];
   constexpr int kSt = F32 ? 32 : 16;
+  constexpr bool kKeep = VPT <= 2;
   const bool post = a.w_post != nullptr, next = a.w_next != nullptr, has_dh = a.dh != nullptr;
   const bool elem = s.gate == MOE_GATE_ELEMENT, token = s.gate == MOE_GATE_TOKEN;
   const bool has_y = post || s.gate != MOE_GATE_NONE;   // y itself is needed
   const bool is_out = a.dy != nullptr;                  // the norm before a block has no y side
   const bool dot_y = post || token;
+  const float* channel = s.gate == MOE_GATE_CHANNEL ? static_cast<const float*>(a.gate) : nullptr;
   Arrays in;
   in.p[0] = static_cast<const char*>(a.dh), in.bytes[0] = has_dh ? kSt : 0;
   in.p[1] = static_cast<const char*>(a.h), in.bytes[1] = next ? kSt : 0;
@@ -251,23 +296,6 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
   const int off_n = off_h + (next ? s.vecs * kSt : 0);
   const int off_y = off_n + (next ? s.vecs * 16 : 0);
   const int off_g = off_y + (has_y ? s.vecs * 16 : 0);
-
-  float gw[VPT][8], wn[VPT][8], acc_y[VPT][8], acc_n[VPT][8];
-#pragma unroll
-  for (int k = 0; k < VPT; ++k) {
-    const int v = threadIdx.x + k * blockDim.x;
-    const bool col = v < s.vecs;
-    float g[8];
-    load_weights(a.w_post, v, col, gw[k], 1.0f);
-    load_weights(s.gate == MOE_GATE_CHANNEL ? static_cast<const float*>(a.gate) : nullptr, v, col, g,
-                 1.0f);
-    load_weights(a.w_next, v, col, wn[k], 0.0f);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      gw[k][j] *= g[j];
-      acc_y[k][j] = acc_n[k][j] = 0.0f;
-    }
-  }
   const int step = gridDim.x;
   const float inv_d = 1.0f / static_cast<float>(s.d);
   int flip = 0, slot = 0;
@@ -276,6 +304,20 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
     const long long r = blockIdx.x + (long long)i * step;
     if (r < s.rows) fetch_row<5, VPT>(in, ring + (size_t)i * stage_bytes, r, s.vecs);
     copies_commit();
+  }
+  const auto weight_y = [&](int v, bool col) {
+    F8 w = weights(a.w_post, v, col, 1.0f);
+    return channel ? w * weights(channel, v, col, 1.0f) : w;
+  };
+  F8 keep_y[kKeep ? VPT : 1], keep_n[kKeep ? VPT : 1], acc_y[VPT], acc_n[VPT];
+#pragma unroll
+  for (int k = 0; k < VPT; ++k) {
+    const int v = threadIdx.x + k * blockDim.x;
+    if (kKeep) {
+      keep_y[k] = weight_y(v, v < s.vecs);
+      keep_n[k] = weights(a.w_next, v, v < s.vecs, 0.0f);
+    }
+    acc_y[k] = acc_n[k] = all(0.0f);
   }
   for (long long row = blockIdx.x; row < s.rows; row += step) {
     {
@@ -290,88 +332,60 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
     const char* st = ring + (size_t)slot * stage_bytes;
     slot = slot + 1 == STAGES ? 0 : slot + 1;
 
-    float q[3] = {0.0f, 0.0f, 0.0f};   // sum a hh, sum u (dh + rh a), sum u hh
+    float2 qa = both(0.0f), qg = qa, qh = qa;   // sums of a h, u (dh + rh a) and u h (h, u: no r)
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       const int v = threadIdx.x + k * blockDim.x;
       if (v >= s.vecs) continue;
-      float dh[8] = {}, h[8] = {}, dn[8] = {};
-      if (has_dh) read8<F32>(st + (size_t)v * kSt, dh);
+      F8 dh = all(0.0f), h = dh;
+      if (has_dh) dh = read8<F32>(st + (size_t)v * kSt);
       if (next) {
-        read8<F32>(st + off_h + (size_t)v * kSt, h);
-        read8<false>(st + off_n + (size_t)v * 16, dn);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          h[j] *= rh;
-          dn[j] *= wn[k][j];
-          q[0] = __fmaf_rn(dn[j], h[j], q[0]);
-          dh[j] = __fmaf_rn(rh, dn[j], dh[j]);
-        }
+        h = read8<F32>(st + off_h + (size_t)v * kSt);
+        const F8 d = read8<false>(st + off_n + (size_t)v * 16) *
+                     (kKeep ? keep_n[k] : weights(a.w_next, v, true, 0.0f));
+        dot(d, h, qa);
+        dh = fma(d, rh, dh);
       }
       if (dot_y) {
-        float y[8], g[8];
-        read8<false>(st + off_y + (size_t)v * 16, y);
-        if (elem) read8<false>(st + off_g + (size_t)v * 16, g);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          float u = y[j] * gw[k][j];
-          if (elem) u *= g[j];
-          q[1] = __fmaf_rn(u, dh[j], q[1]);
-          q[2] = __fmaf_rn(u, h[j], q[2]);
-        }
+        F8 u = read8<false>(st + off_y + (size_t)v * 16) * (kKeep ? keep_y[k] : weight_y(v, true));
+        if (elem) u = u * read8<false>(st + off_g + (size_t)v * 16);
+        dot(u, dh, qg);
+        dot(u, h, qh);
       }
     }
+    float q[3] = {qa.x + qa.y, qg.x + qg.y, qh.x + qh.y};
     if (next || dot_y) cta_sum<3>(q, sums, flip);
-    const float c1 = q[0] * inv_d;
-    const float along = s.out * ry * (q[1] - rh * c1 * q[2]);   // sum out G s (no token gate)
+    const float c1 = rh * q[0] * inv_d;                          // mean a hh
+    const float along = s.out * ry * (q[1] - rh * c1 * (rh * q[2]));   // sum out G s, no token gate
     const float mean = gt * along * inv_d;
     if (token && a.dgate && threadIdx.x == 0) static_cast<float*>(a.dgate)[row] = along;
+    const float hc = -c1 * rh;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       const int v = threadIdx.x + k * blockDim.x;
       if (v >= s.vecs) continue;
       const size_t at = (size_t)row * s.vecs + v;
-      float G[8] = {};
-      if (has_dh) read8<F32>(st + (size_t)v * kSt, G);
+      F8 G = all(0.0f);
+      if (has_dh) G = read8<F32>(st + (size_t)v * kSt);
       if (next) {
-        float h[8], dn[8];
-        read8<F32>(st + off_h + (size_t)v * kSt, h);
-        read8<false>(st + off_n + (size_t)v * 16, dn);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float hh = h[j] * rh;
-          G[j] = __fmaf_rn(rh, __fmaf_rn(dn[j], wn[k][j], -hh * c1), G[j]);
-          acc_n[k][j] = __fmaf_rn(dn[j], hh, acc_n[k][j]);
-        }
+        const F8 h = read8<F32>(st + off_h + (size_t)v * kSt);
+        const F8 dn = read8<false>(st + off_n + (size_t)v * 16);
+        G = fma(fma(dn, kKeep ? keep_n[k] : weights(a.w_next, v, true, 0.0f), h * hc), rh, G);
+        acc_n[k] = fma(dn, h * rh, acc_n[k]);
       }
-      if (a.dx) {
-        float o[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = s.res * G[j];
-        write8<F32>(static_cast<char*>(a.dx) + at * kSt, o);
-      }
+      if (a.dx) write8<F32>(static_cast<char*>(a.dx) + at * kSt, G * s.res);
       if (!is_out) continue;
-      float y[8] = {}, g[8], o[8];
-      if (has_y) read8<false>(st + off_y + (size_t)v * 16, y);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) G[j] *= s.out;
+      G = G * (s.out * gt);
+      const F8 gw = kKeep ? keep_y[k] : weight_y(v, true);
+      F8 yh = all(0.0f);
+      if (has_y) yh = read8<false>(st + off_y + (size_t)v * 16) * ry;
       if (elem) {
-        read8<false>(st + off_g + (size_t)v * 16, g);
-        if (a.dgate) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) o[j] = G[j] * y[j] * ry * gw[k][j];
-          write8<false>(static_cast<char*>(a.dgate) + at * 16, o);
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) G[j] *= g[j];
+        if (a.dgate) write8<false>(static_cast<char*>(a.dgate) + at * 16, G * yh * gw);
+        G = G * read8<false>(st + off_g + (size_t)v * 16);
       }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float yh = y[j] * ry, u = gt * G[j];
-        acc_y[k][j] = __fmaf_rn(u, yh, acc_y[k][j]);
-        o[j] = post ? ry * __fmaf_rn(u, gw[k][j], -yh * mean) : u * gw[k][j];
-      }
-      write8<false>(static_cast<char*>(a.dy) + at * 16, o);
+      acc_y[k] = fma(G, yh, acc_y[k]);
+      write8<false>(static_cast<char*>(a.dy) + at * 16,
+                    post ? fma(yh, -mean, G * gw) * ry : G * gw);
     }
   }
   if (!partial) return;
@@ -423,16 +437,16 @@ __global__ void __launch_bounds__(kColThreads) norm_columns_kernel(ColSums a) {
   }
 }
 
-// Threads of a CTA, vectors a thread and the CTAs that an SM takes at once.
+// Vectors a thread, threads of a CTA and the CTAs that an SM takes at once.
 struct Plan {
   int vpt, threads, per_sm;
 };
 Plan plan_of(int d) {
   const int vecs = d / 8;
   Plan p;
-  p.vpt = vecs > kMaxThreads ? 2 : 1;
+  p.vpt = vecs <= 256 ? 1 : vecs <= 1024 ? 2 : 4;
   p.threads = ((vecs + p.vpt - 1) / p.vpt + 31) / 32 * 32;
-  p.per_sm = kMaxThreads / p.threads;
+  p.per_sm = most_threads(p.vpt) * most_ctas(p.vpt) / p.threads;
   return p;
 }
 unsigned grid_of(int rows, const Plan& p) {
@@ -440,15 +454,21 @@ unsigned grid_of(int rows, const Plan& p) {
   return rows < most ? rows : most;
 }
 
-constexpr int kFwdStages = 4, kGradStages = 3;
+// Stages of the ring: as many as the SM's CTAs can have, 4 at most. (The widest row of a gradient,
+// 16384 columns with an fp32 stream and a gate of their own, is 224 KB: one stage.)
+int stages_of(size_t stage, const Plan& p) {
+  const size_t all = stage * p.per_sm;
+  return all * 4 <= 220 * 1024 ? 4 : all * 3 <= 220 * 1024 ? 3 : all * 2 <= 224 * 1024 ? 2 : 1;
+}
 
 template <typename K>
-cudaError_t set_smem(K kern, size_t bytes) {
-  return ensure_smem_limit(reinterpret_cast<const void*>(kern), bytes);
+cudaError_t set_smem(K kern, size_t bytes) {   // (1 KB more: the static arrays count, too)
+  return ensure_smem_limit(reinterpret_cast<const void*>(kern), bytes + 1024);
 }
 
 template <bool F32, int VPT, int STAGES>
-cudaError_t run_fwd(const Shape& s, const NormFwd& a, const Plan& p, int stage, cudaStream_t st) {
+cudaError_t run(const Shape& s, const NormFwd& a, const Plan& p, int stage, float*,
+                cudaStream_t st) {
   auto kern = norm_kernel<F32, VPT, STAGES>;
   const size_t smem = (size_t)STAGES * stage;
   const cudaError_t e = set_smem(kern, smem);
@@ -456,16 +476,32 @@ cudaError_t run_fwd(const Shape& s, const NormFwd& a, const Plan& p, int stage, 
   return launch_kernel(kern, dim3(grid_of(s.rows, p)), dim3(p.threads), smem, st, false, s, a,
                        stage);
 }
-
 template <bool F32, int VPT, int STAGES>
-cudaError_t run_grad(const Shape& s, const NormGrad& a, const Plan& p, int stage, float* partial,
-                     cudaStream_t st) {
+cudaError_t run(const Shape& s, const NormGrad& a, const Plan& p, int stage, float* partial,
+                cudaStream_t st) {
   auto kern = norm_grad_kernel<F32, VPT, STAGES>;
   const size_t smem = (size_t)STAGES * stage;
   const cudaError_t e = set_smem(kern, smem);
   if (e != cudaSuccess) return e;
   return launch_kernel(kern, dim3(grid_of(s.rows, p)), dim3(p.threads), smem, st, false, s, a, stage,
                        partial);
+}
+template <bool F32, int VPT, typename A>
+cudaError_t run_stages(const Shape& s, const A& a, const Plan& p, int stage, float* partial,
+                       cudaStream_t st) {
+  switch (stages_of(stage, p)) {
+    case 4: return run<F32, VPT, 4>(s, a, p, stage, partial, st);
+    case 3: return run<F32, VPT, 3>(s, a, p, stage, partial, st);
+    case 2: return run<F32, VPT, 2>(s, a, p, stage, partial, st);
+    default: return run<F32, VPT, 1>(s, a, p, stage, partial, st);
+  }
+}
+template <bool F32, typename A>
+cudaError_t run_any(const Shape& s, const A& a, const Plan& p, int stage, float* partial,
+                    cudaStream_t st) {
+  return p.vpt == 1   ? run_stages<F32, 1>(s, a, p, stage, partial, st)
+         : p.vpt == 2 ? run_stages<F32, 2>(s, a, p, stage, partial, st)
+                      : run_stages<F32, 4>(s, a, p, stage, partial, st);
 }
 
 Shape shape_of(const moe_norm_cfg& c) {
@@ -484,18 +520,8 @@ cudaError_t launch_norm(const moe_norm_cfg& c, const NormFwd& a, cudaStream_t st
   const bool f32 = c.stream_dtype == MOE_F32;
   const int stage = s.vecs * ((f32 ? 32 : 16) + (a.y ? 16 : 0) +
                               (c.gate == MOE_GATE_ELEMENT ? 16 : 0));
-  // widest row: 16384 columns of fp32 stream, y and an element gate are 128 KB a stage: one stage
-  const bool deep = (size_t)stage * kFwdStages * p.per_sm <= 200 * 1024;
-  if (p.vpt == 1) {
-    if (f32) return deep ? run_fwd<true, 1, kFwdStages>(s, a, p, stage, st)
-                         : run_fwd<true, 1, 2>(s, a, p, stage, st);
-    return deep ? run_fwd<false, 1, kFwdStages>(s, a, p, stage, st)
-                : run_fwd<false, 1, 2>(s, a, p, stage, st);
-  }
-  const bool two = (size_t)stage * 2 <= 220 * 1024;
-  if (f32) return two ? run_fwd<true, 2, 2>(s, a, p, stage, st)
-                      : run_fwd<true, 2, 1>(s, a, p, stage, st);
-  return run_fwd<false, 2, 2>(s, a, p, stage, st);
+  return f32 ? run_any<true>(s, a, p, stage, nullptr, st)
+             : run_any<false>(s, a, p, stage, nullptr, st);
 }
 
 cudaError_t launch_norm_grad(const moe_norm_cfg& c, const NormGrad& a, bool accumulate, void* ws,
@@ -511,28 +537,9 @@ cudaError_t launch_norm_grad(const moe_norm_cfg& c, const NormGrad& a, bool accu
   const bool sums = a.dw_post || a.dw_next || (channel && a.dgate);
   float* partial =
       sums ? reinterpret_cast<float*>(static_cast<char*>(ws) + kWsHead) : nullptr;
-  cudaError_t e;
   if (s.rows > 0) {
-    const size_t per_sm = (size_t)stage * p.per_sm;
-    const int stages = per_sm * kGradStages <= 220 * 1024 ? kGradStages
-                       : per_sm * 2 <= 220 * 1024         ? 2
-                                                          : 1;
-#define MOE_GRAD_CASE(F, V, S) \
-  if (f32 == F && p.vpt == V && stages == S) e = run_grad<F, V, S>(s, a, p, stage, partial, st)
-    e = cudaErrorInvalidValue;
-    MOE_GRAD_CASE(false, 1, 3);
-    MOE_GRAD_CASE(false, 1, 2);
-    MOE_GRAD_CASE(false, 1, 1);
-    MOE_GRAD_CASE(true, 1, 3);
-    MOE_GRAD_CASE(true, 1, 2);
-    MOE_GRAD_CASE(true, 1, 1);
-    MOE_GRAD_CASE(false, 2, 3);
-    MOE_GRAD_CASE(false, 2, 2);
-    MOE_GRAD_CASE(false, 2, 1);
-    MOE_GRAD_CASE(true, 2, 3);
-    MOE_GRAD_CASE(true, 2, 2);
-    MOE_GRAD_CASE(true, 2, 1);
-#undef MOE_GRAD_CASE
+    const cudaError_t e = f32 ? run_any<true>(s, a, p, stage, partial, st)
+                              : run_any<false>(s, a, p, stage, partial, st);
     if (e != cudaSuccess) return e;
   }
   if (!sums) return cudaSuccess;

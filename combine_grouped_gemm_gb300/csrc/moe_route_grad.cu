@@ -592,7 +592,8 @@ cudaError_t launch_route_grad(const moe_cfg& c, const void* x, const float* w_ga
   Entry* list = reinterpret_cast<Entry*>(w + L.list);
   float* partial = reinterpret_cast<float*>(w + L.partial);
   const size_t masks = sizeof(ListSmem) + sizeof(uint32_t) * kMaskStride * (size_t)c.E;
-  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(route_grad_list_kernel), masks);
+  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(route_grad_list_kernel),
+                                    masks + 1024);   // (the static array counts, too)
   if (e != cudaSuccess) return e;
   e = launch_kernel(route_grad_list_kernel, dim3(L.chunks), dim3(kListThreads), masks, st, false,
                     topk_idx, topk_s, dtopk_w, c.T, c.k, L.kp, c.E, c.route_scale, L.chunk, L.stride,

@@ -519,8 +519,7 @@ def test_adamw_8_bit_code_by_code(moe, sizes, clip):
         factor = None
         if clip:
             moe.grad_norm(plan, state, norm)
-            if float(norm) > f(0.01):
-                factor = f(0.01) / norm.cpu().numpy()[0]
+            factor = min(f(0.01) * (f(1) / norm.cpu().numpy()[0]), f(1))
         moe.adamw(cfg, plan, state, norm if clip else None)
         for a, b in zip(before, T):
             n = a["p"].numel()
