@@ -7,6 +7,7 @@
 // next rows' copies in flight; a thread reads only what its own cp.async brought, so the ring needs
 // no barrier. The one barrier of a reduction over a row is the one between its warps' partial sums.
 #include "moe_device.cuh"
+#include "moe_f32x2.cuh"
 
 namespace moe {
 namespace {
@@ -20,87 +21,51 @@ struct Shape {
   int gate;
 };
 
-// 8 columns as fp32 pairs, whose operations are one instruction a pair.
+// 8 columns as fp32 pairs.
 struct F8 {
-  float2 p[4];
+  f32x2 p[4];
 };
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 x, y, z;\n\t"
-      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-      "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
+__device__ __forceinline__ F8 all(f32x2 v) { return F8{{v, v, v, v}}; }
+__device__ __forceinline__ F8 mul(const F8& a, const F8& b) {
+  return F8{{mul2(a.p[0], b.p[0]), mul2(a.p[1], b.p[1]), mul2(a.p[2], b.p[2]),
+             mul2(a.p[3], b.p[3])}};
 }
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n\t.reg .b64 x, y, z, w;\n\t"
-      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
-      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
-__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
-__device__ __forceinline__ F8 operator*(const F8& a, const F8& b) {
-  F8 r;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) r.p[i] = mul2(a.p[i], b.p[i]);
-  return r;
-}
-__device__ __forceinline__ F8 operator*(const F8& a, float b) {
-  F8 r;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) r.p[i] = mul2(a.p[i], both(b));
-  return r;
-}
+__device__ __forceinline__ F8 mul(const F8& a, f32x2 b) { return mul(a, all(b)); }
 __device__ __forceinline__ F8 fma(const F8& a, const F8& b, const F8& c) {
-  F8 r;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) r.p[i] = fma2(a.p[i], b.p[i], c.p[i]);
-  return r;
+  return F8{{fma2(a.p[0], b.p[0], c.p[0]), fma2(a.p[1], b.p[1], c.p[1]),
+             fma2(a.p[2], b.p[2], c.p[2]), fma2(a.p[3], b.p[3], c.p[3])}};
 }
-__device__ __forceinline__ F8 fma(const F8& a, float b, const F8& c) {
-  F8 r;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) r.p[i] = fma2(a.p[i], both(b), c.p[i]);
-  return r;
-}
+__device__ __forceinline__ F8 fma(const F8& a, f32x2 b, const F8& c) { return fma(a, all(b), c); }
 // adds the products of the columns to a pair of sums
-__device__ __forceinline__ void dot(const F8& a, const F8& b, float2& sum) {
+__device__ __forceinline__ void dot(const F8& a, const F8& b, f32x2& sum) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) sum = fma2(a.p[i], b.p[i], sum);
 }
-__device__ __forceinline__ F8 all(float v) { return F8{{both(v), both(v), both(v), both(v)}}; }
 
 // 8 columns of bf16 (16 bytes) or, F32, of fp32 (32 bytes).
 template <bool F32>
 __device__ __forceinline__ F8 read8(const char* at) {
   if (F32) {
-    const float4 a = *reinterpret_cast<const float4*>(at);
-    const float4 b = *reinterpret_cast<const float4*>(at + 16);
-    return F8{{make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y),
-               make_float2(b.z, b.w)}};
+    const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(at);
+    const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(at + 16);
+    return F8{{a.x, a.y, b.x, b.y}};
   }
   const uint4 v = *reinterpret_cast<const uint4*>(at);
-  return F8{{make_float2(bf16_lo(v.x), bf16_hi(v.x)), make_float2(bf16_lo(v.y), bf16_hi(v.y)),
-             make_float2(bf16_lo(v.z), bf16_hi(v.z)), make_float2(bf16_lo(v.w), bf16_hi(v.w))}};
+  return F8{{pair_of_bf16(v.x), pair_of_bf16(v.y), pair_of_bf16(v.z), pair_of_bf16(v.w)}};
 }
 template <bool F32>
 __device__ __forceinline__ void write8(char* at, const F8& f) {
   if (F32) {
-    *reinterpret_cast<float4*>(at) = make_float4(f.p[0].x, f.p[0].y, f.p[1].x, f.p[1].y);
-    *reinterpret_cast<float4*>(at + 16) = make_float4(f.p[2].x, f.p[2].y, f.p[3].x, f.p[3].y);
+    *reinterpret_cast<ulonglong2*>(at) = make_ulonglong2(f.p[0], f.p[1]);
+    *reinterpret_cast<ulonglong2*>(at + 16) = make_ulonglong2(f.p[2], f.p[3]);
   } else {
-    *reinterpret_cast<uint4*>(at) =
-        make_uint4(pack_bf16x2(f.p[0].x, f.p[0].y), pack_bf16x2(f.p[1].x, f.p[1].y),
-                   pack_bf16x2(f.p[2].x, f.p[2].y), pack_bf16x2(f.p[3].x, f.p[3].y));
+    *reinterpret_cast<uint4*>(at) = make_uint4(bf16_of_pair(f.p[0]), bf16_of_pair(f.p[1]),
+                                               bf16_of_pair(f.p[2]), bf16_of_pair(f.p[3]));
   }
 }
 // 8 columns of a weight, `none` where there is no weight or no column.
 __device__ __forceinline__ F8 weights(const float* w, int vec, bool in, float none) {
-  if (!w || !in) return all(none);
+  if (!w || !in) return all(both(none));
   return read8<true>(reinterpret_cast<const char*>(w) + (size_t)vec * 32);
 }
 
@@ -116,29 +81,56 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// K sums over the CTA, every thread gets them, in a fixed order. buf: 2 x 32 x K floats, the halves
-// used in turn (flip), so that one barrier a reduction is enough.
-template <int K>
-__device__ __forceinline__ void cta_sum(float (&v)[K], float* buf, int& flip) {
+// Sums over the CTA (16 warps at most) that every thread gets, in a fixed order. buf: two halves of
+// 16 floats a sum, used in turn (flip), so that one barrier a reduction is enough.
+__device__ __forceinline__ float lanes_xor(float v, int o) {
+  return __shfl_xor_sync(0xffffffffu, v, o);
+}
+__device__ __forceinline__ void cta_sum(float& v, float* buf, int& flip) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-    for (int i = 0; i < K; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+  for (int o = 16; o > 0; o >>= 1) v += lanes_xor(v, o);
   const int warps = blockDim.x >> 5;
   if (warps == 1) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float* b = buf + flip * 32 * K;
+  float* b = buf + flip * 16;
   flip ^= 1;
-  if (lane == 0)
-#pragma unroll
-    for (int i = 0; i < K; ++i) b[i * 32 + warp] = v[i];
+  if (lane == 0) b[warp] = v;
   __syncthreads();
+  v = (lane & 15) < warps ? b[lane & 15] : 0.0f;
 #pragma unroll
-  for (int i = 0; i < K; ++i) v[i] = lane < warps ? b[i * 32 + lane] : 0.0f;
+  for (int o = 8; o > 0; o >>= 1) v += lanes_xor(v, o);
+}
+// Three of them in 16 shuffles: lanes that have handed on a sum go on with another one.
+__device__ __forceinline__ void cta_sum3(float (&v)[3], float* buf, int& flip) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const bool up = lane & 16;
+  float a = (up ? v[1] : v[0]) + lanes_xor(up ? v[0] : v[1], 16);   // lanes 0-15: 0, 16-31: 1
+  float c = v[2] + lanes_xor(v[2], 16);
+  const bool third = lane & 8;
+  a = (third ? c : a) + lanes_xor(third ? a : c, 8);   // lanes 8-15 and 24-31: sum 2
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
+  for (int o = 4; o > 0; o >>= 1) a += lanes_xor(a, o);
+  if (warps == 1) {
+    v[0] = __shfl_sync(0xffffffffu, a, 0);
+    v[1] = __shfl_sync(0xffffffffu, a, 16);
+    v[2] = __shfl_sync(0xffffffffu, a, 8);
+    return;
+  }
+  float* b = buf + flip * 48;
+  flip ^= 1;
+  if ((lane & 7) == 0 && lane != 24) b[lane * 2 % 48 + warp] = a;   // lane 0: 0, 16: 1 (at 32), 8: 2
+  __syncthreads();
+  const int l = lane & 15;
+  a = l < warps ? b[(up ? 32 : 0) + l] : 0.0f;
+  c = l < warps ? b[16 + l] : 0.0f;
 #pragma unroll
-    for (int i = 0; i < K; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+  for (int o = 8; o > 0; o >>= 1) {
+    a += lanes_xor(a, o);
+    c += lanes_xor(c, o);
+  }
+  v[0] = __shfl_sync(0xffffffffu, a, 0);
+  v[1] = __shfl_sync(0xffffffffu, a, 16);
+  v[2] = c;
 }
 
 // 1/sqrt(mean + eps). rsqrtf is off by 2^-22 at most, a sixteenth of what the sum may be.
@@ -146,31 +138,14 @@ __device__ __forceinline__ float inv_root(float sum, float inv_d, float eps) {
   return rsqrtf(__fmaf_rn(sum, inv_d, eps));
 }
 
-// The arrays of a row in the ring: slot(array, vec) of a stage. Sizes in bytes a vector.
-struct Arrays {
-  const char* p[5];
-  int bytes[5];   // 16 or 32; 0: not there
-};
-
-// Starts the copies of one row (this thread's vectors) into a stage.
-template <int N, int VPT>
-__device__ __forceinline__ void fetch_row(const Arrays& a, char* stage, long long row, int vecs) {
-  char* dst = stage;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int b = a.bytes[i];
-    if (b == 0) continue;
-#pragma unroll
-    for (int k = 0; k < VPT; ++k) {
-      const int v = threadIdx.x + k * blockDim.x;
-      if (v < vecs) {
-        const char* src = a.p[i] + ((size_t)row * vecs + v) * b;
-        copy16(dst + (size_t)v * b, src);
-        if (b == 32) copy16(dst + (size_t)v * b + 16, src + 16);
-      }
-    }
-    dst += (size_t)vecs * b;
-  }
+// Starts the copy of this thread's 8 columns of a row (element number at of the array) into its place
+// of a stage, 16 bytes or, WIDE, 32.
+template <bool WIDE>
+__device__ __forceinline__ void fetch8(char* to, int v, const void* from, size_t at) {
+  constexpr int kBytes = WIDE ? 32 : 16;
+  const char* src = static_cast<const char*>(from) + at * kBytes;
+  copy16(to + (size_t)v * kBytes, src);
+  if (WIDE) copy16(to + (size_t)v * kBytes + 16, src + 16);
 }
 
 // Most threads of a CTA that takes VPT vectors a thread, and the CTAs of that size an SM holds.
@@ -181,24 +156,31 @@ template <bool F32, int VPT, int STAGES>
 __global__ void __launch_bounds__(most_threads(VPT), most_ctas(VPT))
     norm_kernel(Shape s, NormFwd a, int stage_bytes) {
   extern __shared__ __align__(16) char ring[];
-  __shared__ float sums[2 * 32];
+  __shared__ float sums[2 * 16];
   constexpr int kSt = F32 ? 32 : 16;
   const bool has_y = a.y != nullptr, post = a.w_post != nullptr, next = a.w_next != nullptr;
   const bool elem = s.gate == MOE_GATE_ELEMENT;
-  Arrays in;
-  in.p[0] = static_cast<const char*>(a.x), in.bytes[0] = kSt;
-  in.p[1] = static_cast<const char*>(a.y), in.bytes[1] = has_y ? 16 : 0;
-  in.p[2] = static_cast<const char*>(a.gate), in.bytes[2] = elem ? 16 : 0;
   const int off_y = s.vecs * kSt, off_g = off_y + (has_y ? s.vecs * 16 : 0);
   const int step = gridDim.x;
   const float inv_d = 1.0f / static_cast<float>(s.d);
   int flip = 0, slot = 0;
+  const auto fetch = [&](long long row, int to) {
+    if (row < s.rows) {
+      char* st = ring + (size_t)to * stage_bytes;
 #pragma unroll
-  for (int i = 0; i < STAGES - 1; ++i) {
-    const long long r = blockIdx.x + (long long)i * step;
-    if (r < s.rows) fetch_row<3, VPT>(in, ring + (size_t)i * stage_bytes, r, s.vecs);
+      for (int k = 0; k < VPT; ++k) {
+        const int v = threadIdx.x + k * blockDim.x;
+        const size_t at = (size_t)row * s.vecs + v;
+        if (v >= s.vecs) continue;
+        fetch8<F32>(st, v, a.x, at);
+        if (has_y) fetch8<false>(st + off_y, v, a.y, at);
+        if (elem) fetch8<false>(st + off_g, v, a.gate, at);
+      }
+    }
     copies_commit();
-  }
+  };
+#pragma unroll
+  for (int i = 0; i < STAGES - 1; ++i) fetch(blockIdx.x + (long long)i * step, i);
   // what a column's normed output is multiplied by: out, the channel gate and the weight; and the
   // next norm's weight
   F8 gw[VPT], wn[VPT];
@@ -207,23 +189,18 @@ __global__ void __launch_bounds__(most_threads(VPT), most_ctas(VPT))
     const int v = threadIdx.x + k * blockDim.x;
     const bool col = v < s.vecs;
     const float* g = s.gate == MOE_GATE_CHANNEL ? static_cast<const float*>(a.gate) : nullptr;
-    gw[k] = weights(a.w_post, v, col, 1.0f) * weights(g, v, col, 1.0f) * s.out;
+    gw[k] = mul(mul(weights(a.w_post, v, col, 1.0f), weights(g, v, col, 1.0f)), both(s.out));
     wn[k] = weights(a.w_next, v, col, 0.0f);
   }
   for (long long row = blockIdx.x; row < s.rows; row += step) {
-    {
-      const long long ahead = row + (long long)(STAGES - 1) * step;
-      const int to = slot == 0 ? STAGES - 1 : slot - 1;
-      if (ahead < s.rows) fetch_row<3, VPT>(in, ring + (size_t)to * stage_bytes, ahead, s.vecs);
-      copies_commit();
-    }
+    fetch(row + (long long)(STAGES - 1) * step, slot == 0 ? STAGES - 1 : slot - 1);
     float factor = 1.0f;   // of this row's y
     if (s.gate == MOE_GATE_TOKEN) factor = static_cast<const float*>(a.gate)[row];
     copies_wait<STAGES - 1>();
     const char* st = ring + (size_t)slot * stage_bytes;
     slot = slot + 1 == STAGES ? 0 : slot + 1;
     if (post) {
-      float2 q = both(0.0f);
+      f32x2 q = both(0.0f);
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
         const int v = threadIdx.x + k * blockDim.x;
@@ -231,14 +208,14 @@ __global__ void __launch_bounds__(most_threads(VPT), most_ctas(VPT))
         const F8 y = read8<false>(st + off_y + (size_t)v * 16);
         dot(y, y, q);
       }
-      float sum[1] = {q.x + q.y};
-      cta_sum<1>(sum, sums, flip);
-      const float r = inv_root(sum[0], inv_d, s.eps);
+      float sum = sum_of(q);
+      cta_sum(sum, sums, flip);
+      const float r = inv_root(sum, inv_d, s.eps);
       if (threadIdx.x == 0 && a.rstd_y) a.rstd_y[row] = r;
       factor *= r;
     }
     F8 h[VPT];
-    float2 q = both(0.0f);
+    f32x2 q = both(0.0f);
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       const int v = threadIdx.x + k * blockDim.x;
@@ -246,22 +223,23 @@ __global__ void __launch_bounds__(most_threads(VPT), most_ctas(VPT))
       h[k] = read8<F32>(st + (size_t)v * kSt);
       if (has_y) {
         F8 y = read8<false>(st + off_y + (size_t)v * 16);
-        if (elem) y = y * read8<false>(st + off_g + (size_t)v * 16);
-        h[k] = fma(y * factor, gw[k], h[k] * s.res);
+        if (elem) y = mul(y, read8<false>(st + off_g + (size_t)v * 16));
+        h[k] = fma(mul(y, both(factor)), gw[k], mul(h[k], both(s.res)));
         write8<F32>(static_cast<char*>(a.h) + ((size_t)row * s.vecs + v) * kSt, h[k]);
       }
       dot(h[k], h[k], q);
     }
     if (!next) continue;
-    float sum[1] = {q.x + q.y};
-    cta_sum<1>(sum, sums, flip);
-    const float r = inv_root(sum[0], inv_d, s.eps);
+    float sum = sum_of(q);
+    cta_sum(sum, sums, flip);
+    const float r = inv_root(sum, inv_d, s.eps);
     if (threadIdx.x == 0 && a.rstd_h) a.rstd_h[row] = r;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       const int v = threadIdx.x + k * blockDim.x;
       if (v >= s.vecs) continue;
-      write8<false>(static_cast<char*>(a.n) + ((size_t)row * s.vecs + v) * 16, h[k] * r * wn[k]);
+      write8<false>(static_cast<char*>(a.n) + ((size_t)row * s.vecs + v) * 16,
+                    mul(mul(h[k], both(r)), wn[k]));
     }
   }
 }
@@ -277,7 +255,7 @@ template <bool F32, int VPT, int STAGES>
 __global__ void __launch_bounds__(most_threads(VPT), most_ctas(VPT))
     norm_grad_kernel(Shape s, NormGrad a, int stage_bytes, float* partial) {
   extern __shared__ __align__(16) char ring[];
-  __shared__ float sums[2 * 32 * 3];
+  __shared__ float sums[2 * 16 * 3];
   constexpr int kSt = F32 ? 32 : 16;
   constexpr bool kKeep = VPT <= 2;
   const bool post = a.w_post != nullptr, next = a.w_next != nullptr, has_dh = a.dh != nullptr;
@@ -286,12 +264,6 @@ __global__ void __launch_bounds__(most_threads(VPT), most_ctas(VPT))
   const bool is_out = a.dy != nullptr;                  // the norm before a block has no y side
   const bool dot_y = post || token;
   const float* channel = s.gate == MOE_GATE_CHANNEL ? static_cast<const float*>(a.gate) : nullptr;
-  Arrays in;
-  in.p[0] = static_cast<const char*>(a.dh), in.bytes[0] = has_dh ? kSt : 0;
-  in.p[1] = static_cast<const char*>(a.h), in.bytes[1] = next ? kSt : 0;
-  in.p[2] = static_cast<const char*>(a.dn), in.bytes[2] = next ? 16 : 0;
-  in.p[3] = static_cast<const char*>(a.y), in.bytes[3] = has_y ? 16 : 0;
-  in.p[4] = static_cast<const char*>(a.gate), in.bytes[4] = elem ? 16 : 0;
   const int off_h = has_dh ? s.vecs * kSt : 0;
   const int off_n = off_h + (next ? s.vecs * kSt : 0);
   const int off_y = off_n + (next ? s.vecs * 16 : 0);
@@ -299,15 +271,30 @@ __global__ void __launch_bounds__(most_threads(VPT), most_ctas(VPT))
   const int step = gridDim.x;
   const float inv_d = 1.0f / static_cast<float>(s.d);
   int flip = 0, slot = 0;
+  const auto fetch = [&](long long row, int to) {
+    if (row < s.rows) {
+      char* st = ring + (size_t)to * stage_bytes;
 #pragma unroll
-  for (int i = 0; i < STAGES - 1; ++i) {
-    const long long r = blockIdx.x + (long long)i * step;
-    if (r < s.rows) fetch_row<5, VPT>(in, ring + (size_t)i * stage_bytes, r, s.vecs);
+      for (int k = 0; k < VPT; ++k) {
+        const int v = threadIdx.x + k * blockDim.x;
+        const size_t at = (size_t)row * s.vecs + v;
+        if (v >= s.vecs) continue;
+        if (has_dh) fetch8<F32>(st, v, a.dh, at);
+        if (next) {
+          fetch8<F32>(st + off_h, v, a.h, at);
+          fetch8<false>(st + off_n, v, a.dn, at);
+        }
+        if (has_y) fetch8<false>(st + off_y, v, a.y, at);
+        if (elem) fetch8<false>(st + off_g, v, a.gate, at);
+      }
+    }
     copies_commit();
-  }
+  };
+#pragma unroll
+  for (int i = 0; i < STAGES - 1; ++i) fetch(blockIdx.x + (long long)i * step, i);
   const auto weight_y = [&](int v, bool col) {
     F8 w = weights(a.w_post, v, col, 1.0f);
-    return channel ? w * weights(channel, v, col, 1.0f) : w;
+    return channel ? mul(w, weights(channel, v, col, 1.0f)) : w;
   };
   F8 keep_y[kKeep ? VPT : 1], keep_n[kKeep ? VPT : 1], acc_y[VPT], acc_n[VPT];
 #pragma unroll
@@ -317,75 +304,72 @@ __global__ void __launch_bounds__(most_threads(VPT), most_ctas(VPT))
       keep_y[k] = weight_y(v, v < s.vecs);
       keep_n[k] = weights(a.w_next, v, v < s.vecs, 0.0f);
     }
-    acc_y[k] = acc_n[k] = all(0.0f);
+    acc_y[k] = acc_n[k] = all(0);
   }
   for (long long row = blockIdx.x; row < s.rows; row += step) {
-    {
-      const long long ahead = row + (long long)(STAGES - 1) * step;
-      const int to = slot == 0 ? STAGES - 1 : slot - 1;
-      if (ahead < s.rows) fetch_row<5, VPT>(in, ring + (size_t)to * stage_bytes, ahead, s.vecs);
-      copies_commit();
-    }
+    fetch(row + (long long)(STAGES - 1) * step, slot == 0 ? STAGES - 1 : slot - 1);
     const float rh = next ? a.rstd_h[row] : 0.0f, ry = post ? a.rstd_y[row] : 1.0f;
     const float gt = token ? static_cast<const float*>(a.gate)[row] : 1.0f;
     copies_wait<STAGES - 1>();
     const char* st = ring + (size_t)slot * stage_bytes;
     slot = slot + 1 == STAGES ? 0 : slot + 1;
 
-    float2 qa = both(0.0f), qg = qa, qh = qa;   // sums of a h, u (dh + rh a) and u h (h, u: no r)
+    const f32x2 rh2 = both(rh);
+    f32x2 qa = 0, qg = 0, qh = 0;   // sums of a h, u (dh + rh a) and u h (h, u: without their r)
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       const int v = threadIdx.x + k * blockDim.x;
       if (v >= s.vecs) continue;
-      F8 dh = all(0.0f), h = dh;
+      F8 dh = all(0), h = dh;
       if (has_dh) dh = read8<F32>(st + (size_t)v * kSt);
       if (next) {
         h = read8<F32>(st + off_h + (size_t)v * kSt);
-        const F8 d = read8<false>(st + off_n + (size_t)v * 16) *
-                     (kKeep ? keep_n[k] : weights(a.w_next, v, true, 0.0f));
+        const F8 d = mul(read8<false>(st + off_n + (size_t)v * 16),
+                         kKeep ? keep_n[k] : weights(a.w_next, v, true, 0.0f));
         dot(d, h, qa);
-        dh = fma(d, rh, dh);
+        dh = fma(d, rh2, dh);
       }
       if (dot_y) {
-        F8 u = read8<false>(st + off_y + (size_t)v * 16) * (kKeep ? keep_y[k] : weight_y(v, true));
-        if (elem) u = u * read8<false>(st + off_g + (size_t)v * 16);
+        F8 u = mul(read8<false>(st + off_y + (size_t)v * 16),
+                   kKeep ? keep_y[k] : weight_y(v, true));
+        if (elem) u = mul(u, read8<false>(st + off_g + (size_t)v * 16));
         dot(u, dh, qg);
         dot(u, h, qh);
       }
     }
-    float q[3] = {qa.x + qa.y, qg.x + qg.y, qh.x + qh.y};
-    if (next || dot_y) cta_sum<3>(q, sums, flip);
-    const float c1 = rh * q[0] * inv_d;                          // mean a hh
+    float q[3] = {sum_of(qa), sum_of(qg), sum_of(qh)};
+    if (next || dot_y) cta_sum3(q, sums, flip);
+    const float c1 = rh * q[0] * inv_d;                                // mean a hh
     const float along = s.out * ry * (q[1] - rh * c1 * (rh * q[2]));   // sum out G s, no token gate
     const float mean = gt * along * inv_d;
     if (token && a.dgate && threadIdx.x == 0) static_cast<float*>(a.dgate)[row] = along;
-    const float hc = -c1 * rh;
+    const f32x2 hc = both(-c1 * rh), out = both(s.out * gt), ry2 = both(ry), back = both(-mean);
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       const int v = threadIdx.x + k * blockDim.x;
       if (v >= s.vecs) continue;
       const size_t at = (size_t)row * s.vecs + v;
-      F8 G = all(0.0f);
+      F8 G = all(0);
       if (has_dh) G = read8<F32>(st + (size_t)v * kSt);
       if (next) {
         const F8 h = read8<F32>(st + off_h + (size_t)v * kSt);
         const F8 dn = read8<false>(st + off_n + (size_t)v * 16);
-        G = fma(fma(dn, kKeep ? keep_n[k] : weights(a.w_next, v, true, 0.0f), h * hc), rh, G);
-        acc_n[k] = fma(dn, h * rh, acc_n[k]);
+        G = fma(fma(dn, kKeep ? keep_n[k] : weights(a.w_next, v, true, 0.0f), mul(h, hc)), rh2, G);
+        acc_n[k] = fma(dn, mul(h, rh2), acc_n[k]);
       }
-      if (a.dx) write8<F32>(static_cast<char*>(a.dx) + at * kSt, G * s.res);
+      if (a.dx) write8<F32>(static_cast<char*>(a.dx) + at * kSt, mul(G, both(s.res)));
       if (!is_out) continue;
-      G = G * (s.out * gt);
+      G = mul(G, out);
       const F8 gw = kKeep ? keep_y[k] : weight_y(v, true);
-      F8 yh = all(0.0f);
-      if (has_y) yh = read8<false>(st + off_y + (size_t)v * 16) * ry;
+      F8 yh = all(0);
+      if (has_y) yh = mul(read8<false>(st + off_y + (size_t)v * 16), ry2);
       if (elem) {
-        if (a.dgate) write8<false>(static_cast<char*>(a.dgate) + at * 16, G * yh * gw);
-        G = G * read8<false>(st + off_g + (size_t)v * 16);
+        if (a.dgate) write8<false>(static_cast<char*>(a.dgate) + at * 16, mul(mul(G, yh), gw));
+        G = mul(G, read8<false>(st + off_g + (size_t)v * 16));
       }
       acc_y[k] = fma(G, yh, acc_y[k]);
-      write8<false>(static_cast<char*>(a.dy) + at * 16,
-                    post ? fma(yh, -mean, G * gw) * ry : G * gw);
+      G = mul(G, gw);
+      write8<false>(static_cast<char*>(a.dy) + at * 16, post ? mul(fma(yh, back, G), ry2) : G);
     }
   }
   if (!partial) return;

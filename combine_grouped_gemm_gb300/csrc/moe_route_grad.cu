@@ -13,6 +13,7 @@
 #include <algorithm>
 
 #include "moe_device.cuh"
+#include "moe_f32x2.cuh"
 
 namespace moe {
 namespace {
@@ -21,13 +22,9 @@ constexpr int kSms = 152;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
-// Two fp32 fused multiply-adds in one instruction, the factor shared.
-__device__ __forceinline__ void fma2(float2& c, float a, float2 b) {
-  asm("{\n\t.reg .b64 x, y, z;\n\t"
-      "mov.b64 x, {%2, %2};\n\tmov.b64 y, {%3, %4};\n\tmov.b64 z, {%0, %1};\n\t"
-      "fma.rn.f32x2 z, x, y, z;\n\tmov.b64 {%0, %1}, z;\n\t}"
-      : "+f"(c.x), "+f"(c.y)
-      : "f"(a), "f"(b.x), "f"(b.y));
+__device__ __forceinline__ float4 four(f32x2 a, f32x2 b) {
+  const float2 x = halves(a), y = halves(b);
+  return make_float4(x.x, x.y, y.x, y.y);
 }
 __device__ __forceinline__ void copy16(void* smem, const void* gmem) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(smem)), "l"(gmem)
@@ -233,13 +230,13 @@ __device__ __forceinline__ void dx_short(const Pick* __restrict__ picks,
   const long long t = item / parts;
   const int v = static_cast<int>(item - t * parts) * 32 + (threadIdx.x & 31);
   if (t >= T || v >= vecs) return;
-  float2 acc[4] = {};
+  f32x2 acc[4] = {};
   if (dx_in) {
     const uint4 u = dx_in[(size_t)t * vecs + v];
-    acc[0] = make_float2(bf16_lo(u.x), bf16_hi(u.x));
-    acc[1] = make_float2(bf16_lo(u.y), bf16_hi(u.y));
-    acc[2] = make_float2(bf16_lo(u.z), bf16_hi(u.z));
-    acc[3] = make_float2(bf16_lo(u.w), bf16_hi(u.w));
+    acc[0] = pair_of_bf16(u.x);
+    acc[1] = pair_of_bf16(u.y);
+    acc[2] = pair_of_bf16(u.z);
+    acc[3] = pair_of_bf16(u.w);
   }
   const int4* two = reinterpret_cast<const int4*>(picks + (size_t)t * kp);
 #pragma unroll 4
@@ -248,19 +245,19 @@ __device__ __forceinline__ void dx_short(const Pick* __restrict__ picks,
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int e = j ? p.z : p.x;
-      const float z = __int_as_float(j ? p.w : p.y);
+      const f32x2 z2 = both(__int_as_float(j ? p.w : p.y));
       if (e == E) continue;
       const float4* w = reinterpret_cast<const float4*>(w_gate + (size_t)e * d) + 2 * v;
       const float4 a = w[0], b = w[1];
-      fma2(acc[0], z, make_float2(a.x, a.y));
-      fma2(acc[1], z, make_float2(a.z, a.w));
-      fma2(acc[2], z, make_float2(b.x, b.y));
-      fma2(acc[3], z, make_float2(b.z, b.w));
+      acc[0] = fma2(z2, pair(a.x, a.y), acc[0]);
+      acc[1] = fma2(z2, pair(a.z, a.w), acc[1]);
+      acc[2] = fma2(z2, pair(b.x, b.y), acc[2]);
+      acc[3] = fma2(z2, pair(b.z, b.w), acc[3]);
     }
   }
   dx[(size_t)t * vecs + v] =
-      make_uint4(pack_bf16x2(acc[0].x, acc[0].y), pack_bf16x2(acc[1].x, acc[1].y),
-                 pack_bf16x2(acc[2].x, acc[2].y), pack_bf16x2(acc[3].x, acc[3].y));
+      make_uint4(bf16_of_pair(acc[0]), bf16_of_pair(acc[1]),
+                 bf16_of_pair(acc[2]), bf16_of_pair(acc[3]));
 }
 
 // A warp takes 256 columns of one expert's gate weights, over all chunks in order; x comes from L2.
@@ -274,7 +271,7 @@ __device__ __forceinline__ void dw_short(const uint4* __restrict__ x,
   const int e = static_cast<int>(item / parts);
   const int v = static_cast<int>(item - (long long)e * parts) * 32 + (threadIdx.x & 31);
   if (e >= E || v >= vecs) return;
-  float2 acc[4] = {};
+  f32x2 acc[4] = {};
   for (int c = 0; c < chunks; ++c) {
     const int2 run = runs[(size_t)c * E + e];
     const Entry* in = list + (size_t)c * stride;
@@ -283,15 +280,14 @@ __device__ __forceinline__ void dw_short(const uint4* __restrict__ x,
     for (int i = run.x; i < run.y; ++i) {
       const Entry q = in[i];
       const uint4 u = rows[(size_t)(entry_row(q) >> 7) * vecs];
-      fma2(acc[0], q.dz, make_float2(bf16_lo(u.x), bf16_hi(u.x)));
-      fma2(acc[1], q.dz, make_float2(bf16_lo(u.y), bf16_hi(u.y)));
-      fma2(acc[2], q.dz, make_float2(bf16_lo(u.z), bf16_hi(u.z)));
-      fma2(acc[3], q.dz, make_float2(bf16_lo(u.w), bf16_hi(u.w)));
+      acc[0] = fma2(both(q.dz), pair_of_bf16(u.x), acc[0]);
+      acc[1] = fma2(both(q.dz), pair_of_bf16(u.y), acc[1]);
+      acc[2] = fma2(both(q.dz), pair_of_bf16(u.z), acc[2]);
+      acc[3] = fma2(both(q.dz), pair_of_bf16(u.w), acc[3]);
     }
   }
   float4* o = reinterpret_cast<float4*>(dw_gate + (size_t)e * d) + 2 * v;
-  float4 a = make_float4(acc[0].x, acc[0].y, acc[1].x, acc[1].y);
-  float4 b = make_float4(acc[2].x, acc[2].y, acc[3].x, acc[3].y);
+  float4 a = four(acc[0], acc[1]), b = four(acc[2], acc[3]);
   if (accumulate) {
     const float4 p = o[0], q = o[1];
     a.x += p.x, a.y += p.y, a.z += p.z, a.w += p.w;
@@ -364,26 +360,27 @@ __global__ void __launch_bounds__(kDxThreads, 1) route_grad_dx_slab_kernel(
     };
     if (t0 + mine < t1) fetch(t0 + mine);
     for (int t = t0 + mine; t < t1; t += kAtOnce) {
-      float2 acc[8];
+      f32x2 acc[8];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const uint4 u = u_next[i];
-        acc[4 * i] = make_float2(bf16_lo(u.x), bf16_hi(u.x));
-        acc[4 * i + 1] = make_float2(bf16_lo(u.y), bf16_hi(u.y));
-        acc[4 * i + 2] = make_float2(bf16_lo(u.z), bf16_hi(u.z));
-        acc[4 * i + 3] = make_float2(bf16_lo(u.w), bf16_hi(u.w));
+        acc[4 * i] = pair_of_bf16(u.x);
+        acc[4 * i + 1] = pair_of_bf16(u.y);
+        acc[4 * i + 2] = pair_of_bf16(u.z);
+        acc[4 * i + 3] = pair_of_bf16(u.w);
       }
       int4 p[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) p[i] = p_next[i];
       if (t + kAtOnce < t1) fetch(t + kAtOnce);
       const auto add = [&](int e, float z) {
+        const f32x2 z2 = both(z);
         const char* row = w + e * kRow;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float4 x = *reinterpret_cast<const float4*>(row + i * kQuarter);
-          fma2(acc[2 * i], z, make_float2(x.x, x.y));
-          fma2(acc[2 * i + 1], z, make_float2(x.z, x.w));
+          acc[2 * i] = fma2(z2, pair(x.x, x.y), acc[2 * i]);
+          acc[2 * i + 1] = fma2(z2, pair(x.z, x.w), acc[2 * i + 1]);
         }
       };
 #pragma unroll
@@ -400,10 +397,10 @@ __global__ void __launch_bounds__(kDxThreads, 1) route_grad_dx_slab_kernel(
       uint4* o = dx + (size_t)t * (d / 8) + col;
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        o[i] = make_uint4(pack_bf16x2(acc[4 * i].x, acc[4 * i].y),
-                          pack_bf16x2(acc[4 * i + 1].x, acc[4 * i + 1].y),
-                          pack_bf16x2(acc[4 * i + 2].x, acc[4 * i + 2].y),
-                          pack_bf16x2(acc[4 * i + 3].x, acc[4 * i + 3].y));
+        o[i] = make_uint4(bf16_of_pair(acc[4 * i]),
+                          bf16_of_pair(acc[4 * i + 1]),
+                          bf16_of_pair(acc[4 * i + 2]),
+                          bf16_of_pair(acc[4 * i + 3]));
     }
     at += t1 - t0;
   }
@@ -476,7 +473,7 @@ __global__ void __launch_bounds__(kDwThreads, 1) route_grad_dw_slab_kernel(
     // the run that comes in from the slice before, if it does: its sum goes to the side row
     bool head = begin > 0 && begin < end && !(in[4 * begin - 4].at & 1);
     int side = -1;
-    float2 acc[4] = {};
+    f32x2 acc[4] = {};
     for (int at = begin; at < end; ++at) {
       Entry q[4];
       uint4 u[4];
@@ -492,16 +489,15 @@ __global__ void __launch_bounds__(kDwThreads, 1) route_grad_dw_slab_kernel(
       for (int i = 0; i < 4; ++i) u[i] = *reinterpret_cast<const uint4*>(tile + entry_row(q[i]));
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        fma2(acc[0], q[i].dz, make_float2(bf16_lo(u[i].x), bf16_hi(u[i].x)));
-        fma2(acc[1], q[i].dz, make_float2(bf16_lo(u[i].y), bf16_hi(u[i].y)));
-        fma2(acc[2], q[i].dz, make_float2(bf16_lo(u[i].z), bf16_hi(u[i].z)));
-        fma2(acc[3], q[i].dz, make_float2(bf16_lo(u[i].w), bf16_hi(u[i].w)));
+        acc[0] = fma2(both(q[i].dz), pair_of_bf16(u[i].x), acc[0]);
+        acc[1] = fma2(both(q[i].dz), pair_of_bf16(u[i].y), acc[1]);
+        acc[2] = fma2(both(q[i].dz), pair_of_bf16(u[i].z), acc[2]);
+        acc[3] = fma2(both(q[i].dz), pair_of_bf16(u[i].w), acc[3]);
       }
       if ((q[0].at & 1) || at == end - 1) {   // the run ends here, or goes on in the next slice
         const int e = q[0].at >> 16;
         float4* to = reinterpret_cast<float4*>(head ? sm.side[slice] : sm.sums[e]) + l;
-        float4 a = make_float4(acc[0].x, acc[0].y, acc[1].x, acc[1].y);
-        float4 h = make_float4(acc[2].x, acc[2].y, acc[3].x, acc[3].y);
+        float4 a = four(acc[0], acc[1]), h = four(acc[2], acc[3]);
         if (head) {
           side = e;
         } else {
@@ -513,7 +509,7 @@ __global__ void __launch_bounds__(kDwThreads, 1) route_grad_dw_slab_kernel(
         to[8] = h;
         head = false;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] = make_float2(0.0f, 0.0f);
+        for (int i = 0; i < 4; ++i) acc[i] = 0;
       }
     }
     if (l == 0) sm.side_expert[slice] = side;
