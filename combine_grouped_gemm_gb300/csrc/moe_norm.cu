@@ -306,34 +306,46 @@ __global__ void __launch_bounds__(most_threads(VPT), most_ctas(VPT))
     }
     acc_y[k] = acc_n[k] = all(0);
   }
+  // a row's factors are loaded a row ahead
+  const auto factors = [&](long long row, float& rh, float& ry, float& gt) {
+    if (row >= s.rows) return;
+    if (next) rh = a.rstd_h[row];
+    if (post) ry = a.rstd_y[row];
+    if (token) gt = static_cast<const float*>(a.gate)[row];
+  };
+  float rh_next = 0.0f, ry_next = 1.0f, gt_next = 1.0f;
+  factors(blockIdx.x, rh_next, ry_next, gt_next);
   for (long long row = blockIdx.x; row < s.rows; row += step) {
     fetch(row + (long long)(STAGES - 1) * step, slot == 0 ? STAGES - 1 : slot - 1);
-    const float rh = next ? a.rstd_h[row] : 0.0f, ry = post ? a.rstd_y[row] : 1.0f;
-    const float gt = token ? static_cast<const float*>(a.gate)[row] : 1.0f;
+    const float rh = rh_next, ry = ry_next, gt = gt_next;
+    factors(row + step, rh_next, ry_next, gt_next);
     copies_wait<STAGES - 1>();
     const char* st = ring + (size_t)slot * stage_bytes;
     slot = slot + 1 == STAGES ? 0 : slot + 1;
 
     const f32x2 rh2 = both(rh);
+    F8 G[VPT];   // dh + rh a, of which the next norm's mean is still to be taken
     f32x2 qa = 0, qg = 0, qh = 0;   // sums of a h, u (dh + rh a) and u h (h, u: without their r)
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       const int v = threadIdx.x + k * blockDim.x;
       if (v >= s.vecs) continue;
-      F8 dh = all(0), h = dh;
-      if (has_dh) dh = read8<F32>(st + (size_t)v * kSt);
+      F8 h = all(0);
+      G[k] = h;
+      if (has_dh) G[k] = read8<F32>(st + (size_t)v * kSt);
       if (next) {
         h = read8<F32>(st + off_h + (size_t)v * kSt);
-        const F8 d = mul(read8<false>(st + off_n + (size_t)v * 16),
-                         kKeep ? keep_n[k] : weights(a.w_next, v, true, 0.0f));
+        const F8 dn = read8<false>(st + off_n + (size_t)v * 16);
+        acc_n[k] = fma(dn, mul(h, rh2), acc_n[k]);
+        const F8 d = mul(dn, kKeep ? keep_n[k] : weights(a.w_next, v, true, 0.0f));
         dot(d, h, qa);
-        dh = fma(d, rh2, dh);
+        G[k] = fma(d, rh2, G[k]);
       }
       if (dot_y) {
         F8 u = mul(read8<false>(st + off_y + (size_t)v * 16),
                    kKeep ? keep_y[k] : weight_y(v, true));
         if (elem) u = mul(u, read8<false>(st + off_g + (size_t)v * 16));
-        dot(u, dh, qg);
+        dot(u, G[k], qg);
         dot(u, h, qh);
       }
     }
@@ -343,33 +355,27 @@ __global__ void __launch_bounds__(most_threads(VPT), most_ctas(VPT))
     const float along = s.out * ry * (q[1] - rh * c1 * (rh * q[2]));   // sum out G s, no token gate
     const float mean = gt * along * inv_d;
     if (token && a.dgate && threadIdx.x == 0) static_cast<float*>(a.dgate)[row] = along;
-    const f32x2 hc = both(-c1 * rh), out = both(s.out * gt), ry2 = both(ry), back = both(-mean);
+    const f32x2 hc = both(-c1 * rh * rh), res = both(s.res);
+    // dy = ry (u gw - yh mean), u = out gate G; acc_y adds u yh: both from u ry and y itself
+    const f32x2 out = both(s.out * gt * ry), back = both(-ry * ry * mean);
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       const int v = threadIdx.x + k * blockDim.x;
       if (v >= s.vecs) continue;
       const size_t at = (size_t)row * s.vecs + v;
-      F8 G = all(0);
-      if (has_dh) G = read8<F32>(st + (size_t)v * kSt);
-      if (next) {
-        const F8 h = read8<F32>(st + off_h + (size_t)v * kSt);
-        const F8 dn = read8<false>(st + off_n + (size_t)v * 16);
-        G = fma(fma(dn, kKeep ? keep_n[k] : weights(a.w_next, v, true, 0.0f), mul(h, hc)), rh2, G);
-        acc_n[k] = fma(dn, mul(h, rh2), acc_n[k]);
-      }
-      if (a.dx) write8<F32>(static_cast<char*>(a.dx) + at * kSt, mul(G, both(s.res)));
+      if (next) G[k] = fma(read8<F32>(st + off_h + (size_t)v * kSt), hc, G[k]);
+      if (a.dx) write8<F32>(static_cast<char*>(a.dx) + at * kSt, mul(G[k], res));
       if (!is_out) continue;
-      G = mul(G, out);
+      F8 u = mul(G[k], out), y = all(0);
       const F8 gw = kKeep ? keep_y[k] : weight_y(v, true);
-      F8 yh = all(0);
-      if (has_y) yh = mul(read8<false>(st + off_y + (size_t)v * 16), ry2);
+      if (has_y) y = read8<false>(st + off_y + (size_t)v * 16);
       if (elem) {
-        if (a.dgate) write8<false>(static_cast<char*>(a.dgate) + at * 16, mul(mul(G, yh), gw));
-        G = mul(G, read8<false>(st + off_g + (size_t)v * 16));
+        if (a.dgate) write8<false>(static_cast<char*>(a.dgate) + at * 16, mul(mul(u, y), gw));
+        u = mul(u, read8<false>(st + off_g + (size_t)v * 16));
       }
-      acc_y[k] = fma(G, yh, acc_y[k]);
-      G = mul(G, gw);
-      write8<false>(static_cast<char*>(a.dy) + at * 16, post ? mul(fma(yh, back, G), ry2) : G);
+      acc_y[k] = fma(u, y, acc_y[k]);
+      u = mul(u, gw);
+      write8<false>(static_cast<char*>(a.dy) + at * 16, post ? fma(y, back, u) : u);
     }
   }
   if (!partial) return;
