@@ -16,7 +16,8 @@ constexpr int kGpuSms = 152;   // grids are sized for GB300
 constexpr int kWsHead = 256;   // the status word's place at the head of the scratch
 
 struct Shape {
-  int rows, d, vecs;   // vecs = d / 8
+  int rows, d;
+  unsigned vecs;   // d / 8
   float eps, res, out;
   int gate;
 };
@@ -42,35 +43,57 @@ __device__ __forceinline__ void dot(const F8& a, const F8& b, f32x2& sum) {
   for (int i = 0; i < 4; ++i) sum = fma2(a.p[i], b.p[i], sum);
 }
 
-// 8 columns of bf16 (16 bytes) or, F32, of fp32 (32 bytes).
-template <bool F32>
-__device__ __forceinline__ F8 read8(const char* at) {
-  if (F32) {
-    const ulonglong2 a = *reinterpret_cast<const ulonglong2*>(at);
-    const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(at + 16);
+// Vector v of a row in an array of fp32 (WIDE) or bf16, each access 16 bytes a thread where it can be.
+// With a bf16 stream a vector is 8 consecutive columns. With an fp32 stream (SPLIT) it is 4 columns of
+// the row's first half and 4 of its second, so that neighbouring threads take neighbouring 16 bytes of
+// the fp32 arrays and 8 of the bf16 ones; 8 consecutive columns would leave every second 16 bytes to
+// the other access of the thread.
+template <bool WIDE, bool SPLIT>
+__device__ __forceinline__ F8 read8(const char* row, unsigned v, unsigned vecs) {
+  if (WIDE) {
+    const ulonglong2* at = reinterpret_cast<const ulonglong2*>(row);
+    const ulonglong2 a = at[SPLIT ? v : 2 * v], b = at[SPLIT ? vecs + v : 2 * v + 1];
     return F8{{a.x, a.y, b.x, b.y}};
   }
-  const uint4 v = *reinterpret_cast<const uint4*>(at);
-  return F8{{pair_of_bf16(v.x), pair_of_bf16(v.y), pair_of_bf16(v.z), pair_of_bf16(v.w)}};
-}
-template <bool F32>
-__device__ __forceinline__ void write8(char* at, const F8& f) {
-  if (F32) {
-    *reinterpret_cast<ulonglong2*>(at) = make_ulonglong2(f.p[0], f.p[1]);
-    *reinterpret_cast<ulonglong2*>(at + 16) = make_ulonglong2(f.p[2], f.p[3]);
+  uint2 a, b;
+  if (SPLIT) {
+    a = reinterpret_cast<const uint2*>(row)[v], b = reinterpret_cast<const uint2*>(row)[vecs + v];
   } else {
-    *reinterpret_cast<uint4*>(at) = make_uint4(bf16_of_pair(f.p[0]), bf16_of_pair(f.p[1]),
-                                               bf16_of_pair(f.p[2]), bf16_of_pair(f.p[3]));
+    const uint4 u = reinterpret_cast<const uint4*>(row)[v];
+    a = make_uint2(u.x, u.y), b = make_uint2(u.z, u.w);
+  }
+  return F8{{pair_of_bf16(a.x), pair_of_bf16(a.y), pair_of_bf16(b.x), pair_of_bf16(b.y)}};
+}
+template <bool WIDE, bool SPLIT>
+__device__ __forceinline__ void write8(char* row, unsigned v, unsigned vecs, const F8& f) {
+  if (WIDE) {
+    ulonglong2* at = reinterpret_cast<ulonglong2*>(row);
+    at[SPLIT ? v : 2 * v] = make_ulonglong2(f.p[0], f.p[1]);
+    at[SPLIT ? vecs + v : 2 * v + 1] = make_ulonglong2(f.p[2], f.p[3]);
+    return;
+  }
+  const uint2 a = make_uint2(bf16_of_pair(f.p[0]), bf16_of_pair(f.p[1]));
+  const uint2 b = make_uint2(bf16_of_pair(f.p[2]), bf16_of_pair(f.p[3]));
+  if (SPLIT) {
+    reinterpret_cast<uint2*>(row)[v] = a;
+    reinterpret_cast<uint2*>(row)[vecs + v] = b;
+  } else {
+    reinterpret_cast<uint4*>(row)[v] = make_uint4(a.x, a.y, b.x, b.y);
   }
 }
-// 8 columns of a weight, `none` where there is no weight or no column.
-__device__ __forceinline__ F8 weights(const float* w, int vec, bool in, float none) {
-  if (!w || !in) return all(both(none));
-  return read8<true>(reinterpret_cast<const char*>(w) + (size_t)vec * 32);
+// A vector of a weight, `none` where there is no weight or no column.
+template <bool SPLIT>
+__device__ __forceinline__ F8 weights(const float* w, unsigned v, unsigned vecs, float none) {
+  if (!w || v >= vecs) return all(both(none));
+  return read8<true, SPLIT>(reinterpret_cast<const char*>(w), v, vecs);
 }
 
 __device__ __forceinline__ void copy16(char* smem, const char* gmem) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(smem)), "l"(gmem)
+               : "memory");
+}
+__device__ __forceinline__ void copy8(char* smem, const char* gmem) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_addr(smem)), "l"(gmem)
                : "memory");
 }
 __device__ __forceinline__ void copies_commit() {
@@ -81,8 +104,8 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// Sums over the CTA (16 warps at most) that every thread gets, in a fixed order. buf: two halves of
-// 16 floats a sum, used in turn (flip), so that one barrier a reduction is enough.
+// Sums over the CTA that every thread gets, in a fixed order. buf: two halves of 32 floats a sum, used
+// in turn (flip), so that one barrier a reduction is enough.
 __device__ __forceinline__ float lanes_xor(float v, int o) {
   return __shfl_xor_sync(0xffffffffu, v, o);
 }
@@ -92,45 +115,42 @@ __device__ __forceinline__ void cta_sum(float& v, float* buf, int& flip) {
   const int warps = blockDim.x >> 5;
   if (warps == 1) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float* b = buf + flip * 16;
+  float* b = buf + flip * 32;
   flip ^= 1;
   if (lane == 0) b[warp] = v;
   __syncthreads();
-  v = (lane & 15) < warps ? b[lane & 15] : 0.0f;
+  v = lane < warps ? b[lane] : 0.0f;
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) v += lanes_xor(v, o);
+  for (int o = 16; o > 0; o >>= 1) v += lanes_xor(v, o);
 }
-// Three of them in 16 shuffles: lanes that have handed on a sum go on with another one.
-__device__ __forceinline__ void cta_sum3(float (&v)[3], float* buf, int& flip) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  const bool up = lane & 16;
-  float a = (up ? v[1] : v[0]) + lanes_xor(up ? v[0] : v[1], 16);   // lanes 0-15: 0, 16-31: 1
-  float c = v[2] + lanes_xor(v[2], 16);
-  const bool third = lane & 8;
-  a = (third ? c : a) + lanes_xor(third ? a : c, 8);   // lanes 8-15 and 24-31: sum 2
+// Three sums over a warp in six shuffles: lanes that have handed on one go on with another. Lane 0
+// ends with the first, lane 16 with the second, lane 8 with the third.
+__device__ __forceinline__ float lanes_sum3(const float (&v)[3]) {
+  const bool up = threadIdx.x & 16, third = threadIdx.x & 8;
+  float a = (up ? v[1] : v[0]) + lanes_xor(up ? v[0] : v[1], 16);
+  const float c = v[2] + lanes_xor(v[2], 16);
+  a = (third ? c : a) + lanes_xor(third ? a : c, 8);
 #pragma unroll
   for (int o = 4; o > 0; o >>= 1) a += lanes_xor(a, o);
-  if (warps == 1) {
-    v[0] = __shfl_sync(0xffffffffu, a, 0);
-    v[1] = __shfl_sync(0xffffffffu, a, 16);
-    v[2] = __shfl_sync(0xffffffffu, a, 8);
-    return;
-  }
-  float* b = buf + flip * 48;
-  flip ^= 1;
-  if ((lane & 7) == 0 && lane != 24) b[lane * 2 % 48 + warp] = a;   // lane 0: 0, 16: 1 (at 32), 8: 2
-  __syncthreads();
-  const int l = lane & 15;
-  a = l < warps ? b[(up ? 32 : 0) + l] : 0.0f;
-  c = l < warps ? b[16 + l] : 0.0f;
+  return a;
+}
+__device__ __forceinline__ void cta_sum3(float (&v)[3], float* buf, int& flip) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  float a = lanes_sum3(v);
+  if (warps > 1) {
+    float* b = buf + flip * 96;
+    flip ^= 1;
+    if (lane == 0) b[warp] = a;
+    if (lane == 16) b[32 + warp] = a;
+    if (lane == 8) b[64 + warp] = a;
+    __syncthreads();
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) {
-    a += lanes_xor(a, o);
-    c += lanes_xor(c, o);
+    for (int i = 0; i < 3; ++i) v[i] = lane < warps ? b[32 * i + lane] : 0.0f;
+    a = lanes_sum3(v);
   }
   v[0] = __shfl_sync(0xffffffffu, a, 0);
   v[1] = __shfl_sync(0xffffffffu, a, 16);
-  v[2] = c;
+  v[2] = __shfl_sync(0xffffffffu, a, 8);
 }
 
 // 1/sqrt(mean + eps). rsqrtf is off by 2^-22 at most, a sixteenth of what the sum may be.
@@ -138,14 +158,28 @@ __device__ __forceinline__ float inv_root(float sum, float inv_d, float eps) {
   return rsqrtf(__fmaf_rn(sum, inv_d, eps));
 }
 
-// Starts the copy of this thread's 8 columns of a row (element number at of the array) into its place
-// of a stage, 16 bytes or, WIDE, 32.
+// A row of an array. (Its address is the same in all threads and the offset in it has 32 bits: that is
+// one addressing mode, where a 64-bit offset of each thread costs several instructions an access.)
 template <bool WIDE>
-__device__ __forceinline__ void fetch8(char* to, int v, const void* from, size_t at) {
-  constexpr int kBytes = WIDE ? 32 : 16;
-  const char* src = static_cast<const char*>(from) + at * kBytes;
-  copy16(to + (size_t)v * kBytes, src);
-  if (WIDE) copy16(to + (size_t)v * kBytes + 16, src + 16);
+__device__ __forceinline__ const char* row_of(const void* array, size_t row, unsigned vecs) {
+  return static_cast<const char*>(array) + row * vecs * (WIDE ? 32u : 16u);
+}
+template <bool WIDE>
+__device__ __forceinline__ char* row_of(void* array, size_t row, unsigned vecs) {
+  return static_cast<char*>(array) + row * vecs * (WIDE ? 32u : 16u);
+}
+// Starts the copy of vector v of a row to its place in a stage.
+template <bool WIDE, bool SPLIT>
+__device__ __forceinline__ void fetch8(char* to, const char* row, unsigned v, unsigned vecs) {
+  if (WIDE) {
+    copy16(to + v * 16, row + v * 16);
+    copy16(to + (vecs + v) * 16, row + (vecs + v) * 16);
+  } else if (SPLIT) {
+    copy8(to + v * 8, row + v * 8);
+    copy8(to + (vecs + v) * 8, row + (vecs + v) * 8);
+  } else {
+    copy16(to + v * 16, row + v * 16);
+  }
 }
 
 // Most threads of a CTA that takes VPT vectors a thread, and the CTAs of that size an SM holds.
@@ -156,8 +190,8 @@ template <bool F32, int VPT, int STAGES>
 __global__ void __launch_bounds__(most_threads(VPT), most_ctas(VPT))
     norm_kernel(Shape s, NormFwd a, int stage_bytes) {
   extern __shared__ __align__(16) char ring[];
-  __shared__ float sums[2 * 16];
-  constexpr int kSt = F32 ? 32 : 16;
+  __shared__ float sums[2 * 32];
+  constexpr unsigned kSt = F32 ? 32 : 16;
   const bool has_y = a.y != nullptr, post = a.w_post != nullptr, next = a.w_next != nullptr;
   const bool elem = s.gate == MOE_GATE_ELEMENT;
   const int off_y = s.vecs * kSt, off_g = off_y + (has_y ? s.vecs * 16 : 0);
@@ -166,15 +200,17 @@ __global__ void __launch_bounds__(most_threads(VPT), most_ctas(VPT))
   int flip = 0, slot = 0;
   const auto fetch = [&](long long row, int to) {
     if (row < s.rows) {
-      char* st = ring + (size_t)to * stage_bytes;
+      char* st = ring + to * stage_bytes;
+      const char* x = row_of<F32>(a.x, row, s.vecs);
+      const char* y = row_of<false>(a.y, row, s.vecs);
+      const char* g = row_of<false>(a.gate, row, s.vecs);
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
-        const int v = threadIdx.x + k * blockDim.x;
-        const size_t at = (size_t)row * s.vecs + v;
+        const unsigned v = threadIdx.x + k * blockDim.x;
         if (v >= s.vecs) continue;
-        fetch8<F32>(st, v, a.x, at);
-        if (has_y) fetch8<false>(st + off_y, v, a.y, at);
-        if (elem) fetch8<false>(st + off_g, v, a.gate, at);
+        fetch8<F32, F32>(st, x, v, s.vecs);
+        if (has_y) fetch8<false, F32>(st + off_y, y, v, s.vecs);
+        if (elem) fetch8<false, F32>(st + off_g, g, v, s.vecs);
       }
     }
     copies_commit();
@@ -186,26 +222,25 @@ __global__ void __launch_bounds__(most_threads(VPT), most_ctas(VPT))
   F8 gw[VPT], wn[VPT];
 #pragma unroll
   for (int k = 0; k < VPT; ++k) {
-    const int v = threadIdx.x + k * blockDim.x;
-    const bool col = v < s.vecs;
+    const unsigned v = threadIdx.x + k * blockDim.x;
     const float* g = s.gate == MOE_GATE_CHANNEL ? static_cast<const float*>(a.gate) : nullptr;
-    gw[k] = mul(mul(weights(a.w_post, v, col, 1.0f), weights(g, v, col, 1.0f)), both(s.out));
-    wn[k] = weights(a.w_next, v, col, 0.0f);
+    gw[k] = mul(mul(weights<F32>(a.w_post, v, s.vecs, 1.0f), weights<F32>(g, v, s.vecs, 1.0f)), both(s.out));
+    wn[k] = weights<F32>(a.w_next, v, s.vecs, 0.0f);
   }
   for (long long row = blockIdx.x; row < s.rows; row += step) {
     fetch(row + (long long)(STAGES - 1) * step, slot == 0 ? STAGES - 1 : slot - 1);
     float factor = 1.0f;   // of this row's y
     if (s.gate == MOE_GATE_TOKEN) factor = static_cast<const float*>(a.gate)[row];
     copies_wait<STAGES - 1>();
-    const char* st = ring + (size_t)slot * stage_bytes;
+    const char* st = ring + slot * stage_bytes;
     slot = slot + 1 == STAGES ? 0 : slot + 1;
     if (post) {
       f32x2 q = both(0.0f);
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
-        const int v = threadIdx.x + k * blockDim.x;
+        const unsigned v = threadIdx.x + k * blockDim.x;
         if (v >= s.vecs) continue;
-        const F8 y = read8<false>(st + off_y + (size_t)v * 16);
+        const F8 y = read8<false, F32>(st + off_y, v, s.vecs);
         dot(y, y, q);
       }
       float sum = sum_of(q);
@@ -218,14 +253,14 @@ __global__ void __launch_bounds__(most_threads(VPT), most_ctas(VPT))
     f32x2 q = both(0.0f);
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      const int v = threadIdx.x + k * blockDim.x;
+      const unsigned v = threadIdx.x + k * blockDim.x;
       if (v >= s.vecs) continue;
-      h[k] = read8<F32>(st + (size_t)v * kSt);
+      h[k] = read8<F32, F32>(st, v, s.vecs);
       if (has_y) {
-        F8 y = read8<false>(st + off_y + (size_t)v * 16);
-        if (elem) y = mul(y, read8<false>(st + off_g + (size_t)v * 16));
+        F8 y = read8<false, F32>(st + off_y, v, s.vecs);
+        if (elem) y = mul(y, read8<false, F32>(st + off_g, v, s.vecs));
         h[k] = fma(mul(y, both(factor)), gw[k], mul(h[k], both(s.res)));
-        write8<F32>(static_cast<char*>(a.h) + ((size_t)row * s.vecs + v) * kSt, h[k]);
+        write8<F32, F32>(row_of<F32>(a.h, row, s.vecs), v, s.vecs, h[k]);
       }
       dot(h[k], h[k], q);
     }
@@ -236,10 +271,10 @@ __global__ void __launch_bounds__(most_threads(VPT), most_ctas(VPT))
     if (threadIdx.x == 0 && a.rstd_h) a.rstd_h[row] = r;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      const int v = threadIdx.x + k * blockDim.x;
+      const unsigned v = threadIdx.x + k * blockDim.x;
       if (v >= s.vecs) continue;
-      write8<false>(static_cast<char*>(a.n) + ((size_t)row * s.vecs + v) * 16,
-                    mul(mul(h[k], both(r)), wn[k]));
+      write8<false, F32>(row_of<false>(a.n, row, s.vecs), v, s.vecs,
+                         mul(mul(h[k], both(r)), wn[k]));
     }
   }
 }
@@ -255,8 +290,8 @@ template <bool F32, int VPT, int STAGES>
 __global__ void __launch_bounds__(most_threads(VPT), most_ctas(VPT))
     norm_grad_kernel(Shape s, NormGrad a, int stage_bytes, float* partial) {
   extern __shared__ __align__(16) char ring[];
-  __shared__ float sums[2 * 16 * 3];
-  constexpr int kSt = F32 ? 32 : 16;
+  __shared__ float sums[2 * 32 * 3];
+  constexpr unsigned kSt = F32 ? 32 : 16;
   constexpr bool kKeep = VPT <= 2;
   const bool post = a.w_post != nullptr, next = a.w_next != nullptr, has_dh = a.dh != nullptr;
   const bool elem = s.gate == MOE_GATE_ELEMENT, token = s.gate == MOE_GATE_TOKEN;
@@ -273,36 +308,40 @@ __global__ void __launch_bounds__(most_threads(VPT), most_ctas(VPT))
   int flip = 0, slot = 0;
   const auto fetch = [&](long long row, int to) {
     if (row < s.rows) {
-      char* st = ring + (size_t)to * stage_bytes;
+      char* st = ring + to * stage_bytes;
+      const char* dh = row_of<F32>(a.dh, row, s.vecs);
+      const char* h = row_of<F32>(a.h, row, s.vecs);
+      const char* dn = row_of<false>(a.dn, row, s.vecs);
+      const char* y = row_of<false>(a.y, row, s.vecs);
+      const char* g = row_of<false>(a.gate, row, s.vecs);
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
-        const int v = threadIdx.x + k * blockDim.x;
-        const size_t at = (size_t)row * s.vecs + v;
+        const unsigned v = threadIdx.x + k * blockDim.x;
         if (v >= s.vecs) continue;
-        if (has_dh) fetch8<F32>(st, v, a.dh, at);
+        if (has_dh) fetch8<F32, F32>(st, dh, v, s.vecs);
         if (next) {
-          fetch8<F32>(st + off_h, v, a.h, at);
-          fetch8<false>(st + off_n, v, a.dn, at);
+          fetch8<F32, F32>(st + off_h, h, v, s.vecs);
+          fetch8<false, F32>(st + off_n, dn, v, s.vecs);
         }
-        if (has_y) fetch8<false>(st + off_y, v, a.y, at);
-        if (elem) fetch8<false>(st + off_g, v, a.gate, at);
+        if (has_y) fetch8<false, F32>(st + off_y, y, v, s.vecs);
+        if (elem) fetch8<false, F32>(st + off_g, g, v, s.vecs);
       }
     }
     copies_commit();
   };
 #pragma unroll
   for (int i = 0; i < STAGES - 1; ++i) fetch(blockIdx.x + (long long)i * step, i);
-  const auto weight_y = [&](int v, bool col) {
-    F8 w = weights(a.w_post, v, col, 1.0f);
-    return channel ? mul(w, weights(channel, v, col, 1.0f)) : w;
+  const auto weight_y = [&](unsigned v) {
+    F8 w = weights<F32>(a.w_post, v, s.vecs, 1.0f);
+    return channel ? mul(w, weights<F32>(channel, v, s.vecs, 1.0f)) : w;
   };
   F8 keep_y[kKeep ? VPT : 1], keep_n[kKeep ? VPT : 1], acc_y[VPT], acc_n[VPT];
 #pragma unroll
   for (int k = 0; k < VPT; ++k) {
-    const int v = threadIdx.x + k * blockDim.x;
+    const unsigned v = threadIdx.x + k * blockDim.x;
     if (kKeep) {
-      keep_y[k] = weight_y(v, v < s.vecs);
-      keep_n[k] = weights(a.w_next, v, v < s.vecs, 0.0f);
+      keep_y[k] = weight_y(v);
+      keep_n[k] = weights<F32>(a.w_next, v, s.vecs, 0.0f);
     }
     acc_y[k] = acc_n[k] = all(0);
   }
@@ -320,7 +359,7 @@ __global__ void __launch_bounds__(most_threads(VPT), most_ctas(VPT))
     const float rh = rh_next, ry = ry_next, gt = gt_next;
     factors(row + step, rh_next, ry_next, gt_next);
     copies_wait<STAGES - 1>();
-    const char* st = ring + (size_t)slot * stage_bytes;
+    const char* st = ring + slot * stage_bytes;
     slot = slot + 1 == STAGES ? 0 : slot + 1;
 
     const f32x2 rh2 = both(rh);
@@ -328,23 +367,23 @@ __global__ void __launch_bounds__(most_threads(VPT), most_ctas(VPT))
     f32x2 qa = 0, qg = 0, qh = 0;   // sums of a h, u (dh + rh a) and u h (h, u: without their r)
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      const int v = threadIdx.x + k * blockDim.x;
+      const unsigned v = threadIdx.x + k * blockDim.x;
       if (v >= s.vecs) continue;
       F8 h = all(0);
       G[k] = h;
-      if (has_dh) G[k] = read8<F32>(st + (size_t)v * kSt);
+      if (has_dh) G[k] = read8<F32, F32>(st, v, s.vecs);
       if (next) {
-        h = read8<F32>(st + off_h + (size_t)v * kSt);
-        const F8 dn = read8<false>(st + off_n + (size_t)v * 16);
+        h = read8<F32, F32>(st + off_h, v, s.vecs);
+        const F8 dn = read8<false, F32>(st + off_n, v, s.vecs);
         acc_n[k] = fma(dn, mul(h, rh2), acc_n[k]);
-        const F8 d = mul(dn, kKeep ? keep_n[k] : weights(a.w_next, v, true, 0.0f));
+        const F8 d = mul(dn, kKeep ? keep_n[k] : weights<F32>(a.w_next, v, s.vecs, 0.0f));
         dot(d, h, qa);
         G[k] = fma(d, rh2, G[k]);
       }
       if (dot_y) {
-        F8 u = mul(read8<false>(st + off_y + (size_t)v * 16),
-                   kKeep ? keep_y[k] : weight_y(v, true));
-        if (elem) u = mul(u, read8<false>(st + off_g + (size_t)v * 16));
+        F8 u = mul(read8<false, F32>(st + off_y, v, s.vecs),
+                   kKeep ? keep_y[k] : weight_y(v));
+        if (elem) u = mul(u, read8<false, F32>(st + off_g, v, s.vecs));
         dot(u, G[k], qg);
         dot(u, h, qh);
       }
@@ -360,41 +399,47 @@ __global__ void __launch_bounds__(most_threads(VPT), most_ctas(VPT))
     const f32x2 out = both(s.out * gt * ry), back = both(-ry * ry * mean);
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      const int v = threadIdx.x + k * blockDim.x;
+      const unsigned v = threadIdx.x + k * blockDim.x;
       if (v >= s.vecs) continue;
-      const size_t at = (size_t)row * s.vecs + v;
-      if (next) G[k] = fma(read8<F32>(st + off_h + (size_t)v * kSt), hc, G[k]);
-      if (a.dx) write8<F32>(static_cast<char*>(a.dx) + at * kSt, mul(G[k], res));
+      if (next) G[k] = fma(read8<F32, F32>(st + off_h, v, s.vecs), hc, G[k]);
+      if (a.dx) write8<F32, F32>(row_of<F32>(a.dx, row, s.vecs), v, s.vecs, mul(G[k], res));
       if (!is_out) continue;
       F8 u = mul(G[k], out), y = all(0);
-      const F8 gw = kKeep ? keep_y[k] : weight_y(v, true);
-      if (has_y) y = read8<false>(st + off_y + (size_t)v * 16);
+      const F8 gw = kKeep ? keep_y[k] : weight_y(v);
+      if (has_y) y = read8<false, F32>(st + off_y, v, s.vecs);
       if (elem) {
-        if (a.dgate) write8<false>(static_cast<char*>(a.dgate) + at * 16, mul(mul(u, y), gw));
-        u = mul(u, read8<false>(st + off_g + (size_t)v * 16));
+        if (a.dgate)
+          write8<false, F32>(row_of<false>(a.dgate, row, s.vecs), v, s.vecs,
+                         mul(mul(u, y), gw));
+        u = mul(u, read8<false, F32>(st + off_g, v, s.vecs));
       }
       acc_y[k] = fma(u, y, acc_y[k]);
       u = mul(u, gw);
-      write8<false>(static_cast<char*>(a.dy) + at * 16, post ? fma(y, back, u) : u);
+      write8<false, F32>(row_of<false>(a.dy, row, s.vecs), v, s.vecs,
+                         post ? fma(y, back, u) : u);
     }
   }
+  pdl_trigger();
   if (!partial) return;
-  // partial sums of this CTA: [0][cta][d] acc_y, [1][cta][d] acc_n
+  // partial sums of this CTA: [cta][d] acc_y if there is a y side, [cta][d] acc_n if there is a next
 #pragma unroll
   for (int k = 0; k < VPT; ++k) {
-    const int v = threadIdx.x + k * blockDim.x;
+    const unsigned v = threadIdx.x + k * blockDim.x;
     if (v >= s.vecs) continue;
-    char* p = reinterpret_cast<char*>(partial) + ((size_t)blockIdx.x * s.vecs + v) * 32;
-    write8<true>(p, acc_y[k]);
-    write8<true>(p + (size_t)gridDim.x * s.vecs * 32, acc_n[k]);
+    if (has_y) write8<true, F32>(row_of<true>(partial, blockIdx.x, s.vecs), v, s.vecs, acc_y[k]);
+    if (next)
+      write8<true, F32>(row_of<true>(partial, blockIdx.x + (has_y ? gridDim.x : 0), s.vecs), v,
+                        s.vecs, acc_n[k]);
   }
 }
 
 // Column sums over the CTAs' partial sums: a warp's lanes are 32 columns, a CTA's warps take parts of
-// the CTAs one after another, joined in order. blockIdx.y: 0 the sums over yh, 1 those over hh.
+// the CTAs one after another, joined in order. The grid's first half (or all of it) takes the sums
+// over yh, if there are any, the other one those over hh.
 struct ColSums {
   const float* partial;
   int ctas, d;
+  int sides;                         // 1: yh, 2: hh, 3: both
   const float *w_post, *gate;        // gate: a channel gate, else NULL
   float *dw_post, *dgate, *dw_next;  // NULL: not wanted
   int accumulate;
@@ -403,7 +448,8 @@ constexpr int kColThreads = 512;
 __global__ void __launch_bounds__(kColThreads) norm_columns_kernel(ColSums a) {
   __shared__ float part[kColThreads / 32][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
-  const bool y_side = blockIdx.y == 0;
+  const bool y_side = blockIdx.y == 0 && (a.sides & 1);
+  pdl_wait();
   if (y_side ? !a.dw_post && !a.dgate : !a.dw_next) return;
   const float* p = a.partial + (size_t)blockIdx.y * a.ctas * a.d;
   float sum = 0.0f;
@@ -495,7 +541,7 @@ cudaError_t run_any(const Shape& s, const A& a, const Plan& p, int stage, float*
 }
 
 Shape shape_of(const moe_norm_cfg& c) {
-  return Shape{c.rows, c.d, c.d / 8, c.eps, c.res_scale, c.out_scale, c.gate};
+  return Shape{c.rows, c.d, (unsigned)(c.d / 8), c.eps, c.res_scale, c.out_scale, c.gate};
 }
 
 }  // namespace
@@ -508,7 +554,7 @@ cudaError_t launch_norm(const moe_norm_cfg& c, const NormFwd& a, cudaStream_t st
   const Shape s = shape_of(c);
   const Plan p = plan_of(c.d);
   const bool f32 = c.stream_dtype == MOE_F32;
-  const int stage = s.vecs * ((f32 ? 32 : 16) + (a.y ? 16 : 0) +
+  const int stage = (int)s.vecs * ((f32 ? 32 : 16) + (a.y ? 16 : 0) +
                               (c.gate == MOE_GATE_ELEMENT ? 16 : 0));
   return f32 ? run_any<true>(s, a, p, stage, nullptr, st)
              : run_any<false>(s, a, p, stage, nullptr, st);
@@ -522,7 +568,7 @@ cudaError_t launch_norm_grad(const moe_norm_cfg& c, const NormGrad& a, bool accu
   const bool channel = c.gate == MOE_GATE_CHANNEL;
   const bool has_y = a.w_post || c.gate != MOE_GATE_NONE;
   const int b = f32 ? 32 : 16;
-  const int stage = s.vecs * ((a.dh ? b : 0) + (next ? b + 16 : 0) + (has_y ? 16 : 0) +
+  const int stage = (int)s.vecs * ((a.dh ? b : 0) + (next ? b + 16 : 0) + (has_y ? 16 : 0) +
                               (c.gate == MOE_GATE_ELEMENT ? 16 : 0));
   const bool sums = a.dw_post || a.dw_next || (channel && a.dgate);
   float* partial =
@@ -533,11 +579,12 @@ cudaError_t launch_norm_grad(const moe_norm_cfg& c, const NormGrad& a, bool accu
     if (e != cudaSuccess) return e;
   }
   if (!sums) return cudaSuccess;
-  ColSums cs{partial, s.rows > 0 ? (int)grid_of(s.rows, p) : 0, s.d, a.w_post,
+  const int sides = (has_y ? 1 : 0) | (next ? 2 : 0);
+  ColSums cs{partial, s.rows > 0 ? (int)grid_of(s.rows, p) : 0, s.d, sides, a.w_post,
              channel ? static_cast<const float*>(a.gate) : nullptr, a.dw_post,
              channel ? static_cast<float*>(a.dgate) : nullptr, a.dw_next, accumulate};
-  return launch_kernel(norm_columns_kernel, dim3((s.d + 31) / 32, 2), dim3(kColThreads), 0, st,
-                       false, cs);
+  return launch_kernel(norm_columns_kernel, dim3((s.d + 31) / 32, sides == 3 ? 2 : 1),
+                       dim3(kColThreads), 0, st, s.rows > 0, cs);
 }
 
 }  // namespace moe
