@@ -915,3 +915,37 @@ class MoELayer:
             self._run(self._x_dev, self._y_dev, s, None)
             y_host.copy_(self._y_dev, non_blocking=True)
         return y_host
+
+
+class MoEBlock:
+    """A block of the residual stream around a MoELayer, for serving:
+
+        h = res_scale x + out_scale gate norm(layer(norm(x) w_in)) w_out
+
+    ``h = block(x)``; with w_next (the weight of the next block's first norm) ``h, n = block(x, n)``:
+    n is what the next block's layer takes, normed in the pass that ends this block, and n given is
+    that of the block before (None: normed here). w_in, w_out (None: no norm behind the layer),
+    w_next: fp32 [d]; gate: None, fp32 [d], fp32 [T][1] or bf16 [T][d]; x bf16 or fp32 [T][d]."""
+
+    def __init__(self, layer: MoELayer, w_in, w_out=None, gate=None, w_next=None, eps=1e-6,
+                 res_scale=1.0, out_scale=1.0):
+        self.layer, self.w_in, self.w_out = layer, w_in, w_out
+        self.gate, self.w_next, self.eps = gate, w_next, eps
+        self.scales = dict(res_scale=res_scale, out_scale=out_scale)
+        shape, dev = (layer.cfg.T, layer.cfg.d), layer.w_gate.device
+        self.n = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        self.y = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+
+    def __call__(self, x, n=None, h=None, stream=None):
+        """h may be x itself. The n that is returned is the block's own buffer."""
+        if n is None:
+            n = self.n
+            norm_in(x, self.w_in, n, eps=self.eps, stream=stream)
+        if h is None:
+            h = torch.empty_like(x)
+        self.layer(n, self.y, stream)
+        # the layer's output has been read where the next norm's takes its place
+        n_next = self.y if self.w_next is not None else None
+        norm_out(self.y, x, self.w_out, self.gate, self.w_next, h, n_next, eps=self.eps,
+                 stream=stream, **self.scales)
+        return h if n_next is None else (h, n_next)
