@@ -5,7 +5,6 @@
 // The tensors are cut into chunks, which the CTAs of one grid take in turn; the table of the tensors
 // travels as a kernel argument, so the step needs no device table and a captured one keeps its own.
 #include "moe_device.cuh"
-#include "moe_f32x2.cuh"
 
 namespace moe {
 namespace {
@@ -47,7 +46,7 @@ __device__ __forceinline__ int tensor_of(const Table<CAP>& tab, uint32_t chunk) 
   return lo;
 }
 
-// Four values of a gradient from element i on (cnt of them exist; the others are 0).
+// Four values from element i on, of which cnt exist (none, if it is negative); the others are 0.
 __device__ __forceinline__ float4 load_grad(const void* g, bool f32, long long i, int cnt) {
   float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (f32) {
@@ -80,27 +79,26 @@ __device__ __forceinline__ uint32_t load_codes(const char* q, int cnt) {
     if (j < cnt) v |= static_cast<uint32_t>(static_cast<uint8_t>(q[j])) << (8 * j);
   return v;
 }
-__device__ __forceinline__ void store4(float* p, const float2 (&v)[2], int cnt) {
-  if (cnt == 4) {
-    __stcs(reinterpret_cast<float4*>(p), make_float4(v[0].x, v[0].y, v[1].x, v[1].y));
+__device__ __forceinline__ void store4(float* p, const float4& v, int cnt) {
+  if (cnt >= 4) {
+    __stcs(reinterpret_cast<float4*>(p), v);
     return;
   }
-  if (cnt > 0) p[0] = v[0].x;
-  if (cnt > 1) p[1] = v[0].y;
-  if (cnt > 2) p[2] = v[1].x;
+  if (cnt > 0) p[0] = v.x;
+  if (cnt > 1) p[1] = v.y;
+  if (cnt > 2) p[2] = v.z;
 }
-__device__ __forceinline__ void store4_bf16(__nv_bfloat16* p, const float2 (&v)[2], int cnt) {
-  if (cnt == 4) {
-    __stcs(reinterpret_cast<uint2*>(p),
-           make_uint2(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y)));
+__device__ __forceinline__ void store4_bf16(__nv_bfloat16* p, const float4& v, int cnt) {
+  if (cnt >= 4) {
+    __stcs(reinterpret_cast<uint2*>(p), make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w)));
     return;
   }
-  if (cnt > 0) p[0] = __float2bfloat16_rn(v[0].x);
-  if (cnt > 1) p[1] = __float2bfloat16_rn(v[0].y);
-  if (cnt > 2) p[2] = __float2bfloat16_rn(v[1].x);
+  if (cnt > 0) p[0] = __float2bfloat16_rn(v.x);
+  if (cnt > 1) p[1] = __float2bfloat16_rn(v.y);
+  if (cnt > 2) p[2] = __float2bfloat16_rn(v.z);
 }
 __device__ __forceinline__ void store_codes(char* q, uint32_t v, int cnt) {
-  if (cnt == 4) {
+  if (cnt >= 4) {
     __stcs(reinterpret_cast<uint32_t*>(q), v);
     return;
   }
@@ -230,117 +228,85 @@ __device__ __forceinline__ Scalars scalars(const Hyper& h, const State* state, c
   return sc;
 }
 
-// A pair of elements: the new moments and the parameters. Each product and sum of the moments is
-// rounded by itself, so that 8-bit moments can be checked code by code. (They are written one by one:
-// the assembler joins a mul2 and an add2 of its result into one operation of one rounding, .rn or
-// not.) The parameter's quotient takes the hardware's reciprocal (1 ulp).
+// One element: the new moments and the parameter. Each product and sum of the moments is rounded by
+// itself, so that 8-bit moments can be checked code by code; the parameter's quotient takes the
+// hardware's reciprocal (1 ulp).
 __device__ __forceinline__ float recip(float v) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
 }
-__device__ __forceinline__ void update(const Scalars& sc, float decay, f32x2 g2, f32x2& p, float2& m,
-                                       float2& v, float2& root) {
-  if (sc.clip) g2 = mul2(g2, both(sc.factor));
-  const auto mean = [](float b, float old, float n, float now) {
-    return __fadd_rn(__fmul_rn(b, old), __fmul_rn(n, now));
-  };
-  const float2 g = halves(g2), gg = halves(mul2(g2, g2));
-  m = make_float2(mean(sc.b1, m.x, sc.n1, g.x), mean(sc.b1, m.y, sc.n1, g.y));
-  v = make_float2(mean(sc.b2, v.x, sc.n2, gg.x), mean(sc.b2, v.y, sc.n2, gg.y));
-  root = make_float2(__fsqrt_rn(v.x), __fsqrt_rn(v.y));
-  const float2 den = halves(fma2(pair(root.x, root.y), both(sc.root), both(sc.eps)));
-  const f32x2 quot = mul2(pair(m.x, m.y), pair(recip(den.x), recip(den.y)));
-  p = fma2(both(-decay), p, p);
-  p = fma2(both(-sc.move), quot, p);
+__device__ __forceinline__ void update(const Scalars& sc, float decay, float g, float& p, float& m,
+                                       float& v, float& root) {
+  if (sc.clip) g = __fmul_rn(g, sc.factor);
+  m = __fadd_rn(__fmul_rn(sc.b1, m), __fmul_rn(sc.n1, g));
+  v = __fadd_rn(__fmul_rn(sc.b2, v), __fmul_rn(sc.n2, __fmul_rn(g, g)));
+  root = __fsqrt_rn(v);
+  const float quot = m * recip(__fmaf_rn(root, sc.root, sc.eps));
+  p = __fmaf_rn(-sc.move, quot, __fmaf_rn(-decay, p, p));
 }
 
-// The largest of a warp's non-negative numbers (their order is that of their bits).
-__device__ __forceinline__ float warp_max(float v) {
-  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
+// The largest of 16 lanes' non-negative numbers (their order is that of their bits).
+__device__ __forceinline__ float half_warp_max(float v) {
+  const uint32_t lanes = (threadIdx.x & 16) ? 0xffff0000u : 0xffffu;
+  return __uint_as_float(__reduce_max_sync(lanes, __float_as_uint(v)));
 }
 
-// |x| / scale, the IEEE quotients (up to 448 and a rounding). By the correctly rounded reciprocal and
-// one correction step (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000
-// processor", 1990) where nothing of it can leave the fp32 range, by division otherwise.
-__device__ __forceinline__ f32x2 quotients(float2 x, float scale, f32x2 r, bool plain) {
-  const f32x2 a = pair(fabsf(x.x), fabsf(x.y));
-  if (plain) {
-    const f32x2 q0 = mul2(a, r);
-    return fma2(fma2(q0, both(scale), minus(a)), minus(r), q0);
-  }
-  return pair(__fdiv_rn(fabsf(x.x), scale), __fdiv_rn(fabsf(x.y), scale));
-}
-
-// The steps below choose by saturation (0 or 1 on the FMA pipe) rather than by comparison and select
-// (two operations of the ALU pipe, which has half its rate and the integer work beside it).
-__device__ __forceinline__ float is_positive(float v, float big) {   // v * big >= 1 where v > 0
+// 1 where v > 0 (and v * big >= 1), else 0; a NaN gives 0. (By saturation on the FMA pipe: comparison
+// and select are two operations of the ALU pipe, which the integer work beside them fills.)
+__device__ __forceinline__ float is_positive(float v, float big) {
   float r;
   asm("mul.rn.sat.f32 %0, %1, %2;" : "=f"(r) : "f"(v), "f"(big));
   return r;
 }
-
-// A pair of quotients rounded up or down to e4m3 by 16 random bits each. With the random bits added
-// below the code's last bit, cutting off what is below it rounds up with odds of the distance from the
-// lower code. Below 2^-6 the steps are 2^-9: with 2^-6 added they lie at the same bits. (What is past
-// 448 by a rounding is cut or, as a code, saturated.)
-__device__ __forceinline__ f32x2 shift_of(f32x2 q) {   // 2^-6 where q < 2^-6, else 0
-  const float2 f = halves(fma2(q, both(-0x1p40f), both(0x1p34f)));
-  return mul2(pair(__saturatef(f.x), __saturatef(f.y)), both(0x1p-6f));
-}
+__device__ __forceinline__ float below_2_6(float q) { return __saturatef(__fmaf_rn(q, -0x1p40f, 0x1p34f)); }
 __device__ __forceinline__ float cut(uint32_t bits) { return __uint_as_float(bits & 0xfff00000u); }
-__device__ __forceinline__ f32x2 round_e4m3(f32x2 q, uint32_t r0, uint32_t r1) {
-  const f32x2 shift = shift_of(q);
-  const float2 y = halves(add2(q, shift));
-  return add2(pair(cut(__float_as_uint(y.x) + r0 * 16), cut(__float_as_uint(y.y) + r1 * 16)),
-              minus(shift));
+
+// A quotient rounded up or down to e4m3 by 16 random bits. With the random bits added below the code's
+// last bit, cutting off what is below it rounds up with odds of the distance from the lower code.
+// Below 2^-6 the steps are 2^-9: with 2^-6 added they lie at the same bits. (What is past 448 by a
+// rounding is cut or, as a code, saturated.)
+__device__ __forceinline__ float round_e4m3(float q, uint32_t r16) {
+  const float s = below_2_6(q), y = __fmaf_rn(s, 0x1p-6f, q);
+  return __fmaf_rn(s, -0x1p-6f, cut(__float_as_uint(y) + r16 * 16));
 }
 // The same for the root of a second moment, with odds that keep the mean of its square, (q^2 - lo^2)
-// / (hi^2 - lo^2): odds linear in q would add the rounding's variance to v each step, several percent
-// of v in the long run. A root above 0 keeps a code above 0.
-__device__ __forceinline__ f32x2 round_root_e4m3(f32x2 q, float2 root, uint32_t r0, uint32_t r1) {
-  const f32x2 back = minus(shift_of(q));
-  const float2 y = halves(add2(q, minus(back)));
-  const float cx = cut(__float_as_uint(y.x)), cy = cut(__float_as_uint(y.y));
-  const f32x2 lo = add2(pair(cx, cy), back);   // exact, and so are hi, hi - lo and hi + lo
-  const f32x2 hi = add2(pair(__uint_as_float(__float_as_uint(cx) + 0x100000u),
-                             __uint_as_float(__float_as_uint(cy) + 0x100000u)),
-                        back);
-  const f32x2 gap = add2(hi, minus(lo));
-  const f32x2 odds = mul2(add2(q, minus(lo)), add2(q, lo)), whole = mul2(gap, add2(hi, lo));
+// / (hi^2 - lo^2): odds linear in q would add the rounding's variance to v each step, several
+// percent of v in the long run. A root above 0 keeps a code above 0.
+__device__ __forceinline__ float round_root_e4m3(float q, float root, uint32_t r16) {
+  const float s = below_2_6(q), y = __fmaf_rn(s, 0x1p-6f, q), c = cut(__float_as_uint(y));
+  const float lo = __fmaf_rn(s, -0x1p-6f, c);   // exact, as are hi, hi - lo and hi + lo
+  const float hi = __fmaf_rn(s, -0x1p-6f, __uint_as_float(__float_as_uint(c) + 0x100000u));
+  const float gap = __fadd_rn(hi, -lo);
+  const float odds = __fmul_rn(__fadd_rn(q, -lo), __fadd_rn(q, lo));
+  const float whole = __fmul_rn(gap, __fadd_rn(hi, lo));
   // r / 2^16 as the fraction of a number between 1 and 2
-  const f32x2 r = add2(pair(__uint_as_float(0x3f800000u + r0 * 128),
-                            __uint_as_float(0x3f800000u + r1 * 128)),
-                       both(-1.0f));
+  const float r = __fadd_rn(__uint_as_float(0x3f800000u + r16 * 128), -1.0f);
   // up where r whole, rounded, < odds. (A difference that is no multiple of 2^-100 leaves a value
-  // below the lowest code, which the next line makes that code.)
-  const float2 rr = halves(r), w = halves(whole), o = halves(odds);
-  const float2 ahead = make_float2(__fadd_rn(o.x, -__fmul_rn(rr.x, w.x)),
-                                   __fadd_rn(o.y, -__fmul_rn(rr.y, w.y)));
-  const float2 u = halves(fma2(pair(is_positive(ahead.x, 0x1p100f), is_positive(ahead.y, 0x1p100f)),
-                               gap, lo));
-  const float2 least = halves(mul2(pair(is_positive(root.x, 0x1p100f), is_positive(root.y, 0x1p100f)),
-                                   both(0x1p-9f)));
-  float2 v;   // (a NaN stays one)
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(v.x) : "f"(u.x), "f"(least.x));
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(v.y) : "f"(u.y), "f"(least.y));
-  return pair(v.x, v.y);
+  // below the lowest code, which the next lines make that code.)
+  const float up = is_positive(__fadd_rn(odds, -__fmul_rn(r, whole)), 0x1p100f);
+  const float u = __fmaf_rn(up, gap, lo), least = is_positive(root, 0x1p100f) * 0x1p-9f;
+  float v;   // (a NaN stays one)
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(v) : "f"(u), "f"(least));
+  return v;
 }
-__device__ __forceinline__ uint32_t pack_codes(float2 a, float2 b) {
-  return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3)) |
-         static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3)) << 16;
+__device__ __forceinline__ uint32_t pack_codes(const float* v) {
+  return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(v[0], v[1]), __NV_SATFINITE,
+                                                        __NV_E4M3)) |
+         static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(v[2], v[3]), __NV_SATFINITE,
+                                                        __NV_E4M3))
+             << 16;
 }
-__device__ __forceinline__ f32x2 codes2(uint32_t c, float s) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
-      static_cast<__nv_fp8x2_storage_t>(c & 0xffffu), __NV_E4M3);
-  const float2 f = __half22float2(__half2(h));
-  return mul2(pair(f.x, f.y), both(s));
+__device__ __forceinline__ void codes4(uint32_t c, float s, float* f) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+        static_cast<__nv_fp8x2_storage_t>((c >> (16 * i)) & 0xffffu), __NV_E4M3);
+    const float2 v = __half22float2(__half2(h));
+    f[2 * i] = __fmul_rn(v.x, s);
+    f[2 * i + 1] = __fmul_rn(v.y, s);
+  }
 }
-__device__ __forceinline__ float block_scale(float amax) {
-  return amax > 0.0f ? __fmul_rn(amax, 1.0f / 448.0f) : 1.0f;
-}
-// (the reciprocal, its correction and the quotient stay inside the fp32 range)
-__device__ __forceinline__ bool plain_scale(float s) { return s > 0x1p-60f && s < 0x1p100f; }
 
 // The last call of a step: the last CTA to end counts it. (Every CTA has read the state before it
 // took its ticket.)
@@ -351,121 +317,29 @@ __device__ __forceinline__ void finish(const Hyper& h, State* state, bool more) 
   state->c2 = h.beta2 * state->c2 + (1.0 - h.beta2);
 }
 
-// A lane's four elements of a block, and the step on them. The pointers are the lane's own; cnt of
-// the elements exist.
-struct Pointers {
-  const char* g;
-  char *p, *w, *m, *v;
-  float *ms, *vs;   // of the warp's block
-};
-template <int BITS>
-__device__ __forceinline__ Pointers pointers(const moe_adam_tensor& e, long long block) {
-  const long long at = block * kBlock + (threadIdx.x & 31) * 4;
-  constexpr int kMoment = BITS == 8 ? 1 : 4;
-  Pointers r;
-  r.g = static_cast<const char*>(e.g) + at * (e.g_dtype == MOE_F32 ? 4 : 2);
-  r.p = reinterpret_cast<char*>(e.p) + at * 4;
-  r.w = e.w ? static_cast<char*>(e.w) + at * 2 : nullptr;
-  r.m = static_cast<char*>(e.m) + at * kMoment;
-  r.v = static_cast<char*>(e.v) + at * kMoment;
-  r.ms = BITS == 8 ? e.m_scale + block : nullptr;
-  r.vs = BITS == 8 ? e.v_scale + block : nullptr;
-  return r;
-}
+// ------------------------------------------------------------------------------------------
+// Moments in 32 bits: four elements a lane at once, loads a step ahead. 11.9 GB for 398 M parameters
+// and their norm: bound by memory.
+// ------------------------------------------------------------------------------------------
 struct Four {
-  f32x2 g[2], p[2];
-  float2 m[2], v[2];
+  float4 g, p, m, v;
 };
-
-__device__ __forceinline__ void from_codes(Four& f, uint32_t qm, uint32_t qv, float sm, float sv) {
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    f.m[j] = halves(codes2(qm >> (16 * j), sm));
-    const f32x2 u = codes2(qv >> (16 * j), sv);
-    f.v[j] = halves(mul2(u, u));
-  }
+__device__ __forceinline__ Four load_four(const moe_adam_tensor& e, long long at, int cnt) {
+  return Four{load_grad(e.g, e.g_dtype == MOE_F32, at, cnt), load4(e.p + at, cnt),
+              load4(static_cast<const float*>(e.m) + at, cnt),
+              load4(static_cast<const float*>(e.v) + at, cnt)};
 }
-
-template <int BITS>
-__device__ __forceinline__ void step_four(const Scalars& sc, float decay, uint32_t key, long long block,
-                                          const Pointers& to, int i, int cnt, Four& f) {
-  float2 root[2];
-  update(sc, decay, f.g[0], f.p[0], f.m[0], f.v[0], root[0]);
-  update(sc, decay, f.g[1], f.p[1], f.m[1], f.v[1], root[1]);
-  const float2 p[2] = {halves(f.p[0]), halves(f.p[1])};
-  // i: steps of the CTA past the pointers
-  store4(reinterpret_cast<float*>(to.p) + i * kStep, p, cnt);
-  if (to.w) store4_bf16(reinterpret_cast<__nv_bfloat16*>(to.w) + i * kStep, p, cnt);
-  if (BITS == 32) {
-    store4(reinterpret_cast<float*>(to.m) + i * kStep, f.m, cnt);
-    store4(reinterpret_cast<float*>(to.v) + i * kStep, f.v, cnt);
-    return;
-  }
-  const int lane = threadIdx.x & 31;
-  // (fmaxf leaves a NaN out)
-  const float am = warp_max(fmaxf(fmaxf(fabsf(f.m[0].x), fabsf(f.m[0].y)),
-                                  fmaxf(fabsf(f.m[1].x), fabsf(f.m[1].y))));
-  const float av = warp_max(fmaxf(fmaxf(root[0].x, root[0].y), fmaxf(root[1].x, root[1].y)));
-  const float sm = block_scale(am), sv = block_scale(av);
-  const f32x2 rm = both(__frcp_rn(sm)), rv = both(__frcp_rn(sv));
-  const bool plain = plain_scale(sm) && plain_scale(sv);
-  const uint32_t from = mix(key ^ static_cast<uint32_t>(block)) + lane * 4 * kGolden;
-  float2 cm[2], cv[2];
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    // the halves of the hash x ^ (x >> 16)
-    const uint32_t x0 = premix(from + 2 * j * kGolden), x1 = premix(from + (2 * j + 1) * kGolden);
-    const uint32_t h0 = x0 >> 16, h1 = x1 >> 16;
-    const float2 q = halves(round_e4m3(quotients(f.m[j], sm, rm, plain), h0, h1));
-    cm[j] = make_float2(copysignf(q.x, f.m[j].x), copysignf(q.y, f.m[j].y));
-    cv[j] = halves(round_root_e4m3(quotients(root[j], sv, rv, plain), root[j], (x0 ^ h0) & 0xffffu,
-                                   (x1 ^ h1) & 0xffffu));
-  }
-  store_codes(to.m + i * kStep, pack_codes(cm[0], cm[1]), cnt);
-  store_codes(to.v + i * kStep, pack_codes(cv[0], cv[1]), cnt);
-  if (lane == 0) {
-    to.ms[i * (kStep / kBlock)] = sm;
-    to.vs[i * (kStep / kBlock)] = sv;
-  }
-}
-
-// Loads straight from memory: a step ahead with 32-bit moments, and where a tensor ends.
-template <int BITS>
-__device__ __forceinline__ Four load_four(const Pointers& from, bool g_f32, int i, int cnt) {
-  Four f;
-  const float4 g = load_grad(from.g, g_f32, (long long)i * kStep, cnt);
-  const float4 p = load4(reinterpret_cast<const float*>(from.p) + i * kStep, cnt);
-  f.g[0] = pair(g.x, g.y), f.g[1] = pair(g.z, g.w);
-  f.p[0] = pair(p.x, p.y), f.p[1] = pair(p.z, p.w);
-  if (BITS == 32) {
-    const float4 m = load4(reinterpret_cast<const float*>(from.m) + i * kStep, cnt);
-    const float4 v = load4(reinterpret_cast<const float*>(from.v) + i * kStep, cnt);
-    f.m[0] = make_float2(m.x, m.y), f.m[1] = make_float2(m.z, m.w);
-    f.v[0] = make_float2(v.x, v.y), f.v[1] = make_float2(v.z, v.w);
-  } else {
-    from_codes(f, load_codes(from.m + i * kStep, cnt), load_codes(from.v + i * kStep, cnt),
-               from.ms[i * (kStep / kBlock)], from.vs[i * (kStep / kBlock)]);
-  }
-  return f;
-}
-
-// The elements past a tensor's last whole chunk, tensor by tensor a CTA.
-template <int CAP, int BITS>
-__device__ __forceinline__ void tails(const Table<CAP>& tab, const Scalars& sc) {
-  const int lane = threadIdx.x & 31;
-  // (the first whole chunks go to the first CTAs: the tails to the last ones)
-  for (int t = gridDim.x - 1 - blockIdx.x; t < tab.n; t += gridDim.x) {
-    const moe_adam_tensor& e = tab.t[t];
-    const uint32_t key = BITS == 8 ? mix(e.seed ^ (sc.step * kGolden)) : 0;
-    for (long long block = e.n / kChunk * (kChunk / kBlock) + (threadIdx.x >> 5);
-         block * kBlock < e.n; block += kThreads / 32) {   // whole warps
-      const long long left = e.n - block * kBlock - lane * 4;
-      const int cnt = left >= 4 ? 4 : left > 0 ? (int)left : 0;
-      const Pointers at = pointers<BITS>(e, block);
-      Four f = load_four<BITS>(at, e.g_dtype == MOE_F32, 0, cnt);
-      step_four<BITS>(sc, sc.lr * e.weight_decay, key, block, at, 0, cnt, f);
-    }
-  }
+__device__ __forceinline__ void step_four(const Scalars& sc, const moe_adam_tensor& e, float decay,
+                                          long long at, int cnt, Four f) {
+  float root;
+  update(sc, decay, f.g.x, f.p.x, f.m.x, f.v.x, root);
+  update(sc, decay, f.g.y, f.p.y, f.m.y, f.v.y, root);
+  update(sc, decay, f.g.z, f.p.z, f.m.z, f.v.z, root);
+  update(sc, decay, f.g.w, f.p.w, f.m.w, f.v.w, root);
+  store4(e.p + at, f.p, cnt);
+  if (e.w) store4_bf16(static_cast<__nv_bfloat16*>(e.w) + at, f.p, cnt);
+  store4(static_cast<float*>(e.m) + at, f.m, cnt);
+  store4(static_cast<float*>(e.v) + at, f.v, cnt);
 }
 
 template <int CAP>
@@ -481,33 +355,117 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constan
   for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
     const int t = tensor_of(tab, c);
     const moe_adam_tensor& e = tab.t[t];
-    const long long first =
-        (long long)(c - tab.first[t]) * (kChunk / kBlock) + (threadIdx.x >> 5);
-    const Pointers at = pointers<32>(e, first);
-    const bool f32 = e.g_dtype == MOE_F32;
+    const long long first = (long long)(c - tab.first[t]) * kChunk + threadIdx.x * 4;
     const float decay = sc.lr * e.weight_decay;
-    Four next = load_four<32>(at, f32, 0, 4);
+    Four next = load_four(e, first, 4);
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-      Four now = next;
-      if (i + 1 < kSteps) next = load_four<32>(at, f32, i + 1, 4);
-      step_four<32>(sc, decay, 0, first, at, i, 4, now);
+      const Four now = next;
+      if (i + 1 < kSteps) next = load_four(e, first + (i + 1) * kStep, 4);
+      step_four(sc, e, decay, first + i * kStep, 4, now);
     }
   }
-  tails<CAP, 32>(tab, sc);
+  // the elements past the whole chunks, tensor by tensor a CTA (the last CTAs: the first ones have
+  // had the odd chunks)
+  for (int t = gridDim.x - 1 - blockIdx.x; t < tab.n; t += gridDim.x) {
+    const moe_adam_tensor& e = tab.t[t];
+    for (long long at = e.n / kChunk * kChunk + threadIdx.x * 4; at < e.n; at += kStep) {
+      const int cnt = e.n - at >= 4 ? 4 : (int)(e.n - at);
+      step_four(sc, e, sc.lr * e.weight_decay, at, cnt, load_four(e, at, cnt));
+    }
+  }
   finish(hyper, state, more);
 }
 
-// 8-bit moments: the arithmetic of the rounding bounds it, not memory. Each thread's elements come
-// through stages of its own in shared memory, a chunk ahead, and a CTA takes neighbouring chunks, so
-// that addresses are constants past a chunk's pointers. 398 M parameters, bf16 gradients: 1.59 ms
-// (4.0 TB/s); with loads to registers a step ahead 1.93 ms, waiting for memory half of the time; with
-// the ring but its addresses computed for each step 1.88 ms, 145 instructions an element.
+// ------------------------------------------------------------------------------------------
+// Moments in 8 bits: eight elements a lane at once, so that 16 lanes hold a block and what is done
+// once for it (scales, reciprocals, the key of its random numbers) is shared by eight elements. The
+// arithmetic of the rounding bounds it beside memory (FIGURES). Each thread's elements come through
+// two stages of its own in shared memory, and a CTA takes neighbouring chunks.
+// ------------------------------------------------------------------------------------------
+constexpr int kStep8 = 8 * kThreads, kSteps8 = kChunk / kStep8;
 struct Stage8 {
-  float4 g[kThreads];    // bf16 gradients: 8 bytes used
-  float4 p[kThreads];
-  uint32_t m[kThreads], v[kThreads];
+  uint4 g[2][kThreads];   // bf16 gradients: the first
+  float4 p[2][kThreads];
+  uint2 m[kThreads], v[kThreads];
 };
+struct Eight {
+  float g[8], p[8], m[8], v[8];
+};
+__device__ __forceinline__ void put4(float* f, const float4& v) {
+  f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+}
+__device__ __forceinline__ float4 get4(const float* f) {
+  return make_float4(f[0], f[1], f[2], f[3]);
+}
+
+// at: of the lane's first element, whose block is the lane's; cnt: how many exist
+__device__ __forceinline__ void step_eight(const Scalars& sc, const moe_adam_tensor& e, float decay,
+                                           uint32_t key, long long at, int cnt, Eight& f) {
+  const long long block = at / kBlock;
+  const int place = threadIdx.x & 15;
+  float root[8], am = 0.0f, av = 0.0f;   // (fmaxf leaves a NaN out)
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    update(sc, decay, f.g[j], f.p[j], f.m[j], f.v[j], root[j]);
+    am = fmaxf(am, fabsf(f.m[j]));
+    av = fmaxf(av, root[j]);
+  }
+  __nv_bfloat16* w = static_cast<__nv_bfloat16*>(e.w) + at;
+  if (cnt == 8) {
+    __stcs(reinterpret_cast<float4*>(e.p + at), get4(f.p));
+    __stcs(reinterpret_cast<float4*>(e.p + at) + 1, get4(f.p + 4));
+    if (e.w)
+      __stcs(reinterpret_cast<uint4*>(w),
+             make_uint4(pack_bf16x2(f.p[0], f.p[1]), pack_bf16x2(f.p[2], f.p[3]),
+                        pack_bf16x2(f.p[4], f.p[5]), pack_bf16x2(f.p[6], f.p[7])));
+  } else {
+    store4(e.p + at, get4(f.p), cnt);
+    store4(e.p + at + 4, get4(f.p + 4), cnt - 4);
+    if (e.w) {
+      store4_bf16(w, get4(f.p), cnt);
+      store4_bf16(w + 4, get4(f.p + 4), cnt - 4);
+    }
+  }
+  // scale and reciprocal of the one moment in the even lanes, of the other in the odd ones
+  const float sm0 = half_warp_max(am), sv0 = half_warp_max(av);
+  const float amax = (threadIdx.x & 1) ? sv0 : sm0;
+  const float scale = amax > 0.0f ? __fmul_rn(amax, 1.0f / 448.0f) : 1.0f;
+  const float inv = __frcp_rn(scale);
+  // where the reciprocal, its correction and the quotient stay inside the fp32 range
+  const bool plain = __all_sync(0xffffffffu, scale > 0x1p-60f && scale < 0x1p100f);
+  const float sm = __shfl_sync(0xffffffffu, scale, 0, 16), sv = __shfl_sync(0xffffffffu, scale, 1, 16);
+  const float rm = __shfl_sync(0xffffffffu, inv, 0, 16), rv = __shfl_sync(0xffffffffu, inv, 1, 16);
+  // |x| / scale, the IEEE quotient, by the correctly rounded reciprocal and one correction step
+  // (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor", 1990)
+  const auto quotient = [&](float x, float s, float r) {
+    if (!plain) return __fdiv_rn(x, s);
+    const float q = __fmul_rn(x, r);
+    return __fmaf_rn(__fmaf_rn(-q, s, x), r, q);
+  };
+  const uint32_t from = mix(key ^ static_cast<uint32_t>(block)) + place * 8 * kGolden;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    // the halves of the hash x ^ (x >> 16)
+    const uint32_t x = premix(from + j * kGolden), h = x >> 16;
+    const float q = round_e4m3(quotient(fabsf(f.m[j]), sm, rm), h);
+    f.m[j] = copysignf(q, f.m[j]);
+    f.v[j] = round_root_e4m3(quotient(root[j], sv, rv), root[j], (x ^ h) & 0xffffu);
+  }
+  char *qm = static_cast<char*>(e.m) + at, *qv = static_cast<char*>(e.v) + at;
+  if (cnt == 8) {
+    __stcs(reinterpret_cast<uint2*>(qm), make_uint2(pack_codes(f.m), pack_codes(f.m + 4)));
+    __stcs(reinterpret_cast<uint2*>(qv), make_uint2(pack_codes(f.v), pack_codes(f.v + 4)));
+  } else {
+    store_codes(qm, pack_codes(f.m), cnt);
+    store_codes(qm + 4, pack_codes(f.m + 4), cnt - 4);
+    store_codes(qv, pack_codes(f.v), cnt);
+    store_codes(qv + 4, pack_codes(f.v + 4), cnt - 4);
+  }
+  if (place < 2 && (cnt == 8 || block * kBlock < e.n))
+    (place ? e.v_scale : e.m_scale)[block] = scale;
+}
+
 template <int BYTES>
 __device__ __forceinline__ void copy_in(void* to, const void* from) {
   if (BYTES == 16)
@@ -532,69 +490,103 @@ __global__ void __launch_bounds__(kThreads, 4) adamw8_kernel(const __grid_consta
     return;
   }
   const int tid = threadIdx.x, lane = tid & 31;
-  constexpr int kBlocks = kChunk / kBlock, kWarps = kThreads / 32;
   uint32_t c = (uint32_t)((unsigned long long)chunks * blockIdx.x / gridDim.x);
   const uint32_t end = (uint32_t)((unsigned long long)chunks * (blockIdx.x + 1) / gridDim.x);
   // the chunk that is copied, one before the one that is worked on
   int t_in = 0;
-  Pointers in;
-  float scale_in = 0.0f;   // lanes 0-3: of m, steps 0-3; lanes 4-7: of v
-  bool f32_in = true;
+  long long at_in = 0;     // of this thread's first element
+  float scale_in = 0.0f;   // lanes 0-3: of m, steps 0 and 1, the warp's two blocks; lanes 4-7: of v
   const auto enter = [&](uint32_t chunk) {
     if (chunk >= end) return;
     t_in = tensor_of(tab, chunk);
     const moe_adam_tensor& e = tab.t[t_in];
-    in = pointers<8>(e, (long long)(chunk - tab.first[t_in]) * kBlocks + (tid >> 5));
-    f32_in = e.g_dtype == MOE_F32;
-    if (lane < 8) scale_in = (lane < 4 ? in.ms : in.vs)[(lane & 3) * kWarps];
+    const long long first = (long long)(chunk - tab.first[t_in]) * kChunk;
+    at_in = first + tid * 8;
+    if (lane < 8)
+      scale_in = (lane < 4 ? e.m_scale : e.v_scale)[first / kBlock + (tid >> 5) * 2 +
+                                                    (lane & 1) + (lane & 2) * (kStep8 / kBlock / 2)];
   };
   const auto copy = [&](uint32_t chunk, int i) {
     if (chunk < end) {
+      const moe_adam_tensor& e = tab.t[t_in];
+      const long long at = at_in + i * kStep8;
       Stage8& st = ring[i];
-      if (f32_in)
-        copy_in<16>(&st.g[tid], in.g + (size_t)i * kStep * 4);
-      else
-        copy_in<8>(&st.g[tid], in.g + (size_t)i * kStep * 2);
-      copy_in<16>(&st.p[tid], in.p + (size_t)i * kStep * 4);
-      copy_in<4>(&st.m[tid], in.m + (size_t)i * kStep);
-      copy_in<4>(&st.v[tid], in.v + (size_t)i * kStep);
+      if (e.g_dtype == MOE_F32) {
+        copy_in<16>(&st.g[0][tid], static_cast<const float*>(e.g) + at);
+        copy_in<16>(&st.g[1][tid], static_cast<const float*>(e.g) + at + 4);
+      } else {
+        copy_in<16>(&st.g[0][tid], static_cast<const __nv_bfloat16*>(e.g) + at);
+      }
+      copy_in<16>(&st.p[0][tid], e.p + at);
+      copy_in<16>(&st.p[1][tid], e.p + at + 4);
+      copy_in<8>(&st.m[tid], static_cast<const char*>(e.m) + at);
+      copy_in<8>(&st.v[tid], static_cast<const char*>(e.v) + at);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
   enter(c);
 #pragma unroll
-  for (int i = 0; i < kSteps; ++i) copy(c, i);
+  for (int i = 0; i < kSteps8; ++i) copy(c, i);
   for (; c < end; ++c) {
-    const int t = t_in;
-    const Pointers at = in;
+    const moe_adam_tensor& e = tab.t[t_in];
+    const long long at = at_in;
     const float scales = scale_in;
-    const bool f32 = f32_in;
-    const moe_adam_tensor& e = tab.t[t];
     const float decay = sc.lr * e.weight_decay;
     const uint32_t key = mix(e.seed ^ (sc.step * kGolden));
-    const long long first = (long long)(c - tab.first[t]) * kBlocks + (tid >> 5);
     enter(c + 1);
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      asm volatile("cp.async.wait_group %0;" ::"n"(kSteps - 1) : "memory");
+#pragma unroll 1
+    for (int i = 0; i < kSteps8; ++i) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kSteps8 - 1) : "memory");
       const Stage8& st = ring[i];
-      Four f;
-      const float4 p = st.p[tid];
-      f.p[0] = pair(p.x, p.y), f.p[1] = pair(p.z, p.w);
-      if (f32) {
-        const float4 g = st.g[tid];
-        f.g[0] = pair(g.x, g.y), f.g[1] = pair(g.z, g.w);
+      Eight f;
+      const uint4 g = st.g[0][tid];
+      if (e.g_dtype == MOE_F32) {
+        put4(f.g, *reinterpret_cast<const float4*>(&st.g[0][tid]));
+        put4(f.g + 4, *reinterpret_cast<const float4*>(&st.g[1][tid]));
       } else {
-        const uint2 g = *reinterpret_cast<const uint2*>(&st.g[tid]);
-        f.g[0] = pair_of_bf16(g.x), f.g[1] = pair_of_bf16(g.y);
+        put4(f.g, make_float4(bf16_lo(g.x), bf16_hi(g.x), bf16_lo(g.y), bf16_hi(g.y)));
+        put4(f.g + 4, make_float4(bf16_lo(g.z), bf16_hi(g.z), bf16_lo(g.w), bf16_hi(g.w)));
       }
-      from_codes(f, st.m[tid], st.v[tid], __shfl_sync(0xffffffffu, scales, i),
-                 __shfl_sync(0xffffffffu, scales, 4 + i));
+      put4(f.p, st.p[0][tid]);
+      put4(f.p + 4, st.p[1][tid]);
+      const uint2 qm = st.m[tid], qv = st.v[tid];
+      const int of = 2 * i + (lane >> 4);
+      const float sm = __shfl_sync(0xffffffffu, scales, of);
+      const float sv = __shfl_sync(0xffffffffu, scales, 4 + of);
       copy(c + 1, i);   // into the place that has just been read
-      step_four<8>(sc, decay, key, first + i * kWarps, at, i, 4, f);
+      codes4(qm.x, sm, f.m);
+      codes4(qm.y, sm, f.m + 4);
+      codes4(qv.x, sv, f.v);
+      codes4(qv.y, sv, f.v + 4);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f.v[j] = __fmul_rn(f.v[j], f.v[j]);
+      step_eight(sc, e, decay, key, at + i * kStep8, 8, f);
     }
   }
-  tails<CAP, 8>(tab, sc);
+  for (int t = gridDim.x - 1 - blockIdx.x; t < tab.n; t += gridDim.x) {   // as above
+    const moe_adam_tensor& e = tab.t[t];
+    const uint32_t key = mix(e.seed ^ (sc.step * kGolden));
+    const bool f32 = e.g_dtype == MOE_F32;
+    long long at = e.n / kChunk * kChunk + tid * 8;
+    for (; at - lane * 8 < e.n; at += kStep8) {   // whole warps
+      const int cnt = e.n - at >= 8 ? 8 : e.n > at ? (int)(e.n - at) : 0;
+      Eight f;
+      put4(f.g, load_grad(e.g, f32, at, cnt < 4 ? cnt : 4));
+      put4(f.g + 4, load_grad(e.g, f32, at + 4, cnt - 4));
+      put4(f.p, load4(e.p + at, cnt < 4 ? cnt : 4));
+      put4(f.p + 4, load4(e.p + at + 4, cnt - 4));
+      const char *qm = static_cast<const char*>(e.m) + at, *qv = static_cast<const char*>(e.v) + at;
+      const float sm = cnt > 0 ? e.m_scale[at / kBlock] : 0.0f;
+      const float sv = cnt > 0 ? e.v_scale[at / kBlock] : 0.0f;
+      codes4(load_codes(qm, cnt < 4 ? cnt : 4), sm, f.m);
+      codes4(load_codes(qm + 4, cnt - 4), sm, f.m + 4);
+      codes4(load_codes(qv, cnt < 4 ? cnt : 4), sv, f.v);
+      codes4(load_codes(qv + 4, cnt - 4), sv, f.v + 4);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f.v[j] = __fmul_rn(f.v[j], f.v[j]);
+      step_eight(sc, e, sc.lr * e.weight_decay, key, at, cnt, f);
+    }
+  }
   finish(hyper, state, more);
 }
 
@@ -632,7 +624,7 @@ cudaError_t adam_cap(const moe_adam_cfg& c, const moe_adam_tensor* t, int n, boo
   const Hyper h{c.lr, c.beta1, c.beta2, c.max_norm, static_cast<float>(c.eps), c.lr_dev};
   const bool held = c.state_bits == 8;
   auto kern = held ? adamw8_kernel<CAP> : adamw_kernel<CAP>;
-  const size_t smem = held ? kSteps * sizeof(Stage8) : 0;
+  const size_t smem = held ? kSteps8 * sizeof(Stage8) : 0;
   const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), smem + 1024);
   if (e != cudaSuccess) return e;
   return launch_kernel(kern, dim3(grid_of(chunks + n, 4)), dim3(kThreads), smem, st, false, tab, h,
