@@ -186,7 +186,7 @@ struct Scalars {
   float root;             // 1 / sqrt(1 - b2^t)
   float lr, eps;
   uint32_t step;
-  bool skip, clip;
+  bool skip;
 };
 
 // "lowbias32" (C. Wellons, 2018), and the same without its last step
@@ -222,7 +222,6 @@ __device__ __forceinline__ Scalars scalars(const Hyper& h, const State* state, c
     sc.factor = h.max_norm > 0.0
                     ? fminf(__fmul_rn(static_cast<float>(h.max_norm), __frcp_rn(total)), 1.0f)
                     : 1.0f;
-    sc.clip = sc.factor < 1.0f;
   }
   __syncthreads();
   return sc;
@@ -238,7 +237,7 @@ __device__ __forceinline__ float recip(float v) {
 }
 __device__ __forceinline__ void update(const Scalars& sc, float decay, float g, float& p, float& m,
                                        float& v, float& root) {
-  if (sc.clip) g = __fmul_rn(g, sc.factor);
+  g = __fmul_rn(g, sc.factor);   // (1 where nothing is clipped)
   m = __fadd_rn(__fmul_rn(sc.b1, m), __fmul_rn(sc.n1, g));
   v = __fadd_rn(__fmul_rn(sc.b2, v), __fmul_rn(sc.n2, __fmul_rn(g, g)));
   root = __fsqrt_rn(v);
@@ -275,11 +274,10 @@ __device__ __forceinline__ float round_e4m3(float q, uint32_t r16) {
 // percent of v in the long run. A root above 0 keeps a code above 0.
 __device__ __forceinline__ float round_root_e4m3(float q, float root, uint32_t r16) {
   const float s = below_2_6(q), y = __fmaf_rn(s, 0x1p-6f, q), c = cut(__float_as_uint(y));
-  const float lo = __fmaf_rn(s, -0x1p-6f, c);   // exact, as are hi, hi - lo and hi + lo
-  const float hi = __fmaf_rn(s, -0x1p-6f, __uint_as_float(__float_as_uint(c) + 0x100000u));
-  const float gap = __fadd_rn(hi, -lo);
+  const float lo = __fmaf_rn(s, -0x1p-6f, c);   // exact, as are hi - lo (a step) and hi + lo
+  const float gap = __uint_as_float((__float_as_uint(c) & 0x7f800000u) - 0x01800000u);
   const float odds = __fmul_rn(__fadd_rn(q, -lo), __fadd_rn(q, lo));
-  const float whole = __fmul_rn(gap, __fadd_rn(hi, lo));
+  const float whole = __fmul_rn(gap, __fmaf_rn(2.0f, lo, gap));
   // r / 2^16 as the fraction of a number between 1 and 2
   const float r = __fadd_rn(__uint_as_float(0x3f800000u + r16 * 128), -1.0f);
   // up where r whole, rounded, < odds. (A difference that is no multiple of 2^-100 leaves a value
@@ -436,22 +434,26 @@ __device__ __forceinline__ void step_eight(const Scalars& sc, const moe_adam_ten
   const bool plain = __all_sync(0xffffffffu, scale > 0x1p-60f && scale < 0x1p100f);
   const float sm = __shfl_sync(0xffffffffu, scale, 0, 16), sv = __shfl_sync(0xffffffffu, scale, 1, 16);
   const float rm = __shfl_sync(0xffffffffu, inv, 0, 16), rv = __shfl_sync(0xffffffffu, inv, 1, 16);
-  // |x| / scale, the IEEE quotient, by the correctly rounded reciprocal and one correction step
-  // (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor", 1990)
-  const auto quotient = [&](float x, float s, float r) {
-    if (!plain) return __fdiv_rn(x, s);
-    const float q = __fmul_rn(x, r);
-    return __fmaf_rn(__fmaf_rn(-q, s, x), r, q);
-  };
   const uint32_t from = mix(key ^ static_cast<uint32_t>(block)) + place * 8 * kGolden;
+  const auto hold = [&](auto quotient) {   // |x| / scale, the IEEE quotient
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    // the halves of the hash x ^ (x >> 16)
-    const uint32_t x = premix(from + j * kGolden), h = x >> 16;
-    const float q = round_e4m3(quotient(fabsf(f.m[j]), sm, rm), h);
-    f.m[j] = copysignf(q, f.m[j]);
-    f.v[j] = round_root_e4m3(quotient(root[j], sv, rv), root[j], (x ^ h) & 0xffffu);
-  }
+    for (int j = 0; j < 8; ++j) {
+      // the halves of the hash x ^ (x >> 16)
+      const uint32_t x = premix(from + j * kGolden), h = x >> 16;
+      const float q = round_e4m3(quotient(fabsf(f.m[j]), sm, rm), h);
+      f.m[j] = copysignf(q, f.m[j]);
+      f.v[j] = round_root_e4m3(quotient(root[j], sv, rv), root[j], (x ^ h) & 0xffffu);
+    }
+  };
+  // By the correctly rounded reciprocal and one correction step (P. Markstein, "Computation of
+  // elementary functions on the IBM RISC System/6000 processor", 1990).
+  if (plain)
+    hold([](float x, float s, float r) {
+      const float q = __fmul_rn(x, r);
+      return __fmaf_rn(__fmaf_rn(-q, s, x), r, q);
+    });
+  else
+    hold([](float x, float s, float) { return __fdiv_rn(x, s); });
   char *qm = static_cast<char*>(e.m) + at, *qv = static_cast<char*>(e.v) + at;
   if (cnt == 8) {
     __stcs(reinterpret_cast<uint2*>(qm), make_uint2(pack_codes(f.m), pack_codes(f.m + 4)));
