@@ -2,14 +2,16 @@
 // gradient of the routing weights scale * p,
 //   dz_i = scale p_i (1 - s_i) (dw_i - sum_j p_j dw_j)
 // is the gradient of the k chosen logits, the only ones that the weights depend on: a sparse [T][E]
-// matrix of k entries a row. Tokens take dz . w_gate, gate weights dz^T . x.
+// matrix of k entries a row. Tokens take dz . w_gate, gate weights dz^T . x. Both products do 2 T k d
+// operations on operands that several choices share, so what bounds them is the operands' way into
+// registers: T k d elements each, fp32 for the tokens and bf16 for the gate weights.
 //
-// 1. A CTA per chunk of tokens computes dz and lists the chunk's choices expert by expert, in the
-//    order of the tokens (a counting sort).
-// 2. Tokens: dx.  3. Gate weights: dw_gate.
-// Both products do 2 T k d operations on operands that k choices share: their traffic to registers,
-// T k d elements, is what bounds them, so long batches keep a slab of columns in shared memory (dx:
-// the gate weights', dw: a chunk of the tokens') and short ones read through L2.
+// 1. Counts: a CTA per chunk of tokens computes dz and counts the chunk's choices of each expert.
+// 2. Lists: the choices expert by expert, in the order of the tokens, cut into segments.
+// 3. Products: the tokens' dx from the gate weights (long batches: from a slab of columns of them in
+//    shared memory), the segments' sums of x from L2, at the same time.
+// 4. The segments' sums are joined in order, so that the result does not depend on the order of work.
+// A short batch takes one launch for all of it.
 #include <algorithm>
 
 #include "moe_device.cuh"
@@ -19,23 +21,10 @@ namespace moe {
 namespace {
 
 constexpr int kSms = 152;
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
 
-__device__ __forceinline__ float4 four(f32x2 a, f32x2 b) {
-  const float2 x = halves(a), y = halves(b);
-  return make_float4(x.x, x.y, y.x, y.y);
-}
 __device__ __forceinline__ void copy16(void* smem, const void* gmem) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(smem)), "l"(gmem)
                : "memory");
-}
-__device__ __forceinline__ void copies_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void copies_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // ------------------------------------------------------------------------------------------
@@ -43,534 +32,554 @@ __device__ __forceinline__ void copies_wait() {
 // ------------------------------------------------------------------------------------------
 constexpr int kMostChunk = 320;      // tokens of a chunk
 constexpr int kMostList = 2560;      // choices of a chunk
-constexpr int kMostParts = 16;
-constexpr int kDwCols = 64, kDwExperts = 256;   // of a CTA in dw's long form
-
-// A choice in a chunk's list: its token in the chunk and dz. An expert's run of them starts at a
-// multiple of 4 and is filled up to one with entries of token kMostChunk and dz 0, so that four
-// entries have one expert; the first of the four says which, and whether they end the run.
-//   at: token * 128 (the byte offset of 64 bf16 columns in a tile of x) | last | expert of the block
-//   of kDwExperts << 16
-struct Entry {
-  uint32_t at;
-  float dz;
-};
-__device__ __forceinline__ int entry_row(const Entry& e) { return e.at & 0xff80u; }
 
 // A choice of a token: its expert (E: none, with dz 0), and dz. Tokens have an even number of them.
 struct Pick {
   int32_t expert;
   float dz;
 };
-
-struct Layout {   // the status word comes first
-  size_t picks, runs, list, partial, total;
-  int chunk, chunks, kp;   // tokens of a chunk, chunks, choices of a token rounded up to even
-  int stride;              // list entries of a chunk
-  int parts;               // of the chunks in dw's long form; 0: the short one
+// A choice in the lists.
+struct Entry {
+  int32_t token;
+  float dz;
 };
 
-// dw's long form: parts of the chunks, so that the last wave of CTAs is nearly full. Least waves
-// times chunks of a part (one more for the sums, written and joined).
-int parts_of(const moe_cfg& c, int chunks) {
-  const long long units = (long long)(c.d / kDwCols) * ((c.E + kDwExperts - 1) / kDwExperts);
-  int parts = 1;
-  long long best = -1;
-  for (int p = 1; p <= kMostParts && p <= chunks; ++p) {
-    const long long waves = (units * p + kSms - 1) / kSms;
-    const long long cost = waves * ((chunks + p - 1) / p + 1);
-    if (best < 0 || cost < best) best = cost, parts = p;
-  }
-  return parts;
-}
+struct Layout {   // the status word comes first
+  size_t queue;      // int32: the next item of the products' work
+  size_t picks;      // Pick [T][kp]
+  size_t counts;     // int32 [chunks][E]
+  size_t starts;     // int32 [E + 1]: of the experts' lists
+  size_t segments;   // int32 [E + 1]: the experts' first segments
+  size_t list;       // Entry [T * k]
+  size_t partial;    // fp32 [segments][d]: sums of the segments of experts with several
+  size_t total;
+  int chunk, chunks, kp;   // tokens of a chunk, chunks, choices of a token rounded up to even
+  int segment;             // choices of a segment
+  bool one_launch, slab;
+};
 
 Layout layout(const moe_cfg& c) {
   const auto up = [](size_t v) { return (v + 255) & ~static_cast<size_t>(255); };
   Layout L;
+  const size_t tk = (size_t)c.T * c.k;
   L.chunk = kMostList / c.k < kMostChunk ? kMostList / c.k / 8 * 8 : kMostChunk;
   L.chunks = (int)(((long long)c.T + L.chunk - 1) / L.chunk);
   L.kp = (c.k + 1) / 2 * 2;
+  // a segment: the work of the SMs' warps some eight times over, in powers of two from 32 to 1024
+  const double per = (double)tk * ((c.d + 255) / 256) / (8.0 * kSms * 32);
+  for (L.segment = 32; L.segment < 1024 && L.segment < per;) L.segment *= 2;
+  L.one_launch = tk <= 1024;
+  L.slab = c.T >= 1024;
   size_t o = 256;
-  L.picks = o;     o = up(o + sizeof(Pick) * (size_t)c.T * L.kp);
-  L.runs = o;      o = up(o + sizeof(int2) * (size_t)L.chunks * c.E);
-  L.stride = (L.chunk * c.k + 3 * std::min(c.E, L.chunk * c.k) + 3) / 4 * 4;
-  L.list = o;      o = up(o + sizeof(Entry) * (size_t)L.chunks * L.stride);
-  // The long forms from 512 tokens on (7168 columns, 8 of 256 experts, us, short and long: 256 tokens
-  // 27 and 36, 512 36 and 44, 1024 55 and 57, 2048 87 and 81, 4096 152 and 130, evenly loaded; with
-  // one expert chosen by half of the tokens the short form takes twice as long, the long one does not).
-  L.parts = c.T >= 512 ? parts_of(c, L.chunks) : 0;
-  L.partial = o;   o = up(o + (L.parts > 1 ? sizeof(float) * (size_t)L.parts * c.E * c.d : 0));
+  L.queue = o;     o = up(o + sizeof(int32_t));
+  if (!L.one_launch) {
+    L.picks = o;     o = up(o + sizeof(Pick) * (size_t)c.T * L.kp);
+    L.counts = o;    o = up(o + sizeof(int32_t) * (size_t)L.chunks * c.E);
+    L.starts = o;    o = up(o + sizeof(int32_t) * (c.E + 1));
+    L.segments = o;  o = up(o + sizeof(int32_t) * (c.E + 1));
+    L.list = o;      o = up(o + sizeof(Entry) * tk);
+    L.partial = o;   o = up(o + sizeof(float) * (tk / L.segment + c.E) * c.d);
+  }
   L.total = o;
   return L;
 }
 
+__device__ __forceinline__ int checked(int e, int E, uint32_t* status) {
+  if (e >= 0 && e < E) return e;
+  if (e != -1) raise_status(status, MOE_DEV_BOUNDS);
+  return -1;
+}
+
+// Lanes that take a token's choices, one each: a power of two, kp at least.
+__host__ __device__ __forceinline__ int lanes_of(int kp) {
+  int w = 2;
+  while (w < kp) w *= 2;
+  return w;
+}
+// A choice and its dz, from its lane's expert (-1: none), score and gradient of the weight; `in`: there
+// is such a choice. A second choice of one expert is added to its first and becomes none itself. The
+// lanes of a token are neighbours, `width` of them; all lanes of the warp take part.
+__device__ __forceinline__ Pick pick_of(int e, float s, float g, bool in, int width, float scale,
+                                        int E) {
+  const auto sum_of_token = [&](float v) {
+    for (int o = width / 2; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+  };
+  const float p = s * (1.0f / sum_of_token(in ? s : 0.0f));
+  const float dot = sum_of_token(in ? p * g : 0.0f);
+  const bool live = in && e >= 0;
+  if (!live) e = -1;
+  const float z = live ? scale * p * (1.0f - s) * (g - dot) : 0.0f;
+  float mine = z;
+  bool second = false;
+  const int lane = threadIdx.x & 31;
+  for (int o = 1; o < width; ++o) {
+    const int other = __shfl_xor_sync(0xffffffffu, e, o);
+    const float add = __shfl_xor_sync(0xffffffffu, z, o);
+    if (live && other == e) {
+      if ((lane ^ o) < lane)
+        second = true;
+      else
+        mine += add;
+    }
+  }
+  return live && !second ? Pick{e, mine} : Pick{E, 0.0f};
+}
+
 // ------------------------------------------------------------------------------------------
-// 1. dz, the tokens' picks, and each chunk's list: runs[chunk][expert] is the start and the end of the
-// expert's run. Choices outside [0, E) are in no list; a token's second choice of one expert is added
-// to its first.
-//
-// The order inside a run is that of the tokens: a bit mask of them for each expert (set by atomic
-// ORs, whose order does not matter) gives a choice's place by counting the bits below its own.
+// 1. dz, the tokens' picks, the chunk's counts
 // ------------------------------------------------------------------------------------------
 constexpr int kListThreads = 512, kListWarps = kListThreads / 32;
-constexpr int kMaskWords = kMostChunk / 32, kMaskStride = kMaskWords + 1;   // (odd: bank conflicts)
-struct ListSmem {
-  int expert[kMostList];
-  float dz[kMostList], grad[kMostList];
-};
-__global__ void __launch_bounds__(kListThreads) route_grad_list_kernel(
-    const int32_t* __restrict__ idx, const float* __restrict__ score, const float* __restrict__ dw,
-    int T, int k, int kp, int E, float scale, int chunk, int stride, Pick* __restrict__ picks,
-    int2* __restrict__ runs, Entry* __restrict__ list, uint32_t* status) {
-  extern __shared__ __align__(16) char raw[];
-  __shared__ int warp_sum[kListWarps];
-  ListSmem& sm = *reinterpret_cast<ListSmem*>(raw);
-  int* expert = sm.expert;
-  float *dz = sm.dz, *grad = sm.grad;
-  uint32_t* mask = reinterpret_cast<uint32_t*>(raw + sizeof(ListSmem));   // [E][kMaskStride]
-  int2* run = reinterpret_cast<int2*>(grad);                               // [E], from the scan on
-  const int t0 = blockIdx.x * chunk, nt = min(chunk, T - t0), n = nt * k;
-  const size_t base = (size_t)t0 * k;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// (a token has at most twice as many lanes as choices)
+constexpr int kPasses = 2 * kMostList / kListThreads;
 
-  for (int i = threadIdx.x; i < n; i += kListThreads) {
-    const int e = idx[base + i];
-    const bool in = e >= 0 && e < E;
-    if (!in && e != -1) raise_status(status, MOE_DEV_BOUNDS);
-    expert[i] = in ? e : -1;
-    dz[i] = score[base + i];
-    grad[i] = dw[base + i];
-  }
-  for (int i = threadIdx.x; i < E * kMaskStride; i += kListThreads) mask[i] = 0;
+__global__ void __launch_bounds__(kListThreads) route_grad_count_kernel(
+    const int32_t* __restrict__ idx, const float* __restrict__ score, const float* __restrict__ dw,
+    int T, int k, int kp, int E, float scale, int chunk, Pick* __restrict__ picks,
+    int32_t* __restrict__ counts, int32_t* queue, uint32_t* status) {
+  __shared__ int hist[1024];
+  const int t0 = blockIdx.x * chunk, nt = min(chunk, T - t0);
+  const int width = lanes_of(kp), j = threadIdx.x & (width - 1), per = kListThreads / width;
+  for (int e = threadIdx.x; e < E; e += kListThreads) hist[e] = 0;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *queue = 0;
   __syncthreads();
   pdl_trigger();
-  bool twice = false;
-  for (int i = threadIdx.x; i < n; i += kListThreads) {
-    const int e = expert[i], t = i / k;
-    if (e < 0) continue;
-    const uint32_t bit = 1u << (t & 31);
-    twice |= (atomicOr(&mask[e * kMaskStride + (t >> 5)], bit) & bit) != 0;
-  }
-  for (int t = threadIdx.x; t < nt; t += kListThreads) {
-    float *s = dz + t * k, *g = grad + t * k;
-    float sum = 0.0f, dot = 0.0f;
-    for (int i = 0; i < k; ++i) sum += s[i];
-    const float inv = 1.0f / sum;
-    for (int i = 0; i < k; ++i) dot = __fmaf_rn(s[i] * inv, g[i], dot);
-    for (int i = 0; i < k; ++i)
-      s[i] = expert[t * k + i] >= 0 ? scale * (s[i] * inv) * (1.0f - s[i]) * (g[i] - dot) : 0.0f;
-  }
-  if (__syncthreads_or(twice)) {
-    for (int t = threadIdx.x; t < nt; t += kListThreads)
-      for (int i = t * k + 1; i < (t + 1) * k; ++i)
-        for (int j = t * k; j < i && expert[i] >= 0; ++j)
-          if (expert[j] == expert[i]) {
-            dz[j] += dz[i];
-            dz[i] = 0.0f;
-            expert[i] = -1;
-          }
-    __syncthreads();
-  }
-  for (int i = threadIdx.x; i < nt * kp; i += kListThreads) {
-    const int t = i / kp, j = i - t * kp;
-    const int e = j < k ? expert[t * k + j] : -1;
-    picks[(size_t)(t0 + t) * kp + j] = e >= 0 ? Pick{e, dz[t * k + j]} : Pick{E, 0.0f};
-  }
-  // starts of the runs. Thread i: experts 2i, 2i + 1
-  int count[2], own = 0;
+  // a chunk takes kPasses rounds at most: all their loads first
+  int e[kPasses];
+  float s[kPasses], g[kPasses];
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const int e = threadIdx.x * 2 + q;
-    count[q] = 0;
-    if (e < E)
-      for (int w = 0; w < kMaskWords; ++w) count[q] += __popc(mask[e * kMaskStride + w]);
-    own += (count[q] + 3) / 4 * 4;
+  for (int i = 0; i < kPasses; ++i) {
+    const int t = i * per + threadIdx.x / width;
+    e[i] = -1, s[i] = g[i] = 0.0f;
+    if (t < nt && j < k) {
+      const size_t at = (size_t)(t0 + t) * k + j;
+      e[i] = checked(idx[at], E, status), s[i] = score[at], g[i] = dw[at];
+    }
   }
-  int incl = own;
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    if (i * per >= nt) break;   // whole warps
+    const int t = i * per + threadIdx.x / width;
+    const Pick p = pick_of(e[i], s[i], g[i], t < nt && j < k, width, scale, E);
+    if (t >= nt || j >= kp) continue;
+    if (p.expert < E) atomicAdd(&hist[p.expert], 1);
+    picks[(size_t)(t0 + t) * kp + j] = p;
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += kListThreads) counts[(size_t)blockIdx.x * E + e] = hist[e];
+}
+
+// ------------------------------------------------------------------------------------------
+// 2. The lists. A choice's place: its expert's start, the choices of the chunks before, and those of
+// its own chunk's tokens before, counted in a bit mask of the expert's tokens (set by atomic ORs, whose
+// order does not matter). Every CTA adds up all counts for itself; the first one writes the starts.
+// ------------------------------------------------------------------------------------------
+constexpr int kOwn = (kMostList + kMostChunk) / kListThreads + 1;   // picks of a thread, at most
+constexpr int kMaskWords = kMostChunk / 32, kMaskStride = kMaskWords + 1;   // (odd: bank conflicts)
+
+// Exclusive sums of two numbers over the CTA's threads.
+__device__ __forceinline__ int2 cta_scan(int2 own, int2* warp_sum) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int2 incl = own;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
+    const int x = __shfl_up_sync(0xffffffffu, incl.x, o);
+    const int y = __shfl_up_sync(0xffffffffu, incl.y, o);
+    if (lane >= o) incl.x += x, incl.y += y;
   }
   if (lane == 31) warp_sum[warp] = incl;
   __syncthreads();
-  int at = incl - own;
-  for (int w = 0; w < warp; ++w) at += warp_sum[w];
-  Entry* out = list + (size_t)blockIdx.x * stride;
+  int2 at = make_int2(incl.x - own.x, incl.y - own.y);
+  for (int w = 0; w < warp; ++w) at.x += warp_sum[w].x, at.y += warp_sum[w].y;
+  return at;
+}
+
+__global__ void __launch_bounds__(kListThreads) route_grad_list_kernel(
+    const Pick* __restrict__ picks, const int32_t* __restrict__ counts, int T, int kp, int E,
+    int chunk, int chunks, int segment, int32_t* __restrict__ starts, int32_t* __restrict__ segments,
+    Entry* __restrict__ list) {
+  extern __shared__ __align__(16) char raw[];
+  __shared__ int2 warp_sum[kListWarps];
+  int* first = reinterpret_cast<int*>(raw);                              // [E]: in the list
+  uint32_t* mask = reinterpret_cast<uint32_t*>(first + E);               // [E][kMaskStride]
+  uint16_t* before = reinterpret_cast<uint16_t*>(mask + E * kMaskStride);   // [E][kMaskStride]
+  const int t0 = blockIdx.x * chunk, nt = min(chunk, T - t0);
+  for (int i = threadIdx.x; i < E * kMaskStride; i += kListThreads) mask[i] = 0;
+  __syncthreads();
+  pdl_wait();
+  const Pick* from = picks + (size_t)t0 * kp;
+  Pick mine[kOwn];   // this thread's
 #pragma unroll
+  for (int i = 0; i < kOwn; ++i) {
+    const int at = threadIdx.x + i * kListThreads;
+    mine[i] = at < nt * kp ? from[at] : Pick{E, 0.0f};
+  }
+  // Thread i: experts 2i, 2i + 1
+  int total[2] = {0, 0}, ahead[2] = {0, 0};
+  const int e0 = threadIdx.x * 2;
+  if (e0 < E)
+#pragma unroll 8
+    for (int c = 0; c < chunks; ++c)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int n = e0 + q < E ? counts[(size_t)c * E + e0 + q] : 0;
+        total[q] += n;
+        ahead[q] += c < (int)blockIdx.x ? n : 0;
+      }
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) {
+    const int t = (threadIdx.x + i * kListThreads) / kp;
+    if (mine[i].expert < E)
+      atomicOr(&mask[mine[i].expert * kMaskStride + (t >> 5)], 1u << (t & 31));
+  }
+  const auto segs = [&](int n) { return (n + segment - 1) / segment; };
+  int2 at = cta_scan(make_int2(total[0] + total[1], segs(total[0]) + segs(total[1])), warp_sum);
   for (int q = 0; q < 2; ++q) {
-    const int e = threadIdx.x * 2 + q;
+    const int e = e0 + q;
     if (e >= E) break;
-    run[e] = make_int2(at, at + count[q]);
-    runs[(size_t)blockIdx.x * E + e] = run[e];
-    for (int i = count[q]; i & 3; ++i) out[at + i] = Entry{(uint32_t)kMostChunk * 128, 0.0f};
-    at += (count[q] + 3) / 4 * 4;
+    first[e] = at.x + ahead[q];
+    if (blockIdx.x == 0) starts[e] = at.x, segments[e] = at.y;
+    at.x += total[q];
+    at.y += segs(total[q]);
+    if (blockIdx.x == 0 && e == E - 1) starts[E] = at.x, segments[E] = at.y;
+    int sum = 0;   // (the masks are complete: cta_scan had a barrier)
+    for (int w = 0; w < kMaskWords; ++w) {
+      before[e * kMaskStride + w] = static_cast<uint16_t>(sum);
+      sum += __popc(mask[e * kMaskStride + w]);
+    }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < n; i += kListThreads) {
-    const int e = expert[i], t = i / k;
-    if (e < 0) continue;
-    const uint32_t* m = mask + e * kMaskStride;
-    int rank = __popc(m[t >> 5] & ((1u << (t & 31)) - 1u));
-    for (int w = 0; w < t >> 5; ++w) rank += __popc(m[w]);
-    const int2 r = run[e];
-    const uint32_t last = r.x + rank + 4 >= r.y ? 1u : 0u;
-    out[r.x + rank] = Entry{(uint32_t)(t * 128) | last | (uint32_t)(e % kDwExperts) << 16, dz[i]};
+  pdl_trigger();
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) {
+    const Pick p = mine[i];
+    if (p.expert >= E) continue;
+    const int t = (threadIdx.x + i * kListThreads) / kp;
+    const int w = p.expert * kMaskStride + (t >> 5);
+    const int rank = before[w] + __popc(mask[w] & ((1u << (t & 31)) - 1u));
+    list[first[p.expert] + rank] = Entry{t0 + t, p.dz};
   }
 }
 
 // ------------------------------------------------------------------------------------------
-// 2. dx
+// 3. The products. Work is handed out from a queue, a warp an item: 256 columns of a token's dx or of
+// a segment's sum (column blocks one after another: a block of x stays in L2 while it is used).
 // ------------------------------------------------------------------------------------------
-// A warp takes 256 columns of a token, the gate weights come from L2.
-__device__ __forceinline__ void dx_short(const Pick* __restrict__ picks,
-                                         const float* __restrict__ w_gate, const uint4* dx_in,
-                                         uint4* dx, int T, int kp, int E, int d, long long item) {
-  const int vecs = d / 8, parts = (vecs + 31) / 32;
-  const long long t = item / parts;
-  const int v = static_cast<int>(item - t * parts) * 32 + (threadIdx.x & 31);
-  if (t >= T || v >= vecs) return;
-  f32x2 acc[4] = {};
-  if (dx_in) {
-    const uint4 u = dx_in[(size_t)t * vecs + v];
-    acc[0] = pair_of_bf16(u.x);
-    acc[1] = pair_of_bf16(u.y);
-    acc[2] = pair_of_bf16(u.z);
-    acc[3] = pair_of_bf16(u.w);
+__device__ __forceinline__ void add8(f32x2 (&acc)[4], float z, const uint4& u) {
+  const f32x2 z2 = both(z);
+  acc[0] = fma2(z2, pair_of_bf16(u.x), acc[0]);
+  acc[1] = fma2(z2, pair_of_bf16(u.y), acc[1]);
+  acc[2] = fma2(z2, pair_of_bf16(u.z), acc[2]);
+  acc[3] = fma2(z2, pair_of_bf16(u.w), acc[3]);
+}
+__device__ __forceinline__ void add8(f32x2 (&acc)[4], float z, const ulonglong2& a,
+                                     const ulonglong2& b) {
+  const f32x2 z2 = both(z);
+  acc[0] = fma2(z2, a.x, acc[0]);
+  acc[1] = fma2(z2, a.y, acc[1]);
+  acc[2] = fma2(z2, b.x, acc[2]);
+  acc[3] = fma2(z2, b.y, acc[3]);
+}
+__device__ __forceinline__ void load8(f32x2 (&acc)[4], const uint4* at) {
+  const uint4 u = at ? *at : make_uint4(0, 0, 0, 0);
+  acc[0] = pair_of_bf16(u.x), acc[1] = pair_of_bf16(u.y);
+  acc[2] = pair_of_bf16(u.z), acc[3] = pair_of_bf16(u.w);
+}
+__device__ __forceinline__ uint4 bf16_of8(const f32x2* a) {
+  return make_uint4(bf16_of_pair(a[0]), bf16_of_pair(a[1]), bf16_of_pair(a[2]), bf16_of_pair(a[3]));
+}
+// acc to 8 columns of an fp32 row, or added to them
+__device__ __forceinline__ void store8(float* row, int v, const f32x2 (&acc)[4], bool add) {
+  float4* o = reinterpret_cast<float4*>(row) + 2 * v;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float2 x = halves(acc[2 * i]), y = halves(acc[2 * i + 1]);
+    float4 r = make_float4(x.x, x.y, y.x, y.y);
+    if (add) {
+      const float4 p = o[i];
+      r.x += p.x, r.y += p.y, r.z += p.z, r.w += p.w;
+    }
+    o[i] = r;
   }
-  const int4* two = reinterpret_cast<const int4*>(picks + (size_t)t * kp);
-#pragma unroll 4
-  for (int i = 0; i < kp / 2; ++i) {
+}
+
+struct Args {
+  const uint4* x;
+  const float* w_gate;
+  const uint4* dx_in;
+  uint4* dx;
+  float* dw_gate;
+  const Pick* picks;
+  const int32_t *starts, *segments;
+  const Entry* list;
+  float* partial;
+  int32_t* queue;
+  int T, kp, E, d, segment;
+  bool accumulate;
+  long long per_cta;   // slab: (slab, token) pairs of a CTA
+};
+
+__device__ __forceinline__ void dx_item(const Args& a, int t, int v) {
+  const int vecs = a.d / 8;
+  if (v >= vecs) return;
+  const size_t at = (size_t)t * vecs + v;
+  f32x2 acc[4];
+  load8(acc, a.dx_in ? a.dx_in + at : nullptr);
+  const int4* two = reinterpret_cast<const int4*>(a.picks + (size_t)t * a.kp);
+#pragma unroll 2
+  for (int i = 0; i < a.kp / 2; ++i) {
     const int4 p = two[i];   // expert, dz, expert, dz
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int e = j ? p.z : p.x;
-      const f32x2 z2 = both(__int_as_float(j ? p.w : p.y));
-      if (e == E) continue;
-      const float4* w = reinterpret_cast<const float4*>(w_gate + (size_t)e * d) + 2 * v;
-      const float4 a = w[0], b = w[1];
-      acc[0] = fma2(z2, pair(a.x, a.y), acc[0]);
-      acc[1] = fma2(z2, pair(a.z, a.w), acc[1]);
-      acc[2] = fma2(z2, pair(b.x, b.y), acc[2]);
-      acc[3] = fma2(z2, pair(b.z, b.w), acc[3]);
+      if (e == a.E) continue;
+      const ulonglong2* w = reinterpret_cast<const ulonglong2*>(a.w_gate + (size_t)e * a.d) + 2 * v;
+      add8(acc, __int_as_float(j ? p.w : p.y), w[0], w[1]);
     }
   }
-  dx[(size_t)t * vecs + v] =
-      make_uint4(bf16_of_pair(acc[0]), bf16_of_pair(acc[1]),
-                 bf16_of_pair(acc[2]), bf16_of_pair(acc[3]));
+  a.dx[at] = bf16_of8(acc);
 }
 
-// A warp takes 256 columns of one expert's gate weights, over all chunks in order; x comes from L2.
-__device__ __forceinline__ void dw_short(const uint4* __restrict__ x,
-                                         const int2* __restrict__ runs,
-                                         const Entry* __restrict__ list,
-                                         float* __restrict__ dw_gate, int chunk, int chunks,
-                                         int stride, int E, int d, bool accumulate,
-                                         long long item) {
-  const int vecs = d / 8, parts = (vecs + 31) / 32;
-  const int e = static_cast<int>(item / parts);
-  const int v = static_cast<int>(item - (long long)e * parts) * 32 + (threadIdx.x & 31);
-  if (e >= E || v >= vecs) return;
+__device__ __forceinline__ void dw_item(const Args& a, int segment, int v) {
+  int lo = 0, hi = a.E - 1;   // the expert: the last whose first segment is at or before this one
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (a.segments[mid] <= segment)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  const int vecs = a.d / 8, s0 = a.segments[lo];
+  const int from = a.starts[lo] + (segment - s0) * a.segment;
+  const int to = min(from + a.segment, a.starts[lo + 1]);
+  if (v >= vecs) return;
+  const uint4* x = a.x + v;
   f32x2 acc[4] = {};
-  for (int c = 0; c < chunks; ++c) {
-    const int2 run = runs[(size_t)c * E + e];
-    const Entry* in = list + (size_t)c * stride;
-    const uint4* rows = x + (size_t)c * chunk * vecs + v;
 #pragma unroll 4
-    for (int i = run.x; i < run.y; ++i) {
-      const Entry q = in[i];
-      const uint4 u = rows[(size_t)(entry_row(q) >> 7) * vecs];
-      acc[0] = fma2(both(q.dz), pair_of_bf16(u.x), acc[0]);
-      acc[1] = fma2(both(q.dz), pair_of_bf16(u.y), acc[1]);
-      acc[2] = fma2(both(q.dz), pair_of_bf16(u.z), acc[2]);
-      acc[3] = fma2(both(q.dz), pair_of_bf16(u.w), acc[3]);
-    }
+  for (int i = from; i < to; ++i) {
+    const Entry q = a.list[i];
+    add8(acc, q.dz, x[(size_t)q.token * vecs]);
   }
-  float4* o = reinterpret_cast<float4*>(dw_gate + (size_t)e * d) + 2 * v;
-  float4 a = four(acc[0], acc[1]), b = four(acc[2], acc[3]);
-  if (accumulate) {
-    const float4 p = o[0], q = o[1];
-    a.x += p.x, a.y += p.y, a.z += p.z, a.w += p.w;
-    b.x += q.x, b.y += q.y, b.z += q.z, b.w += q.w;
-  }
-  o[0] = a;
-  o[1] = b;
-}
-
-// Short batches: both products in one launch, dx by the first dx_ctas CTAs.
-__global__ void __launch_bounds__(kThreads) route_grad_short_kernel(
-    const Pick* __restrict__ picks, const int2* __restrict__ runs, const Entry* __restrict__ list, const float* __restrict__ w_gate, const uint4* __restrict__ x,
-    const uint4* dx_in, uint4* dx, float* __restrict__ dw_gate, int T, int kp, int E, int d,
-    int chunk, int chunks, int stride, bool accumulate, unsigned dx_ctas) {
-  pdl_wait();
-  const int warp = threadIdx.x >> 5;
-  if (blockIdx.x < dx_ctas)
-    dx_short(picks, w_gate, dx_in, dx, T, kp, E, d, (long long)blockIdx.x * kWarps + warp);
+  if (a.segments[lo + 1] - s0 == 1)
+    store8(a.dw_gate + (size_t)lo * a.d, v, acc, a.accumulate);
   else
-    dw_short(x, runs, list, dw_gate, chunk, chunks, stride, E, d, accumulate,
-             (long long)(blockIdx.x - dx_ctas) * kWarps + warp);
+    store8(a.partial + (size_t)segment * a.d, v, acc, false);
 }
 
-// Long batches: a CTA keeps C columns of all gate weights in shared memory, and a row of zeros for
-// picks that are none. The (slab of columns, token) pairs, slab by slab, are dealt to the CTAs in
-// equal runs, so that a CTA loads one slab or two. C / 16 lanes take a token, 16 columns a lane, so
-// that the picks, which all of a token's lanes read, cost little beside the weights.
+// Long batches: half of a CTA's warps keep C columns of all gate weights in shared memory, and a row
+// of zeros for picks that are none. The (slab of columns, token) pairs, slab by slab, are dealt to the
+// CTAs in equal runs, so that a CTA loads one slab or two. C / 16 lanes take a token, 16 columns a
+// lane, so that the picks, which all of a token's lanes read, cost little beside the weights.
 constexpr int kDxThreads = 512;
+__device__ __forceinline__ void dx_barrier() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kDxThreads) : "memory");
+}
 template <int C>
-__global__ void __launch_bounds__(kDxThreads, 1) route_grad_dx_slab_kernel(
-    const Pick* __restrict__ picks, const float* __restrict__ w_gate, const uint4* dx_in, uint4* dx,
-    int T, int kp, int E, int d, long long per_cta) {
-  extern __shared__ __align__(16) char slab[];
+__device__ __forceinline__ void dx_slabs(const Args& a, char* slab) {
   // a row: the lanes' columns 0-3 one after another, then their columns 4-7, 8-11, 12-15
   constexpr int kLanes = C / 16, kAtOnce = kDxThreads / kLanes, kRow = C * 4, kQuarter = C;
-  const long long work = (long long)(d / C) * T;
-  long long at = blockIdx.x * per_cta;
-  const long long end = min(at + per_cta, work);
+  const long long work = (long long)(a.d / C) * a.T;
+  long long at = blockIdx.x * a.per_cta;
+  const long long end = min(at + a.per_cta, work);
   const int l = threadIdx.x % kLanes, mine = threadIdx.x / kLanes;
   for (int i = threadIdx.x; i < C; i += kDxThreads)
-    reinterpret_cast<float*>(slab + (size_t)E * kRow)[i] = 0.0f;
-  pdl_wait();
-  pdl_trigger();
+    reinterpret_cast<float*>(slab + (size_t)a.E * kRow)[i] = 0.0f;
   while (at < end) {
-    const int s = static_cast<int>(at / T), t0 = static_cast<int>(at - (long long)s * T);
-    const int t1 = static_cast<int>(min((long long)T, t0 + (end - at)));
-    __syncthreads();   // the slab before this one has been read
-    for (int i = threadIdx.x; i < E * (C / 4); i += kDxThreads) {
+    const int s = static_cast<int>(at / a.T), t0 = static_cast<int>(at - (long long)s * a.T);
+    const int t1 = static_cast<int>(min((long long)a.T, t0 + (end - at)));
+    dx_barrier();   // the slab before this one has been read
+    for (int i = threadIdx.x; i < a.E * (C / 4); i += kDxThreads) {
       const int e = i / (C / 4), v = i % (C / 4);
       copy16(slab + (size_t)e * kRow + (v & 3) * kQuarter + (v >> 2) * 16,
-             w_gate + (size_t)e * d + s * C + v * 4);
+             a.w_gate + (size_t)e * a.d + s * C + v * 4);
     }
-    copies_commit();
-    copies_wait<0>();
-    __syncthreads();
+    asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+    dx_barrier();
     const char* w = slab + l * 16;
-    const size_t col = (size_t)s * (C / 8) + l * 2;
-    // a token's dx_in and first eight picks are loaded while the one before it is worked on
-    uint4 u_next[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-    int4 p_next[4];
+    const unsigned vecs = a.d / 8, col = s * (C / 8) + l * 2;
+    // a token's dx_in is loaded while the one before it is worked on
+    uint4 next[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
     const auto fetch = [&](int t) {
-      if (dx_in) {
-        u_next[0] = dx_in[(size_t)t * (d / 8) + col];
-        u_next[1] = dx_in[(size_t)t * (d / 8) + col + 1];
-      }
-      const int4* p = reinterpret_cast<const int4*>(picks + (size_t)t * kp);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (2 * i < kp) p_next[i] = p[i];
+      if (!a.dx_in || t >= t1) return;
+      const uint4* from = a.dx_in + (size_t)t * vecs + col;
+      next[0] = from[0];
+      next[1] = from[1];
     };
-    if (t0 + mine < t1) fetch(t0 + mine);
+    fetch(t0 + mine);
     for (int t = t0 + mine; t < t1; t += kAtOnce) {
       f32x2 acc[8];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const uint4 u = u_next[i];
-        acc[4 * i] = pair_of_bf16(u.x);
-        acc[4 * i + 1] = pair_of_bf16(u.y);
-        acc[4 * i + 2] = pair_of_bf16(u.z);
-        acc[4 * i + 3] = pair_of_bf16(u.w);
+        acc[4 * i] = pair_of_bf16(next[i].x), acc[4 * i + 1] = pair_of_bf16(next[i].y);
+        acc[4 * i + 2] = pair_of_bf16(next[i].z), acc[4 * i + 3] = pair_of_bf16(next[i].w);
       }
-      int4 p[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) p[i] = p_next[i];
-      if (t + kAtOnce < t1) fetch(t + kAtOnce);
+      const int4* two = reinterpret_cast<const int4*>(a.picks + (size_t)t * a.kp);
       const auto add = [&](int e, float z) {
-        const f32x2 z2 = both(z);
         const char* row = w + e * kRow;
+        const f32x2 z2 = both(z);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float4 x = *reinterpret_cast<const float4*>(row + i * kQuarter);
-          acc[2 * i] = fma2(z2, pair(x.x, x.y), acc[2 * i]);
-          acc[2 * i + 1] = fma2(z2, pair(x.z, x.w), acc[2 * i + 1]);
+          const ulonglong2 u = *reinterpret_cast<const ulonglong2*>(row + i * kQuarter);
+          acc[2 * i] = fma2(z2, u.x, acc[2 * i]);
+          acc[2 * i + 1] = fma2(z2, u.y, acc[2 * i + 1]);
         }
       };
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (2 * i < kp) {
-          add(p[i].x, __int_as_float(p[i].y));
-          add(p[i].z, __int_as_float(p[i].w));
-        }
-      for (int i = 4; i < kp / 2; ++i) {
-        const int4 q = reinterpret_cast<const int4*>(picks + (size_t)t * kp)[i];
+      int4 p = two[0];
+      fetch(t + kAtOnce);
+#pragma unroll 2
+      for (int i = 0; i < a.kp / 2; ++i) {
+        const int4 q = p;
+        if (i + 1 < a.kp / 2) p = two[i + 1];
         add(q.x, __int_as_float(q.y));
         add(q.z, __int_as_float(q.w));
       }
-      uint4* o = dx + (size_t)t * (d / 8) + col;
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        o[i] = make_uint4(bf16_of_pair(acc[4 * i]),
-                          bf16_of_pair(acc[4 * i + 1]),
-                          bf16_of_pair(acc[4 * i + 2]),
-                          bf16_of_pair(acc[4 * i + 3]));
+      uint4* o = a.dx + (size_t)t * vecs + col;
+      o[0] = bf16_of8(acc);
+      o[1] = bf16_of8(acc + 4);
     }
     at += t1 - t0;
   }
 }
 
-// ------------------------------------------------------------------------------------------
-// 3. dw_gate, long batches: a CTA takes 64 columns of up to 256 experts over a part of the chunks;
-// their sums are in shared memory, and so are, for the present chunk and the next, x's tile and the
-// list. Each 8 lanes take an equal part of the list, however the experts are loaded: 8 columns a
-// lane, a run of one expert's choices added up in registers and then added to the expert's sums. A
-// part's first run may belong to the expert that the part before it ends with: its sum goes to a side
-// row, and the side rows are added in order after the chunk.
-// ------------------------------------------------------------------------------------------
-constexpr int kDwThreads = 512, kDwSlices = kDwThreads / 8;
-struct DwSmem {
-  float sums[kDwExperts][kDwCols];   // columns 8j .. 8j + 3 at 4j, 8j + 4 .. 8j + 7 at 32 + 4j
-  char tile[2][(kMostChunk + 1) * 128];   // the last row: zeros
-  Entry list[2][kMostList + 3 * kDwExperts];
-  float side[kDwSlices][kDwCols];    // as sums
-  int side_expert[kDwSlices];
-  int entries[2];                    // of the block's experts in the list
-};
-static_assert(sizeof(DwSmem) <= 227 * 1024, "one CTA an SM");
-
-__global__ void __launch_bounds__(kDwThreads, 1) route_grad_dw_slab_kernel(
-    const char* __restrict__ x, const int2* __restrict__ runs, const Entry* __restrict__ list,
-    float* __restrict__ out, int T, int chunk, int chunks,
-    int stride, int k, int E, int d, int parts, bool accumulate) {
-  extern __shared__ __align__(16) char raw[];
-  DwSmem& sm = *reinterpret_cast<DwSmem*>(raw);
-  const int lane = threadIdx.x & 31, l = threadIdx.x & 7, slice = threadIdx.x >> 3;
-  const int col0 = blockIdx.x * kDwCols, e0 = blockIdx.y * kDwExperts, ne = min(kDwExperts, E - e0);
-  const int part = blockIdx.z;
-  const int c0 = (int)((long long)chunks * part / parts);
-  const int c1 = (int)((long long)chunks * (part + 1) / parts);
-  for (int i = threadIdx.x; i < kDwExperts * kDwCols; i += kDwThreads) sm.sums[0][i] = 0.0f;
-  if (threadIdx.x < 16)
-    *reinterpret_cast<uint4*>(sm.tile[threadIdx.x >> 3] + kMostChunk * 128 + l * 16) =
-        make_uint4(0, 0, 0, 0);
+// C: columns of a slab; 0: the tokens' items come first in the queue.
+constexpr int product_threads(int C) { return C ? 1024 : 256; }
+constexpr int product_ctas(int C) { return C ? 1 : 5; }   // an SM
+template <int C>
+__global__ void __launch_bounds__(product_threads(C), product_ctas(C))
+    route_grad_products_kernel(const Args a) {
+  extern __shared__ __align__(16) char slab[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
-  pdl_trigger();
-
-  const auto fetch = [&](int c, int b) {
-    const int t0 = c * chunk, nt = min(chunk, T - t0);
-    const int2* run = runs + (size_t)c * E + e0;
-    const int from = run[0].x, to = (run[ne - 1].y + 3) / 4 * 4;
-    if (threadIdx.x == 0) sm.entries[b] = to - from;
-    for (int i = threadIdx.x; i < nt * 8; i += kDwThreads)
-      copy16(sm.tile[b] + i * 16,
-             x + ((size_t)(t0 + (i >> 3)) * d + col0) * 2 + (size_t)(i & 7) * 16);
-    const Entry* in = list + (size_t)c * stride + from;
-    for (int i = threadIdx.x; i < (to - from) / 2; i += kDwThreads)
-      copy16(&sm.list[b][2 * i], in + 2 * i);
-    copies_commit();
+  if (C > 0 && warp < kDxThreads / 32) dx_slabs<C ? C : 128>(a, slab);
+  const int blocks = (a.d / 8 + 31) / 32, segments = a.segments[a.E];
+  const long long dx_items = C > 0 ? 0 : (long long)a.T * blocks;
+  const long long items = dx_items + (long long)segments * blocks;
+  // the warps that begin with items have their first ones by number, the queue those after
+  constexpr int kFirst = C > 0 ? kDxThreads / 32 : 0;
+  const int beginners = product_threads(C) / 32 - kFirst, known = gridDim.x * beginners;
+  const auto take = [&]() {
+    int i = 0;
+    if (lane == 0) i = atomicAdd(a.queue, 1);
+    return known + __shfl_sync(0xffffffffu, i, 0);
   };
-  if (c0 < c1) fetch(c0, 0);
-  for (int c = c0; c < c1; ++c) {
-    const int b = (c - c0) & 1;
-    if (c + 1 < c1)
-      fetch(c + 1, b ^ 1);
-    else
-      copies_commit();
-    copies_wait<1>();
-    __syncthreads();
-    // fours of entries of this slice
-    const int n = sm.entries[b] / 4, per = (n + kDwSlices - 1) / kDwSlices;
-    const int begin = min(slice * per, n), end = min(begin + per, n);
-    const Entry* in = sm.list[b];
-    const char* tile = sm.tile[b] + l * 16;
-    // the run that comes in from the slice before, if it does: its sum goes to the side row
-    bool head = begin > 0 && begin < end && !(in[4 * begin - 4].at & 1);
-    int side = -1;
-    f32x2 acc[4] = {};
-    for (int at = begin; at < end; ++at) {
-      Entry q[4];
-      uint4 u[4];
-      {
-        const int4 a = *reinterpret_cast<const int4*>(in + 4 * at);
-        const int4 h = *reinterpret_cast<const int4*>(in + 4 * at + 2);
-        q[0] = Entry{(uint32_t)a.x, __int_as_float(a.y)};
-        q[1] = Entry{(uint32_t)a.z, __int_as_float(a.w)};
-        q[2] = Entry{(uint32_t)h.x, __int_as_float(h.y)};
-        q[3] = Entry{(uint32_t)h.z, __int_as_float(h.w)};
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) u[i] = *reinterpret_cast<const uint4*>(tile + entry_row(q[i]));
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        acc[0] = fma2(both(q[i].dz), pair_of_bf16(u[i].x), acc[0]);
-        acc[1] = fma2(both(q[i].dz), pair_of_bf16(u[i].y), acc[1]);
-        acc[2] = fma2(both(q[i].dz), pair_of_bf16(u[i].z), acc[2]);
-        acc[3] = fma2(both(q[i].dz), pair_of_bf16(u[i].w), acc[3]);
-      }
-      if ((q[0].at & 1) || at == end - 1) {   // the run ends here, or goes on in the next slice
-        const int e = q[0].at >> 16;
-        float4* to = reinterpret_cast<float4*>(head ? sm.side[slice] : sm.sums[e]) + l;
-        float4 a = four(acc[0], acc[1]), h = four(acc[2], acc[3]);
-        if (head) {
-          side = e;
-        } else {
-          const float4 p = to[0], r = to[8];
-          a.x += p.x, a.y += p.y, a.z += p.z, a.w += p.w;
-          h.x += r.x, h.y += r.y, h.z += r.z, h.w += r.w;
-        }
-        to[0] = a;
-        to[8] = h;
-        head = false;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] = 0;
-      }
+  int item = warp >= kFirst ? blockIdx.x * beginners + warp - kFirst : take();
+  while (item < items) {
+    const int next = take();
+    if (item < dx_items) {
+      const int t = item / blocks;
+      dx_item(a, t, (item - t * blocks) * 32 + lane);
+    } else {
+      const int i = static_cast<int>(item - dx_items), block = i / segments;
+      dw_item(a, i - block * segments, block * 32 + lane);
     }
-    if (l == 0) sm.side_expert[slice] = side;
-    __syncthreads();
-    {   // the side rows of experts e % 8 = mine by the same threads, in order
-      const int col = threadIdx.x % kDwCols, mine = threadIdx.x / kDwCols;
-      const int ea = sm.side_expert[lane], eb = sm.side_expert[32 + lane];
-      uint32_t ma = __ballot_sync(0xffffffffu, ea >= 0 && ea % 8 == mine);
-      uint32_t mb = __ballot_sync(0xffffffffu, eb >= 0 && eb % 8 == mine);
-      while (ma | mb) {
-        const int w = ma ? __ffs(ma) - 1 : 31 + __ffs(mb);
-        if (ma)
-          ma &= ma - 1;
-        else
-          mb &= mb - 1;
-        sm.sums[sm.side_expert[w]][col] += sm.side[w][col];
-      }
-    }
-    __syncthreads();
-  }
-  __syncthreads();
-  float* to = out + (size_t)part * E * d;
-  for (int i = threadIdx.x; i < ne * (kDwCols / 4); i += kDwThreads) {
-    const int e = i / (kDwCols / 4), v = i % (kDwCols / 4);
-    float4 s = reinterpret_cast<const float4*>(sm.sums[e])[(v & 1) * 8 + (v >> 1)];
-    float4* o = reinterpret_cast<float4*>(to + (size_t)(e0 + e) * d + col0) + v;
-    if (accumulate) {
-      const float4 p = *o;
-      s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w;
-    }
-    *o = s;
+    item = next;
   }
 }
 
-// The parts' sums, in order.
-__global__ void __launch_bounds__(kThreads) route_grad_join_kernel(
-    const float4* __restrict__ partial, float4* __restrict__ dw_gate, size_t n, int parts,
-    bool accumulate) {
-  const size_t i = (size_t)blockIdx.x * kThreads + threadIdx.x;
+// ------------------------------------------------------------------------------------------
+// 4. Experts with several segments, or none: their sums, in order.
+// ------------------------------------------------------------------------------------------
+constexpr int kJoinThreads = 256;
+__global__ void __launch_bounds__(kJoinThreads) route_grad_join_kernel(
+    const float4* __restrict__ partial, const int32_t* __restrict__ segments,
+    float4* __restrict__ dw_gate, int quads, bool accumulate) {
+  const int e = blockIdx.y, v = blockIdx.x * kJoinThreads + threadIdx.x;
   pdl_wait();
-  if (i >= n) return;
-  float4 s = partial[i];
-  const auto add = [&](const float4& v) { s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w; };
+  const int s0 = segments[e], s1 = segments[e + 1];
+  if (s1 - s0 == 1 || v >= quads || (s0 == s1 && accumulate)) return;
+  float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const auto add = [&](const float4& p) { s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w; };
 #pragma unroll 4
-  for (int p = 1; p < parts; ++p) add(partial[(size_t)p * n + i]);
-  if (accumulate) add(dw_gate[i]);
-  dw_gate[i] = s;
+  for (int i = s0; i < s1; ++i) add(partial[(size_t)i * quads + v]);
+  float4* o = dw_gate + (size_t)e * quads + v;
+  if (accumulate) add(*o);
+  *o = s;
+}
+
+// ------------------------------------------------------------------------------------------
+// A short batch: every CTA works out all choices' dz for itself, then its warps take items: 256 columns
+// of a token's dx, or of an expert's dw_gate, whose choices are found by looking through all of them.
+// ------------------------------------------------------------------------------------------
+constexpr int kShortThreads = 1024, kShortWarps = kShortThreads / 32;
+constexpr int kShortChoices = 1024;
+__global__ void __launch_bounds__(kShortThreads) route_grad_short_kernel(
+    const int32_t* __restrict__ idx, const float* __restrict__ score, const float* __restrict__ dw,
+    const Args a, int k, float scale, uint32_t* status) {
+  __shared__ int expert[2 * kShortChoices];   // [T][kp]
+  __shared__ float dz[2 * kShortChoices];
+  __shared__ int found[kShortWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, kp = a.kp;
+  {
+    const int width = lanes_of(kp), j = threadIdx.x & (width - 1), per = kShortThreads / width;
+    for (int b = 0; b < a.T; b += per) {   // whole warps
+      const int t = b + threadIdx.x / width;
+      const bool in = t < a.T && j < k;
+      int e = -1;
+      float s = 0.0f, g = 0.0f;
+      if (in) e = checked(idx[t * k + j], a.E, status), s = score[t * k + j], g = dw[t * k + j];
+      const Pick p = pick_of(e, s, g, in, width, scale, a.E);
+      if (t < a.T && j < kp) expert[t * kp + j] = p.expert, dz[t * kp + j] = p.dz;
+    }
+  }
+  __syncthreads();
+  const int vecs = a.d / 8, blocks = (vecs + 31) / 32, dx_items = a.T * blocks;
+  const int items = dx_items + a.E * blocks, step = gridDim.x * kShortWarps;
+  for (int item = blockIdx.x * kShortWarps + warp; item < items; item += step) {
+    if (item < dx_items) {
+      const int t = item / blocks, v = (item - t * blocks) * 32 + lane;
+      if (v >= vecs) continue;
+      const size_t at = (size_t)t * vecs + v;
+      f32x2 acc[4];
+      load8(acc, a.dx_in ? a.dx_in + at : nullptr);
+#pragma unroll 4
+      for (int i = t * kp; i < t * kp + kp; ++i) {
+        const int e = expert[i];
+        if (e == a.E) continue;
+        const ulonglong2* w = reinterpret_cast<const ulonglong2*>(a.w_gate + (size_t)e * a.d) + 2 * v;
+        add8(acc, dz[i], w[0], w[1]);
+      }
+      a.dx[at] = bf16_of8(acc);
+      continue;
+    }
+    const int i = item - dx_items, e = i / blocks, v = (i - e * blocks) * 32 + lane;
+    f32x2 acc[4] = {};
+    int n = 0;   // choices found, 32 at most before they are added
+    bool any = false;
+    const auto flush = [&]() {
+      __syncwarp();
+      if (v < vecs)
+#pragma unroll 4
+        for (int q = 0; q < n; ++q) {
+          const int c = found[warp][q];
+          add8(acc, dz[c], a.x[(size_t)(c / kp) * vecs + v]);
+        }
+      any |= n > 0;
+      n = 0;
+      __syncwarp();
+    };
+    for (int b = 0; b < a.T * kp; b += 32) {
+      const bool hit = b + lane < a.T * kp && expert[b + lane] == e;
+      const uint32_t hits = __ballot_sync(0xffffffffu, hit);
+      if (!hits) continue;
+      if (n + __popc(hits) > 32) flush();
+      if (hit) found[warp][n + __popc(hits & ((1u << lane) - 1u))] = b + lane;
+      n += __popc(hits);
+    }
+    flush();
+    if (v < vecs && (any || !a.accumulate))
+      store8(a.dw_gate + (size_t)e * a.d, v, acc, a.accumulate);
+  }
 }
 
 template <int C>
-cudaError_t dx_slab(const moe_cfg& c, const Pick* picks, const float* w_gate, const void* dx_in,
-                    void* dx, int kp, cudaStream_t st) {
-  auto kern = route_grad_dx_slab_kernel<C>;
-  const size_t smem = (size_t)(c.E + 1) * C * 4;
+cudaError_t run_products(Args a, cudaStream_t st) {
+  auto kern = route_grad_products_kernel<C>;
+  const size_t smem = C ? (size_t)(a.E + 1) * C * 4 : 0;
   const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
-  const long long work = (long long)(c.d / C) * c.T;
-  const long long per = (work + kSms - 1) / kSms;
-  return launch_kernel(kern, dim3((unsigned)((work + per - 1) / per)), dim3(kDxThreads), smem, st,
-                       true, picks, w_gate, static_cast<const uint4*>(dx_in),
-                       static_cast<uint4*>(dx), c.T, kp, c.E, c.d, per);
+  if (C > 0) a.per_cta = ((long long)(a.d / std::max(C, 1)) * a.T + kSms - 1) / kSms;
+  return launch_kernel(kern, dim3(kSms * product_ctas(C)), dim3(product_threads(C)), smem, st, true,
+                       a);
 }
 
 }  // namespace
@@ -583,47 +592,54 @@ cudaError_t launch_route_grad(const moe_cfg& c, const void* x, const float* w_ga
                               void* ws, cudaStream_t st) {
   const Layout L = layout(c);
   char* w = static_cast<char*>(ws);
-  Pick* picks = reinterpret_cast<Pick*>(w + L.picks);
-  int2* runs = reinterpret_cast<int2*>(w + L.runs);
-  Entry* list = reinterpret_cast<Entry*>(w + L.list);
-  float* partial = reinterpret_cast<float*>(w + L.partial);
-  const size_t masks = sizeof(ListSmem) + sizeof(uint32_t) * kMaskStride * (size_t)c.E;
-  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(route_grad_list_kernel),
-                                    masks + 1024);   // (the static array counts, too)
-  if (e != cudaSuccess) return e;
-  e = launch_kernel(route_grad_list_kernel, dim3(L.chunks), dim3(kListThreads), masks, st, false,
-                    topk_idx, topk_s, dtopk_w, c.T, c.k, L.kp, c.E, c.route_scale, L.chunk, L.stride,
-                    picks, runs, list, static_cast<uint32_t*>(ws));
-  if (e != cudaSuccess) return e;
-  const Pick* pk = picks;
-  const int2* rn = runs;
-  const Entry* ls = list;
-  if (L.parts == 0) {
-    const long long parts = (c.d / 8 + 31) / 32;
-    const auto ctas = [](long long warps) { return (unsigned)((warps + kWarps - 1) / kWarps); };
-    const unsigned dx_ctas = ctas(c.T * parts);
-    return launch_kernel(route_grad_short_kernel, dim3(dx_ctas + ctas(c.E * parts)), dim3(kThreads),
-                         0, st, true, pk, rn, ls, w_gate, static_cast<const uint4*>(x),
-                         static_cast<const uint4*>(dx_in), static_cast<uint4*>(dx), dw_gate, c.T,
-                         L.kp, c.E, c.d, L.chunk, L.chunks, L.stride, accumulate, dx_ctas);
+  uint32_t* status = static_cast<uint32_t*>(ws);
+  Args a{};
+  a.x = static_cast<const uint4*>(x);
+  a.w_gate = w_gate;
+  a.dx_in = static_cast<const uint4*>(dx_in);
+  a.dx = static_cast<uint4*>(dx);
+  a.dw_gate = dw_gate;
+  a.T = c.T, a.kp = L.kp, a.E = c.E, a.d = c.d, a.segment = L.segment;
+  a.accumulate = accumulate;
+  const long long blocks = (c.d / 8 + 31) / 32;
+  if (L.one_launch) {
+    const long long items = (c.T + c.E) * blocks;
+    const unsigned ctas = (unsigned)std::min((items + kShortWarps - 1) / kShortWarps, (long long)kSms);
+    return launch_kernel(route_grad_short_kernel, dim3(ctas), dim3(kShortThreads), 0, st, false,
+                         topk_idx, topk_s, dtopk_w, a, c.k, c.route_scale, status);
   }
-  const size_t row = 4 * (size_t)(c.E + 1);
-  e = row * 128 <= 227 * 1024  ? dx_slab<128>(c, pk, w_gate, dx_in, dx, L.kp, st)
-      : row * 64 <= 227 * 1024 ? dx_slab<64>(c, pk, w_gate, dx_in, dx, L.kp, st)
-                               : dx_slab<32>(c, pk, w_gate, dx_in, dx, L.kp, st);
+  Pick* picks = reinterpret_cast<Pick*>(w + L.picks);
+  int32_t* counts = reinterpret_cast<int32_t*>(w + L.counts);
+  int32_t* starts = reinterpret_cast<int32_t*>(w + L.starts);
+  int32_t* segments = reinterpret_cast<int32_t*>(w + L.segments);
+  Entry* list = reinterpret_cast<Entry*>(w + L.list);
+  a.queue = reinterpret_cast<int32_t*>(w + L.queue);
+  a.partial = reinterpret_cast<float*>(w + L.partial);
+  a.picks = picks, a.starts = starts, a.segments = segments, a.list = list;
+  cudaError_t e = launch_kernel(route_grad_count_kernel, dim3(L.chunks), dim3(kListThreads), 0, st,
+                                false, topk_idx, topk_s, dtopk_w, c.T, c.k, L.kp, c.E,
+                                c.route_scale, L.chunk, picks, counts, a.queue, status);
   if (e != cudaSuccess) return e;
-  const int slabs = c.d / kDwCols, blocks = (c.E + kDwExperts - 1) / kDwExperts;
-  e = ensure_smem_limit(reinterpret_cast<const void*>(route_grad_dw_slab_kernel), sizeof(DwSmem));
+  const size_t smem = (size_t)c.E * (4 + kMaskStride * (4 + 2));
+  e = ensure_smem_limit(reinterpret_cast<const void*>(route_grad_list_kernel),
+                        smem + 1024);   // (the static array counts, too)
   if (e != cudaSuccess) return e;
-  e = launch_kernel(route_grad_dw_slab_kernel, dim3(slabs, blocks, L.parts), dim3(kDwThreads),
-                    sizeof(DwSmem), st, true, static_cast<const char*>(x), rn, ls,
-                    L.parts > 1 ? partial : dw_gate, c.T, L.chunk, L.chunks, L.stride, c.k, c.E, c.d,
-                    L.parts, L.parts == 1 && accumulate);
-  if (e != cudaSuccess || L.parts == 1) return e;
-  const size_t n = (size_t)c.E * c.d / 4;
-  return launch_kernel(route_grad_join_kernel, dim3((unsigned)((n + kThreads - 1) / kThreads)),
-                       dim3(kThreads), 0, st, true, reinterpret_cast<const float4*>(partial),
-                       reinterpret_cast<float4*>(dw_gate), n, L.parts, accumulate);
+  e = launch_kernel(route_grad_list_kernel, dim3(L.chunks), dim3(kListThreads), smem, st, true,
+                    static_cast<const Pick*>(picks), static_cast<const int32_t*>(counts), c.T, L.kp,
+                    c.E, L.chunk, L.chunks, L.segment, starts, segments, list);
+  if (e != cudaSuccess) return e;
+  const size_t row = 4 * (size_t)(c.E + 1), most = 227 * 1024;
+  e = !L.slab            ? run_products<0>(a, st)
+      : row * 128 <= most ? run_products<128>(a, st)
+      : row * 64 <= most  ? run_products<64>(a, st)
+                          : run_products<32>(a, st);
+  if (e != cudaSuccess) return e;
+  const int quads = c.d / 4;
+  return launch_kernel(route_grad_join_kernel,
+                       dim3((quads + kJoinThreads - 1) / kJoinThreads, c.E), dim3(kJoinThreads), 0,
+                       st, true, reinterpret_cast<const float4*>(a.partial),
+                       static_cast<const int32_t*>(segments), reinterpret_cast<float4*>(dw_gate),
+                       quads, accumulate);
 }
 
 }  // namespace moe
