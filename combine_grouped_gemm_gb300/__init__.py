@@ -538,9 +538,19 @@ def _stream_type(fn, name, t):
     return t.dtype
 
 
-def _norm_cfg(rows, d, st, eps=0.0, res=1.0, out=1.0, gate=MOE_GATE_NONE):
-    return ctypes.byref(NormCfg(rows, d, eps, res, out,
-                                MOE_F32 if st is torch.float32 else MOE_BF16, gate))
+_norm_cfgs = {}   # moe_norm_cfg's fields -> the struct by reference (calls only read it)
+
+
+def _norm_cfg(*key):
+    """rows, d, stream's type, eps, res_scale, out_scale, gate"""
+    c = _norm_cfgs.get(key)
+    if c is None:
+        if len(_norm_cfgs) >= 4096:   # sizes that differ from call to call
+            _norm_cfgs.clear()
+        rows, d, st, eps, res, out, gate = key
+        c = _norm_cfgs[key] = ctypes.byref(NormCfg(
+            rows, d, eps, res, out, MOE_F32 if st is torch.float32 else MOE_BF16, gate))
+    return c
 
 
 def _gate_of(fn, gate, rows, d):
@@ -560,7 +570,12 @@ def _gate_of(fn, gate, rows, d):
 
 
 def _opt(fn, dev, name, t, dtype, *shape):
-    return None if t is None else _need(fn, dev, name, t, dtype, *shape)
+    if t is None:
+        return None
+    if (t.__class__ is torch.Tensor and t.dtype is dtype and t.shape == shape
+            and t.get_device() == dev and t.is_contiguous()):
+        return t.data_ptr()
+    return _need(fn, dev, name, t, dtype, *shape)
 
 
 def norm_ws_bytes(rows, d) -> int:
@@ -588,10 +603,10 @@ def norm_in(x, w, n, rstd=None, eps=1e-6, stream=None):
     fn, dev, f32 = "moe_norm_in", _device(), torch.float32
     rows, d = _rows_cols(fn, "x", x)
     st = _stream_type(fn, "x", x)
-    _check(fn, _lib.moe_norm_in(_norm_cfg(rows, d, st, eps), _need(fn, dev, "x", x, st, rows, d),
-                                _need(fn, dev, "w", w, f32, d),
-                                _need(fn, dev, "n", n, torch.bfloat16, rows, d),
-                                _opt(fn, dev, "rstd", rstd, f32, rows), _stream(stream, dev)))
+    _check(fn, _lib.moe_norm_in(
+        _norm_cfg(rows, d, st, eps, 1.0, 1.0, 0), _need(fn, dev, "x", x, st, rows, d),
+        _need(fn, dev, "w", w, f32, d), _need(fn, dev, "n", n, torch.bfloat16, rows, d),
+        _opt(fn, dev, "rstd", rstd, f32, rows), _stream(stream, dev)))
 
 
 def norm_in_grad(dn, x, w, rstd, dres, dx, dw, ws, accumulate=False, stream=None):
@@ -601,8 +616,8 @@ def norm_in_grad(dn, x, w, rstd, dres, dx, dw, ws, accumulate=False, stream=None
     rows, d = _rows_cols(fn, "x", x)
     st = _stream_type(fn, "x", x)
     _check(fn, _lib.moe_norm_in_grad(
-        _norm_cfg(rows, d, st), _need(fn, dev, "dn", dn, torch.bfloat16, rows, d),
-        _need(fn, dev, "x", x, st, rows, d), _need(fn, dev, "w", w, f32, d),
+        _norm_cfg(rows, d, st, 0.0, 1.0, 1.0, 0),
+        _need(fn, dev, "dn", dn, torch.bfloat16, rows, d), _need(fn, dev, "x", x, st, rows, d), _need(fn, dev, "w", w, f32, d),
         _need(fn, dev, "rstd", rstd, f32, rows), _opt(fn, dev, "dres", dres, st, rows, d),
         _need(fn, dev, "dx", dx, st, rows, d), _opt(fn, dev, "dw", dw, f32, d),
         1 if accumulate else 0, _norm_ws(fn, dev, rows, d, ws), _stream(stream, dev)))
