@@ -713,13 +713,15 @@ class AdamTensors:
     """The tensors of an AdamW step, checked once and held: a list of dicts with p (fp32), g (fp32
     or bf16), w (bf16 copy of p, or None), m, v (fp32; 8 bits: bytes) and, with state_bits 8,
     m_scale and v_scale (fp32, one per 128 elements); optional weight_decay (0) and seed (the
-    tensor's place in the list). All contiguous, on one device; step by step, the same storage."""
+    tensor's place in the list). All contiguous, on one device. The plan keeps these very tensors:
+    another one put into a dict later is not seen."""
 
     def __init__(self, tensors, state_bits=32):
         fn, dev = "AdamTensors", _device()
         if state_bits not in (32, 8):
             raise ValueError(f"{fn}: state_bits must be 32 or 8")
-        self.state_bits, self.device, self.tensors = state_bits, dev, list(tensors)
+        self.state_bits, self.device = state_bits, dev
+        self.tensors = [dict(t) for t in tensors]   # (references: the pointers stay valid)
         f32, n = torch.float32, len(self.tensors)
         self.array = (AdamTensorC * n)()
         for i, (t, c) in enumerate(zip(self.tensors, self.array)):
@@ -952,15 +954,18 @@ class MoEBlock:
         self.y = torch.empty(shape, dtype=torch.bfloat16, device=dev)
 
     def __call__(self, x, n=None, h=None, stream=None):
-        """h may be x itself. The n that is returned is the block's own buffer."""
+        """h may be x itself. The n that is returned is a buffer of the block's own, which its next
+        call but one (or one without n) writes over."""
         if n is None:
             n = self.n
             norm_in(x, self.w_in, n, eps=self.eps, stream=stream)
         if h is None:
             h = torch.empty_like(x)
-        self.layer(n, self.y, stream)
+        # (a block that is called with its own n, layers that share weights: the other buffer)
+        y = self.n if n.data_ptr() == self.y.data_ptr() else self.y
+        self.layer(n, y, stream)
         # the layer's output has been read where the next norm's takes its place
-        n_next = self.y if self.w_next is not None else None
-        norm_out(self.y, x, self.w_out, self.gate, self.w_next, h, n_next, eps=self.eps,
+        n_next = y if self.w_next is not None else None
+        norm_out(y, x, self.w_out, self.gate, self.w_next, h, n_next, eps=self.eps,
                  stream=stream, **self.scales)
         return h if n_next is None else (h, n_next)

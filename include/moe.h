@@ -460,7 +460,7 @@ int moe_combine_grad(int32_t T, int32_t k, int32_t d, int32_t rows, const void* 
 typedef struct moe_norm_cfg {
   int32_t rows;           /* >= 0 */
   int32_t d;              /* d % 8 == 0, d <= 16384; rows * d < 2^37 */
-  float eps;              /* finite, >= 0 */
+  float eps;              /* finite, >= 0 (0: a row of zeros has no norm, and gives NaN) */
   float res_scale;        /* res: factor of the residual stream (norm_out) */
   float out_scale;        /* out: factor of the block's gated output (norm_out) */
   int32_t stream_dtype;   /* MOE_BF16 or MOE_F32: type of the residual stream (x, h, dh, dx) */
@@ -469,7 +469,8 @@ typedef struct moe_norm_cfg {
 
 /* RMS norm before a block: r = 1/sqrt(mean_j x_j^2 + eps) of each row, n = bf16(x r w).
  * x [rows][d] of the stream's type, w fp32 [d], n bf16 [rows][d] (may take the place of a bf16 x),
- * rstd fp32 [rows]: r, kept for the gradient (NULL: not wanted). Sums in fp32 here and below. */
+ * rstd fp32 [rows]: r, kept for the gradient (NULL: not wanted). Squares and sums in fp32 here and
+ * below: values past 1e19 leave its range. */
 int moe_norm_in(const moe_norm_cfg* cfg, const void* x, const float* w, void* n, float* rstd,
                 cudaStream_t stream);
 
@@ -590,7 +591,8 @@ int moe_adamw(const moe_adam_cfg* cfg, const moe_adam_tensor* tensors, int32_t n
 
 /* norm = sqrt of the sum of all g^2 (device fp32 scalar; squares in fp32, so that a gradient past
  * 1e19 counts as infinite). Of the tensors, g, g_dtype and n count. With `more` the sum goes on in
- * the next call and norm is not written. */
+ * the next call and norm is not written (a norm that was broken off is ended by a call with n = 0).
+ * Calls that may overlap on the GPU need states of their own, here and in moe_adamw. */
 int moe_grad_norm(const moe_adam_tensor* tensors, int32_t n, int32_t more, void* state,
                   float* norm, cudaStream_t stream);
 

@@ -221,6 +221,13 @@ def test_serving_block_is_its_stages(moe, T, st):
     hh = torch.empty_like(x)
     moe.norm_out(y, h, w[3], None, None, hh, None)
     assert torch.equal(hh, h2)
+    # called again with its own n (layers that share weights): as from a copy of it
+    a, m = first(x)
+    keep = m.clone()
+    b1, m1 = first(a, m)
+    b1, m1 = b1.clone(), m1.clone()
+    b2, m2 = first(a, keep)
+    assert torch.equal(b1, b2) and torch.equal(m1, m2)
     # the norm of h as it was stored is a rounding away from the one handed on: h's own (2^-8 of each
     # column, and of r_h at most as much again) and the results' two
     moe.norm_in(h1, w[2], nn)
