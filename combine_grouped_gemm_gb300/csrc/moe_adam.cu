@@ -212,9 +212,11 @@ __device__ __forceinline__ Scalars scalars(const Hyper& h, const State* state, c
     sc.n1 = static_cast<float>(1.0 - h.beta1);
     sc.b2 = static_cast<float>(h.beta2);
     sc.n2 = static_cast<float>(1.0 - h.beta2);
-    sc.move = static_cast<float>(lr / c1);
-    sc.root = static_cast<float>(1.0 / sqrt(c2));
+    // (the corrections themselves need fp64, as sums of small parts; quotient and root do not, and
+    // fp64 division and root take microseconds here)
     sc.lr = static_cast<float>(lr);
+    sc.move = __fdiv_rn(sc.lr, static_cast<float>(c1));
+    sc.root = __frsqrt_rn(static_cast<float>(c2));
     sc.eps = h.eps;
     sc.step = static_cast<uint32_t>(state->step + 1);
     const float total = norm ? *norm : 0.0f;
