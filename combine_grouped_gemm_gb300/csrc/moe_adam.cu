@@ -131,6 +131,7 @@ template <int CAP>
 __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_constant__ Table<CAP> tab,
                                                              uint32_t chunks, State* state,
                                                              float* norm, bool more) {
+  pdl_trigger();
   double acc = 0.0;
   for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
     const int t = tensor_of(tab, c);
@@ -204,6 +205,7 @@ constexpr uint32_t kGolden = 0x9e3779b9u;
 
 __device__ __forceinline__ Scalars scalars(const Hyper& h, const State* state, const float* norm) {
   __shared__ Scalars sc;
+  pdl_wait();
   if (threadIdx.x == 0) {
     const double c1 = h.beta1 * state->c1 + (1.0 - h.beta1);
     const double c2 = h.beta2 * state->c2 + (1.0 - h.beta2);
@@ -631,8 +633,10 @@ cudaError_t adam_cap(const moe_adam_cfg& c, const moe_adam_tensor* t, int n, boo
   const size_t smem = held ? kSteps8 * sizeof(Stage8) : 0;
   const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), smem + 1024);
   if (e != cudaSuccess) return e;
-  return launch_kernel(kern, dim3(grid_of(chunks + n, 4)), dim3(kThreads), smem, st, false, tab, h,
-                       chunks, state, norm, more);
+  // with a norm: launched while its kernel, the one before, still runs (2.1 M parameters in fp32, norm
+  // and step: 18.4 us, 20.7 one after the other)
+  return launch_kernel(kern, dim3(grid_of(chunks + n, 4)), dim3(kThreads), smem, st, norm != nullptr,
+                       tab, h, chunks, state, norm, more);
 }
 
 // a short table for the few tensors of one layer, so that the launch carries less
