@@ -1,9 +1,13 @@
 // AdamW over a list of tensors in one launch, moments in 32 or 8 bits, and the norm of all their
-// gradients. Both stream their arrays from HBM once: 30 bytes a parameter with fp32 gradients, fp32
-// moments and a bf16 copy, 18.1 with 8-bit moments; the norm reads the gradients alone.
+// gradients:
+//   g' = g min(1, max_norm / |g|)    m = b1 m + (1 - b1) g'    v = b2 v + (1 - b2) g'^2
+//   p -= lr wd p + lr / (1 - b1^t) m / (sqrt(v / (1 - b2^t)) + eps)
+// Both stream their arrays from HBM once: 30 bytes a parameter with fp32 gradients, fp32 moments
+// and a bf16 copy, 18.1 with 8-bit moments; the norm reads the gradients alone.
 //
-// The tensors are cut into chunks, which the CTAs of one grid take in turn; the table of the tensors
-// travels as a kernel argument, so the step needs no device table and a captured one keeps its own.
+// The tensors are cut into chunks, which the CTAs of one grid take in turn; the table of the
+// tensors travels as a kernel argument, so the step needs no device table and a captured one keeps
+// its own.
 #include "moe_device.cuh"
 
 namespace moe {
@@ -255,26 +259,29 @@ __device__ __forceinline__ float half_warp_max(float v) {
   return __uint_as_float(__reduce_max_sync(lanes, __float_as_uint(v)));
 }
 
-// 1 where v > 0 (and v * big >= 1), else 0; a NaN gives 0. (By saturation on the FMA pipe: comparison
-// and select are two operations of the ALU pipe, which the integer work beside them fills.)
+// 1 where v > 0 (and v * big >= 1), else 0; a NaN gives 0. (By saturation on the FMA pipe:
+// comparison and select are two operations of the ALU pipe, which the integer work beside them
+// fills.)
 __device__ __forceinline__ float is_positive(float v, float big) {
   float r;
   asm("mul.rn.sat.f32 %0, %1, %2;" : "=f"(r) : "f"(v), "f"(big));
   return r;
 }
-__device__ __forceinline__ float below_2_6(float q) { return __saturatef(__fmaf_rn(q, -0x1p40f, 0x1p34f)); }
+__device__ __forceinline__ float below_2_6(float q) {
+  return __saturatef(__fmaf_rn(q, -0x1p40f, 0x1p34f));
+}
 __device__ __forceinline__ float cut(uint32_t bits) { return __uint_as_float(bits & 0xfff00000u); }
 
-// A quotient rounded up or down to e4m3 by 16 random bits. With the random bits added below the code's
-// last bit, cutting off what is below it rounds up with odds of the distance from the lower code.
-// Below 2^-6 the steps are 2^-9: with 2^-6 added they lie at the same bits. (What is past 448 by a
-// rounding is cut or, as a code, saturated.)
+// A quotient rounded up or down to e4m3 by 16 random bits. With the random bits added below the
+// code's last bit, cutting off what is below it rounds up with odds of the distance from the lower
+// code. Below 2^-6 the steps are 2^-9: with 2^-6 added they lie at the same bits. (What is past 448
+// by a rounding is cut or, as a code, saturated.)
 __device__ __forceinline__ float round_e4m3(float q, uint32_t r16) {
   const float s = below_2_6(q), y = __fmaf_rn(s, 0x1p-6f, q);
   return __fmaf_rn(s, -0x1p-6f, cut(__float_as_uint(y) + r16 * 16));
 }
-// The same for the root of a second moment, with odds that keep the mean of its square, (q^2 - lo^2)
-// / (hi^2 - lo^2): odds linear in q would add the rounding's variance to v each step, several
+// The same for the root of a second moment, with odds that keep the mean of its square, (q^2 -
+// lo^2) / (hi^2 - lo^2): odds linear in q would add the rounding's variance to v each step, several
 // percent of v in the long run. A root above 0 keeps a code above 0.
 __device__ __forceinline__ float round_root_e4m3(float q, float root, uint32_t r16) {
   const float s = below_2_6(q), y = __fmaf_rn(s, 0x1p-6f, q), c = cut(__float_as_uint(y));
@@ -320,8 +327,8 @@ __device__ __forceinline__ void finish(const Hyper& h, State* state, bool more) 
 }
 
 // ------------------------------------------------------------------------------------------
-// Moments in 32 bits: four elements a lane at once, loads a step ahead. 11.9 GB for 398 M parameters
-// and their norm: bound by memory.
+// Moments in 32 bits: four elements a lane at once, loads a step ahead. 398 M parameters with fp32
+// gradients and their norm: 2.05 ms for 13.5 GB, 6.6 TB/s: bound by memory.
 // ------------------------------------------------------------------------------------------
 struct Four {
   float4 g, p, m, v;
@@ -381,9 +388,12 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constan
 
 // ------------------------------------------------------------------------------------------
 // Moments in 8 bits: eight elements a lane at once, so that 16 lanes hold a block and what is done
-// once for it (scales, reciprocals, the key of its random numbers) is shared by eight elements. The
-// arithmetic of the rounding bounds it beside memory (FIGURES). Each thread's elements come through
-// two stages of its own in shared memory, and a CTA takes neighbouring chunks.
+// once for it (scales, reciprocals, the key of its random numbers) is shared by eight elements.
+// Each thread's elements come through two stages of its own in shared memory, and a CTA takes
+// neighbouring chunks. 398 M parameters, bf16 gradients, no norm: 1.32 ms, 4.9 TB/s. Some 100
+// instructions an element bound it, beside the update's the hash, the quotients and the rounding of
+// two codes: the issue slots are four fifths full. (Four elements a lane 1.93 ms; loads through
+// shared memory 1.59; eight a lane 1.41; one branch a block 1.32.)
 // ------------------------------------------------------------------------------------------
 constexpr int kStep8 = 8 * kThreads, kSteps8 = kChunk / kStep8;
 struct Stage8 {
@@ -436,8 +446,9 @@ __device__ __forceinline__ void step_eight(const Scalars& sc, const moe_adam_ten
   const float inv = __frcp_rn(scale);
   // where the reciprocal, its correction and the quotient stay inside the fp32 range
   const bool plain = __all_sync(0xffffffffu, scale > 0x1p-60f && scale < 0x1p100f);
-  const float sm = __shfl_sync(0xffffffffu, scale, 0, 16), sv = __shfl_sync(0xffffffffu, scale, 1, 16);
-  const float rm = __shfl_sync(0xffffffffu, inv, 0, 16), rv = __shfl_sync(0xffffffffu, inv, 1, 16);
+  const auto of_half = [](float v, int lane) { return __shfl_sync(0xffffffffu, v, lane, 16); };
+  const float sm = of_half(scale, 0), sv = of_half(scale, 1);
+  const float rm = of_half(inv, 0), rv = of_half(inv, 1);
   const uint32_t from = mix(key ^ static_cast<uint32_t>(block)) + place * 8 * kGolden;
   const auto hold = [&](auto quotient) {   // |x| / scale, the IEEE quotient
 #pragma unroll
@@ -633,8 +644,8 @@ cudaError_t adam_cap(const moe_adam_cfg& c, const moe_adam_tensor* t, int n, boo
   const size_t smem = held ? kSteps8 * sizeof(Stage8) : 0;
   const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), smem + 1024);
   if (e != cudaSuccess) return e;
-  // with a norm: launched while its kernel, the one before, still runs (2.1 M parameters in fp32, norm
-  // and step: 18.4 us, 20.7 one after the other)
+  // with a norm: launched while its kernel, the one before, still runs (2.1 M parameters in fp32,
+  // norm and step: 18.4 us, 20.7 one after the other)
   return launch_kernel(kern, dim3(grid_of(chunks + n, 4)), dim3(kThreads), smem, st, norm != nullptr,
                        tab, h, chunks, state, norm, more);
 }

@@ -1,6 +1,7 @@
-// Pairs of fp32 numbers in one 64-bit register pair, for the instructions that work on both at once.
-// (Held as 64-bit values, so that the halves stay in neighbouring registers: as structs of two floats
-// they were copied together before each operation, at more than the cost of the operations saved.)
+// Pairs of fp32 numbers in one 64-bit register pair, for the instructions that work on both at
+// once: half as many instructions for sums and products. (The compiler joins a product and a sum of
+// pairs into one operation that rounds once. Where each is to be rounded by itself, scalars are
+// used.)
 #pragma once
 
 #include <stdint.h>

@@ -2,16 +2,26 @@
 // gradient of the routing weights scale * p,
 //   dz_i = scale p_i (1 - s_i) (dw_i - sum_j p_j dw_j)
 // is the gradient of the k chosen logits, the only ones that the weights depend on: a sparse [T][E]
-// matrix of k entries a row. Tokens take dz . w_gate, gate weights dz^T . x. Both products do 2 T k d
-// operations on operands that several choices share, so what bounds them is the operands' way into
-// registers: T k d elements each, fp32 for the tokens and bf16 for the gate weights.
+// matrix of k entries a row. Tokens take dz . w_gate, gate weights dz^T . x. Both products do 2 T k
+// d operations on operands that several choices share, so what bounds them is the operands' way
+// into registers: T k d elements each, fp32 for the tokens and bf16 for the gate weights. (As dense
+// products on the tensor cores, fp32 factors as sums of two or three bf16 ones, they would be six
+// products of 2 T E d operations, 190 us at the rate of the library's for the batch below, without
+// the rest.)
 //
 // 1. Counts: a CTA per chunk of tokens computes dz and counts the chunk's choices of each expert.
 // 2. Lists: the choices expert by expert, in the order of the tokens, cut into segments.
-// 3. Products: the tokens' dx from the gate weights (long batches: from a slab of columns of them in
+// 3. Products: the tokens' dx from the gate weights (long batches: from a slab of columns of them
+// in
 //    shared memory), the segments' sums of x from L2, at the same time.
-// 4. The segments' sums are joined in order, so that the result does not depend on the order of work.
+// 4. The segments' sums are joined in order: the result does not depend on the order of work.
 // A short batch takes one launch for all of it.
+//
+// Measured, d = 7168, 256 experts, 8 choices: 16384 tokens 281 us, 2048 tokens 56 (count 4, lists
+// 6, products 46, join 2), 64 tokens 8.6. The 16384 tokens' operands are 5.6 GB on their way
+// through the SMs' shared memory and L1, 155 us at 128 bytes a clock and SM, of which L2 hands out
+// the segments' rows at some 8 TB/s. (Tokens and gate weights one after the other, the latter
+// summed chunk by chunk in shared memory: 370 us; first form 3431.)
 #include <algorithm>
 
 #include "moe_device.cuh"
@@ -62,7 +72,8 @@ Layout layout(const moe_cfg& c) {
   const auto up = [](size_t v) { return (v + 255) & ~static_cast<size_t>(255); };
   Layout L;
   const size_t tk = (size_t)c.T * c.k;
-  // 64 chunks, of 64 tokens at least: 2048 tokens' counts and lists take 3.7 + 6.3 us in chunks of 64,
+  // 64 chunks, of 64 tokens at least: 2048 tokens' counts and lists take 3.7 + 6.3 us in chunks of
+  // 64,
   // 8.4 + 13 in chunks of 320, 3.7 + 8.2 in chunks of 32 (whose counts are more to add up)
   L.chunk = std::min({std::max((c.T + 63) / 64, 64), kMostList / c.k, kMostChunk}) / 8 * 8;
   L.chunks = (int)(((long long)c.T + L.chunk - 1) / L.chunk);
@@ -101,9 +112,9 @@ __host__ __device__ __forceinline__ int lanes_of(int kp) {
   while (w < kp) w *= 2;
   return w;
 }
-// A choice and its dz, from its lane's expert (-1: none), score and gradient of the weight; `in`: there
-// is such a choice. A second choice of one expert is added to its first and becomes none itself. The
-// lanes of a token are neighbours, `width` of them; all lanes of the warp take part.
+// A choice and its dz, from its lane's expert (-1: none), score and gradient of the weight; `in`:
+// there is such a choice. A second choice of one expert is added to its first and becomes none
+// itself. The lanes of a token are neighbours, `width` of them; all lanes of the warp take part.
 __device__ __forceinline__ Pick pick_of(int e, float s, float g, bool in, int width, float scale,
                                         int E) {
   const auto sum_of_token = [&](float v) {
@@ -175,9 +186,10 @@ __global__ void __launch_bounds__(kListThreads) route_grad_count_kernel(
 }
 
 // ------------------------------------------------------------------------------------------
-// 2. The lists. A choice's place: its expert's start, the choices of the chunks before, and those of
-// its own chunk's tokens before, counted in a bit mask of the expert's tokens (set by atomic ORs, whose
-// order does not matter). Every CTA adds up all counts for itself; the first one writes the starts.
+// 2. The lists. A choice's place: its expert's start, the choices of the chunks before, and those
+// of its own chunk's tokens before, counted in a bit mask of the expert's tokens (set by atomic
+// ORs, whose order does not matter). Every CTA adds up all counts for itself; the first one writes
+// the starts.
 // ------------------------------------------------------------------------------------------
 constexpr int kOwn = (kMostList + kMostChunk) / kListThreads + 1;   // picks of a thread, at most
 constexpr int kMaskWords = kMostChunk / 32, kMaskStride = kMaskWords + 1;   // (odd: bank conflicts)
@@ -201,8 +213,8 @@ __device__ __forceinline__ int2 cta_scan(int2 own, int2* warp_sum) {
 
 __global__ void __launch_bounds__(kListThreads) route_grad_list_kernel(
     const Pick* __restrict__ picks, const int32_t* __restrict__ counts, int T, int kp, int E,
-    int chunk, int chunks, int segment, int32_t* __restrict__ starts, int32_t* __restrict__ segments,
-    Entry* __restrict__ list) {
+    int chunk, int chunks, int segment, int32_t* __restrict__ starts,
+    int32_t* __restrict__ segments, Entry* __restrict__ list) {
   extern __shared__ __align__(16) char raw[];
   __shared__ int2 warp_sum[kListWarps];
   int* first = reinterpret_cast<int*>(raw);                              // [E]: in the list
@@ -267,8 +279,8 @@ __global__ void __launch_bounds__(kListThreads) route_grad_list_kernel(
 }
 
 // ------------------------------------------------------------------------------------------
-// 3. The products. Work is handed out from a queue, a warp an item: 256 columns of a token's dx or of
-// a segment's sum (column blocks one after another: a block of x stays in L2 while it is used).
+// 3. The products. Work is handed out from a queue, a warp an item: 256 columns of a token's dx or
+// of a segment's sum (column blocks one after another: a block of x stays in L2 while it is used).
 // ------------------------------------------------------------------------------------------
 __device__ __forceinline__ void add8(f32x2 (&acc)[4], float z, const uint4& u) {
   const f32x2 z2 = both(z);
@@ -388,10 +400,11 @@ __device__ __forceinline__ void dw_item(const Args& a, int segment, int v) {
     store8(a.partial + (size_t)segment * a.d, v, acc, false);
 }
 
-// Long batches: half of a CTA's warps keep C columns of all gate weights in shared memory, and a row
-// of zeros for picks that are none. The (slab of columns, token) pairs, slab by slab, are dealt to the
-// CTAs in equal runs, so that a CTA loads one slab or two. C / 16 lanes take a token, 16 columns a
-// lane, so that the picks, which all of a token's lanes read, cost little beside the weights.
+// Long batches: half of a CTA's warps keep C columns of all gate weights in shared memory, and a
+// row of zeros for picks that are none. The (slab of columns, token) pairs, slab by slab, are dealt
+// to the CTAs in equal runs, so that a CTA loads one slab or two. C / 16 lanes take a token, 16
+// columns a lane, so that the picks, which all of a token's lanes read, cost little beside the
+// weights.
 constexpr int kDxThreads = 512;
 __device__ __forceinline__ void dx_barrier() {
   asm volatile("bar.sync 1, %0;" ::"n"(kDxThreads) : "memory");
@@ -465,7 +478,8 @@ __device__ __forceinline__ void dx_slabs(const Args& a, char* slab) {
   }
 }
 
-// C: columns of a slab; 0: the tokens' items come first in the queue.
+// C: columns of a slab; 0: the tokens' items come first in the queue, and five CTAs an SM, since
+// there is no slab, keep more loads in flight.
 constexpr int product_threads(int C) { return C ? 1024 : 256; }
 constexpr int product_ctas(int C) { return C ? 1 : 5; }   // an SM
 template <int C>
@@ -521,8 +535,11 @@ __global__ void __launch_bounds__(kJoinThreads) route_grad_join_kernel(
 }
 
 // ------------------------------------------------------------------------------------------
-// A short batch: every CTA works out all choices' dz for itself, then its warps take items: 256 columns
-// of a token's dx, or of an expert's dw_gate, whose choices are found by looking through all of them.
+// A short batch, of 1024 choices at most: every CTA works out all choices' dz for itself, then its
+// warps take items: 256 columns of a token's dx, or of an expert's dw_gate, whose choices are found
+// by looking through all of them. (64 tokens of 8 choices: 15 us with the call's cold start, 128:
+// 22 and 28 through the lists; 160 tokens take 27 through the lists, and the search grows with the
+// tokens.)
 // ------------------------------------------------------------------------------------------
 constexpr int kShortThreads = 1024, kShortWarps = kShortThreads / 32;
 constexpr int kShortChoices = 1024;
@@ -559,8 +576,9 @@ __global__ void __launch_bounds__(kShortThreads) route_grad_short_kernel(
       for (int i = t * kp; i < t * kp + kp; ++i) {
         const int e = expert[i];
         if (e == a.E) continue;
-        const ulonglong2* w = reinterpret_cast<const ulonglong2*>(a.w_gate + (size_t)e * a.d) + 2 * v;
-        add8(acc, dz[i], w[0], w[1]);
+        const float* w = a.w_gate + (size_t)e * a.d + 8 * v;
+        add8(acc, dz[i], *reinterpret_cast<const ulonglong2*>(w),
+             *reinterpret_cast<const ulonglong2*>(w + 4));
       }
       a.dx[at] = bf16_of8(acc);
       continue;
@@ -628,7 +646,8 @@ cudaError_t launch_route_grad(const moe_cfg& c, const void* x, const float* w_ga
   const long long blocks = (c.d / 8 + 31) / 32;
   if (L.one_launch) {
     const long long items = (c.T + c.E) * blocks;
-    const unsigned ctas = (unsigned)std::min((items + kShortWarps - 1) / kShortWarps, (long long)kSms);
+    const long long full = (items + kShortWarps - 1) / kShortWarps;
+    const unsigned ctas = (unsigned)std::min(full, (long long)kSms);
     return launch_kernel(route_grad_short_kernel, dim3(ctas), dim3(kShortThreads), 0, st, false,
                          topk_idx, topk_s, dtopk_w, a, c.k, c.route_scale, status);
   }

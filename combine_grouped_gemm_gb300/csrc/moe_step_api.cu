@@ -1,5 +1,5 @@
-// C ABI of the calls around the layer in a training step (declared in include/moe.h): the norms, the
-// router's gradient and the optimiser. Argument checks only; nothing here allocates or waits.
+// C ABI of the calls around the layer in a training step (declared in include/moe.h): the norms,
+// the router's gradient and the optimiser. Argument checks only; nothing here allocates or waits.
 #include <math.h>
 
 #include <algorithm>
