@@ -617,7 +617,8 @@ def norm_in_grad(dn, x, w, rstd, dres, dx, dw, ws, accumulate=False, stream=None
     st = _stream_type(fn, "x", x)
     _check(fn, _lib.moe_norm_in_grad(
         _norm_cfg(rows, d, st, 0.0, 1.0, 1.0, 0),
-        _need(fn, dev, "dn", dn, torch.bfloat16, rows, d), _need(fn, dev, "x", x, st, rows, d), _need(fn, dev, "w", w, f32, d),
+        _need(fn, dev, "dn", dn, torch.bfloat16, rows, d), _need(fn, dev, "x", x, st, rows, d),
+        _need(fn, dev, "w", w, f32, d),
         _need(fn, dev, "rstd", rstd, f32, rows), _opt(fn, dev, "dres", dres, st, rows, d),
         _need(fn, dev, "dx", dx, st, rows, d), _opt(fn, dev, "dw", dw, f32, d),
         1 if accumulate else 0, _norm_ws(fn, dev, rows, d, ws), _stream(stream, dev)))
@@ -713,15 +714,18 @@ class AdamTensors:
     """The tensors of an AdamW step, checked once and held: a list of dicts with p (fp32), g (fp32
     or bf16), w (bf16 copy of p, or None), m, v (fp32; 8 bits: bytes) and, with state_bits 8,
     m_scale and v_scale (fp32, one per 128 elements); optional weight_decay (0) and seed (the
-    tensor's place in the list). All contiguous, on one device. The plan keeps these very tensors:
-    another one put into a dict later is not seen."""
+    tensor's place in the list). All contiguous, on one device, and no two may overlap. The plan
+    keeps these very arrays: another one put into a dict or under a tensor (``t.data = ...``) later
+    is not seen."""
 
     def __init__(self, tensors, state_bits=32):
         fn, dev = "AdamTensors", _device()
         if state_bits not in (32, 8):
             raise ValueError(f"{fn}: state_bits must be 32 or 8")
         self.state_bits, self.device = state_bits, dev
-        self.tensors = [dict(t) for t in tensors]   # (references: the pointers stay valid)
+        # (references of its own to the memory: the pointers stay valid)
+        self.tensors = [{k: v.detach() if isinstance(v, torch.Tensor) else v for k, v in t.items()}
+                        for t in tensors]
         f32, n = torch.float32, len(self.tensors)
         self.array = (AdamTensorC * n)()
         for i, (t, c) in enumerate(zip(self.tensors, self.array)):
@@ -749,6 +753,11 @@ class AdamTensors:
         base = ctypes.addressof(self.array)
         self.parts = [(base + i * size, min(MOE_ADAM_TENSORS, n - i), i + MOE_ADAM_TENSORS < n)
                       for i in range(0, max(n, 1), MOE_ADAM_TENSORS)]
+        if len(self.parts) > 1:   # (each call of a step checks its own arrays)
+            spans = sorted((v.data_ptr(), v.data_ptr() + v.nbytes) for t in self.tensors
+                           for v in t.values() if isinstance(v, torch.Tensor) and v.numel())
+            if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
+                raise ValueError(f"{fn}: two of the arrays overlap")
 
 
 _adam_bytes = []

@@ -174,6 +174,11 @@ class MoETrainBlock:
     def __init__(self, cfg, w_gate, bias, weights: dict, w_in, w_out=None, gate=None, eps=1e-6,
                  res_scale=1.0, out_scale=1.0, stream_dtype=torch.bfloat16, device="cuda",
                  grad_dtype=torch.float32):
+        for name, w in (("w_in", w_in), ("w_out", w_out), ("gate", gate)):
+            if (name == "w_in" or w is not None) and (
+                    not isinstance(w, torch.Tensor) or w.dtype is not torch.float32
+                    or w.shape != (cfg.d,)):
+                raise ValueError(f"MoETrainBlock: {name} must be an fp32 tensor ({cfg.d},)")
         self.layer = MoETrainLayer(cfg, w_gate, bias, weights, device, grad_dtype,
                                    train_router=True)
         self.w_in, self.w_out, self.gate = w_in, w_out, gate
@@ -207,7 +212,7 @@ class MoETrainBlock:
                     or t.shape != self.shape):
                 raise ValueError(f"MoETrainBlock.forward: {name} must be a {self.stream_dtype} "
                                  f"tensor {self.shape}")
-        if h is x:
+        if h is not None and h.data_ptr() == x.data_ptr():
             raise ValueError("MoETrainBlock.forward: x is kept for backward: h must be another")
         self._x = None
         if h is None:

@@ -275,3 +275,17 @@ def test_binding_refuses_other_tensors(moe):
     assert moe.adam_step(s) == 7
     c1, c2 = s[16:32].view(torch.float64)
     assert float(c1) == 1 - 0.9 ** 7 and float(c2) == 1 - 0.99 ** 7
+
+
+def test_train_block_checks_its_weights():
+    import dataclasses
+
+    import synth
+    from combine_grouped_gemm_gb300.train import MoETrainBlock
+    cfg = dataclasses.replace(synth.CONFIGS["tiny"], R=1)
+    good = torch.ones(cfg.d)
+    for name, w in (("w_in", None), ("w_in", good.bfloat16()), ("w_out", torch.ones(cfg.d + 1)),
+                    ("gate", torch.ones(cfg.T, 1)), ("gate", 0.5)):
+        kw = {"w_in": good, "w_out": good, "gate": good, name: w}
+        with pytest.raises(ValueError, match=name):
+            MoETrainBlock(cfg, None, None, {}, kw["w_in"], kw["w_out"], kw["gate"])
