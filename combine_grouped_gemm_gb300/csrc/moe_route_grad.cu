@@ -357,8 +357,13 @@ __device__ __forceinline__ void dx_item(const Args& a, int t, int v) {
   a.dx[at] = bf16_of8(acc);
 }
 
+// 32 choices of a warp's segment.
+struct Staged {
+  int4 token[8];
+  float4 dz[8];
+};
 template <int kAtOnce>   // rows of x in flight
-__device__ __forceinline__ void dw_item(const Args& a, int segment, int v) {
+__device__ __forceinline__ void dw_item(const Args& a, Staged& staged, int segment, int v) {
   int lo = 0, hi = a.E - 1;   // the expert: the last whose first segment is at or before this one
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -373,25 +378,39 @@ __device__ __forceinline__ void dw_item(const Args& a, int segment, int v) {
   const int lane = threadIdx.x & 31;
   const uint4* x = a.x + min(v, vecs - 1);
   f32x2 acc[4] = {};
-  // A lane holds one of 32 choices, the next 32 on their way.
+  // 32 choices at a time go through shared memory, the next 32 on their way.
   const auto fetch = [&](int i) { return i < to ? a.list[i] : Entry{0, 0.0f}; };
+  const int* tokens = reinterpret_cast<const int*>(staged.token);
+  const float* dzs = reinterpret_cast<const float*>(staged.dz);
   Entry next = fetch(from + lane);
   for (int i = from; i < to; i += 32) {
-    const Entry q = next;
+    __syncwarp();
+    reinterpret_cast<int*>(staged.token)[lane] = next.token;
+    reinterpret_cast<float*>(staged.dz)[lane] = next.dz;
+    __syncwarp();
     next = fetch(i + 32 + lane);
     const int n = min(32, to - i);
     int j = 0;
     for (; j + kAtOnce <= n; j += kAtOnce) {
       uint4 u[kAtOnce];
 #pragma unroll
-      for (int c = 0; c < kAtOnce; ++c)
-        u[c] = x[(size_t)__shfl_sync(0xffffffffu, q.token, j + c) * vecs];
+      for (int c = 0; c < kAtOnce; c += 4) {
+        const int4 t = staged.token[(j + c) / 4];
+        u[c] = x[(size_t)t.x * vecs];
+        u[c + 1] = x[(size_t)t.y * vecs];
+        u[c + 2] = x[(size_t)t.z * vecs];
+        u[c + 3] = x[(size_t)t.w * vecs];
+      }
 #pragma unroll
-      for (int c = 0; c < kAtOnce; ++c) add8(acc, __shfl_sync(0xffffffffu, q.dz, j + c), u[c]);
+      for (int c = 0; c < kAtOnce; c += 4) {
+        const float4 z = staged.dz[(j + c) / 4];
+        add8(acc, z.x, u[c]);
+        add8(acc, z.y, u[c + 1]);
+        add8(acc, z.z, u[c + 2]);
+        add8(acc, z.w, u[c + 3]);
+      }
     }
-    for (; j < n; ++j)
-      add8(acc, __shfl_sync(0xffffffffu, q.dz, j),
-           x[(size_t)__shfl_sync(0xffffffffu, q.token, j) * vecs]);
+    for (; j < n; ++j) add8(acc, dzs[j], x[(size_t)tokens[j] * vecs]);
   }
   if (v >= vecs) return;
   if (a.segments[lo + 1] - s0 == 1)
@@ -487,12 +506,14 @@ __device__ __forceinline__ void dx_slabs(const Args& a, char* slab) {
 // there is no slab, keep more loads in flight.
 constexpr int product_threads(int C) { return C ? 1024 : 256; }
 constexpr int product_ctas(int C) { return C ? 1 : 5; }   // an SM
+constexpr int staged_bytes(int C) { return product_threads(C) / 32 * (int)sizeof(Staged); }
 template <int C>
 __global__ void __launch_bounds__(product_threads(C), product_ctas(C))
     route_grad_products_kernel(const Args a) {
-  extern __shared__ __align__(16) char slab[];
+  extern __shared__ __align__(16) char raw[];
+  Staged* staged = reinterpret_cast<Staged*>(raw);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (C > 0 && warp < kDxThreads / 32) dx_slabs<C ? C : 128>(a, slab);
+  if (C > 0 && warp < kDxThreads / 32) dx_slabs<C ? C : 128>(a, raw + staged_bytes(C));
   pdl_wait();
   const int blocks = (a.d / 8 + 31) / 32, segments = a.segments[a.E];
   const long long dx_items = C > 0 ? 0 : (long long)a.T * blocks;
@@ -513,7 +534,7 @@ __global__ void __launch_bounds__(product_threads(C), product_ctas(C))
       dx_item(a, t, (item - t * blocks) * 32 + lane);
     } else {
       const int i = static_cast<int>(item - dx_items), block = i / segments;
-      dw_item<C ? 8 : 4>(a, i - block * segments, block * 32 + lane);
+      dw_item<C ? 8 : 4>(a, staged[warp], i - block * segments, block * 32 + lane);
     }
     item = next;
   }
@@ -522,7 +543,7 @@ __global__ void __launch_bounds__(product_threads(C), product_ctas(C))
 // ------------------------------------------------------------------------------------------
 // 4. Experts with several segments, or none: their sums, in order.
 // ------------------------------------------------------------------------------------------
-constexpr int kJoinThreads = 128;
+constexpr int kJoinThreads = 256;
 __global__ void __launch_bounds__(kJoinThreads) route_grad_join_kernel(
     const float4* __restrict__ partial, const int32_t* __restrict__ segments,
     float4* __restrict__ dw_gate, int quads, bool accumulate) {
@@ -532,7 +553,7 @@ __global__ void __launch_bounds__(kJoinThreads) route_grad_join_kernel(
   if (s1 - s0 == 1 || v >= quads || (s0 == s1 && accumulate)) return;
   float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   const auto add = [&](const float4& p) { s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w; };
-  constexpr int kAtOnce = 16;   // (an expert that every token chose has a hundred segments)
+  constexpr int kAtOnce = 8;   // (an expert that every token chose has a hundred segments)
   for (int i = s0; i < s1; i += kAtOnce) {
     float4 p[kAtOnce];
 #pragma unroll
@@ -629,7 +650,7 @@ __global__ void __launch_bounds__(kShortThreads) route_grad_short_kernel(
 template <int C>
 cudaError_t run_products(Args a, cudaStream_t st) {
   auto kern = route_grad_products_kernel<C>;
-  const size_t smem = C ? (size_t)(a.E + 1) * C * 4 : 0;
+  const size_t smem = staged_bytes(C) + (size_t)(a.E + 1) * C * 4;
   const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
   if (C > 0) a.per_cta = ((long long)(a.d / std::max(C, 1)) * a.T + kSms - 1) / kSms;
@@ -684,7 +705,7 @@ cudaError_t launch_route_grad(const moe_cfg& c, const void* x, const float* w_ga
                     static_cast<const Pick*>(picks), static_cast<const int32_t*>(counts), c.T, L.kp,
                     c.E, L.chunk, L.chunks, L.segment, starts, segments, list);
   if (e != cudaSuccess) return e;
-  const size_t row = 4 * (size_t)(c.E + 1), most = 227 * 1024;
+  const size_t row = 4 * (size_t)(c.E + 1), most = 227 * 1024 - staged_bytes(32);
   e = !L.slab            ? run_products<0>(a, st)
       : row * 128 <= most ? run_products<128>(a, st)
       : row * 64 <= most  ? run_products<64>(a, st)
