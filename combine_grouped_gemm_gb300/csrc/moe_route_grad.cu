@@ -11,17 +11,16 @@
 //
 // 1. Counts: a CTA per chunk of tokens computes dz and counts the chunk's choices of each expert.
 // 2. Lists: the choices expert by expert, in the order of the tokens, cut into segments.
-// 3. Products: the tokens' dx from the gate weights (long batches: from a slab of columns of them
-// in
+// 3. Products: the tokens' dx from the gate weights (long batches: from a slab of their columns in
 //    shared memory), the segments' sums of x from L2, at the same time.
 // 4. The segments' sums are joined in order: the result does not depend on the order of work.
 // A short batch takes one launch for all of it.
 //
-// Measured, d = 7168, 256 experts, 8 choices: 16384 tokens 281 us, 2048 tokens 56 (count 4, lists
-// 6, products 46, join 2), 64 tokens 8.6. The 16384 tokens' operands are 5.6 GB on their way
-// through the SMs' shared memory and L1, 155 us at 128 bytes a clock and SM, of which L2 hands out
-// the segments' rows at some 8 TB/s. (Tokens and gate weights one after the other, the latter
-// summed chunk by chunk in shared memory: 370 us; first form 3431.)
+// Measured, d = 7168, 256 experts, 8 choices: 16384 tokens 263 us, 2048 tokens 52 (count 4, lists 3,
+// products 43, join 2), 64 tokens 8.6. The 16384 tokens' operands are 5.6 GB on their way through
+// the SMs' shared memory and L1, 155 us at 128 bytes a clock and SM, of which L2 hands out the
+// segments' rows at some 8 TB/s. (Tokens and gate weights one after the other, the latter summed
+// chunk by chunk in shared memory: 370 us; first form 3431.)
 #include <algorithm>
 
 #include "moe_device.cuh"
@@ -235,15 +234,24 @@ __global__ void __launch_bounds__(kListThreads) route_grad_list_kernel(
   // Thread i: experts 2i, 2i + 1
   int total[2] = {0, 0}, ahead[2] = {0, 0};
   const int e0 = threadIdx.x * 2;
-  if (e0 < E)
-#pragma unroll 8
-    for (int c = 0; c < chunks; ++c)
+  if (e0 < E) {
+    constexpr int kAtOnce = 16;   // chunks (2048 tokens: 55 -> 52 us; 8 at once as a plain loop)
+    for (int c0 = 0; c0 < chunks; c0 += kAtOnce) {
+      int n[kAtOnce][2];
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int n = e0 + q < E ? counts[(size_t)c * E + e0 + q] : 0;
-        total[q] += n;
-        ahead[q] += c < (int)blockIdx.x ? n : 0;
-      }
+      for (int c = 0; c < kAtOnce; ++c)
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          n[c][q] = c0 + c < chunks && e0 + q < E ? counts[(size_t)(c0 + c) * E + e0 + q] : 0;
+#pragma unroll
+      for (int c = 0; c < kAtOnce; ++c)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          total[q] += n[c][q];
+          ahead[q] += c0 + c < (int)blockIdx.x ? n[c][q] : 0;
+        }
+    }
+  }
 #pragma unroll
   for (int i = 0; i < kOwn; ++i) {
     const int t = (threadIdx.x + i * kListThreads) / kp;
