@@ -192,8 +192,8 @@ __device__ __forceinline__ void fetch8(char* to, const char* row, unsigned v, un
 }
 
 // Most threads of a CTA that takes VPT vectors a thread, and the CTAs of that size an SM holds.
-constexpr int most_threads(int vpt) { return vpt == 1 ? 256 : 512; }
-constexpr int most_ctas(int vpt) { return vpt == 1 ? 3 : 1; }
+constexpr int most_threads(int vpt) { return vpt == 1 ? 128 : 512; }
+constexpr int most_ctas(int vpt) { return vpt == 1 ? 6 : 1; }
 
 template <bool F32, int VPT, int STAGES>
 __global__ void __launch_bounds__(most_threads(VPT), most_ctas(VPT))
@@ -496,15 +496,16 @@ __global__ void __launch_bounds__(kColThreads) norm_columns_kernel(ColSums a) {
 
 // Vectors a thread, threads of a CTA and the CTAs that an SM takes at once. Two vectors where they
 // fit a CTA of 512 threads, whose registers then hold weights and sums of 16 columns each: 16384
-// rows of 7168 forward 144 us, with one vector and 896 threads 195. Up to 2048 columns one vector,
-// so that several CTAs of 64 to 256 threads share an SM; above 8192 four.
+// rows of 7168 forward 144 us, with one vector and 896 threads 195; gradient of 32768 rows of 1504
+// 108 us, with one 130. Up to 1024 columns one vector: 65536 rows of 520 forward 66 us, gradient
+// 126, with two 73 and 132. Above 8192 columns four, whose sums leave no registers for the weights.
 struct Plan {
   int vpt, threads, per_sm;
 };
 Plan plan_of(int d) {
   const int vecs = d / 8;
   Plan p;
-  p.vpt = vecs <= 256 ? 1 : vecs <= 1024 ? 2 : 4;
+  p.vpt = vecs <= 128 ? 1 : vecs <= 1024 ? 2 : 4;
   p.threads = ((vecs + p.vpt - 1) / p.vpt + 31) / 32 * 32;
   p.per_sm = most_threads(p.vpt) * most_ctas(p.vpt) / p.threads;
   return p;
