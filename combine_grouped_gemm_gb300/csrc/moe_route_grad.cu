@@ -77,11 +77,15 @@ Layout layout(const moe_cfg& c) {
   L.chunk = std::min({std::max((c.T + 63) / 64, 64), kMostList / c.k, kMostChunk}) / 8 * 8;
   L.chunks = (int)(((long long)c.T + L.chunk - 1) / L.chunk);
   L.kp = (c.k + 1) / 2 * 2;
-  // a segment: the work of the SMs' warps some eight times over, in powers of two from 128 to 1024
-  // (2048 tokens of 8 choices, 256 experts, 7168 columns: 59 us in segments of 128, 64 of 32; 16384
-  // tokens: 280 in segments of 128, 297 of 256)
-  const double per = (double)tk * ((c.d + 255) / 256) / (8.0 * kSms * 32);
-  for (L.segment = 128; L.segment < 1024 && L.segment < per;) L.segment *= 2;
+  // a segment: a power of two from 32 to 128 that leaves each of the products' warps one to work on
+  // (1500 tokens of 8 choices, 16 experts, 256 columns: 22 us, with segments of 128 30; 2048 tokens,
+  // 256 experts, 7168 columns: 59 us in segments of 128, 64 of 32, which have to be joined); above, up
+  // to 1024, the work of the SMs' warps some eight times over (16384 tokens of those: 280 us in
+  // segments of 128, 297 of 256)
+  const double work = (double)tk * ((c.d + 255) / 256), warps = kSms * 16;
+  L.segment = 32;
+  while (L.segment < 128 && work / (2 * L.segment) >= warps) L.segment *= 2;
+  while (L.segment >= 128 && L.segment < 1024 && work / L.segment > 16 * warps) L.segment *= 2;
   L.one_launch = tk <= 1024;
   // (512 tokens: 36.5 us with slabs, 39 without; 256: 32.4 and 30.4)
   L.slab = c.T >= 512;
@@ -549,28 +553,43 @@ __global__ void __launch_bounds__(product_threads(C), product_ctas(C))
 }
 
 // ------------------------------------------------------------------------------------------
-// 4. Experts with several segments, or none: their sums, in order.
+// 4. Experts with several segments, or none: their sums, in order, eight segments at once, since an
+// expert that every token chose has hundreds. PARTS of a CTA's threads take every PARTS-th segment:
+// 4 while all CTAs run at the same time (16384 tokens of 4 unequal choices, 32 experts, 1024 columns:
+// 49 us, with one part 59), else 1 (256 experts, 7168 columns: 263 us, with 4 parts 270, since most of
+// the 7168 CTAs have one segment and nothing to do).
 // ------------------------------------------------------------------------------------------
 constexpr int kJoinThreads = 256;
+template <int PARTS>
 __global__ void __launch_bounds__(kJoinThreads) route_grad_join_kernel(
     const float4* __restrict__ partial, const int32_t* __restrict__ segments,
     float4* __restrict__ dw_gate, int quads, bool accumulate) {
-  const int e = blockIdx.y, v = blockIdx.x * kJoinThreads + threadIdx.x;
+  constexpr int kQuads = kJoinThreads / PARTS;
+  __shared__ float4 sums[PARTS][kQuads];
+  const int e = blockIdx.y, column = threadIdx.x % kQuads, part = threadIdx.x / kQuads;
+  const int v = blockIdx.x * kQuads + column;
   pdl_wait();
   const int s0 = segments[e], s1 = segments[e + 1];
-  if (s1 - s0 == 1 || v >= quads || (s0 == s1 && accumulate)) return;
+  if (s1 - s0 == 1 || (s0 == s1 && accumulate)) return;   // whole CTAs
   float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   const auto add = [&](const float4& p) { s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w; };
-  constexpr int kAtOnce = 8;   // (an expert that every token chose has a hundred segments)
-  for (int i = s0; i < s1; i += kAtOnce) {
+  constexpr int kAtOnce = 8;
+  for (int i = s0 + part; v < quads && i < s1; i += kAtOnce * PARTS) {
     float4 p[kAtOnce];
 #pragma unroll
     for (int j = 0; j < kAtOnce; ++j)
-      if (i + j < s1) p[j] = partial[(size_t)(i + j) * quads + v];
+      if (i + j * PARTS < s1) p[j] = partial[(size_t)(i + j * PARTS) * quads + v];
 #pragma unroll
     for (int j = 0; j < kAtOnce; ++j)
-      if (i + j < s1) add(p[j]);
+      if (i + j * PARTS < s1) add(p[j]);
   }
+  if (PARTS > 1) {
+    sums[part][column] = s;
+    __syncthreads();
+  }
+  if (part > 0 || v >= quads) return;
+#pragma unroll
+  for (int i = 1; i < PARTS; ++i) add(sums[i][column]);
   float4* o = dw_gate + (size_t)e * quads + v;
   if (accumulate) add(*o);
   *o = s;
@@ -632,7 +651,7 @@ __global__ void __launch_bounds__(kShortThreads) route_grad_short_kernel(
     const auto flush = [&]() {
       __syncwarp();
       if (v < vecs)
-#pragma unroll 4
+#pragma unroll 8
         for (int q = 0; q < n; ++q) {
           const int c = found[warp][q];
           add8(acc, dz[c], a.x[(size_t)(c / kp) * vecs + v]);
@@ -720,11 +739,16 @@ cudaError_t launch_route_grad(const moe_cfg& c, const void* x, const float* w_ga
                           : run_products<32>(a, st);
   if (e != cudaSuccess) return e;
   const int quads = c.d / 4;
-  return launch_kernel(route_grad_join_kernel,
-                       dim3((quads + kJoinThreads - 1) / kJoinThreads, c.E), dim3(kJoinThreads), 0,
-                       st, true, reinterpret_cast<const float4*>(a.partial),
-                       static_cast<const int32_t*>(segments), reinterpret_cast<float4*>(dw_gate),
-                       quads, accumulate);
+  const auto join = [&](auto kern, int parts) {
+    const int columns = kJoinThreads / parts;
+    return launch_kernel(kern, dim3((quads + columns - 1) / columns, c.E), dim3(kJoinThreads), 0, st,
+                         true, reinterpret_cast<const float4*>(a.partial),
+                         static_cast<const int32_t*>(segments), reinterpret_cast<float4*>(dw_gate),
+                         quads, accumulate);
+  };
+  return (long long)c.E * quads * 4 <= 8ll * kSms * kJoinThreads
+             ? join(route_grad_join_kernel<4>, 4)
+             : join(route_grad_join_kernel<1>, 1);
 }
 
 }  // namespace moe
