@@ -7,7 +7,7 @@ import torch
 
 from test_block_gpu import setup
 from test_step_gpu import (ADAM_SIZES, BF, F32, adam_tensors, check_route, copy_of, normal,
-                           route_cfg, route_inputs)
+                           route_cfg, route_inputs, route_reference)
 
 pytestmark = pytest.mark.gpu
 
@@ -197,3 +197,134 @@ def test_norms_captured_beside_other_sizes(moe, gate, st):
         run(b)
         for n in a:
             assert torch.equal(a[n], b[n]), n
+
+
+@pytest.mark.parametrize("before", ["nothing", "fill", "copy", "join", "fork"])
+def test_adamw_captured_behind_other_work(moe, before):
+    """The step with a norm captured where the norm's kernel is not the node before it: first of the
+    graph, behind a fill or a copy, behind two streams that meet, and on a stream of its own."""
+    A = adam_tensors([70_000, 33], 32, [F32], seed=1)
+    B = copy_of(A)
+    cfg = moe.AdamCfg(lr=1e-3, beta1=0.9, beta2=0.99, eps=1e-8, max_norm=0.05)
+    pa, sa = moe.AdamTensors(A), moe.adam_state(0, 0.9, 0.99)
+    pb, sb = moe.AdamTensors(B), moe.adam_state(0, 0.9, 0.99)
+    norm, other = torch.full((1,), 0.5, device="cuda"), torch.zeros(1 << 22, device="cuda")
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        if before == "nothing":
+            moe.adamw(cfg, pa, sa, norm)
+        elif before in ("fill", "copy"):
+            if before == "fill":
+                other.zero_()
+            A[0]["g"].copy_(B[0]["g"])
+            moe.adamw(cfg, pa, sa, norm)
+        else:
+            side.wait_stream(main)
+            with torch.cuda.stream(side):
+                A[0]["g"].copy_(B[0]["g"])
+                other.add_(1.0)
+                if before == "fork":
+                    moe.adamw(cfg, pa, sa, norm)
+            if before == "join":
+                norm.add_(0.0)
+                main.wait_stream(side)
+                moe.adamw(cfg, pa, sa, norm)
+            else:
+                main.wait_stream(side)
+    for step in range(3):
+        B[0]["g"].copy_(normal(step, 70_000, std=1e-3, dtype=F32))
+        if before == "nothing":
+            A[0]["g"].copy_(B[0]["g"])
+        graph.replay()
+        moe.adamw(cfg, pb, sb, norm)
+        for a, b in zip(A, B):
+            for n in ("p", "m", "v"):
+                assert torch.equal(a[n], b[n]), (step, n)
+    assert moe.adam_step(sa) == 3
+
+
+def test_norms_past_2_31_elements(moe):
+    """Rows whose offsets do not fit 31 bits of elements, nor 32 of bytes: the first and last rows are
+    what calls of these rows alone give, the weights' gradients those of a sum over parts."""
+    rows, d, part = 270_000, 8192, 3000
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    one = torch.randn((part, d), generator=g, device="cuda").to(BF)
+    x, dn = one.repeat(rows // part, 1), one.flip(0).repeat(rows // part, 1)
+    w = normal(4, d, std=0.2, mean=1.0, dtype=F32)
+    n, r = torch.empty_like(x), torch.empty(rows, device="cuda")
+    moe.norm_in(x, w, n, r)
+    n1, r1 = torch.empty_like(one), torch.empty(part, device="cuda")
+    moe.norm_in(one, w, n1, r1)
+    for k in (0, rows // part // 2, rows // part - 1):
+        assert torch.equal(n[k * part:(k + 1) * part], n1)
+        assert torch.equal(r[k * part:(k + 1) * part], r1)
+    dw, ws = torch.empty_like(w), torch.empty(moe.norm_ws_bytes(rows, d), dtype=torch.uint8,
+                                              device="cuda")
+    moe.norm_in_grad(dn, x, w, r, x, n, dw, ws)
+    dx1, dw1 = torch.empty_like(one), torch.empty_like(w)
+    moe.norm_in_grad(dn[:part], one, w, r1, one, dx1, dw1, ws)
+    for k in (0, rows // part // 2, rows // part - 1):
+        assert torch.equal(n[k * part:(k + 1) * part], dx1)
+    xh = one.double() * r1.double()[:, None]
+    ref, mag = (one.flip(0).double() * xh).sum(0), (one.flip(0).double() * xh).abs().sum(0)
+    # each of 152 CTAs' 1800 rows in fp32, then 152 sums
+    assert bool(((dw.double() - ref * (rows // part)).abs()
+                 <= 2000 * 2.0 ** -24 * mag * (rows // part)).all())
+
+
+def test_route_grad_past_2_31_elements(moe):
+    T, d, E, k = 300_032, 7168, 16, 2
+    q = route_inputs(T, 128, E, k, 0.5, seed=3)
+    part = normal(5, 1024, d)
+    x = part.repeat(T // 1024, 1)
+    w = normal(6, E, d, std=0.05, dtype=F32)
+    c = route_cfg(moe, T, d, E, k)
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    moe.route_grad(c, x, w, q["idx"], q["s"], q["dw"], x, dx, dw, route_ws(moe, c))
+    for t0 in (0, T // 2, T - 1000):
+        few = slice(t0, t0 + 1000)
+        cf = route_cfg(moe, 1000, d, E, k)
+        dxf, dwf = torch.empty_like(x[few]), torch.empty_like(w)
+        moe.route_grad(cf, x[few], w, q["idx"][few], q["s"][few], q["dw"][few], x[few], dxf, dwf,
+                       route_ws(moe, cf))
+        assert torch.equal(dx[few], dxf)
+    Z, M = route_reference(q, 2.5, E)
+    X = part.double()
+    folded = Z.view(-1, 1024, E).sum(0), M.view(-1, 1024, E).sum(0)
+    ref, mag = folded[0].t() @ X, folded[1].t() @ X.abs()
+    # segments of at most 1024 choices in fp32, then at most 600 of them, and dz's own k + 9 roundings
+    assert bool(((dw.double() - ref).abs() <= 1700 * 2.0 ** -24 * mag + 1e-30).all())
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_past_2_31_elements(moe, bits):
+    """A tensor of more than 2^31 elements: its ends are what a step over them alone gives (in 8 bits
+    the random numbers go by the block, so there only the first end has the same)."""
+    n, end = 2 ** 31 + 128 * 1000 + 5, 128 * 1000 + 5
+    big = adam_tensors([end], bits, [BF], seed=4, copies=False)[0]
+
+    def repeated(t):   # the tensor's last `end` elements, and its first ones, are t's
+        out = torch.zeros(n * t.numel() // end if t.numel() == end else (n + 127) // 128,
+                          dtype=t.dtype, device="cuda")
+        out[:t.numel()] = t
+        out[-t.numel():] = t
+        return out
+    long = {k: repeated(v) if isinstance(v, torch.Tensor) else v for k, v in big.items()}
+    cfg = moe.AdamCfg(lr=1e-3, beta1=0.9, beta2=0.99, eps=1e-8, max_norm=1e9)
+    pa, sa = moe.AdamTensors([long], state_bits=bits), moe.adam_state(0, 0.9, 0.99)
+    pb, sb = moe.AdamTensors([big], state_bits=bits), moe.adam_state(0, 0.9, 0.99)
+    norm = torch.zeros(1, device="cuda")
+    moe.grad_norm(pa, sa, norm)
+    exact = math.sqrt(2 * float(big["g"].double().square().sum()))
+    assert abs(float(norm) - exact) <= 4 * 2.0 ** -24 * exact
+    moe.adamw(cfg, pa, sa, norm)
+    moe.adamw(cfg, pb, sb, norm)
+    for k in ("p", "m", "v") + (("m_scale", "v_scale") if bits == 8 else ()):
+        a, b = long[k], big[k]
+        assert torch.equal(a[:b.numel()], b), k
+        if bits == 32 or k not in ("m", "v"):
+            assert torch.equal(a[-b.numel():], b), k
+        assert bool((a[b.numel() + 128:b.numel() + 10 ** 6] == (1.0 if "scale" in k else 0)).all())
