@@ -16,7 +16,7 @@
 // 4. The segments' sums are joined in order: the result does not depend on the order of work.
 // A short batch takes one launch for all of it.
 //
-// Measured, d = 7168, 256 experts, 8 choices: 16384 tokens 263 us, 2048 tokens 52 (count 4, lists 3,
+// Measured, d = 7168, 256 experts, 8 choices: 16384 tokens 260 us, 2048 tokens 52 (count 4, lists 3,
 // products 43, join 2), 64 tokens 8.6. The 16384 tokens' operands are 5.6 GB on their way through
 // the SMs' shared memory and L1, 155 us at 128 bytes a clock and SM, of which L2 hands out the
 // segments' rows at some 8 TB/s. (Tokens and gate weights one after the other, the latter summed
@@ -64,7 +64,7 @@ struct Layout {   // the status word comes first
   size_t total;
   int chunk, chunks, kp;   // tokens of a chunk, chunks, choices of a token rounded up to even
   int segment;             // choices of a segment
-  bool one_launch, slab;
+  bool one_launch;
 };
 
 Layout layout(const moe_cfg& c) {
@@ -87,8 +87,6 @@ Layout layout(const moe_cfg& c) {
   while (L.segment < 128 && work / (2 * L.segment) >= warps) L.segment *= 2;
   while (L.segment >= 128 && L.segment < 1024 && work / L.segment > 16 * warps) L.segment *= 2;
   L.one_launch = tk <= 1024;
-  // (512 tokens: 36.5 us with slabs, 39 without; 256: 32.4 and 30.4)
-  L.slab = c.T >= 512;
   size_t o = 256;
   L.queue = o;     o = up(o + sizeof(int32_t));
   if (!L.one_launch) {
@@ -291,8 +289,9 @@ __global__ void __launch_bounds__(kListThreads) route_grad_list_kernel(
 }
 
 // ------------------------------------------------------------------------------------------
-// 3. The products. Work is handed out from a queue, a warp an item: 256 columns of a token's dx or
-// of a segment's sum (column blocks one after another: a block of x stays in L2 while it is used).
+// 3. The products. A warp takes an item at a time: 256 columns of a token's dx or of a segment's sum;
+// the segments from a queue (column blocks one after another: a block of x stays in L2 while it is
+// used).
 // ------------------------------------------------------------------------------------------
 __device__ __forceinline__ void add8(f32x2 (&acc)[4], float z, const uint4& u) {
   const f32x2 z2 = both(z);
@@ -442,10 +441,9 @@ __device__ __forceinline__ void dx_barrier() {
 }
 template <int C>
 __device__ __forceinline__ void dx_slabs(const Args& a, char* slab) {
-  // a row: the lanes' columns 0-3 one after another, then their columns 4-7, 8-11, 12-15. Fewer than 128
-  // columns leave 2 or 4 of these quarters in one line of the 32 banks: their order in it differs
-  // from expert to expert, so that the tokens of a warp meet less (16384 tokens, 1024 experts:
-  // 606 -> 438 us, 512 experts: 368 -> 323)
+  // a row: the lanes' columns 0-3 one after another, then their columns 4-7, 8-11, 12-15. With 64
+  // columns two of these quarters share a line of the 32 banks: their order in it differs from expert
+  // to expert, so that the tokens of a warp meet less (512 experts, 16384 tokens: 368 -> 323 us)
   constexpr int kLanes = C / 16, kAtOnce = kDxThreads / kLanes, kRow = C * 4, kQuarter = C;
   constexpr int kTurn = 128 / C - 1;
   const long long work = (long long)(a.d / C) * a.T;
@@ -514,8 +512,9 @@ __device__ __forceinline__ void dx_slabs(const Args& a, char* slab) {
   }
 }
 
-// C: columns of a slab; 0: the tokens' items come first in the queue, and five CTAs an SM, since
-// there is no slab, keep more loads in flight.
+// C: columns of a slab; 0: all warps first take tokens, an equal number each (from the queue they would
+// wait for its atomics, a nanosecond an item), and five CTAs an SM, since there is no slab, keep more
+// loads in flight.
 constexpr int product_threads(int C) { return C ? 1024 : 256; }
 constexpr int product_ctas(int C) { return C ? 1 : 5; }   // an SM
 constexpr int staged_bytes(int C) { return product_threads(C) / 32 * (int)sizeof(Staged); }
@@ -528,26 +527,26 @@ __global__ void __launch_bounds__(product_threads(C), product_ctas(C))
   if (C > 0 && warp < kDxThreads / 32) dx_slabs<C ? C : 128>(a, raw + staged_bytes(C));
   pdl_wait();
   const int blocks = (a.d / 8 + 31) / 32, segments = a.segments[a.E];
-  const long long dx_items = C > 0 ? 0 : (long long)a.T * blocks;
-  const long long items = dx_items + (long long)segments * blocks;
-  // the warps that begin with items have their first ones by number, the queue those after
+  const long long items = (long long)segments * blocks;
+  // the warps that begin with segments have their first ones by number, the queue those after
   constexpr int kFirst = C > 0 ? kDxThreads / 32 : 0;
   const int beginners = product_threads(C) / 32 - kFirst, known = gridDim.x * beginners;
   const auto take = [&]() {
     int i = 0;
-    if (lane == 0) i = atomicAdd(a.queue, 1);
+    if (lane == 0 && items > known) i = atomicAdd(a.queue, 1);
     return known + __shfl_sync(0xffffffffu, i, 0);
   };
   int item = warp >= kFirst ? blockIdx.x * beginners + warp - kFirst : take();
-  while (item < items) {
-    const int next = take();
-    if (item < dx_items) {
-      const int t = item / blocks;
-      dx_item(a, t, (item - t * blocks) * 32 + lane);
-    } else {
-      const int i = static_cast<int>(item - dx_items), block = i / segments;
-      dw_item<C ? 8 : 4>(a, staged[warp], i - block * segments, block * 32 + lane);
+  if (C == 0) {
+    const long long dx_items = (long long)a.T * blocks;
+    for (long long i = item; i < dx_items; i += known) {
+      const int t = static_cast<int>(i / blocks);
+      dx_item(a, t, static_cast<int>(i - (long long)t * blocks) * 32 + lane);
     }
+  }
+  while (item < items) {
+    const int next = take(), block = item / segments;
+    dw_item<C ? 8 : 4>(a, staged[warp], item - block * segments, block * 32 + lane);
     item = next;
   }
 }
@@ -732,11 +731,15 @@ cudaError_t launch_route_grad(const moe_cfg& c, const void* x, const float* w_ga
                     static_cast<const Pick*>(picks), static_cast<const int32_t*>(counts), c.T, L.kp,
                     c.E, L.chunk, L.chunks, L.segment, starts, segments, list);
   if (e != cudaSuccess) return e;
-  const size_t row = 4 * (size_t)(c.E + 1), most = 227 * 1024 - staged_bytes(32);
-  e = !L.slab            ? run_products<0>(a, st)
+  // Slabs of 128 columns up to 437 experts, of 64 up to 875, where the tokens are many: 256 experts, 8
+  // choices, 7168 columns, with and without: 16384 tokens 259 and 388 us, 1024 tokens 41 and 45, 512
+  // tokens 33 and 32; 800 experts: 16384 tokens 354 and 407, 2048 tokens 78 both. (With more experts
+  // slabs of 32 columns, whose rows share banks, were slower: 1024 experts, 16384 tokens 427 and 406.)
+  const size_t row = 4 * (size_t)(c.E + 1), most = 227 * 1024 - staged_bytes(128);
+  e = c.T < 1024          ? run_products<0>(a, st)
       : row * 128 <= most ? run_products<128>(a, st)
       : row * 64 <= most  ? run_products<64>(a, st)
-                          : run_products<32>(a, st);
+                          : run_products<0>(a, st);
   if (e != cudaSuccess) return e;
   const int quads = c.d / 4;
   const auto join = [&](auto kern, int parts) {
