@@ -41,6 +41,7 @@ __device__ __forceinline__ void copy16(void* smem, const void* gmem) {
 // ------------------------------------------------------------------------------------------
 constexpr int kMostChunk = 320;      // tokens of a chunk
 constexpr int kMostList = 2560;      // choices of a chunk
+constexpr int kShortChoices = 512;   // of a batch that takes one launch, at most
 
 // A choice of a token: its expert (E: none, with dz 0), and dz. Tokens have an even number of them.
 struct Pick {
@@ -86,7 +87,7 @@ Layout layout(const moe_cfg& c) {
   L.segment = 32;
   while (L.segment < 128 && work / (2 * L.segment) >= warps) L.segment *= 2;
   while (L.segment >= 128 && L.segment < 1024 && work / L.segment > 16 * warps) L.segment *= 2;
-  L.one_launch = tk <= 1024;
+  L.one_launch = tk <= kShortChoices;
   size_t o = 256;
   L.queue = o;     o = up(o + sizeof(int32_t));
   if (!L.one_launch) {
@@ -595,14 +596,13 @@ __global__ void __launch_bounds__(kJoinThreads) route_grad_join_kernel(
 }
 
 // ------------------------------------------------------------------------------------------
-// A short batch, of 1024 choices at most: every CTA works out all choices' dz for itself, then its
+// A short batch, of 512 choices at most: every CTA works out all choices' dz for itself, then its
 // warps take items: 256 columns of a token's dx, or of an expert's dw_gate, whose choices are found
-// by looking through all of them. (64 tokens of 8 choices: 15 us with the call's cold start, 128:
-// 22 and 28 through the lists; 160 tokens take 27 through the lists, and the search grows with the
-// tokens.)
+// by looking through all of them. (7168 columns, 256 experts, 8 choices, from cold caches: 64 tokens 15
+// us, and 23 through the lists, 25 and 22 with choices as uneven as 1/rank^1.2, since a warp adds up
+// all of an expert's; 128 tokens 21 and 25, uneven 40 and 23.)
 // ------------------------------------------------------------------------------------------
 constexpr int kShortThreads = 1024, kShortWarps = kShortThreads / 32;
-constexpr int kShortChoices = 1024;
 __global__ void __launch_bounds__(kShortThreads) route_grad_short_kernel(
     const int32_t* __restrict__ idx, const float* __restrict__ score, const float* __restrict__ dw,
     const Args a, int k, float scale, uint32_t* status) {

@@ -22,12 +22,13 @@ def route_ws(moe, c):
     return torch.zeros(moe.route_grad_ws_bytes(c), dtype=torch.uint8, device="cuda")
 
 
-# 1024 choices: the last in one launch; 512 tokens: the first with a slab, whose columns are 128, 64
-# or 32 by the experts; lists whose last 32 choices are few; chunks of other lengths; the widest row
-BORDERS = [(128, 256, 16, 8), (129, 256, 16, 8), (1024, 128, 8, 1), (1025, 128, 8, 1),
-           (33, 256, 40, 32), (511, 384, 24, 3), (512, 384, 24, 3), (513, 384, 440, 2),
-           (600, 384, 460, 3), (600, 640, 1024, 32), (4097, 256, 64, 2), (5200, 128, 9, 7),
-           (21000, 128, 12, 3), (520, 65536, 4, 2), (2, 65536, 1024, 32)]
+# 512 choices: the last in one launch; 1024 tokens: the first with slabs, of 128 columns up to 437
+# experts, 64 up to 875; lists whose last 32 choices are few; chunks of other lengths; the widest row
+BORDERS = [(64, 256, 16, 8), (65, 256, 16, 8), (128, 256, 16, 8), (512, 128, 8, 1),
+           (513, 128, 8, 1), (17, 256, 40, 32), (33, 256, 40, 32), (511, 384, 24, 3),
+           (1023, 384, 24, 3), (1024, 384, 24, 3), (1030, 384, 437, 2), (1030, 384, 438, 2),
+           (1100, 384, 875, 3), (1100, 384, 876, 3), (1025, 128, 8, 1), (600, 640, 1024, 32),
+           (4097, 256, 64, 2), (5200, 128, 9, 7), (21000, 128, 12, 3), (520, 65536, 4, 2), (2, 65536, 1024, 32)]
 
 
 @pytest.mark.parametrize("T,d,E,k", BORDERS)
