@@ -28,7 +28,8 @@ BORDERS = [(64, 256, 16, 8), (65, 256, 16, 8), (128, 256, 16, 8), (512, 128, 8, 
            (513, 128, 8, 1), (17, 256, 40, 32), (33, 256, 40, 32), (511, 384, 24, 3),
            (1023, 384, 24, 3), (1024, 384, 24, 3), (1030, 384, 437, 2), (1030, 384, 438, 2),
            (1100, 384, 875, 3), (1100, 384, 876, 3), (1025, 128, 8, 1), (600, 640, 1024, 32),
-           (4097, 256, 64, 2), (5200, 128, 9, 7), (21000, 128, 12, 3), (520, 65536, 4, 2), (2, 65536, 1024, 32)]
+           (4097, 256, 64, 2), (5200, 128, 9, 7), (21000, 128, 12, 3),
+           (520, 65536, 4, 2), (2, 65536, 1024, 32)]
 
 
 @pytest.mark.parametrize("T,d,E,k", BORDERS)
