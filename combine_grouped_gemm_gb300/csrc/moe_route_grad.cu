@@ -16,8 +16,8 @@
 // 4. The segments' sums are joined in order: the result does not depend on the order of work.
 // A short batch takes one launch for all of it.
 //
-// Measured, d = 7168, 256 experts, 8 choices: 16384 tokens 260 us, 2048 tokens 52 (count 4, lists 3,
-// products 43, join 2), 64 tokens 8.6. The 16384 tokens' operands are 5.6 GB on their way through
+// Measured, d = 7168, 256 experts, 8 choices: 16384 tokens 247 us, 2048 tokens 51 (count 4, lists 3,
+// products 42, join 2), 64 tokens 8.6. The 16384 tokens' operands are 5.6 GB on their way through
 // the SMs' shared memory and L1, 155 us at 128 bytes a clock and SM, of which L2 hands out the
 // segments' rows at some 8 TB/s. (Tokens and gate weights one after the other, the latter summed
 // chunk by chunk in shared memory: 370 us; first form 3431.)
@@ -309,11 +309,6 @@ __device__ __forceinline__ void add8(f32x2 (&acc)[4], float z, const ulonglong2&
   acc[2] = fma2(z2, b.x, acc[2]);
   acc[3] = fma2(z2, b.y, acc[3]);
 }
-__device__ __forceinline__ void load8(f32x2 (&acc)[4], const uint4* at) {
-  const uint4 u = at ? *at : make_uint4(0, 0, 0, 0);
-  acc[0] = pair_of_bf16(u.x), acc[1] = pair_of_bf16(u.y);
-  acc[2] = pair_of_bf16(u.z), acc[3] = pair_of_bf16(u.w);
-}
 __device__ __forceinline__ uint4 bf16_of8(const f32x2* a) {
   return make_uint4(bf16_of_pair(a[0]), bf16_of_pair(a[1]), bf16_of_pair(a[2]), bf16_of_pair(a[3]));
 }
@@ -348,25 +343,48 @@ struct Args {
   long long per_cta;   // slab: (slab, token) pairs of a CTA
 };
 
-__device__ __forceinline__ void dx_item(const Args& a, int t, int v) {
-  const int vecs = a.d / 8;
-  if (v >= vecs) return;
-  const size_t at = (size_t)t * vecs + v;
+// A lane's 8 of 256 columns of a token's dx: 4 of the first half and 4 of the second (which the last
+// block may lack), so that neighbouring lanes read neighbouring 16 bytes of the gate weights.
+struct DxColumns {
+  size_t at;      // of the row's first columns
+  int c0, c1;     // the same as c0 where there is no second half
   f32x2 acc[4];
-  load8(acc, a.dx_in ? a.dx_in + at : nullptr);
+
+  __device__ __forceinline__ DxColumns(const Args& a, int t, int block)
+      : at((size_t)t * a.d), c0(block * 256 + (threadIdx.x & 31) * 4) {
+    c1 = block * 256 + 128 < a.d ? c0 + 128 : c0;
+    uint2 u = make_uint2(0, 0), v = u;
+    if (a.dx_in) {
+      const __nv_bfloat16* row = reinterpret_cast<const __nv_bfloat16*>(a.dx_in) + at;
+      u = *reinterpret_cast<const uint2*>(row + c0);
+      v = *reinterpret_cast<const uint2*>(row + c1);
+    }
+    acc[0] = pair_of_bf16(u.x), acc[1] = pair_of_bf16(u.y);
+    acc[2] = pair_of_bf16(v.x), acc[3] = pair_of_bf16(v.y);
+  }
+  __device__ __forceinline__ void add(const Args& a, int e, float dz) {
+    const float* w = a.w_gate + (size_t)e * a.d;
+    add8(acc, dz, *reinterpret_cast<const ulonglong2*>(w + c0),
+         *reinterpret_cast<const ulonglong2*>(w + c1));
+  }
+  __device__ __forceinline__ void store(const Args& a) const {
+    __nv_bfloat16* row = reinterpret_cast<__nv_bfloat16*>(a.dx) + at;
+    const uint4 o = bf16_of8(acc);
+    *reinterpret_cast<uint2*>(row + c0) = make_uint2(o.x, o.y);
+    if (c1 != c0) *reinterpret_cast<uint2*>(row + c1) = make_uint2(o.z, o.w);
+  }
+};
+
+__device__ __forceinline__ void dx_item(const Args& a, int t, int block) {
+  DxColumns c(a, t, block);
   const int4* two = reinterpret_cast<const int4*>(a.picks + (size_t)t * a.kp);
 #pragma unroll 2
   for (int i = 0; i < a.kp / 2; ++i) {
     const int4 p = two[i];   // expert, dz, expert, dz
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int e = j ? p.z : p.x;
-      if (e == a.E) continue;
-      const ulonglong2* w = reinterpret_cast<const ulonglong2*>(a.w_gate + (size_t)e * a.d) + 2 * v;
-      add8(acc, __int_as_float(j ? p.w : p.y), w[0], w[1]);
-    }
+    if (p.x != a.E) c.add(a, p.x, __int_as_float(p.y));
+    if (p.z != a.E) c.add(a, p.z, __int_as_float(p.w));
   }
-  a.dx[at] = bf16_of8(acc);
+  c.store(a);
 }
 
 // 32 choices of a warp's segment.
@@ -545,7 +563,7 @@ __global__ void __launch_bounds__(product_threads(C), product_ctas(C))
     const long long dx_items = (long long)a.T * blocks;
     for (long long i = item; i < dx_items; i += known) {
       const int t = static_cast<int>(i / blocks);
-      dx_item(a, t, static_cast<int>(i - (long long)t * blocks) * 32 + lane);
+      dx_item(a, t, static_cast<int>(i - (long long)t * blocks));
     }
   }
   while (item < items) {
@@ -630,20 +648,12 @@ __global__ void __launch_bounds__(kShortThreads) route_grad_short_kernel(
   const int items = dx_items + a.E * blocks, step = gridDim.x * kShortWarps;
   for (int item = blockIdx.x * kShortWarps + warp; item < items; item += step) {
     if (item < dx_items) {
-      const int t = item / blocks, v = (item - t * blocks) * 32 + lane;
-      if (v >= vecs) continue;
-      const size_t at = (size_t)t * vecs + v;
-      f32x2 acc[4];
-      load8(acc, a.dx_in ? a.dx_in + at : nullptr);
+      const int t = item / blocks;
+      DxColumns c(a, t, item - t * blocks);
 #pragma unroll 4
-      for (int i = t * kp; i < t * kp + kp; ++i) {
-        const int e = expert[i];
-        if (e == a.E) continue;
-        const float* w = a.w_gate + (size_t)e * a.d + 8 * v;
-        add8(acc, dz[i], *reinterpret_cast<const ulonglong2*>(w),
-             *reinterpret_cast<const ulonglong2*>(w + 4));
-      }
-      a.dx[at] = bf16_of8(acc);
+      for (int i = t * kp; i < t * kp + kp; ++i)
+        if (expert[i] != a.E) c.add(a, expert[i], dz[i]);
+      c.store(a);
       continue;
     }
     const int i = item - dx_items, e = i / blocks, v = (i - e * blocks) * 32 + lane;
@@ -734,10 +744,10 @@ cudaError_t launch_route_grad(const moe_cfg& c, const void* x, const float* w_ga
                     static_cast<const Pick*>(picks), static_cast<const int32_t*>(counts), c.T, L.kp,
                     c.E, L.chunk, L.chunks, L.segment, starts, segments, list);
   if (e != cudaSuccess) return e;
-  // Slabs of 128 columns up to 437 experts, of 64 up to 875, where the tokens are many: 256 experts, 8
-  // choices, 7168 columns, with and without: 16384 tokens 259 and 388 us, 1024 tokens 41 and 45, 512
-  // tokens 33 and 32; 800 experts: 16384 tokens 354 and 407, 2048 tokens 78 both. (With more experts
-  // slabs of 32 columns, whose rows share banks, were slower: 1024 experts, 16384 tokens 427 and 406.)
+  // Slabs of 128 columns up to 437 experts, of 64 up to 875, where the tokens are many. 8 choices, 7168
+  // columns, with and without: 256 experts, 16384 tokens 245 and 362 us, 1024 tokens 41 and 44; 800
+  // experts, 16384 tokens 352 and 383, 1024 tokens 59 and 56. (Slabs of 32 columns, for more experts,
+  // share banks: 1024 experts, 16384 tokens 427 us, without slabs 381.)
   const size_t row = 4 * (size_t)(c.E + 1), most = 227 * 1024 - staged_bytes(128);
   e = c.T < 1024          ? run_products<0>(a, st)
       : row * 128 <= most ? run_products<128>(a, st)
