@@ -9,6 +9,7 @@ If the shared library is missing, importing this package raises at once: build i
 from __future__ import annotations
 
 import ctypes
+import numbers
 import os
 
 import torch
@@ -548,6 +549,9 @@ def _norm_cfg(*key):
         if len(_norm_cfgs) >= 4096:   # sizes that differ from call to call
             _norm_cfgs.clear()
         rows, d, st, eps, res, out, gate = key
+        # (a tensor would be found again by its identity, whatever it holds by then)
+        if not all(isinstance(v, numbers.Real) for v in (eps, res, out)):
+            raise ValueError("moe_norm: eps, res_scale and out_scale must be numbers")
         c = _norm_cfgs[key] = ctypes.byref(NormCfg(
             rows, d, eps, res, out, MOE_F32 if st is torch.float32 else MOE_BF16, gate))
     return c

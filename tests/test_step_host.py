@@ -289,3 +289,16 @@ def test_train_block_checks_its_weights():
         kw = {"w_in": good, "w_out": good, "gate": good, name: w}
         with pytest.raises(ValueError, match=name):
             MoETrainBlock(cfg, None, None, {}, kw["w_in"], kw["w_out"], kw["gate"])
+
+
+def test_norm_factors_are_numbers():
+    """A tensor as a factor would be kept by its identity, with the value that it had first."""
+    import combine_grouped_gemm_gb300 as moe
+    x, w = torch.zeros(2, 8), torch.ones(8)
+    n = torch.empty(2, 8, dtype=torch.bfloat16)
+    for name in ("res_scale", "out_scale", "eps"):
+        for value in (torch.tensor(0.5), "1", None):
+            with pytest.raises(ValueError, match="numbers"):
+                moe.norm_out(n, x, w, None, None, x, None, **{name: value})
+    with pytest.raises(ValueError, match="numbers"):
+        moe.norm_in(x, w, n, eps=torch.tensor(1e-6))
