@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constan
 // ------------------------------------------------------------------------------------------
 constexpr int kStep8 = 8 * kThreads, kSteps8 = kChunk / kStep8;
 struct Stage8 {
-  uint4 g[2 * kThreads];   // bf16 gradients: the first half
+  uint4 g[2 * kThreads];   // bf16 gradients: half of it
   float4 p[2 * kThreads];
   uint2 m[kThreads], v[kThreads];
 };
@@ -534,6 +534,9 @@ __global__ void __launch_bounds__(kThreads, 4) adamw8_kernel(const __grid_consta
   const int put1 = LINES ? put0 + 32 : tid + kThreads;
   const int get0 = LINES ? warp0 + ((2 * lane) ^ ((lane >> 2) & 1)) : tid;
   const int get1 = LINES ? get0 ^ 1 : tid + kThreads;
+  // bf16 gradients: inside the places of the same warp (LINES: whose barriers order its lanes) or
+  // thread. A warp may be a chunk ahead of another, in a tensor of the other type.
+  const int own_bf16 = LINES ? warp0 + lane : tid;
   const auto copy = [&](uint32_t chunk, int i) {
     if (chunk < end) {
       const moe_adam_tensor& e = tab.t[t_in];
@@ -545,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 4) adamw8_kernel(const __grid_consta
         copy_in<16>(st.g + put0, static_cast<const float*>(e.g) + at0);
         copy_in<16>(st.g + put1, static_cast<const float*>(e.g) + at0 + kNext);
       } else {
-        copy_in<16>(st.g + tid, static_cast<const __nv_bfloat16*>(e.g) + at);
+        copy_in<16>(st.g + own_bf16, static_cast<const __nv_bfloat16*>(e.g) + at);
       }
       copy_in<16>(st.p + put0, e.p + at0);
       copy_in<16>(st.p + put1, e.p + at0 + kNext);
@@ -574,7 +577,7 @@ __global__ void __launch_bounds__(kThreads, 4) adamw8_kernel(const __grid_consta
         put4(f.g, *reinterpret_cast<const float4*>(st.g + get0));
         put4(f.g + 4, *reinterpret_cast<const float4*>(st.g + get1));
       } else {
-        const uint4 g = st.g[tid];
+        const uint4 g = st.g[own_bf16];
         put4(f.g, make_float4(bf16_lo(g.x), bf16_hi(g.x), bf16_lo(g.y), bf16_hi(g.y)));
         put4(f.g + 4, make_float4(bf16_lo(g.z), bf16_hi(g.z), bf16_lo(g.w), bf16_hi(g.w)));
       }
