@@ -574,11 +574,12 @@ typedef struct moe_adam_cfg {
  *   m  = b1 m + (1 - b1) g'                  v = b2 v + (1 - b2) g'^2
  *   p  = p - lr weight_decay p - lr/(1 - b1^t) m / (sqrt(v/(1 - b2^t)) + eps);   w = bf16(p)
  * p moves by the new moments in fp32, before they are put into 8 bits. There, q = |m| / scale or
- * q = sqrt(v) / scale (scale = amax * fp32(1/448) of the block, 1 if amax is 0; max_norm / norm is
- * max_norm * (1/norm); IEEE operations, each of these and of m and v above rounded by itself) is
- * rounded to a neighbouring code at random, by
- * 16 random bits an element from (seed, t, element), with odds that keep the mean of m and of v:
- * with nearest rounding a v with b2 near 1 would not move. A code of v is never 0 where v is not.
+ * q = sqrt(v) / scale (scale = amax * fp32(1/448) of the block; max_norm / norm is max_norm *
+ * (1/norm); IEEE operations, each of these and of m and v above rounded by itself) is rounded to a
+ * neighbouring code at random, by 16 random bits an element from (seed, t, element), with odds that
+ * keep the mean of m and of v: with nearest rounding a v with b2 near 1 would not move. A code of v
+ * is never 0 where v is not. A block whose scale would be below 2^-126 (of m: amax below 5e-36; a
+ * root of v is 0 or above 1e-23) has scale 1 and codes 0.
  * A NaN or an infinity spoils its block.
  * state: moe_adam_query bytes, zeroed once (step 0); it holds the status word, t, the bias
  * corrections and the partial sums of moe_grad_norm. The last call of a step advances t.

@@ -14,6 +14,14 @@ def moe():
     return m
 
 
+def whole_scales(x):
+    """x with the blocks as zeros whose scale, amax * fp32(1/448), is no normal number."""
+    f = np.float32
+    pad = np.concatenate([np.abs(x), np.zeros(-x.size % 128, f)]).reshape(-1, 128)
+    scale = pad.max(1) * (f(1) / f(448))
+    return np.where(np.repeat(scale >= f(2.0 ** -126), 128)[:x.size], x, f(0))
+
+
 def check_steps(a, b, steps):
     """a: a tensor after `steps` steps of AdamW in 8 bits, betas 0.9 and 0.99, from step 1 on; b: before
     them, with the same gradients. The codes and scales of the definition, each one."""
@@ -36,7 +44,7 @@ def check_steps(a, b, steps):
         place = (np.arange(128, dtype=np.uint64) * 0x9E3779B9).astype(np.uint32)
         r = mix(key[:, None] + place[None, :]).reshape(-1)
         for name, x, r16 in (("m", m, r >> np.uint32(16)), ("v", root, r & np.uint32(0xFFFF))):
-            codes[name], codes[name + "_scale"] = hold_reference(x, r16, name == "v")
+            codes[name], codes[name + "_scale"] = hold_reference(whole_scales(x), r16, name == "v")
     np.seterr(**old)
     for name in ("m", "v"):
         assert np.array_equal(a[name + "_scale"].cpu().numpy(), codes[name + "_scale"]), name
@@ -74,3 +82,61 @@ def test_adamw_8_bit_chunk_after_chunk(moe, sizes, gtypes):
         for k in ("p", "m", "v", "m_scale", "v_scale"):
             assert torch.equal(a[k], b[k]), (i, k)
         assert b["w"] is None or torch.equal(a["w"], b["w"])
+
+
+@pytest.mark.parametrize("n", [4096 * 700 + 1000, 3000])
+def test_adamw_8_bit_scales_near_the_end_of_the_range(moe, n):
+    """Moments whose block scales are 2^-149 to 2^-60, few codes above 0, and no gradient: codes and
+    scales as defined, code by code."""
+    T = adam_tensors([n], 8, [F32], seed=2, copies=False)
+    t = T[0]
+    blocks = (n + 127) // 128
+    t["m"].copy_(torch.randint(0, 127, (n,), device="cuda") *
+                 (torch.rand(n, device="cuda") < 0.1)).to(torch.uint8)
+    t["m_scale"].copy_(torch.exp2(torch.linspace(-149, -60, blocks, dtype=torch.float64,
+                                                 device="cuda")))
+    t["v"].fill_(0x38)
+    t["v_scale"].fill_(1e-5)
+    t["g"].zero_()
+    before = copy_of(T)[0]
+    cfg = moe.AdamCfg(lr=1e-3, beta1=0.9, beta2=0.99, eps=1e-8)
+    plan, state = moe.AdamTensors(T, state_bits=8), moe.adam_state(0, 0.9, 0.99)
+    for _ in range(2):
+        moe.adamw(cfg, plan, state)
+    check_steps(t, before, 2)
+
+
+def test_adamw_8_bit_moments_die_out(moe):
+    """No gradient for a thousand steps (an expert without tokens): the first moment's scales pass the
+    end of the fp32 range. The parameters stay finite, and the moment ends at 0."""
+    T = adam_tensors([128 * 9000 + 77], 8, [F32], seed=3, copies=False)
+    t = T[0]
+    t["g"].mul_(torch.rand(t["g"].shape, device="cuda") < 0.02)   # mostly zeros, a few a block
+    cfg = moe.AdamCfg(lr=1e-3, beta1=0.9, beta2=0.95, eps=1e-8)
+    plan, state = moe.AdamTensors(T, state_bits=8), moe.adam_state(0, 0.9, 0.95)
+    moe.adamw(cfg, plan, state)
+    t["g"].zero_()
+    for _ in range(1000):
+        moe.adamw(cfg, plan, state)
+    assert bool(torch.isfinite(t["p"]).all())
+    assert int((t["m"] & 127).max()) == 0 and bool((t["m_scale"] == 1).all())
+
+
+def test_adamw_8_bit_scales_that_underflow(moe):
+    """Ten million elements, nearly all codes 0, scales of 1 to 512 times 2^-149, no gradient."""
+    n = 128 * 80_000
+    T = adam_tensors([n], 8, [BF], seed=4, copies=False)
+    t = T[0]
+    t["m"][::128] = 0x7e
+    t["m_scale"].copy_(torch.arange(80_000, device="cuda", dtype=torch.float64) % 512 + 1)
+    t["m_scale"].mul_(2.0 ** -100).mul_(2.0 ** -49)
+    assert float(t["m_scale"][0]) == 2.0 ** -149 and float(t["m_scale"][511]) == 2.0 ** -140
+    t["v"].fill_(0x38)
+    t["v_scale"].fill_(1e-5)
+    t["g"].zero_()
+    plan, state = moe.AdamTensors(T, state_bits=8), moe.adam_state(0, 0.9, 0.99)
+    cfg = moe.AdamCfg(lr=1e-3, beta1=0.9, beta2=0.99, eps=1e-8)
+    for _ in range(3):
+        moe.adamw(cfg, plan, state)
+        assert bool(torch.isfinite(t["p"]).all())
+        assert int((t["m"] & 127).max()) == 0 and bool((t["m_scale"] == 1).all())
