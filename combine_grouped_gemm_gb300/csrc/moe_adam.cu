@@ -253,7 +253,12 @@ __device__ __forceinline__ void update(const Scalars& sc, float decay, float g, 
   p = __fmaf_rn(-sc.move, quot, __fmaf_rn(-decay, p, p));
 }
 
-// The largest of 16 lanes' non-negative numbers (their order is that of their bits).
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// The largest of 16 lanes' non-negative numbers (their order is that of their bits, a NaN last).
 __device__ __forceinline__ float half_warp_max(float v) {
   const uint32_t lanes = (threadIdx.x & 16) ? 0xffff0000u : 0xffffu;
   return __uint_as_float(__reduce_max_sync(lanes, __float_as_uint(v)));
@@ -295,9 +300,7 @@ __device__ __forceinline__ float round_root_e4m3(float q, float root, uint32_t r
   // below the lowest code, which the next lines make that code.)
   const float up = is_positive(__fadd_rn(odds, -__fmul_rn(r, whole)), 0x1p100f);
   const float u = __fmaf_rn(up, gap, lo), least = is_positive(root, 0x1p100f) * 0x1p-9f;
-  float v;   // (a NaN stays one)
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(v) : "f"(u), "f"(least));
-  return v;
+  return max_or_nan(u, least);
 }
 __device__ __forceinline__ uint32_t pack_codes(const float* v) {
   return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(v[0], v[1]), __NV_SATFINITE,
@@ -416,12 +419,12 @@ __device__ __forceinline__ void step_eight(const Scalars& sc, const moe_adam_ten
                                            uint32_t key, long long at, int cnt, Eight& f) {
   const long long block = at / kBlock;
   const int place = threadIdx.x & 15;
-  float root[8], am = 0.0f, av = 0.0f;   // (fmaxf leaves a NaN out)
+  float root[8], am = 0.0f, av = 0.0f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     update(sc, decay, f.g[j], f.p[j], f.m[j], f.v[j], root[j]);
-    am = fmaxf(am, fabsf(f.m[j]));
-    av = fmaxf(av, root[j]);
+    am = max_or_nan(am, fabsf(f.m[j]));
+    av = max_or_nan(av, root[j]);
   }
   __nv_bfloat16* w = static_cast<__nv_bfloat16*>(e.w) + at;
   if (cnt == 8) {
@@ -444,8 +447,9 @@ __device__ __forceinline__ void step_eight(const Scalars& sc, const moe_adam_ten
   const float amax = (threadIdx.x & 1) ? sv0 : sm0;
   // (A block whose scale would be no normal number, an amax below 5e-36, counts as zeros: its quotients
   // by 1 get code 0. Moments without gradients get there: 0.9 a step from 1e-4, 680 steps. The product
-  // by 1/448 reaches 0 before amax does, and a quotient 0/0 is none.)
-  const float part = __fmul_rn(amax, 1.0f / 448.0f), scale = part >= 0x1p-126f ? part : 1.0f;
+  // by 1/448 reaches 0 before amax does, and a quotient 0/0 is none. A NaN or an infinity in the block
+  // becomes the scale, whatever the codes are.)
+  const float part = __fmul_rn(amax, 1.0f / 448.0f), scale = part < 0x1p-126f ? 1.0f : part;
   const float inv = __frcp_rn(scale);
   // where the reciprocal, its correction and the quotient stay inside the fp32 range
   const bool plain = __all_sync(0xffffffffu, scale > 0x1p-60f && scale < 0x1p100f);

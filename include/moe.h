@@ -580,7 +580,7 @@ typedef struct moe_adam_cfg {
  * keep the mean of m and of v: with nearest rounding a v with b2 near 1 would not move. A code of v
  * is never 0 where v is not. A block whose scale would be below 2^-126 (of m: amax below 5e-36; a
  * root of v is 0 or above 1e-23) has scale 1 and codes 0.
- * A NaN or an infinity spoils its block.
+ * A NaN or an infinity in m or v spoils its block: it becomes the block's scale.
  * state: moe_adam_query bytes, zeroed once (step 0); it holds the status word, t, the bias
  * corrections and the partial sums of moe_grad_norm. The last call of a step advances t.
  * norm: NULL, or the device scalar of moe_grad_norm (needed with max_norm > 0). Where it is not

@@ -140,3 +140,33 @@ def test_adamw_8_bit_scales_that_underflow(moe):
         moe.adamw(cfg, plan, state)
         assert bool(torch.isfinite(t["p"]).all())
         assert int((t["m"] & 127).max()) == 0 and bool((t["m_scale"] == 1).all())
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_adamw_8_bit_what_spoils_a_block(moe, bad):
+    """A NaN or an infinity spoils its block (in whole chunks and past them) and no other: no value of
+    its moments is left, and the next step leaves no parameter of it."""
+    n = 3 * 4096 + 300
+    A = adam_tensors([n], 8, [F32], seed=6)
+    B = copy_of(A)
+    at = [5, 4096 + 128 * 7 + 127, 3 * 4096 + 128, n - 1]
+    spoilt = torch.zeros(n, dtype=torch.bool, device="cuda")
+    for i in at:
+        A[0]["g"][i] = bad
+        spoilt[i // 128 * 128:i // 128 * 128 + 128] = True
+    cfg = moe.AdamCfg(lr=1e-3, beta1=0.9, beta2=0.99, eps=1e-8)
+    pa, sa = moe.AdamTensors(A, state_bits=8), moe.adam_state(0, 0.9, 0.99)
+    pb, sb = moe.AdamTensors(B, state_bits=8), moe.adam_state(0, 0.9, 0.99)
+    a, b = A[0], B[0]
+    for step in range(3):
+        moe.adamw(cfg, pa, sa)
+        moe.adamw(cfg, pb, sb)
+        for k in ("m", "v"):
+            x = a[k].view(torch.float8_e4m3fn).float() * a[k + "_scale"].repeat_interleave(128)[:n]
+            assert torch.equal(~torch.isfinite(x), spoilt), (step, k)
+            assert torch.equal(a[k][~spoilt], b[k][~spoilt])
+        hit = spoilt if step else ~torch.isfinite(a["g"])
+        if step == 0:
+            a["g"].copy_(b["g"])
+        assert torch.equal(~torch.isfinite(a["p"]), hit), step
+        assert torch.equal(a["p"][~spoilt], b["p"][~spoilt])
