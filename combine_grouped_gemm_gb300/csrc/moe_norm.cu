@@ -461,8 +461,8 @@ struct ColSums {
   const float* partial;
   int ctas, d;
   int sides;                         // 1: yh, 2: hh, 3: both
-  const float *w_post, *gate;        // gate: a channel gate, else NULL
-  float *dw_post, *dgate, *dw_next;  // NULL: not wanted
+  const float *w_post, *gate;        // gate: a channel gate, else NULL (and NULL without rows)
+  float *dw_post, *dgate, *dw_next;  // NULL: not wanted; dgate: a channel gate's
   int accumulate;
 };
 constexpr int kColThreads = 512;
@@ -488,7 +488,7 @@ __global__ void __launch_bounds__(kColThreads) norm_columns_kernel(ColSums a) {
   if (y_side) {
     const float g = a.gate ? a.gate[c] : 1.0f, w = a.w_post ? a.w_post[c] : 1.0f;
     put(a.dw_post, g * sum);
-    if (a.gate) put(a.dgate, w * sum);
+    put(a.dgate, w * sum);
   } else {
     put(a.dw_next, sum);
   }

@@ -500,7 +500,8 @@ int moe_norm_out(const moe_norm_cfg* cfg, const void* y, const void* x, const fl
  *   dw_post = sum over rows of ds yh  dw_next = sum over rows of dn hh
  * dx (may take dh's place), dgate, dw_post, dw_next: NULL where not wanted; dy may take dn's place.
  * accumulate: dw_post, dw_next and a CHANNEL gate's dgate are added to. The sums do not depend on
- * the order in which the GPU runs the work. ws as in moe_norm_in_grad. */
+ * the order in which the GPU runs the work. ws as in moe_norm_in_grad. Without rows the gate, too,
+ * may be NULL, and the sums are 0. */
 int moe_norm_out_grad(const moe_norm_cfg* cfg, const void* dh, const void* dn, const void* y,
                       const void* h, const float* w_post, const void* gate, const float* w_next,
                       const float* rstd_y, const float* rstd_h, void* dx, void* dy, void* dgate,

@@ -1,9 +1,11 @@
 """Calls of the training step's operators that their documentation allows and that lie at its edges."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
 
-from test_step_gpu import BF, F32, adam_tensors, copy_of, e4m3_table, hold_reference, mix
+from test_step_gpu import BF, F32, adam_tensors, copy_of, e4m3_table, hold_reference, mix, normal
 
 pytestmark = pytest.mark.gpu
 
@@ -170,3 +172,25 @@ def test_adamw_8_bit_what_spoils_a_block(moe, bad):
             a["g"].copy_(b["g"])
         assert torch.equal(~torch.isfinite(a["p"]), hit), step
         assert torch.equal(a["p"][~spoilt], b["p"][~spoilt])
+
+
+@pytest.mark.parametrize("accumulate", [0, 1])
+def test_norm_gradient_of_no_rows(moe, accumulate):
+    """Without rows the weights' and the channel gate's gradients are 0 (or stay, accumulated), with
+    the gate or, since none of it is read, without."""
+    d = 192
+    w, gate = normal(0, d, dtype=F32), normal(1, d, dtype=F32)
+    ws = torch.empty(moe.norm_ws_bytes(0, d), dtype=torch.uint8, device="cuda")
+    cfg = moe.NormCfg(rows=0, d=d, eps=1e-6, res_scale=1.0, out_scale=1.0,
+                      stream_dtype=moe.MOE_BF16, gate=moe.MOE_GATE_CHANNEL)
+    for g in (gate.data_ptr(), None):
+        out = [torch.full((d,), 7.0 if accumulate else float("nan"), device="cuda")
+               for _ in range(3)]
+        dgate, dw_post, dw_next = [t.data_ptr() for t in out]
+        rc = moe._lib.moe_norm_out_grad(
+            ctypes.byref(cfg), None, None, None, None, w.data_ptr(), g, w.data_ptr(), None, None,
+            None, None, dgate, dw_post, dw_next, accumulate, ws.data_ptr(),
+            torch.cuda.current_stream().cuda_stream)
+        assert rc == 0
+        for t in out:
+            assert bool((t == (7.0 if accumulate else 0.0)).all())
