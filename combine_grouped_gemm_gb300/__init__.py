@@ -963,22 +963,29 @@ class MoEBlock:
         self.gate, self.w_next, self.eps = gate, w_next, eps
         self.scales = dict(res_scale=res_scale, out_scale=out_scale)
         shape, dev = (layer.cfg.T, layer.cfg.d), layer.w_gate.device
-        self.n = torch.empty(shape, dtype=torch.bfloat16, device=dev)
-        self.y = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        # the layer's input and output, and the n that the last call returned
+        self.rows = [torch.empty(shape, dtype=torch.bfloat16, device=dev)
+                     for _ in range(2 if w_next is None else 3)]
+        self._last = None
 
     def __call__(self, x, n=None, h=None, stream=None):
-        """h may be x itself. The n that is returned is a buffer of the block's own, which its next
-        call but one (or one without n) writes over."""
+        """h may be x itself. The n that is returned is a buffer of the block's own: the block's next
+        call leaves it as it is, whatever n that is given, and the one after it may write over it."""
+        free = [t for t in self.rows if t is not self._last]
         if n is None:
-            n = self.n
+            n = free.pop()
             norm_in(x, self.w_in, n, eps=self.eps, stream=stream)
         if h is None:
             h = torch.empty_like(x)
-        # (a block that is called with its own n, layers that share weights: the other buffer)
-        y = self.n if n.data_ptr() == self.y.data_ptr() else self.y
+        # (not n's place, where n is the block's own of an earlier call: layers that share weights)
+        y = next(t for t in free if t.data_ptr() != n.data_ptr())
         self.layer(n, y, stream)
+        if self.w_next is None:
+            norm_out(y, x, self.w_out, self.gate, None, h, None, eps=self.eps, stream=stream,
+                     **self.scales)
+            return h
         # the layer's output has been read where the next norm's takes its place
-        n_next = y if self.w_next is not None else None
-        norm_out(y, x, self.w_out, self.gate, self.w_next, h, n_next, eps=self.eps,
-                 stream=stream, **self.scales)
-        return h if n_next is None else (h, n_next)
+        norm_out(y, x, self.w_out, self.gate, self.w_next, h, y, eps=self.eps, stream=stream,
+                 **self.scales)
+        self._last = y
+        return h, y

@@ -1,10 +1,12 @@
 """Calls of the training step's operators that their documentation allows and that lie at its edges."""
 import ctypes
+import dataclasses
 
 import numpy as np
 import pytest
 import torch
 
+import synth
 from test_step_gpu import BF, F32, adam_tensors, copy_of, e4m3_table, hold_reference, mix, normal
 
 pytestmark = pytest.mark.gpu
@@ -194,3 +196,53 @@ def test_norm_gradient_of_no_rows(moe, accumulate):
         assert rc == 0
         for t in out:
             assert bool((t == (7.0 if accumulate else 0.0)).all())
+
+
+def serving_blocks(moe, T=24):
+    cfg = dataclasses.replace(synth.CONFIGS["tiny"], T=T, d_ff_shared=128)
+    inp = synth.make_router_inputs(cfg, "cuda")
+    W = synth.make_expert_weights(cfg, "cuda")
+    w = [normal(i, cfg.d, std=0.1, mean=1.0, dtype=F32) for i in range(5)]
+    layers = [moe.MoELayer(cfg, inp["w_gate"], inp["bias"], W) for _ in range(2)]
+    A = moe.MoEBlock(layers[0], w[0], w_out=w[1], w_next=w[2])
+    B = moe.MoEBlock(layers[1], w[2], w_out=w[3], w_next=w[4])
+    return cfg, A, B
+
+
+@pytest.mark.parametrize("given", ["another's n", "no n", "its own n", "its own n of before"])
+def test_serving_block_keeps_the_n_it_returned(moe, given):
+    """The n that a block returned is as it was after the block's next call, whatever n that is
+    given, and what the call gives does not depend on the buffer."""
+    cfg, A, _ = serving_blocks(moe)
+    xs = [normal(10 + i, cfg.T, cfg.d) for i in range(6)]
+    outside = [normal(20 + i, cfg.T, cfg.d) for i in range(6)]
+    kept, copies = [], []
+    for i in range(6):
+        n = {"another's n": outside[i], "no n": None,
+             "its own n": kept[-1] if kept else None,
+             "its own n of before": kept[-2] if i > 1 else None}[given]
+        fresh = None if n is None else n.clone()
+        h, m = A(xs[i], n)
+        if kept:
+            assert torch.equal(kept[-1], copies[-1]), i
+        _, other, _ = serving_blocks(moe)
+        h2, m2 = other(xs[i], fresh)
+        assert torch.equal(h, h2) and torch.equal(m, m2), i
+        kept.append(m)
+        copies.append(m.clone())
+
+
+def test_serving_two_batches_through_two_blocks(moe):
+    """Block A takes both micro-batches before block B takes the first."""
+    cfg, A, B = serving_blocks(moe)
+    xs = [normal(10 + i, cfg.T, cfg.d) for i in range(2)]
+    ns = [normal(20 + i, cfg.T, cfg.d) for i in range(2)]
+    want = []
+    for x, n in zip(xs, ns):
+        h, m = A(x, n)
+        h, m = B(h, m)
+        want.append((h.clone(), m.clone()))
+    mid = [A(x, n) for x, n in zip(xs, ns)]
+    for (h, m), (wh, wm) in zip(mid, want):
+        h, m = B(h, m)
+        assert torch.equal(h, wh) and torch.equal(m, wm)
