@@ -258,6 +258,8 @@ class AdamW:
                  state_bits=32, seed=0):
         self.tensors, self.names = [], list(params)
         for i, (weight, grad) in enumerate(params.values()):
+            if weight.requires_grad:   # (the same memory: a step is written into a leaf in place)
+                weight = weight.detach()
             own = weight.dtype is torch.float32
             p = weight if own else weight.float()
             n, dev = weight.numel(), weight.device
@@ -290,17 +292,27 @@ class AdamW:
 
     def state_dict(self):
         """Copies of everything a later load_state_dict needs."""
-        keys = ("p", "m", "v", "m_scale", "v_scale")
         return dict(state=self.state.clone(),
-                    tensors={n: {k: t[k].clone() for k in keys if k in t}
+                    tensors={n: {k: t[k].clone() for k in self._kept(t)}
                              for n, t in zip(self.names, self.tensors)})
 
+    @staticmethod
+    def _kept(t):
+        return [k for k in ("p", "m", "v", "m_scale", "v_scale") if k in t]
+
     def load_state_dict(self, saved):
+        """What state_dict gave, of an optimiser of the same weights and state_bits. One that does not
+        fit is a ValueError, before anything is written."""
         if set(saved["tensors"]) != set(self.names):
             raise ValueError("AdamW.load_state_dict: saved for other weights")
+        if saved["state"].shape != self.state.shape or saved["state"].dtype != self.state.dtype:
+            raise ValueError("AdamW.load_state_dict: state is of another kind")
         for n, t in zip(self.names, self.tensors):
-            for k, v in saved["tensors"][n].items():
-                if k not in t or t[k].shape != v.shape or t[k].dtype != v.dtype:
+            s = saved["tensors"][n]
+            if set(s) != set(self._kept(t)):
+                raise ValueError(f"AdamW.load_state_dict: {n}: saved with other moments")
+            for k, v in s.items():
+                if t[k].shape != v.shape or t[k].dtype != v.dtype:
                     raise ValueError(f"AdamW.load_state_dict: {n}: {k} is of another kind")
         for n, t in zip(self.names, self.tensors):
             for k, v in saved["tensors"][n].items():

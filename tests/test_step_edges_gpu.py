@@ -246,3 +246,43 @@ def test_serving_two_batches_through_two_blocks(moe):
     for (h, m), (wh, wm) in zip(mid, want):
         h, m = B(h, m)
         assert torch.equal(h, wh) and torch.equal(m, wm)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_adamw_of_parameters(moe, bits):
+    """Weights that require gradients: stepped, saved, loaded; and a load that is refused changes
+    nothing."""
+    from combine_grouped_gemm_gb300.train import AdamW
+
+    def make():
+        P = {"a": torch.nn.Parameter(normal(1, 40, 64, std=0.02, dtype=F32)),
+             "b": torch.nn.Parameter(normal(2, 8, 128, std=0.02))}
+        G = {n: normal(7, *p.shape, std=1e-3, dtype=p.dtype) for n, p in P.items()}
+        return P, AdamW({n: (p, G[n]) for n, p in P.items()}, lr=1e-3, state_bits=bits)
+    P, opt = make()
+    opt.step()
+    saved = opt.state_dict()
+    assert not any(v.requires_grad for t in saved["tensors"].values() for v in t.values())
+    opt.step()
+    after = {n: p.detach().clone() for n, p in P.items()}
+    opt.load_state_dict(saved)
+    opt.step()
+    Q, other = make()
+    other.load_state_dict(saved)
+    other.step()
+    for n in P:
+        assert torch.equal(P[n], after[n]) and torch.equal(Q[n], after[n])
+        assert P[n].requires_grad and P[n].is_leaf
+
+    def everything(o):
+        return [o.state] + [v for t in o.tensors for v in t.values() if isinstance(v, torch.Tensor)]
+    before = [v.clone() for v in everything(opt)]
+    less = {n: dict(t) for n, t in saved["tensors"].items()}
+    less["b"].pop("v")
+    short = {n: dict(t) for n, t in saved["tensors"].items()}
+    short["b"]["p"] = short["b"]["p"][:4]
+    for bad in (dict(saved, tensors=less), dict(saved, tensors=short),
+                dict(saved, state=saved["state"][:16])):
+        with pytest.raises(ValueError, match="load_state_dict"):
+            opt.load_state_dict(bad)
+        assert all(torch.equal(a, b) for a, b in zip(before, everything(opt)))
