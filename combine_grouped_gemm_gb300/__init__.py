@@ -5,6 +5,10 @@ and the current CUDA stream to the C ABI declared in include/moe.h, and raises M
 non-zero return code. All the work runs in the library's CUDA kernels; there is no fallback.
 If the shared library is missing, importing this package raises at once: build it with
 ``python combine_grouped_gemm_gb300/build.py``.
+
+A call runs on ``stream`` (None: the current one), and an output that it makes itself belongs to that
+stream, as if it had been made with the stream current. The buffers of a layer or block belong to the
+stream that was current when it was made: another one waits for that once, before its first call.
 """
 from __future__ import annotations
 
@@ -210,6 +214,19 @@ def _s(stream):
             return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _output(shape, dtype, device, stream):
+    """An output that a call on this stream makes. (From the current stream's memory it could be what
+    that stream has given back while its work still reads it.)"""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _s(stream)
+        stream = (torch.cuda.ExternalStream(handle, device=device) if handle > 1 else
+                  torch.cuda.default_stream(device))   # (0 and 1 are that one's names)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 _WEIGHT_KEYS = ("w13", "w13_s", "w2", "w2_s", "ws13", "ws13_s", "ws2", "ws2_s")
@@ -927,7 +944,7 @@ class MoELayer:
 
     def __call__(self, x, y=None, stream=None, events=None):
         if y is None:
-            y = torch.empty((self.cfg.T, self.cfg.d), dtype=torch.bfloat16, device=x.device)
+            y = _output((self.cfg.T, self.cfg.d), torch.bfloat16, x.device, stream)
         self._run(x, y, stream, events)
         return y
 
@@ -935,12 +952,12 @@ class MoELayer:
         """Host-to-host call: copies x_host (pinned bf16 [T][d]) to the device, runs the layer
         and copies the output back into y_host (pinned), all enqueued on the stream. The caller
         synchronises before reading y_host."""
-        if not hasattr(self, "_x_dev"):
-            self._x_dev = torch.empty((self.cfg.T, self.cfg.d), dtype=torch.bfloat16,
-                                      device=self.w_gate.device)
-            self._y_dev = torch.empty_like(self._x_dev)
         s = stream or torch.cuda.current_stream()
         with torch.cuda.stream(s):
+            if not hasattr(self, "_x_dev"):
+                self._x_dev = torch.empty((self.cfg.T, self.cfg.d), dtype=torch.bfloat16,
+                                          device=self.w_gate.device)
+                self._y_dev = torch.empty_like(self._x_dev)
             self._x_dev.copy_(x_host, non_blocking=True)
             self._run(self._x_dev, self._y_dev, s, None)
             y_host.copy_(self._y_dev, non_blocking=True)
@@ -976,7 +993,7 @@ class MoEBlock:
             n = free.pop()
             norm_in(x, self.w_in, n, eps=self.eps, stream=stream)
         if h is None:
-            h = torch.empty_like(x)
+            h = _output(x.shape, x.dtype, x.device, stream)
         # (not n's place, where n is the block's own of an earlier call: layers that share weights)
         y = next(t for t in free if t.data_ptr() != n.data_ptr())
         self.layer(n, y, stream)

@@ -10,8 +10,8 @@ from __future__ import annotations
 
 import torch
 
-from . import (AdamCfg, AdamTensors, Buffers, GroupCfg, MOE_BF16, act_load, act_save, adam_state,
-               adam_step, adamw, combine, combine_grad, dispatch, grad_norm, grouped_mm,
+from . import (AdamCfg, AdamTensors, Buffers, GroupCfg, MOE_BF16, _output, act_load, act_save,
+               adam_state, adam_step, adamw, combine, combine_grad, dispatch, grad_norm, grouped_mm,
                grouped_mm_dw, grouped_mm_dx, grouped_ws_bytes, make_cfg, norm_in, norm_in_grad,
                norm_out, norm_out_grad, norm_ws_bytes, route, route_grad, route_grad_ws_bytes,
                route_save, swiglu_grad, swiglu_save)
@@ -107,7 +107,7 @@ class MoETrainLayer:
                 raise ValueError(f"MoETrainLayer.forward: {name} must be a bf16 tensor {shape}")
         self._saved = False
         if y is None:
-            y = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
+            y = _output(shape, torch.bfloat16, x.device, stream)
         if self.train_router:
             route_save(self.cfg, x, self.w_gate, self.bias, b["topk_idx"], b["topk_w"],
                        self.topk_s, b["ws"], stream)
@@ -216,7 +216,7 @@ class MoETrainBlock:
             raise ValueError("MoETrainBlock.forward: x is kept for backward: h must be another")
         self._x = None
         if h is None:
-            h = torch.empty_like(x)
+            h = _output(x.shape, x.dtype, x.device, stream)
         norm_in(x, self.w_in, self.n, self.rstd_in, eps=self.eps, stream=stream)
         self.layer.forward(self.n, self.y, stream)
         norm_out(self.y, x, self.w_out, self.gate, None, h, None, self.rstd_out, None,

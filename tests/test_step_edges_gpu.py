@@ -286,3 +286,44 @@ def test_adamw_of_parameters(moe, bits):
         with pytest.raises(ValueError, match="load_state_dict"):
             opt.load_state_dict(bad)
         assert all(torch.equal(a, b) for a, b in zip(before, everything(opt)))
+
+
+@pytest.mark.parametrize("which", ["MoELayer", "MoEBlock", "MoETrainLayer", "MoETrainBlock"])
+def test_outputs_belong_to_the_stream_of_the_call(moe, which):
+    """An output that a call makes comes from the memory of the stream that it is given: not from what
+    the current stream has given back, which work of that stream may still read."""
+    from test_block_gpu import setup
+    cfg, inp, W, block, x, dh = setup(48)
+    make = {"MoELayer": lambda: moe.MoELayer(cfg, inp["w_gate"], inp["bias"], W),
+            "MoEBlock": lambda: moe.MoEBlock(moe.MoELayer(cfg, inp["w_gate"], inp["bias"], W),
+                                             block.w_in, w_next=block.w_in),
+            "MoETrainLayer": lambda: block.layer.forward, "MoETrainBlock": lambda: block.forward}
+    call = make[which]()
+    assert moe._output((3,), F32, "cuda", 0).shape == (3,)   # the default stream's handle
+    first = lambda out: out[0] if isinstance(out, tuple) else out   # noqa: E731
+    want = first(call(x)).clone()
+    for stream in (torch.cuda.Stream(), torch.cuda.Stream().cuda_stream):   # object and handle
+        torch.cuda.synchronize()
+        freed = [torch.empty_like(x) for _ in range(64)]
+        places = {t.data_ptr() for t in freed}
+        del freed
+        got = first(call(x, stream=stream))
+        torch.cuda.synchronize()
+        assert got.data_ptr() not in places
+        assert torch.equal(got, want)
+
+
+def test_host_call_on_another_stream(moe):
+    from test_block_gpu import setup
+    cfg, inp, W, block, x, dh = setup(48)
+    layer = moe.MoELayer(cfg, inp["w_gate"], inp["bias"], W)
+    want = layer(x).cpu()
+    x_host, y_host = x.cpu().pin_memory(), torch.empty_like(want).pin_memory()
+    torch.cuda.synchronize()
+    places = {t.data_ptr() for t in [torch.empty_like(x) for _ in range(64)]}
+    for s in (torch.cuda.Stream(), None):
+        y_host.zero_()
+        layer.run_host(x_host, y_host, s)
+        torch.cuda.synchronize()
+        assert torch.equal(y_host, want)
+    assert layer._x_dev.data_ptr() not in places and layer._y_dev.data_ptr() not in places
