@@ -87,7 +87,8 @@ class AdamTensorC(ctypes.Structure):
 
 
 class AdamCfg(ctypes.Structure):
-    """moe_adam_cfg: an AdamW step's rates. state_bits is set from the tensors' plan."""
+    """moe_adam_cfg: an AdamW step's rates. adamw takes state_bits from the tensors' plan and lr_dev
+    from its own argument, and writes nothing into the one that it is given."""
     _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
                 ("eps", ctypes.c_double), ("max_norm", ctypes.c_double),
                 ("lr_dev", ctypes.c_void_p), ("state_bits", ctypes.c_int32),
@@ -838,6 +839,7 @@ def adamw(cfg: AdamCfg, plan: AdamTensors, state, norm=None, stream=None, lr=Non
         if t is not None and (not isinstance(t, torch.Tensor) or t.dtype is not torch.float32
                               or t.numel() != 1):
             raise ValueError(f"{fn}: {name} must be an fp32 CUDA tensor of one element")
+    cfg = AdamCfg.from_buffer_copy(cfg)   # (the caller's may be another call's, too)
     cfg.state_bits = plan.state_bits
     cfg.lr_dev = None if lr is None else _here(fn, dev, "lr", lr)
     st, s = _adam_state(fn, dev, state), _stream(stream, dev)

@@ -1,6 +1,7 @@
 """Calls of the training step's operators that their documentation allows and that lie at its edges."""
 import ctypes
 import dataclasses
+import threading
 
 import numpy as np
 import pytest
@@ -327,3 +328,36 @@ def test_host_call_on_another_stream(moe):
         torch.cuda.synchronize()
         assert torch.equal(y_host, want)
     assert layer._x_dev.data_ptr() not in places and layer._y_dev.data_ptr() not in places
+
+
+def test_adamw_leaves_its_configuration(moe):
+    """One AdamCfg for several plans and threads: a call writes nothing into it."""
+    cfg = moe.AdamCfg(lr=1e-3, beta1=0.9, beta2=0.99, eps=1e-8)
+    was = bytes(cfg)
+    lr = torch.full((1,), 5e-4, device="cuda")
+    runs = []
+    for bits, rate in ((32, lr), (8, None), (32, None), (8, lr)):
+        T = adam_tensors([5000], bits, [F32], seed=bits)
+        runs.append((moe.AdamTensors(T, state_bits=bits), moe.adam_state(0, 0.9, 0.99), rate, T))
+    errors = []
+
+    def work(plan, state, rate, stream):
+        try:
+            for _ in range(200):
+                moe.adamw(cfg, plan, state, stream=stream, lr=rate)
+        except Exception as e:   # noqa: BLE001
+            errors.append(e)
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(*r[:3], torch.cuda.Stream())) for r in runs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors and bytes(cfg) == was
+    for plan, state, rate, T in runs:
+        U = adam_tensors([5000], plan.state_bits, [F32], seed=plan.state_bits)
+        p, s = moe.AdamTensors(U, state_bits=plan.state_bits), moe.adam_state(0, 0.9, 0.99)
+        for _ in range(200):
+            moe.adamw(cfg, p, s, lr=rate)
+        assert torch.equal(T[0]["p"], U[0]["p"])
