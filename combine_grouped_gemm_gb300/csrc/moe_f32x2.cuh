@@ -1,7 +1,7 @@
 // Pairs of fp32 numbers in one 64-bit register pair, for the instructions that work on both at
-// once: half as many instructions for sums and products. (The compiler joins a product and a sum of
-// pairs into one operation that rounds once. Where each is to be rounded by itself, scalars are
-// used.)
+// once: half as many instructions for products, and for those with a sum. (The compiler joins a
+// product and a sum of pairs into one operation that rounds once. Where each is to be rounded by
+// itself, scalars are used.)
 #pragma once
 
 #include <stdint.h>
@@ -30,17 +30,11 @@ __device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
-  f32x2 r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
   f32x2 r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
-__device__ __forceinline__ f32x2 minus(f32x2 v) { return v ^ 0x8000000080000000ull; }
 
 // Two bf16 values of a 32-bit word, and back.
 __device__ __forceinline__ f32x2 pair_of_bf16(uint32_t v) {
