@@ -123,7 +123,8 @@ __device__ __forceinline__ Pick pick_of(int e, float s, float g, bool in, int wi
     for (int o = width / 2; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
   };
-  const float p = s * (1.0f / sum_of_token(in ? s : 0.0f));
+  // (a quotient: the reciprocal of a sum below 3e-39, of logits near -90, would be infinite)
+  const float p = __fdiv_rn(s, sum_of_token(in ? s : 0.0f));
   const float dot = sum_of_token(in ? p * g : 0.0f);
   const bool live = in && e >= 0;
   if (!live) e = -1;

@@ -8,7 +8,8 @@ import pytest
 import torch
 
 import synth
-from test_step_gpu import BF, F32, adam_tensors, copy_of, e4m3_table, hold_reference, mix, normal
+from test_step_gpu import (BF, F32, adam_tensors, check_route, copy_of, e4m3_table, hold_reference,
+                           mix, normal, route_cfg, route_inputs)
 
 pytestmark = pytest.mark.gpu
 
@@ -361,3 +362,15 @@ def test_adamw_leaves_its_configuration(moe):
         for _ in range(200):
             moe.adamw(cfg, p, s, lr=rate)
         assert torch.equal(T[0]["p"], U[0]["p"])
+
+
+@pytest.mark.parametrize("T,k", [(40, 4), (400, 4), (1500, 1)])
+def test_route_grad_of_scores_near_zero(moe, T, k):
+    """Chosen experts with scores of 1e-42 to 1e-36 (logits near -90): the quotients s / sum s are what
+    they are for larger ones, as in the forward pass, though 1 / sum s has left the fp32 range."""
+    d, E = 256, 24
+    q = route_inputs(T, d, E, k, 0.0, seed=11)
+    q["s"] = torch.exp(normal(12, T, k, std=3.0, mean=-90.0, dtype=F32).double()).to(F32)
+    c = route_cfg(moe, T, d, E, k)
+    ws = torch.zeros(moe.route_grad_ws_bytes(c), dtype=torch.uint8, device="cuda")
+    check_route(moe, q, T, d, E, k, c, ws)
