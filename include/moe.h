@@ -470,7 +470,8 @@ typedef struct moe_norm_cfg {
 /* RMS norm before a block: r = 1/sqrt(mean_j x_j^2 + eps) of each row, n = bf16(x r w).
  * x [rows][d] of the stream's type, w fp32 [d], n bf16 [rows][d] (may take the place of a bf16 x),
  * rstd fp32 [rows]: r, kept for the gradient (NULL: not wanted). Squares and sums in fp32 here and
- * below: values past 1e19 leave its range. */
+ * below: values past 1e19 leave its range, and so do, with an eps of 0 or near it, rows of values that
+ * are all below 1e-18. */
 int moe_norm_in(const moe_norm_cfg* cfg, const void* x, const float* w, void* n, float* rstd,
                 cudaStream_t stream);
 
@@ -525,7 +526,8 @@ int moe_route_save(const moe_cfg* cfg, const void* x, const float* w_gate, const
  *   dx[t] = bf16(dx_in[t] + sum_i dz_i w_gate[e_i])          e_i = topk_idx[t][i]
  *   dw_gate[e] = sum of dz x[t] over the choices of e        fp32 [E][d]; accumulate: added to
  * x, dx_in (NULL: none), dx bf16 [T][d]; dx may take dx_in's place. Sums in fp32 in a fixed order.
- * A choice outside [0, E) gets no gradient and gives none (its p counts) and is reported
+ * A choice outside [0, E) gets no gradient and gives none (its p and its dtopk_w, which
+ * moe_combine_grad sets to 0, count in the sums over j) and is reported
  * (MOE_DEV_BOUNDS in the first word of ws; -1, a choice that was dropped, is not reported). Of cfg,
  * T, d, E, k and route_scale count; d <= 65536 and T * d < 2^37 (else MOE_ERR_UNSUPPORTED). ws:
  * moe_route_grad_query bytes; zero its first word once. Calls that may overlap on the GPU need
@@ -592,9 +594,10 @@ int moe_adamw(const moe_adam_cfg* cfg, const moe_adam_tensor* tensors, int32_t n
               void* state, const float* norm, cudaStream_t stream);
 
 /* norm = sqrt of the sum of all g^2 (device fp32 scalar; squares in fp32, so that a gradient past
- * 1e19 counts as infinite). Of the tensors, g, g_dtype and n count. With `more` the sum goes on in
- * the next call and norm is not written (a norm that was broken off is ended by a call with n = 0).
- * Calls that may overlap on the GPU need states of their own, here and in moe_adamw. */
+ * 1e19 counts as infinite and one below 1e-23 as 0). Of the tensors, g, g_dtype and n count. With
+ * `more` the sum goes on in the next call and norm is not written (a norm that was broken off is
+ * ended by a call with n = 0). Calls that may overlap on the GPU need states of their own, here and
+ * in moe_adamw. */
 int moe_grad_norm(const moe_adam_tensor* tensors, int32_t n, int32_t more, void* state,
                   float* norm, cudaStream_t stream);
 
