@@ -211,6 +211,8 @@ namespace {
 int check_route_grad(const moe_cfg* cfg) {
   MOE_CHECK_CFG(cfg);
   if (cfg->d > 65536 || (long long)cfg->T * cfg->d >= 1ll << 37) return MOE_ERR_UNSUPPORTED;
+  // (the kernels' 32-bit places in the lists run up to a segment past the last choice)
+  if ((long long)cfg->T * cfg->k > (1ll << 31) - 2048) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 }  // namespace

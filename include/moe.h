@@ -529,7 +529,8 @@ int moe_route_save(const moe_cfg* cfg, const void* x, const float* w_gate, const
  * A choice outside [0, E) gets no gradient and gives none (its p and its dtopk_w, which
  * moe_combine_grad sets to 0, count in the sums over j) and is reported
  * (MOE_DEV_BOUNDS in the first word of ws; -1, a choice that was dropped, is not reported). Of cfg,
- * T, d, E, k and route_scale count; d <= 65536 and T * d < 2^37 (else MOE_ERR_UNSUPPORTED). ws:
+ * T, d, E, k and route_scale count; d <= 65536, T * d < 2^37 and T * k <= 2^31 - 2048 (else
+ * MOE_ERR_UNSUPPORTED). ws:
  * moe_route_grad_query bytes; zero its first word once. Calls that may overlap on the GPU need
  * workspaces of their own. */
 int moe_route_grad(const moe_cfg* cfg, const void* x, const float* w_gate, const int32_t* topk_idx,
