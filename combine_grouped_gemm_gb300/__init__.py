@@ -220,10 +220,10 @@ def _s(stream):
 def _output(shape, dtype, device, stream):
     """An output that a call on this stream makes. (From the current stream's memory it could be what
     that stream has given back while its work still reads it.)"""
-    if stream is None:
+    handle = None if stream is None else _s(stream)
+    if handle is None or handle == _s(None):
         return torch.empty(shape, dtype=dtype, device=device)
     if not isinstance(stream, torch.cuda.Stream):
-        handle = _s(stream)
         stream = (torch.cuda.ExternalStream(handle, device=device) if handle > 1 else
                   torch.cuda.default_stream(device))   # (0 and 1 are that one's names)
     with torch.cuda.stream(stream):
